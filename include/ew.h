@@ -5,8 +5,8 @@
  * Plain C: no C++ or torch types.  Every operation takes device pointers, an
  * element count n and a HIP stream, validates its arguments on the host,
  * launches one kernel asynchronously on that stream (ew_batch: one per
- * EW_BATCH_MAX items; ew_batch_run: one for any number) and returns a
- * status.
+ * EW_BATCH_MAX items; ew_batch_run: one for any number; the row operators:
+ * up to three) and returns a status.
  *
  * Pages cited (by title and section):
  *   [HyperAI]   HyperAI article on optimising the Elementwise operator
@@ -24,7 +24,8 @@
  *             and keeps no pointer after the call returns (ew_batch and
  *             ew_batch_build alone take transient host memory for their
  *             overlap check).
- * Layout      One-dimensional, contiguous, n elements.  Pointers need only
+ * Layout      One-dimensional, contiguous, n elements (the row operators'
+ *             matrices: see their section).  Pointers need only
  *             element alignment (4 bytes for fp32, 2 bytes for 16-bit data);
  *             16-byte alignment is NOT required: the library peels a scalar
  *             head so that the output's body is 16-byte aligned, streams the
@@ -385,6 +386,210 @@ ew_status_t ew_saxpy_relu_f32(float alpha, const float *x, float *y, size_t n,
  * other operations; the bias pointer is checked after x and y. */
 ew_status_t ew_bias_relu_f32(const float *x, const float *bias, float *y,
                              size_t rows, size_t cols, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Row operators of language models                                          */
+/* ------------------------------------------------------------------------ */
+/* Operations that reduce along the rows of a matrix: the RMS norm with the
+ * residual's addition (plain and 8-bit output, gradient), log probabilities
+ * of given tokens (entropy, top alternatives, gradient) and distillation from
+ * a teacher's top logits (gradient).  Each has an f32, an f16 and a bf16
+ * form; 16-bit data are raw uint16_t bit patterns.
+ *
+ * Matrices    rows x cols, row-major, columns contiguous; row r starts
+ *             r * stride elements after the pointer (stride in elements, at
+ *             least cols; ignored for a single row).  Pointers and strides
+ *             need only element alignment; rows that start on 16-byte
+ *             boundaries are fastest.  Vectors and per-row outputs are
+ *             contiguous.
+ * Sizes       rows and cols below 2^31; offsets are 64-bit.  rows == 0
+ *             returns EW_OK without a launch (the gradient of the norm
+ *             still clears dweight).  cols == 0 returns EW_OK without a
+ *             launch for the norm; a row of logits without columns is a row
+ *             whose mask leaves nothing.
+ * Optional    A pointer documented as optional may be NULL.
+ * Workspace   Device memory of the caller's, 16-byte aligned, of at least the
+ *             bytes the _workspace function gives (EW_ERR_INVALID_ARG if
+ *             fewer are passed); its contents before the call do not matter
+ *             and nothing is kept in it.  0 bytes: it may be NULL.
+ * Aliasing    An output may be exactly an input matrix (same pointer and
+ *             stride) where the operation says so.  Views of one buffer that
+ *             interleave without sharing an element (equal strides, disjoint
+ *             columns) do not overlap.  Any other overlap of an output with
+ *             an input or another output returns EW_ERR_OVERLAP.
+ * Arithmetic  In binary32 (sums, statistics and gradients too), 16-bit data
+ *             widened exactly, each result rounded once to its type, nearest
+ *             even.  No atomics: a call repeated on the same device gives the
+ *             same bits.
+ * Launches    One to three kernels on the stream; nothing synchronises or
+ *             allocates, so calls can be captured in a HIP graph.
+ * Errors      As above, in the same order. */
+
+/* total = round(x + residual), rstd = 1 / sqrt(mean(total^2) + eps),
+ * y = round(total * rstd * weight), row by row.  The norm is that of the
+ * rounded total, which is what a later layer reads back.
+ * residual    optional: without it total is x itself
+ * total       optional, requires residual: the rounded sum
+ * rstd        optional, rows values: what the gradient needs
+ * eps         >= 0 and finite
+ * total may be exactly x or residual (the usual update in place); y may be
+ * exactly x or residual unless total is that one. */
+ew_status_t ew_rmsnorm_f32(const float *x, size_t x_stride, const float *weight,
+                           const float *residual, size_t residual_stride, float *y,
+                           size_t y_stride, float *total, size_t total_stride, float *rstd,
+                           size_t rows, size_t cols, float eps, hipStream_t stream);
+ew_status_t ew_rmsnorm_f16(const uint16_t *x, size_t x_stride, const uint16_t *weight,
+                           const uint16_t *residual, size_t residual_stride, uint16_t *y,
+                           size_t y_stride, uint16_t *total, size_t total_stride, float *rstd,
+                           size_t rows, size_t cols, float eps, hipStream_t stream);
+ew_status_t ew_rmsnorm_bf16(const uint16_t *x, size_t x_stride, const uint16_t *weight,
+                            const uint16_t *residual, size_t residual_stride, uint16_t *y,
+                            size_t y_stride, uint16_t *total, size_t total_stride, float *rstd,
+                            size_t rows, size_t cols, float eps, hipStream_t stream);
+
+/* The same norm with an 8-bit output: each group of columns of a row has
+ * scale = max(max |y| / 448, 2^-126) over its unrounded y, and
+ * q = e4m3(y / scale) (OCP e4m3fn, nearest even, largest value 448).  A NaN
+ * in a group makes its scale NaN.
+ * group       columns per scale: 16, 32, 64, 128 or 256 (the last group of a
+ *             row may be shorter), or 0 for one scale a row
+ * q           rows x cols bytes, row stride q_stride
+ * scales      rows x ceil(cols / group) floats (rows x 1 for group 0) */
+ew_status_t ew_rmsnorm_e4m3_f32(const float *x, size_t x_stride, const float *weight,
+                                const float *residual, size_t residual_stride, uint8_t *q,
+                                size_t q_stride, float *scales, size_t group, float *total,
+                                size_t total_stride, float *rstd, size_t rows, size_t cols,
+                                float eps, hipStream_t stream);
+ew_status_t ew_rmsnorm_e4m3_f16(const uint16_t *x, size_t x_stride, const uint16_t *weight,
+                                const uint16_t *residual, size_t residual_stride, uint8_t *q,
+                                size_t q_stride, float *scales, size_t group, uint16_t *total,
+                                size_t total_stride, float *rstd, size_t rows, size_t cols,
+                                float eps, hipStream_t stream);
+ew_status_t ew_rmsnorm_e4m3_bf16(const uint16_t *x, size_t x_stride, const uint16_t *weight,
+                                 const uint16_t *residual, size_t residual_stride, uint8_t *q,
+                                 size_t q_stride, float *scales, size_t group, uint16_t *total,
+                                 size_t total_stride, float *rstd, size_t rows, size_t cols,
+                                 float eps, hipStream_t stream);
+
+/* The norm's gradient.  x is the normed matrix (the forward call's total),
+ * rstd its statistic, dy the gradient of y and dtotal (optional) that of
+ * total; with n = cols, per row
+ *   dx = round(rstd*weight*dy - x*(rstd^3/n)*sum(x*weight*dy) + dtotal)
+ * (the gradient of the forward call's x and of its residual alike), and
+ *   dweight[c] = sum over rows of dy*x*rstd, in binary32 (optional).
+ * dx may be exactly dy, x or dtotal.  The workspace is needed for dweight
+ * only (without dweight it may be NULL). */
+size_t ew_rmsnorm_grad_workspace(size_t rows, size_t cols);
+ew_status_t ew_rmsnorm_grad_f32(const float *dy, size_t dy_stride, const float *x,
+                                size_t x_stride, const float *weight, const float *rstd,
+                                const float *dtotal, size_t dtotal_stride, float *dx,
+                                size_t dx_stride, float *dweight, void *workspace,
+                                size_t workspace_bytes, size_t rows, size_t cols,
+                                hipStream_t stream);
+ew_status_t ew_rmsnorm_grad_f16(const uint16_t *dy, size_t dy_stride, const uint16_t *x,
+                                size_t x_stride, const uint16_t *weight, const float *rstd,
+                                const uint16_t *dtotal, size_t dtotal_stride, uint16_t *dx,
+                                size_t dx_stride, float *dweight, void *workspace,
+                                size_t workspace_bytes, size_t rows, size_t cols,
+                                hipStream_t stream);
+ew_status_t ew_rmsnorm_grad_bf16(const uint16_t *dy, size_t dy_stride, const uint16_t *x,
+                                 size_t x_stride, const uint16_t *weight, const float *rstd,
+                                 const uint16_t *dtotal, size_t dtotal_stride, uint16_t *dx,
+                                 size_t dx_stride, float *dweight, void *workspace,
+                                 size_t workspace_bytes, size_t rows, size_t cols,
+                                 hipStream_t stream);
+
+/* Log probabilities of given tokens.  With s = scale * logits (scale finite
+ * and > 0: the reciprocal of a temperature), per row
+ *   lse     = log(sum exp(s))                           (optional)
+ *   logp    = s[target] - lse; 0 where target is outside [0, cols), as for
+ *             the padding positions of a batch
+ *   entropy = -sum p log p, p = exp(s - lse)            (optional)
+ *   top_ids, top_logp: the `top` most likely columns, most likely first,
+ *             ties to the lowest column, and their s - lse; rows x top
+ *             values, both or neither; top <= min(64, cols).
+ * A logit of -inf is masked: p = 0 and nothing of it enters the sums.  A row
+ * whose mask leaves nothing has lse = -inf, entropy 0, logp -inf (0 without
+ * a target) and top_logp -inf.  A row that holds a NaN or a scaled logit of
+ * +inf has NaN in lse, entropy, top_logp and the logp of a given target.  For
+ * the ranking a NaN counts as -inf, so top_ids always holds `top` different
+ * columns. */
+size_t ew_logprobs_workspace(size_t rows, size_t cols, size_t top);
+ew_status_t ew_logprobs_f32(const float *logits, size_t stride, const int64_t *targets,
+                            float *logp, float *entropy, float *lse, float *top_logp,
+                            int64_t *top_ids, size_t top, float scale, void *workspace,
+                            size_t workspace_bytes, size_t rows, size_t cols,
+                            hipStream_t stream);
+ew_status_t ew_logprobs_f16(const uint16_t *logits, size_t stride, const int64_t *targets,
+                            float *logp, float *entropy, float *lse, float *top_logp,
+                            int64_t *top_ids, size_t top, float scale, void *workspace,
+                            size_t workspace_bytes, size_t rows, size_t cols,
+                            hipStream_t stream);
+ew_status_t ew_logprobs_bf16(const uint16_t *logits, size_t stride, const int64_t *targets,
+                             float *logp, float *entropy, float *lse, float *top_logp,
+                             int64_t *top_ids, size_t top, float scale, void *workspace,
+                             size_t workspace_bytes, size_t rows, size_t cols,
+                             hipStream_t stream);
+
+/* Their gradient, from the forward call's lse (and entropy):
+ *   dlogits[c] = round(scale * (dlogp * (1[c == target] - p)
+ *                               - dentropy * p * (s - lse + entropy)))
+ * with no dlogp term in a row without a target; 0 where s is -inf and in a
+ * row whose mask leaves nothing (lse = -inf).  dentropy is optional, entropy
+ * required with it.  dlogits may be exactly logits. */
+ew_status_t ew_logprobs_grad_f32(const float *logits, size_t stride, const int64_t *targets,
+                                 const float *lse, const float *entropy, const float *dlogp,
+                                 const float *dentropy, float *dlogits, size_t dlogits_stride,
+                                 float scale, size_t rows, size_t cols, hipStream_t stream);
+ew_status_t ew_logprobs_grad_f16(const uint16_t *logits, size_t stride, const int64_t *targets,
+                                 const float *lse, const float *entropy, const float *dlogp,
+                                 const float *dentropy, uint16_t *dlogits,
+                                 size_t dlogits_stride, float scale, size_t rows, size_t cols,
+                                 hipStream_t stream);
+ew_status_t ew_logprobs_grad_bf16(const uint16_t *logits, size_t stride, const int64_t *targets,
+                                  const float *lse, const float *entropy, const float *dlogp,
+                                  const float *dentropy, uint16_t *dlogits,
+                                  size_t dlogits_stride, float scale, size_t rows, size_t cols,
+                                  hipStream_t stream);
+
+/* Distillation from a teacher's `kept` top logits: teacher and ids are
+ * rows x kept.  An entry whose id is outside [0, cols), or whose scaled
+ * teacher logit is -inf, is dropped; t is the softmax of scale * teacher over
+ * the entries that remain, and with s and lse as for the log probabilities
+ *   loss = sum t * (log t - (s[id] - lse))
+ * per row: 0 if no entry remains; entries whose t underflows (below 2^-126)
+ * add nothing; +inf if another entry meets a masked logit.  A column named twice counts twice.
+ * lse is optional.  scale is finite and > 0, kept <= 2^20. */
+size_t ew_distill_workspace(size_t rows, size_t cols);
+ew_status_t ew_distill_f32(const float *logits, size_t stride, const float *teacher,
+                           const int64_t *ids, size_t kept, float *loss, float *lse, float scale,
+                           void *workspace, size_t workspace_bytes, size_t rows, size_t cols,
+                           hipStream_t stream);
+ew_status_t ew_distill_f16(const uint16_t *logits, size_t stride, const float *teacher,
+                           const int64_t *ids, size_t kept, float *loss, float *lse, float scale,
+                           void *workspace, size_t workspace_bytes, size_t rows, size_t cols,
+                           hipStream_t stream);
+ew_status_t ew_distill_bf16(const uint16_t *logits, size_t stride, const float *teacher,
+                            const int64_t *ids, size_t kept, float *loss, float *lse, float scale,
+                            void *workspace, size_t workspace_bytes, size_t rows, size_t cols,
+                            hipStream_t stream);
+
+/* Its gradient, from the forward call's lse:
+ *   dlogits[c] = round(scale * dloss * (p - sum of t over entries naming c))
+ * and 0 where s is -inf, in a row without a kept entry and in a row whose
+ * mask leaves nothing.  dlogits may be exactly logits. */
+ew_status_t ew_distill_grad_f32(const float *logits, size_t stride, const float *teacher,
+                                const int64_t *ids, size_t kept, const float *lse,
+                                const float *dloss, float *dlogits, size_t dlogits_stride,
+                                float scale, size_t rows, size_t cols, hipStream_t stream);
+ew_status_t ew_distill_grad_f16(const uint16_t *logits, size_t stride, const float *teacher,
+                                const int64_t *ids, size_t kept, const float *lse,
+                                const float *dloss, uint16_t *dlogits, size_t dlogits_stride,
+                                float scale, size_t rows, size_t cols, hipStream_t stream);
+ew_status_t ew_distill_grad_bf16(const uint16_t *logits, size_t stride, const float *teacher,
+                                 const int64_t *ids, size_t kept, const float *lse,
+                                 const float *dloss, uint16_t *dlogits, size_t dlogits_stride,
+                                 float scale, size_t rows, size_t cols, hipStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Status, launch configuration and planning                                */

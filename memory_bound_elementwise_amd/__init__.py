@@ -13,11 +13,13 @@ current stream on the output's device (an integer ``hipStream_t`` is also
 accepted).  Calls are asynchronous, like the C functions.  A tensor argument
 must hold elements of the operation's width, be contiguous, hold at least the
 n elements the call covers and live on a GPU (a strided view's source: every
-element the view touches must lie in its storage); otherwise TypeError or
+element the view touches must lie in its storage; a row operator's matrix:
+rows may lie a stride apart); otherwise TypeError or
 ValueError is raised before the library is called.  Raw integer addresses are
 the caller's responsibility.
 """
 import ctypes
+import math
 import os
 
 __all__ = [
@@ -32,7 +34,13 @@ __all__ = [
     "ew_get_launch_row", "ew_reset_launch_config", "ew_load_launch_table", "ew_make_plan",
     "ew_make_gather_plan", "ew_make_copy2d_plan", "PATHS", "ew_batch", "ew_batch_build",
     "ew_batch_run", "ew_batch_run_static", "BATCH_SCRATCH_BYTES", "EwBatch", "EwBatchItem",
-    "EwBatchPlan", "BATCH_MAX",
+    "EwBatchPlan", "BATCH_MAX", "TOP_MAX", "ew_rmsnorm_f32", "ew_rmsnorm_f16", "ew_rmsnorm_bf16",
+    "ew_rmsnorm_e4m3_f32", "ew_rmsnorm_e4m3_f16", "ew_rmsnorm_e4m3_bf16",
+    "ew_rmsnorm_grad_f32", "ew_rmsnorm_grad_f16", "ew_rmsnorm_grad_bf16",
+    "ew_rmsnorm_grad_workspace", "ew_logprobs_f32", "ew_logprobs_f16", "ew_logprobs_bf16",
+    "ew_logprobs_grad_f32", "ew_logprobs_grad_f16", "ew_logprobs_grad_bf16",
+    "ew_logprobs_workspace", "ew_distill_f32", "ew_distill_f16", "ew_distill_bf16",
+    "ew_distill_grad_f32", "ew_distill_grad_f16", "ew_distill_grad_bf16", "ew_distill_workspace",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -96,6 +104,7 @@ class EwBatchPlan(ctypes.Structure):
                 ("total_n", ctypes.c_uint64)]
 
 
+TOP_MAX = 64            # most alternatives ew_logprobs_* ranks
 BATCH_MAX = 96          # EW_BATCH_MAX: items per kernel launch of ew_batch
 BATCH_SCRATCH_BYTES = 256 * 1024   # EW_BATCH_SCRATCH_BYTES: largest table of ew_batch_run_static
 
@@ -160,6 +169,28 @@ _c = {
                                   ctypes.POINTER(EwPlan)),
     "ew_make_copy2d_plan": _proto("ew_make_copy2d_plan", _int, _vp, ctypes.c_int64,
                                   ctypes.c_int64, _vp, _sz, _sz, _int, ctypes.POINTER(EwPlan)),
+    **{f"ew_rmsnorm_{d}": _proto(f"ew_rmsnorm_{d}", _int, _vp, _sz, _vp, _vp, _sz, _vp, _sz, _vp,
+                                 _sz, _vp, _sz, _sz, ctypes.c_float, _vp) for d in MAP_DTYPES},
+    **{f"ew_rmsnorm_e4m3_{d}": _proto(f"ew_rmsnorm_e4m3_{d}", _int, _vp, _sz, _vp, _vp, _sz, _vp,
+                                      _sz, _vp, _sz, _vp, _sz, _vp, _sz, _sz, ctypes.c_float, _vp)
+       for d in MAP_DTYPES},
+    **{f"ew_rmsnorm_grad_{d}": _proto(f"ew_rmsnorm_grad_{d}", _int, _vp, _sz, _vp, _sz, _vp, _vp,
+                                      _vp, _sz, _vp, _sz, _vp, _vp, _sz, _sz, _sz, _vp)
+       for d in MAP_DTYPES},
+    **{f"ew_logprobs_{d}": _proto(f"ew_logprobs_{d}", _int, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _sz, ctypes.c_float, _vp, _sz, _sz, _sz, _vp)
+       for d in MAP_DTYPES},
+    **{f"ew_logprobs_grad_{d}": _proto(f"ew_logprobs_grad_{d}", _int, _vp, _sz, _vp, _vp, _vp, _vp,
+                                       _vp, _vp, _sz, ctypes.c_float, _sz, _sz, _vp)
+       for d in MAP_DTYPES},
+    **{f"ew_distill_{d}": _proto(f"ew_distill_{d}", _int, _vp, _sz, _vp, _vp, _sz, _vp, _vp,
+                                 ctypes.c_float, _vp, _sz, _sz, _sz, _vp) for d in MAP_DTYPES},
+    **{f"ew_distill_grad_{d}": _proto(f"ew_distill_grad_{d}", _int, _vp, _sz, _vp, _vp, _sz, _vp,
+                                      _vp, _vp, _sz, ctypes.c_float, _sz, _sz, _vp)
+       for d in MAP_DTYPES},
+    "ew_rmsnorm_grad_workspace": _proto("ew_rmsnorm_grad_workspace", _sz, _sz, _sz),
+    "ew_logprobs_workspace": _proto("ew_logprobs_workspace", _sz, _sz, _sz, _sz),
+    "ew_distill_workspace": _proto("ew_distill_workspace", _sz, _sz, _sz),
 }
 
 
@@ -566,6 +597,359 @@ def ew_batch(op, items, alpha=0.0, stream=None):
     of items in one launch per call).  stream defaults to torch's current
     stream on the first tensor's device."""
     EwBatch(op, items, table=False)(alpha, stream)
+
+
+# ---------------------------------------------------------------------------
+# Row operators.  A matrix argument is a tensor whose last dimension is
+# contiguous: one row (1-D), rows a fixed stride apart (2-D), or contiguous
+# with more dimensions (the leading ones are the rows); or an integer address
+# of contiguous rows.  rows and cols default to the first matrix argument's.
+# ---------------------------------------------------------------------------
+
+def _shape(x, rows, cols, role):
+    """(rows, cols) of the call: as given, or of the matrix argument x."""
+    if rows is None or cols is None:
+        if isinstance(x, int):
+            raise ValueError("rows and cols are required when buffers are raw pointers")
+        shape = x.shape
+        if len(shape) == 2:
+            return shape
+        if not shape:
+            raise ValueError(f"{role}: a scalar has no rows")
+        cols = shape[-1]
+        rows = math.prod(shape[:-1])
+    return int(rows), int(cols)
+
+
+def _mat(x, es, rows, cols, role):
+    """(address, row stride) of a matrix argument, checked as _buf checks a
+    contiguous one."""
+    if x is None:
+        return None, 0
+    if isinstance(x, int):
+        return x, cols
+    if x.is_cuda and x.element_size() == es and x.shape == (rows, cols):
+        stride, step = x.stride()
+        if step == 1 and stride >= cols:
+            return x.data_ptr(), stride
+    if x.element_size() != es:
+        raise TypeError(f"{role}: {x.dtype} has {x.element_size()}-byte elements, "
+                        f"the operation takes {es}-byte elements")
+    if x.shape != (rows, cols) and (not x.dim() or x.shape[-1] != cols
+                                    or x.numel() != rows * cols):
+        raise ValueError(f"{role}: shape {tuple(x.shape)}, the call covers {rows} rows of {cols}")
+    stride = cols
+    if x.dim() == 2 and rows > 1 and cols:
+        stride = x.stride(0)
+        if stride < cols or (x.stride(1) != 1 and cols > 1):
+            raise ValueError(f"{role}: strides {x.stride()}; a row's elements must be contiguous "
+                             "and rows must not overlap")
+    elif not x.is_contiguous():
+        raise ValueError(f"{role}: the tensor is not contiguous")
+    if not x.is_cuda:
+        raise ValueError(f"{role}: the tensor is on {x.device}, not on a GPU")
+    return x.data_ptr(), stride
+
+
+def _ids64(x, n, role):
+    """Address of n 64-bit column numbers."""
+    if x is not None and not isinstance(x, int) and x.dtype is not torch.int64:
+        raise TypeError(f"{role}: {x.dtype}, the operation takes int64 columns")
+    return _buf(x, 8, n, role)
+
+
+def _space(x, need):
+    """(address, bytes) of a workspace; an integer address is taken to hold
+    the bytes the call needs."""
+    if x is None:
+        if need:
+            raise ValueError(f"workspace: the call needs {need} bytes")
+        return None, 0
+    if isinstance(x, int):
+        return x, need
+    size = x.numel() * x.element_size()
+    if not x.is_contiguous():
+        raise ValueError("workspace: the tensor is not contiguous")
+    if size < need:
+        raise ValueError(f"workspace: {size} bytes, the call needs {need}")
+    if not x.is_cuda:
+        raise ValueError(f"workspace: the tensor is on {x.device}, not on a GPU")
+    return x.data_ptr(), size
+
+
+def _rmsnorm(name, es, x, weight, y, residual, total, rstd, eps, rows, cols, stream):
+    rows, cols = _shape(x, rows, cols, "x")
+    px, sx = _mat(x, es, rows, cols, "x")
+    pr, sr = _mat(residual, es, rows, cols, "residual")
+    py, sy = _mat(y, es, rows, cols, "y")
+    pt, st = _mat(total, es, rows, cols, "total")
+    _check(_c[name](px, sx, _buf(weight, es, cols, "weight"), pr, sr, py, sy, pt, st,
+                    _buf(rstd, 4, rows, "rstd"), rows, cols, eps, _stream(y, stream)), name)
+
+
+def ew_rmsnorm_f32(x, weight, y, residual=None, total=None, rstd=None, eps=1e-5, rows=None,
+                   cols=None, stream=None):
+    """total = x + residual, y = total / sqrt(mean(total^2) + eps) * weight, row by row
+    (binary32); rstd receives 1 / sqrt(mean(total^2) + eps).  Without a
+    residual the norm is x's.  total may be x or residual, y whichever of
+    them total is not."""
+    _rmsnorm("ew_rmsnorm_f32", 4, x, weight, y, residual, total, rstd, eps, rows, cols, stream)
+
+
+def ew_rmsnorm_f16(x, weight, y, residual=None, total=None, rstd=None, eps=1e-5, rows=None,
+                   cols=None, stream=None):
+    """ew_rmsnorm_f32 on binary16 data: sums in binary32, total and y rounded once each."""
+    _rmsnorm("ew_rmsnorm_f16", 2, x, weight, y, residual, total, rstd, eps, rows, cols, stream)
+
+
+def ew_rmsnorm_bf16(x, weight, y, residual=None, total=None, rstd=None, eps=1e-5, rows=None,
+                    cols=None, stream=None):
+    """ew_rmsnorm_f32 on bfloat16 data: sums in binary32, total and y rounded once each."""
+    _rmsnorm("ew_rmsnorm_bf16", 2, x, weight, y, residual, total, rstd, eps, rows, cols, stream)
+
+
+def _rmsnorm_e4m3(name, es, x, weight, q, scales, group, residual, total, rstd, eps, rows, cols,
+                  stream):
+    rows, cols = _shape(x, rows, cols, "x")
+    px, sx = _mat(x, es, rows, cols, "x")
+    pr, sr = _mat(residual, es, rows, cols, "residual")
+    pq, sq = _mat(q, 1, rows, cols, "q")
+    pt, st = _mat(total, es, rows, cols, "total")
+    group = int(group)
+    if group < 0:
+        raise ValueError(f"group: {group}")
+    groups = -(-cols // group) if group else 1
+    _check(_c[name](px, sx, _buf(weight, es, cols, "weight"), pr, sr, pq, sq,
+                    _buf(scales, 4, rows * groups, "scales"), group, pt, st,
+                    _buf(rstd, 4, rows, "rstd"), rows, cols, eps, _stream(q, stream)), name)
+
+
+def ew_rmsnorm_e4m3_f32(x, weight, q, scales, group=128, residual=None, total=None, rstd=None,
+                        eps=1e-5, rows=None, cols=None, stream=None):
+    """The norm of ew_rmsnorm_f32 in 8 bits: per group of columns (16, 32, 64,
+    128 or 256; 0: the whole row) scale = max(max|y| / 448, 2^-126) and
+    q = e4m3(y / scale), y unrounded."""
+    _rmsnorm_e4m3("ew_rmsnorm_e4m3_f32", 4, x, weight, q, scales, group, residual, total, rstd,
+                  eps, rows, cols, stream)
+
+
+def ew_rmsnorm_e4m3_f16(x, weight, q, scales, group=128, residual=None, total=None, rstd=None,
+                        eps=1e-5, rows=None, cols=None, stream=None):
+    """ew_rmsnorm_e4m3_f32 on binary16 data."""
+    _rmsnorm_e4m3("ew_rmsnorm_e4m3_f16", 2, x, weight, q, scales, group, residual, total, rstd,
+                  eps, rows, cols, stream)
+
+
+def ew_rmsnorm_e4m3_bf16(x, weight, q, scales, group=128, residual=None, total=None, rstd=None,
+                         eps=1e-5, rows=None, cols=None, stream=None):
+    """ew_rmsnorm_e4m3_f32 on bfloat16 data."""
+    _rmsnorm_e4m3("ew_rmsnorm_e4m3_bf16", 2, x, weight, q, scales, group, residual, total, rstd,
+                  eps, rows, cols, stream)
+
+
+def ew_rmsnorm_grad_workspace(rows, cols):
+    """Bytes of workspace ew_rmsnorm_grad_* needs for dweight."""
+    return _c["ew_rmsnorm_grad_workspace"](int(rows), int(cols))
+
+
+def _rmsnorm_grad(name, es, dy, x, weight, rstd, dx, dweight, workspace, dtotal, rows, cols,
+                  stream):
+    rows, cols = _shape(dy, rows, cols, "dy")
+    pdy, sdy = _mat(dy, es, rows, cols, "dy")
+    px, sx = _mat(x, es, rows, cols, "x")
+    pdt, sdt = _mat(dtotal, es, rows, cols, "dtotal")
+    pdx, sdx = _mat(dx, es, rows, cols, "dx")
+    need = _c["ew_rmsnorm_grad_workspace"](rows, cols) if dweight is not None else 0
+    ws, size = _space(workspace, need)
+    _check(_c[name](pdy, sdy, px, sx, _buf(weight, es, cols, "weight"),
+                    _buf(rstd, 4, rows, "rstd"), pdt, sdt, pdx, sdx,
+                    _buf(dweight, 4, cols, "dweight"), ws, size, rows, cols,
+                    _stream(dx, stream)), name)
+
+
+def ew_rmsnorm_grad_f32(dy, x, weight, rstd, dx, dweight=None, workspace=None, dtotal=None,
+                        rows=None, cols=None, stream=None):
+    """Gradient of the RMS norm: x is the normed matrix (the forward call's
+    total), dx = rstd*weight*dy - x*rstd^3*mean(x*weight*dy) + dtotal and
+    dweight = sum over rows of dy*x*rstd (binary32).  dx may be dy, x or dtotal."""
+    _rmsnorm_grad("ew_rmsnorm_grad_f32", 4, dy, x, weight, rstd, dx, dweight, workspace, dtotal,
+                  rows, cols, stream)
+
+
+def ew_rmsnorm_grad_f16(dy, x, weight, rstd, dx, dweight=None, workspace=None, dtotal=None,
+                        rows=None, cols=None, stream=None):
+    """ew_rmsnorm_grad_f32 on binary16 data (dweight in binary32)."""
+    _rmsnorm_grad("ew_rmsnorm_grad_f16", 2, dy, x, weight, rstd, dx, dweight, workspace, dtotal,
+                  rows, cols, stream)
+
+
+def ew_rmsnorm_grad_bf16(dy, x, weight, rstd, dx, dweight=None, workspace=None, dtotal=None,
+                         rows=None, cols=None, stream=None):
+    """ew_rmsnorm_grad_f32 on bfloat16 data (dweight in binary32)."""
+    _rmsnorm_grad("ew_rmsnorm_grad_bf16", 2, dy, x, weight, rstd, dx, dweight, workspace, dtotal,
+                  rows, cols, stream)
+
+
+def ew_logprobs_workspace(rows, cols, top=0):
+    """Bytes of workspace ew_logprobs_* needs."""
+    return _c["ew_logprobs_workspace"](int(rows), int(cols), int(top))
+
+
+def _logprobs(name, es, logits, targets, logp, entropy, lse, top_logp, top_ids, scale, workspace,
+              rows, cols, top, stream):
+    rows, cols = _shape(logits, rows, cols, "logits")
+    if top is None:
+        if isinstance(top_ids, int):
+            raise ValueError("top is required when top_ids is a raw pointer")
+        top = top_ids.shape[-1] if top_ids is not None and top_ids.dim() else 0
+    top = int(top)
+    p, stride = _mat(logits, es, rows, cols, "logits")
+    ws, size = _space(workspace, _c["ew_logprobs_workspace"](rows, cols, top))
+    _check(_c[name](p, stride, _ids64(targets, rows, "targets"), _buf(logp, 4, rows, "logp"),
+                    _buf(entropy, 4, rows, "entropy"), _buf(lse, 4, rows, "lse"),
+                    _buf(top_logp, 4, rows * top, "top_logp"),
+                    _ids64(top_ids, rows * top, "top_ids"), top, scale, ws, size, rows, cols,
+                    _stream(logp, stream)), name)
+
+
+def ew_logprobs_f32(logits, targets, logp, entropy=None, lse=None, top_logp=None, top_ids=None,
+                    scale=1.0, workspace=None, rows=None, cols=None, top=None, stream=None):
+    """Log probabilities of each row's target under softmax(scale * logits) (0
+    where the target is outside [0, cols)), with the entropy, the log of the
+    sum and the most likely columns of each row (top_logp and top_ids: rows x
+    top, ties to the lowest column).  Logits of -inf are masked."""
+    _logprobs("ew_logprobs_f32", 4, logits, targets, logp, entropy, lse, top_logp, top_ids, scale,
+              workspace, rows, cols, top, stream)
+
+
+def ew_logprobs_f16(logits, targets, logp, entropy=None, lse=None, top_logp=None, top_ids=None,
+                    scale=1.0, workspace=None, rows=None, cols=None, top=None, stream=None):
+    """ew_logprobs_f32 on binary16 logits."""
+    _logprobs("ew_logprobs_f16", 2, logits, targets, logp, entropy, lse, top_logp, top_ids, scale,
+              workspace, rows, cols, top, stream)
+
+
+def ew_logprobs_bf16(logits, targets, logp, entropy=None, lse=None, top_logp=None, top_ids=None,
+                     scale=1.0, workspace=None, rows=None, cols=None, top=None, stream=None):
+    """ew_logprobs_f32 on bfloat16 logits."""
+    _logprobs("ew_logprobs_bf16", 2, logits, targets, logp, entropy, lse, top_logp, top_ids, scale,
+              workspace, rows, cols, top, stream)
+
+
+def _logprobs_grad(name, es, logits, targets, lse, dlogp, dlogits, entropy, dentropy, scale, rows,
+                   cols, stream):
+    rows, cols = _shape(logits, rows, cols, "logits")
+    p, stride = _mat(logits, es, rows, cols, "logits")
+    pd, sd = _mat(dlogits, es, rows, cols, "dlogits")
+    _check(_c[name](p, stride, _ids64(targets, rows, "targets"), _buf(lse, 4, rows, "lse"),
+                    _buf(entropy, 4, rows, "entropy"), _buf(dlogp, 4, rows, "dlogp"),
+                    _buf(dentropy, 4, rows, "dentropy"), pd, sd, scale, rows, cols,
+                    _stream(dlogits, stream)), name)
+
+
+def ew_logprobs_grad_f32(logits, targets, lse, dlogp, dlogits, entropy=None, dentropy=None,
+                         scale=1.0, rows=None, cols=None, stream=None):
+    """Gradient of the log probabilities (and, with dentropy, of the entropy)
+    by the logits, from the forward call's lse (and entropy).  dlogits may be
+    logits."""
+    _logprobs_grad("ew_logprobs_grad_f32", 4, logits, targets, lse, dlogp, dlogits, entropy,
+                   dentropy, scale, rows, cols, stream)
+
+
+def ew_logprobs_grad_f16(logits, targets, lse, dlogp, dlogits, entropy=None, dentropy=None,
+                         scale=1.0, rows=None, cols=None, stream=None):
+    """ew_logprobs_grad_f32 on binary16 logits."""
+    _logprobs_grad("ew_logprobs_grad_f16", 2, logits, targets, lse, dlogp, dlogits, entropy,
+                   dentropy, scale, rows, cols, stream)
+
+
+def ew_logprobs_grad_bf16(logits, targets, lse, dlogp, dlogits, entropy=None, dentropy=None,
+                          scale=1.0, rows=None, cols=None, stream=None):
+    """ew_logprobs_grad_f32 on bfloat16 logits."""
+    _logprobs_grad("ew_logprobs_grad_bf16", 2, logits, targets, lse, dlogp, dlogits, entropy,
+                   dentropy, scale, rows, cols, stream)
+
+
+def ew_distill_workspace(rows, cols):
+    """Bytes of workspace ew_distill_* needs."""
+    return _c["ew_distill_workspace"](int(rows), int(cols))
+
+
+def _kept(ids, kept):
+    if kept is not None:
+        return int(kept)
+    if isinstance(ids, int):
+        raise ValueError("kept is required when ids is a raw pointer")
+    return ids.shape[-1]
+
+
+def _distill(name, es, logits, teacher, ids, loss, lse, scale, workspace, rows, cols, kept,
+             stream):
+    rows, cols = _shape(logits, rows, cols, "logits")
+    kept = _kept(ids, kept)
+    p, stride = _mat(logits, es, rows, cols, "logits")
+    ws, size = _space(workspace, _c["ew_distill_workspace"](rows, cols))
+    _check(_c[name](p, stride, _buf(teacher, 4, rows * kept, "teacher"),
+                    _ids64(ids, rows * kept, "ids"), kept, _buf(loss, 4, rows, "loss"),
+                    _buf(lse, 4, rows, "lse"), scale, ws, size, rows, cols,
+                    _stream(loss, stream)), name)
+
+
+def ew_distill_f32(logits, teacher, ids, loss, lse=None, scale=1.0, workspace=None, rows=None,
+                   cols=None, kept=None, stream=None):
+    """Distillation loss of each row: the divergence of softmax(scale * logits)
+    from the softmax of scale * teacher over the teacher's kept entries
+    (teacher, ids: rows x kept; an id outside [0, cols) drops the entry)."""
+    _distill("ew_distill_f32", 4, logits, teacher, ids, loss, lse, scale, workspace, rows, cols,
+             kept, stream)
+
+
+def ew_distill_f16(logits, teacher, ids, loss, lse=None, scale=1.0, workspace=None, rows=None,
+                   cols=None, kept=None, stream=None):
+    """ew_distill_f32 on binary16 logits."""
+    _distill("ew_distill_f16", 2, logits, teacher, ids, loss, lse, scale, workspace, rows, cols,
+             kept, stream)
+
+
+def ew_distill_bf16(logits, teacher, ids, loss, lse=None, scale=1.0, workspace=None, rows=None,
+                    cols=None, kept=None, stream=None):
+    """ew_distill_f32 on bfloat16 logits."""
+    _distill("ew_distill_bf16", 2, logits, teacher, ids, loss, lse, scale, workspace, rows, cols,
+             kept, stream)
+
+
+def _distill_grad(name, es, logits, teacher, ids, lse, dloss, dlogits, scale, rows, cols, kept,
+                  stream):
+    rows, cols = _shape(logits, rows, cols, "logits")
+    kept = _kept(ids, kept)
+    p, stride = _mat(logits, es, rows, cols, "logits")
+    pd, sd = _mat(dlogits, es, rows, cols, "dlogits")
+    _check(_c[name](p, stride, _buf(teacher, 4, rows * kept, "teacher"),
+                    _ids64(ids, rows * kept, "ids"), kept, _buf(lse, 4, rows, "lse"),
+                    _buf(dloss, 4, rows, "dloss"), pd, sd, scale, rows, cols,
+                    _stream(dlogits, stream)), name)
+
+
+def ew_distill_grad_f32(logits, teacher, ids, lse, dloss, dlogits, scale=1.0, rows=None,
+                        cols=None, kept=None, stream=None):
+    """Gradient of the distillation loss by the logits, from the forward
+    call's lse.  dlogits may be logits."""
+    _distill_grad("ew_distill_grad_f32", 4, logits, teacher, ids, lse, dloss, dlogits, scale,
+                  rows, cols, kept, stream)
+
+
+def ew_distill_grad_f16(logits, teacher, ids, lse, dloss, dlogits, scale=1.0, rows=None,
+                        cols=None, kept=None, stream=None):
+    """ew_distill_grad_f32 on binary16 logits."""
+    _distill_grad("ew_distill_grad_f16", 2, logits, teacher, ids, lse, dloss, dlogits, scale,
+                  rows, cols, kept, stream)
+
+
+def ew_distill_grad_bf16(logits, teacher, ids, lse, dloss, dlogits, scale=1.0, rows=None,
+                         cols=None, kept=None, stream=None):
+    """ew_distill_grad_f32 on bfloat16 logits."""
+    _distill_grad("ew_distill_grad_bf16", 2, logits, teacher, ids, lse, dloss, dlogits, scale,
+                  rows, cols, kept, stream)
 
 
 def ew_status_string(status: int) -> str:

@@ -25,7 +25,10 @@ ARCH = "gfx950"
 
 KERNEL_SOURCES = [os.path.join(CSRC, f) for f in
                   ("ew_stream.hip", "ew_batch.hip", "ew_gather.hip", "ew_view.hip")]
-SOURCES = [os.path.join(CSRC, "ew_api.cpp"), *KERNEL_SOURCES]
+# the row operators, whose kernels reduce along rows through LDS
+ROW_KERNEL_SOURCES = [os.path.join(CSRC, f) for f in ("ew_norm.hip", "ew_vocab.hip")]
+SOURCES = [os.path.join(CSRC, "ew_api.cpp"), os.path.join(CSRC, "ew_rows_api.cpp"),
+           *KERNEL_SOURCES, *ROW_KERNEL_SOURCES]
 
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 COMMON_FLAGS = [
@@ -63,12 +66,14 @@ def build(verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
     return out
 
 
-def device_asm(dest_dir: str, verbose: bool = False, extra_flags=()) -> str:
-    """Write the gfx950 assembly of every kernel source to ``dest_dir``, one
-    file per source plus their concatenation; returns the concatenation's path."""
+def device_asm(dest_dir: str, verbose: bool = False, extra_flags=(),
+               sources=tuple(KERNEL_SOURCES)) -> str:
+    """Write the gfx950 assembly of the kernel sources (the elementwise ones
+    unless others are given) to ``dest_dir``, one file per source plus their
+    concatenation; returns the concatenation's path."""
     os.makedirs(dest_dir, exist_ok=True)
     parts = []
-    for src in KERNEL_SOURCES:
+    for src in sources:
         stem = os.path.splitext(os.path.basename(src))[0]
         path = os.path.join(dest_dir, f"{stem}-{ARCH}.s")
         cmd = [hipcc(), *COMMON_FLAGS, *extra_flags, "--cuda-device-only", "-S", "-o", path, src]

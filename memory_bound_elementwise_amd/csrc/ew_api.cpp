@@ -7,6 +7,7 @@
 #include "ew.h"
 #include "ew_batch_args.h"
 #include "ew_gather_args.h"
+#include "ew_host.h"
 #include "ew_internal.h"
 #include "ew_view_args.h"
 
@@ -643,6 +644,11 @@ void gather_plan(const float *in, float *out, size_t n, size_t stride, int cus, 
 }
 
 }  // namespace
+
+ew_status_t host_device(int *cu_count) { return current_device(cu_count); }
+ew_status_t host_fail(hipError_t e) { return fail_hip(e); }
+bool host_log_enabled() { return log_enabled(); }
+
 }  // namespace ew
 
 using namespace ew;
