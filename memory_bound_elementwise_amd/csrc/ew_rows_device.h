@@ -76,6 +76,47 @@ __device__ __forceinline__ float block_reduce(float x, float *scratch)
     return x;
 }
 
+// ---------------------------------------------------------------------------
+// Vectors: the 16-byte vector of an element type and its widening
+// ---------------------------------------------------------------------------
+
+template <typename T>
+struct Vec {
+    static constexpr int N = 16 / (int)sizeof(T);        // elements
+    typedef T type __attribute__((ext_vector_type(N)));
+    typedef float wide __attribute__((ext_vector_type(N)));
+    __device__ static wide widen(u32x4 v)
+    {
+        return __builtin_convertvector(__builtin_bit_cast(type, v), wide);
+    }
+    __device__ static u32x4 narrow(wide v)               // nearest even
+    {
+        return __builtin_bit_cast(u32x4, __builtin_convertvector(v, type));
+    }
+    // every element -inf
+    __device__ static u32x4 masked()
+    {
+        const uint32_t w = sizeof(T) == 4 ? 0xff800000u
+                           : __is_same(T, __bf16) ? 0xff80ff80u : 0xfc00fc00u;
+        return u32x4{w, w, w, w};
+    }
+};
+
+// How a row of n elements starting at p splits: `head` elements up to the
+// first 16-byte boundary, `vectors` aligned vectors, `tail` elements.
+template <typename T>
+struct RowSplit {
+    uint32_t head, vectors, tail;
+    __device__ RowSplit(const T *p, uint32_t n)
+    {
+        const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) % 16);
+        head = (off ? 16 - off : 0) / (uint32_t)sizeof(T);
+        if (head > n) head = n;
+        vectors = (n - head) / Vec<T>::N;
+        tail = n - head - vectors * Vec<T>::N;
+    }
+};
+
 // exp(x) through the hardware's power of two: relative error about
 // |x| * 2^-24 for the arguments of a softmax (x <= 0).
 __device__ __forceinline__ float exp_nat(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }

@@ -9,18 +9,87 @@ namespace ew {
 constexpr int kVocabBlock = 256;
 constexpr int kVocabWaves = kVocabBlock / 64;
 
-// What a softmax over a row needs.  With m the row's largest logit (NaNs
-// ignored) and d = scale * (x - m): z = sum exp(d), b = sum exp(d) * d.  The
-// difference is taken before the product so that d is exactly 0 at the
-// largest logit, whatever its size.  Masked logits (-inf) add nothing; a NaN
-// or +inf makes z a NaN.
+// ---------------------------------------------------------------------------
+// Softmax statistics of a row
+// ---------------------------------------------------------------------------
+
+// With m the largest logit seen (NaNs ignored), c = scale * log2(e) and
+// d = c * (x - m): z = sum 2^d, b = sum 2^d * d.  The difference is taken
+// before the product so that d is exactly 0 at the largest logit, whatever
+// its size.  Masked logits (-inf) add nothing; a NaN or +inf makes z a NaN.
 struct RowSum {
     float m, z, b;
 };
 
+// Where a difference of exponents is -inf its term is 0; this finite stand-in
+// keeps 0 * d from being a NaN, and 2^d is 0 all the same.
+constexpr float kFarBelow = -1e30f;
+
+__device__ __forceinline__ float finite_base(float m) { return m == -kInf ? 0.0f : m; }
+
+// s re-based from s.m to m >= s.m.
+template <bool Ent>
+__device__ __forceinline__ void rebase(RowSum &s, float m, float c)
+{
+    const float shift = __builtin_fmaxf((s.m - finite_base(m)) * c, kFarBelow);
+    const float f = __builtin_amdgcn_exp2f(shift);
+    if constexpr (Ent) s.b = f * __builtin_fmaf(shift, s.z, s.b);
+    s.z *= f;
+    s.m = m;
+}
+
+// N more logits of this lane.  One re-basing for N terms; the maximum costs
+// half an instruction a logit (three operands each).
+template <bool Ent, int N>
+__device__ __forceinline__ float absorb(RowSum &s, const float (&v)[N], float c)
+{
+    float top = v[0];
+#pragma unroll
+    for (int k = 1; k < N; ++k) top = __builtin_fmaxf(top, v[k]);
+    rebase<Ent>(s, __builtin_fmaxf(s.m, top), c);
+    const float base = finite_base(s.m);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float d = (v[k] - base) * c, e = __builtin_amdgcn_exp2f(d);
+        s.z += e;
+        if constexpr (Ent) s.b = __builtin_fmaf(e, __builtin_fmaxf(d, kFarBelow), s.b);
+    }
+    return top;
+}
+
+// The sums of the wave's lanes, in every lane.
+template <bool Ent>
+__device__ __forceinline__ void wave_join(RowSum &s, float c)
+{
+    rebase<Ent>(s, wave_reduce<Max>(s.m), c);
+    s.z = wave_reduce<Sum>(s.z);
+    if constexpr (Ent) s.b = wave_reduce<Sum>(s.b);
+}
+
+// The sums of the block's threads, in every thread; one barrier.
+template <bool Ent>
+__device__ __forceinline__ void block_join(RowSum &s, float c, RowSum *part)
+{
+    wave_join<Ent>(s, c);
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = s;
+    __syncthreads();
+    float m = part[0].m;
+#pragma unroll
+    for (int w = 1; w < kVocabWaves; ++w) m = __builtin_fmaxf(m, part[w].m);
+    RowSum all{m, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kVocabWaves; ++w) {
+        RowSum p = part[w];
+        rebase<Ent>(p, m, c);
+        all.z += p.z;
+        all.b += p.b;
+    }
+    s = all;
+}
+
 // lse and entropy from a row's sums.  empty: the scaled logits are all -inf.
 struct RowStat {
-    float lse, entropy;
+    float lse, entropy, log_z;
     bool empty;
 };
 
@@ -30,123 +99,289 @@ __device__ __forceinline__ RowStat row_stat(const RowSum &s, float scale)
     const float top = s.m * scale;
     // all NaN: m stays -inf while z is a NaN
     st.empty = top == -kInf && s.z == s.z;
-    const float log_z = __builtin_logf(s.z);
-    st.lse = st.empty ? -kInf : top == kInf ? __builtin_nanf("") : top + log_z;
-    st.entropy = st.empty ? 0.0f : st.lse != st.lse ? st.lse : log_z - s.b / s.z;
+    st.log_z = __builtin_logf(s.z);
+    st.lse = st.empty ? -kInf : top == kInf ? __builtin_nanf("") : top + st.log_z;
+    st.entropy = st.empty ? 0.0f
+                 : st.lse != st.lse ? st.lse : __builtin_fmaf(-kLn2, s.b / s.z, st.log_z);
     return st;
 }
 
-// scale * x - lse of one logit, from the sums (exact where x is the largest).
+// scale * x - lse of one logit, from the sums (-log z where x is the largest).
 __device__ __forceinline__ float log_prob(float x, const RowSum &s, const RowStat &st, float scale)
 {
     if (st.empty) return -kInf;
     if (st.lse != st.lse) return st.lse;
-    return (x - s.m) * scale - __builtin_logf(s.z);
+    return (x - s.m) * scale - st.log_z;
 }
 
-template <typename T>
-__device__ RowSum block_row_sum(const T *x, uint32_t cols, float scale, float (*scratch)[kVocabWaves])
-{
-    RowSum s;
-    float m = -kInf;
-    for (uint32_t c = threadIdx.x; c < cols; c += kVocabBlock) m = __builtin_fmaxf(m, (float)x[c]);
-    s.m = block_reduce<Max, kVocabWaves>(m, scratch[0]);
-    const float base = s.m == -kInf ? 0.0f : s.m;
-    float z = 0.0f, b = 0.0f;
-    for (uint32_t c = threadIdx.x; c < cols; c += kVocabBlock) {
-        const float d = ((float)x[c] - base) * scale, e = exp_nat(d);
-        z += e;
-        if (e > 0.0f) b += e * d;
-    }
-    s.z = block_reduce<Sum, kVocabWaves>(z, scratch[1]);
-    s.b = block_reduce<Sum, kVocabWaves>(b, scratch[2]);
-    __syncthreads();
-    return s;
-}
+// ---------------------------------------------------------------------------
+// The largest of a stream of logits
+// ---------------------------------------------------------------------------
 
 // A logit's rank as one number: larger is more likely, ties to the lowest
-// column, a NaN as -inf.  -0 and +0 rank alike.
-__device__ __forceinline__ uint64_t rank_key(float x, uint32_t c)
+// column, a NaN as -inf, -0 as +0.  Never 0.
+__device__ __forceinline__ uint64_t rank_key(float x, uint32_t col)
 {
     if (x != x) x = -kInf;
     x += 0.0f;
     const uint32_t u = __builtin_bit_cast(uint32_t, x);
     const uint32_t k = u & 0x80000000u ? ~u : u | 0x80000000u;
-    return (uint64_t)k << 32 | (uint32_t)~c;
+    return (uint64_t)k << 32 | (uint32_t)~col;
+}
+__device__ __forceinline__ float key_logit(uint64_t key)
+{
+    const uint32_t k = (uint32_t)(key >> 32);
+    return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ uint32_t key_col(uint64_t key) { return ~(uint32_t)key; }
+
+__device__ __forceinline__ uint64_t lane_key(uint64_t k, int lane)
+{
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)k, lane);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kVocabBlock) ew_logprobs_kernel(LogprobsArgs a)
+__device__ __forceinline__ uint32_t lanes_below(uint64_t mask)
 {
-    __shared__ float scratch[3][kVocabWaves];
-    __shared__ uint64_t best[kVocabWaves];
-    for (uint32_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
-        const RowSum s = block_row_sum(x, a.cols, a.scale, scratch);
-        const RowStat st = row_stat(s, a.scale);
-        if (threadIdx.x == 0) {
-            const int64_t t = a.targets[r];
-            const bool given = t >= 0 && t < (int64_t)a.cols;
-            a.logp[r] = given ? log_prob((float)x[t], s, st, a.scale) : 0.0f;
-            if (a.lse) a.lse[r] = st.lse;
-            if (a.entropy) a.entropy[r] = st.entropy;
-        }
-        uint64_t last = ~(uint64_t)0;
-        for (uint32_t k = 0; k < a.top; ++k) {
-            uint64_t key = 0;
-            for (uint32_t c = threadIdx.x; c < a.cols; c += kVocabBlock) {
-                const uint64_t q = rank_key((float)x[c], c);
-                if (q < last && q > key) key = q;
-            }
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                     __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// What this wave's lanes wrote to LDS is visible to its other lanes.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The smallest of the lanes' values, in every lane.
+__device__ __forceinline__ uint32_t wave_min(uint32_t x)
+{
+    const auto step = [](uint32_t v, uint32_t o) { return o < v ? o : v; };
+#define EW_MIN_STEP(ctrl) \
+    x = step(x, (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, ctrl, 0xf, 0xf, true))
+    EW_MIN_STEP(0xB1);
+    EW_MIN_STEP(0x4E);
+    EW_MIN_STEP(0x141);
+    EW_MIN_STEP(0x140);
+#undef EW_MIN_STEP
+    const auto row = [&](int l) { return (uint32_t)__builtin_amdgcn_readlane((int)x, l); };
+    return step(step(row(0), row(16)), step(row(32), row(48)));
+}
+
+// One wave's candidates for the k largest keys of what it has seen: an
+// unordered list in LDS that holds at least the k largest (all, while fewer
+// were seen).  A key enters only above the bar; a list that has grown is cut
+// to its k largest, and the smallest of them becomes the bar.  On logits in
+// no special order few pass it: the first full chunk starts it at the k-th
+// largest of the 64 lanes' maxima.
+constexpr uint32_t kListKeys = 256;
+// A list is cut once it holds this many more than k.
+constexpr uint32_t kListSlack = 32;
+
+struct TopList {
+    uint64_t *keys;      // kListKeys of LDS, this wave's
+    uint32_t count, k;   // the same in every lane, as is the rest
+    uint64_t bar;
+    float bar_logit;     // once closed: no later key with this logit or less enters
+    bool open;           // not yet cut
+
+    __device__ void start(uint64_t *list, uint32_t top)
+    {
+        keys = list;
+        count = 0;
+        k = top;
+        bar = 0;
+        bar_logit = -kInf;
+        open = true;
+    }
+
+    // Cut to the k largest; nothing while there are fewer.  A value with
+    // exactly k keys at or above it is found bit by bit.
+    __device__ void cut()
+    {
+        if (count < k) return;
+        wave_sync();
+        const uint32_t lane = threadIdx.x % 64;
+        if (count > k) {
+            uint64_t own[kListKeys / 64];
 #pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                const uint64_t o = __shfl_xor((unsigned long long)key, d);
-                key = o > key ? o : key;
+            for (uint32_t i = 0; i < kListKeys / 64; ++i)
+                own[i] = i * 64 + lane < count ? keys[i * 64 + lane] : 0;
+            uint64_t at = 0;
+            for (int bit = 63; bit >= 0; --bit) {
+                const uint64_t trial = at | (uint64_t)1 << bit;
+                uint32_t n = 0;
+#pragma unroll
+                for (uint32_t i = 0; i < kListKeys / 64; ++i)
+                    n += __builtin_popcountll(__ballot(own[i] >= trial));
+                if (n >= k) at = trial;
+                if (n == k) break;
             }
-            if (threadIdx.x % 64 == 0) best[threadIdx.x / 64] = key;
-            __syncthreads();
-            last = best[0];
-            for (int w = 1; w < kVocabWaves; ++w) last = best[w] > last ? best[w] : last;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                const uint32_t c = ~(uint32_t)last;
-                a.top_ids[(uint64_t)r * a.top + k] = c;
-                a.top_logp[(uint64_t)r * a.top + k] = log_prob((float)x[c], s, st, a.scale);
+            count = 0;
+#pragma unroll
+            for (uint32_t i = 0; i < kListKeys / 64; ++i) {
+                const bool stay = own[i] >= at;
+                const uint64_t mask = __ballot(stay);
+                if (stay) keys[count + lanes_below(mask)] = own[i];
+                count += __builtin_popcountll(mask);
+            }
+            wave_sync();
+        }
+        const uint64_t key = lane < count ? keys[lane] : ~(uint64_t)0;
+        const uint32_t hi = wave_min((uint32_t)(key >> 32));
+        const uint32_t lo = wave_min((uint32_t)(key >> 32) == hi ? (uint32_t)key : ~0u);
+        bar = (uint64_t)hi << 32 | lo;
+        bar_logit = key_logit(bar);
+        open = false;
+    }
+
+    // Each lane offers one key (0: none).
+    __device__ void offer(uint64_t key)
+    {
+        const bool enter = key > bar;
+        const uint64_t mask = __ballot(enter);
+        if (mask == 0) return;
+        if (enter) keys[count + lanes_below(mask)] = key;
+        count += __builtin_popcountll(mask);
+        if (count > kListKeys - 64) cut();
+    }
+
+    // The k-th largest of the lanes' values becomes the first bar: at least k
+    // keys are at or above it.
+    __device__ void seed(float lane_top)
+    {
+        if (lane_top != lane_top) lane_top = -kInf;
+        uint32_t rank = 0;
+        const uint32_t lane = threadIdx.x % 64;
+#pragma unroll 8
+        for (uint32_t i = 0; i < 64; ++i) {
+            const float o = lane_value(lane_top, i);
+            rank += o > lane_top || (o == lane_top && i < lane);
+        }
+        const float v = lane_value(lane_top, __builtin_ctzll(__ballot(rank == k - 1)));
+        bar = rank_key(v, ~0u);      // below every key of that logit
+    }
+};
+
+// The k largest keys of all waves' lists, best first: lane i of the first
+// wave returns the i-th (0 past their number).  Every wave calls it; the
+// lists are consecutive.  One barrier.
+__device__ __forceinline__ uint64_t block_top(TopList &list, const uint64_t *lists,
+                                              uint32_t *counts)
+{
+    const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    list.cut();
+    if (lane == 0) counts[wave] = list.count;
+    __syncthreads();
+    if (wave != 0) return 0;
+    for (uint32_t w = 1; w < kVocabWaves; ++w)       // at most k <= 64 keys each
+        list.offer(lane < counts[w] ? lists[w * kListKeys + lane] : 0);
+    list.cut();
+    wave_sync();
+    const uint64_t key = lane < list.count ? list.keys[lane] : 0;
+    uint32_t rank = 0;
+    for (uint32_t i = 0; i < list.count; ++i) rank += lane_key(key, i) > key;
+    wave_sync();
+    if (lane < list.count) list.keys[rank] = key;
+    wave_sync();
+    return lane < list.count ? list.keys[lane] : 0;
+}
+
+// ---------------------------------------------------------------------------
+// One pass over a row, or over one of its parts
+// ---------------------------------------------------------------------------
+
+// Elements a lane takes at a time: two 16-byte vectors of 16-bit logits, four
+// of 32-bit ones.
+constexpr int kPerLane = 16;
+
+// The columns of part `part` of `parts` of a row: a range of its aligned
+// vectors; the first part has the head too, the last the tail.
+struct Part {
+    uint32_t lo, hi;
+    bool first, last;
+    __device__ Part(uint32_t vectors, uint32_t part, uint32_t parts)
+    {
+        // whole kilobytes each, so that no two parts share a cache line
+        const uint32_t each = ((vectors + parts - 1) / parts + 63) & ~63u;
+        const uint64_t start = (uint64_t)each * part;
+        lo = start < vectors ? (uint32_t)start : vectors;
+        hi = vectors - lo < each ? vectors : lo + each;
+        first = part == 0;
+        last = part + 1 == parts;
+    }
+};
+
+template <typename T, bool Ent, bool Top>
+__device__ __forceinline__ RowSum stream_part(const T *x, uint32_t cols, const Part &p,
+                                              const RowSplit<T> &split, float c, TopList &list)
+{
+    constexpr int U = kPerLane / Vec<T>::N;
+    constexpr uint32_t kStep = kVocabBlock * U;
+    const uint32_t lane = threadIdx.x % 64;
+    const char *const body = reinterpret_cast<const char *>(x + split.head);
+    RowSum s{-kInf, 0.0f, 0.0f};
+
+    // up to a vector's elements before or after the aligned body: one lane each
+    const auto edge = [&](uint32_t start, uint32_t n) {
+        const bool live = lane < n;
+        const float v[1] = {live ? (float)x[start + lane] : -kInf};
+        absorb<Ent>(s, v, c);
+        if constexpr (Top) list.offer(live ? rank_key(v[0], start + lane) : 0);
+    };
+    if (p.first && threadIdx.x < 64 && split.head) edge(0, split.head);
+
+    u32x4 next[U];
+    const auto fetch = [&](uint32_t v) {       // v: the block's first vector
+        if (p.hi - v >= kStep) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                next[u] = load16<true, sizeof(T)>(body + (uint64_t)(v + threadIdx.x + u * kVocabBlock) * 16);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t i = v + threadIdx.x + u * kVocabBlock;
+                next[u] = i < p.hi ? load16<true, sizeof(T)>(body + (uint64_t)i * 16) : Vec<T>::masked();
+            }
+        }
+    };
+    if (p.lo < p.hi) fetch(p.lo);
+    for (uint32_t v = p.lo; v < p.hi;) {
+        float f[kPerLane];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const typename Vec<T>::wide w = Vec<T>::widen(next[u]);
+#pragma unroll
+            for (int j = 0; j < Vec<T>::N; ++j) f[u * Vec<T>::N + j] = w[j];
+        }
+        const uint32_t at = v;
+        v = p.hi - v > kStep ? v + kStep : p.hi;
+        if (v < p.hi) fetch(v);
+        const float top = absorb<Ent>(s, f, c);
+        if constexpr (Top) {
+            if (list.open || __ballot(top > list.bar_logit) != 0) {
+                if (list.open && list.bar == 0 && p.hi - at >= kStep) list.seed(top);
+#pragma unroll
+                for (int k = 0; k < kPerLane; ++k) {
+                    const uint32_t i = at + threadIdx.x + k / Vec<T>::N * kVocabBlock;
+                    if (__ballot(!(f[k] < key_logit(list.bar))) != 0)
+                        list.offer(i < p.hi ? rank_key(f[k], split.head + i * Vec<T>::N + k % Vec<T>::N)
+                                            : 0);
+                }
+                if (list.open || list.count > list.k + kListSlack) list.cut();
             }
         }
     }
+    if (p.last && threadIdx.x < 64 && split.tail) edge(cols - split.tail, split.tail);
+    return s;
 }
 
-// p = exp(scale * x - lse), at most 1 (a difference of large numbers may
-// round to above 0).
-__device__ __forceinline__ float log_p(float x, float scale, float lse)
-{
-    return min_or_nan(__builtin_fmaf(x, scale, -lse), 0.0f);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kVocabBlock) ew_logprobs_grad_kernel(LogprobsGradArgs a)
-{
-    for (uint32_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
-        T *const dx = static_cast<T *>(a.dlogits) + r * a.dlogits_stride;
-        const int64_t t = a.targets[r];
-        const bool given = t >= 0 && t < (int64_t)a.cols;
-        const float lse = a.lse[r], dlogp = given ? a.dlogp[r] : 0.0f;
-        const float dent = a.dentropy ? a.dentropy[r] : 0.0f, ent = a.dentropy ? a.entropy[r] : 0.0f;
-        for (uint32_t c = threadIdx.x; c < a.cols; c += kVocabBlock) {
-            const float v = (float)x[c];
-            float g = 0.0f;
-            if (v * a.scale != -kInf && lse != -kInf) {
-                const float l = log_p(v, a.scale, lse), p = exp_nat(l);
-                g = -p * (dlogp + dent * (l + ent));
-                if (given && c == (uint32_t)t) g += dlogp;
-                g *= a.scale;
-            }
-            dx[c] = (T)g;
-        }
-    }
-}
+// ---------------------------------------------------------------------------
+// Forward: a block a row, or a block a part of a row and a block a row that
+// joins the parts
+// ---------------------------------------------------------------------------
 
 // The teacher's distribution over its kept entries: the scaled logits'
 // maximum and sum, in every thread.
@@ -179,15 +414,55 @@ __device__ Teacher block_teacher(const float *teacher, const int64_t *ids, uint3
     return t;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kVocabBlock) ew_distill_kernel(DistillArgs a)
-{
-    __shared__ float scratch[3][kVocabWaves];
-    for (uint32_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
+
+// What a forward call does with a row's sums, for all threads of a block.
+struct Logprobs {
+    using Args = LogprobsArgs;
+    struct Ahead {              // loaded before the row is streamed
+        float logit;
+        bool given;
+    };
+    template <typename T>
+    __device__ static Ahead ahead(const Args &a, uint32_t r, const T *x)
+    {
+        const int64_t t = a.targets[r];
+        const bool given = t >= 0 && t < (int64_t)a.cols;
+        return Ahead{given ? (float)x[t] : 0.0f, given};
+    }
+    // key: lane i of the first wave has the i-th best
+    template <typename T>
+    __device__ static void finish(const Args &a, uint32_t r, const T *, const Ahead &h,
+                                  const RowSum &s, uint64_t key, float (*)[kVocabWaves])
+    {
+        const RowStat st = row_stat(s, a.scale);
+        if (threadIdx.x == 0) {
+            a.logp[r] = h.given ? log_prob(h.logit, s, st, a.scale) : 0.0f;
+            if (a.lse) a.lse[r] = st.lse;
+            if (a.entropy) a.entropy[r] = st.entropy;
+        }
+        if (threadIdx.x < a.top) {
+            const uint64_t i = (uint64_t)r * a.top + threadIdx.x;
+            a.top_ids[i] = key_col(key);
+            a.top_logp[i] = log_prob(key_logit(key), s, st, a.scale);
+        }
+    }
+    __device__ static uint32_t top(const Args &a) { return a.top; }
+};
+
+struct Distill {
+    using Args = DistillArgs;
+    struct Ahead {};
+    template <typename T>
+    __device__ static Ahead ahead(const Args &, uint32_t, const T *)
+    {
+        return Ahead{};
+    }
+    template <typename T>
+    __device__ static void finish(const Args &a, uint32_t r, const T *x, const Ahead &,
+                                  const RowSum &s, uint64_t, float (*scratch)[kVocabWaves])
+    {
         const float *const teacher = a.teacher + (uint64_t)r * a.kept;
         const int64_t *const ids = a.ids + (uint64_t)r * a.kept;
-        const RowSum s = block_row_sum(x, a.cols, a.scale, scratch);
         const RowStat st = row_stat(s, a.scale);
         const Teacher t = block_teacher(teacher, ids, a.kept, a.cols, a.scale, scratch);
         const float log_tz = __builtin_logf(t.z);
@@ -196,14 +471,134 @@ __global__ void __launch_bounds__(kVocabBlock) ew_distill_kernel(DistillArgs a)
             const float v = teacher[k] * a.scale;
             if (!kept_entry(ids[k], v, a.cols)) continue;
             const float l = v - t.m - log_tz, p = exp_nat(v - t.m) / t.z;
-            if (p >= 0x1p-126f || p != p) loss += p * (l - log_prob((float)x[ids[k]], s, st, a.scale));
+            if (p >= 0x1p-126f || p != p)
+                loss += p * (l - log_prob((float)x[ids[k]], s, st, a.scale));
         }
         loss = block_reduce<Sum, kVocabWaves>(loss, scratch[2]);
         if (threadIdx.x == 0) {
             a.loss[r] = loss;
             if (a.lse) a.lse[r] = st.lse;
         }
-        __syncthreads();
+    }
+    __device__ static uint32_t top(const Args &) { return 0; }
+};
+
+// The workspace of a call that splits rows: a RowSum padded to 16 bytes for
+// each part of each row, then each part's keys.
+__device__ __forceinline__ float4 *part_sums(void *ws) { return static_cast<float4 *>(ws); }
+__device__ __forceinline__ uint64_t *part_keys(void *ws, uint32_t rows, uint32_t parts)
+{
+    return reinterpret_cast<uint64_t *>(part_sums(ws) + (uint64_t)rows * parts);
+}
+
+template <bool Top>
+struct ForwardShared {
+    RowSum part[kVocabWaves];
+    float scratch[3][kVocabWaves];
+    uint32_t counts[kVocabWaves];
+    uint64_t keys[Top ? kVocabWaves * kListKeys : 1];
+};
+
+template <typename T, class Op, bool Ent, bool Top>
+__global__ void __launch_bounds__(kVocabBlock) ew_vocab_forward_kernel(typename Op::Args a,
+                                                                       uint32_t parts)
+{
+    __shared__ ForwardShared<Top> sh;
+    const uint64_t items = (uint64_t)a.rows * parts;
+    const float c = a.scale * kLog2e;
+    for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const uint32_t r = (uint32_t)(item / parts), part = (uint32_t)(item % parts);
+        const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
+        typename Op::Ahead h{};
+        if (parts == 1) h = Op::ahead(a, r, x);
+        const RowSplit<T> split(x, a.cols);
+        TopList list;
+        if constexpr (Top) list.start(sh.keys + threadIdx.x / 64 * kListKeys, Op::top(a));
+        RowSum s = stream_part<T, Ent, Top>(x, a.cols, Part(split.vectors, part, parts), split, c, list);
+        block_join<Ent>(s, c, sh.part);
+        uint64_t key = 0;
+        if constexpr (Top) key = block_top(list, sh.keys, sh.counts);
+        if (parts == 1) {
+            Op::finish(a, r, x, h, s, key, sh.scratch);
+        } else {
+            if (threadIdx.x == 0) part_sums(a.workspace)[item] = float4{s.m, s.z, s.b, 0.0f};
+            if constexpr (Top)
+                if (threadIdx.x < Op::top(a))
+                    part_keys(a.workspace, a.rows, parts)[item * Op::top(a) + threadIdx.x] = key;
+        }
+        if (item + gridDim.x < items) __syncthreads();
+    }
+}
+
+template <typename T, class Op, bool Ent, bool Top>
+__global__ void __launch_bounds__(kVocabBlock) ew_vocab_join_kernel(typename Op::Args a,
+                                                                    uint32_t parts)
+{
+    __shared__ ForwardShared<Top> sh;
+    const float c = a.scale * kLog2e;
+    for (uint64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
+        const typename Op::Ahead h = Op::ahead(a, (uint32_t)r, x);
+        RowSum s{-kInf, 0.0f, 0.0f};
+        for (uint32_t p = threadIdx.x; p < parts; p += kVocabBlock) {
+            const float4 q = part_sums(a.workspace)[r * parts + p];
+            RowSum o{q.x, q.y, q.z};
+            const float m = __builtin_fmaxf(s.m, o.m);
+            rebase<Ent>(s, m, c);
+            rebase<Ent>(o, m, c);
+            s.z += o.z;
+            s.b += o.b;
+        }
+        block_join<Ent>(s, c, sh.part);
+        uint64_t key = 0;
+        if constexpr (Top) {
+            TopList list;
+            list.start(sh.keys + threadIdx.x / 64 * kListKeys, Op::top(a));
+            const uint32_t n = parts * Op::top(a);
+            const uint64_t *const keys = part_keys(a.workspace, a.rows, parts) + r * n;
+            for (uint32_t i = threadIdx.x / 64 * 64; i < n; i += kVocabBlock) {
+                const uint32_t at = i + threadIdx.x % 64;
+                list.offer(at < n ? keys[at] : 0);
+            }
+            key = block_top(list, sh.keys, sh.counts);
+        }
+        Op::finish(a, (uint32_t)r, x, h, s, key, sh.scratch);
+        if (r + gridDim.x < a.rows) __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients
+// ---------------------------------------------------------------------------
+
+// p = exp(scale * x - lse), at most 1 (a difference of large numbers may
+// round to above 0).
+__device__ __forceinline__ float log_p(float x, float scale, float lse)
+{
+    return min_or_nan(__builtin_fmaf(x, scale, -lse), 0.0f);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kVocabBlock) ew_logprobs_grad_kernel(LogprobsGradArgs a)
+{
+    for (uint32_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
+        T *const dx = static_cast<T *>(a.dlogits) + r * a.dlogits_stride;
+        const int64_t t = a.targets[r];
+        const bool given = t >= 0 && t < (int64_t)a.cols;
+        const float lse = a.lse[r], dlogp = given ? a.dlogp[r] : 0.0f;
+        const float dent = a.dentropy ? a.dentropy[r] : 0.0f, ent = a.dentropy ? a.entropy[r] : 0.0f;
+        for (uint32_t c = threadIdx.x; c < a.cols; c += kVocabBlock) {
+            const float v = (float)x[c];
+            float g = 0.0f;
+            if (v * a.scale != -kInf && lse != -kInf) {
+                const float l = log_p(v, a.scale, lse), p = exp_nat(l);
+                g = -p * (dlogp + dent * (l + ent));
+                if (given && c == (uint32_t)t) g += dlogp;
+                g *= a.scale;
+            }
+            dx[c] = (T)g;
+        }
     }
 }
 
@@ -239,47 +634,86 @@ __global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGra
 // Dispatch
 // ---------------------------------------------------------------------------
 
-size_t logprobs_workspace(uint64_t, uint64_t, uint64_t) { return 0; }
-size_t distill_workspace(uint64_t, uint64_t) { return 0; }
+// Blocks a forward call should have, and the fewest columns of a part.  A
+// function of the sizes alone, so that the workspace is too.
+constexpr uint64_t kWantBlocks = 1024;
+constexpr uint64_t kPartCols = 4096;
+constexpr uint64_t kMaxParts = 256;
+
+static uint32_t row_parts(uint64_t rows, uint64_t cols)
+{
+    if (rows == 0) return 1;
+    const uint64_t most = (cols + kPartCols - 1) / kPartCols;
+    uint64_t parts = (kWantBlocks + rows - 1) / rows;
+    if (parts > most) parts = most;
+    if (parts > kMaxParts) parts = kMaxParts;
+    return parts ? (uint32_t)parts : 1;
+}
+
+size_t logprobs_workspace(uint64_t rows, uint64_t cols, uint64_t top)
+{
+    const uint64_t parts = row_parts(rows, cols);
+    return parts == 1 ? 0 : rows * parts * (sizeof(float4) + top * sizeof(uint64_t));
+}
+size_t distill_workspace(uint64_t rows, uint64_t cols) { return logprobs_workspace(rows, cols, 0); }
 
 #define EW_BY_TYPE(t, K)                                           \
     ((t) == kRowF32 ? reinterpret_cast<const void *>(&K<float>)    \
      : (t) == kRowF16 ? reinterpret_cast<const void *>(&K<_Float16>) \
                       : reinterpret_cast<const void *>(&K<__bf16>))
 
-template <class A>
-static hipError_t go(const void *fn, const A &args, hipStream_t s)
+// Blocks stride over what is beyond this many.
+constexpr uint64_t kMaxGrid = 1 << 20;
+
+template <class... A>
+static hipError_t go(const void *fn, uint64_t blocks, hipStream_t s, A... args)
 {
-    A a = args;
-    void *kargs[] = {&a};
-    const uint32_t grid = a.rows < (1u << 20) ? a.rows : 1u << 20;
-    return hipLaunchKernel(fn, dim3(grid), dim3(kVocabBlock), kargs, 0, s);
+    void *kargs[] = {&args...};
+    return hipLaunchKernel(fn, dim3((uint32_t)(blocks < kMaxGrid ? blocks : kMaxGrid)),
+                           dim3(kVocabBlock), kargs, 0, s);
+}
+
+template <class Op, bool Ent, bool Top>
+static hipError_t forward(RowType t, const typename Op::Args &a, hipStream_t s, const char **path)
+{
+    const uint32_t parts = row_parts(a.rows, a.cols);
+#define EW_FORWARD(K)                                                                      \
+    (t == kRowF32 ? reinterpret_cast<const void *>(&K<float, Op, Ent, Top>)                \
+     : t == kRowF16 ? reinterpret_cast<const void *>(&K<_Float16, Op, Ent, Top>)           \
+                    : reinterpret_cast<const void *>(&K<__bf16, Op, Ent, Top>))
+    const hipError_t e = go(EW_FORWARD(ew_vocab_forward_kernel), (uint64_t)a.rows * parts, s, a, parts);
+    *path = parts == 1 ? "a block a row" : "rows in parts, then joined";
+    if (e != hipSuccess || parts == 1) return e;
+    return go(EW_FORWARD(ew_vocab_join_kernel), a.rows, s, a, parts);
+#undef EW_FORWARD
 }
 
 hipError_t launch_logprobs(RowType t, const LogprobsArgs &a, int, hipStream_t s, const char **path)
 {
-    *path = "a block a row";
-    return go(EW_BY_TYPE(t, ew_logprobs_kernel), a, s);
+    if (a.top)
+        return a.entropy ? forward<Logprobs, true, true>(t, a, s, path)
+                         : forward<Logprobs, false, true>(t, a, s, path);
+    return a.entropy ? forward<Logprobs, true, false>(t, a, s, path)
+                     : forward<Logprobs, false, false>(t, a, s, path);
 }
 
 hipError_t launch_logprobs_grad(RowType t, const LogprobsGradArgs &a, int, hipStream_t s,
                                 const char **path)
 {
     *path = "a block a row";
-    return go(EW_BY_TYPE(t, ew_logprobs_grad_kernel), a, s);
+    return go(EW_BY_TYPE(t, ew_logprobs_grad_kernel), a.rows, s, a);
 }
 
 hipError_t launch_distill(RowType t, const DistillArgs &a, int, hipStream_t s, const char **path)
 {
-    *path = "a block a row";
-    return go(EW_BY_TYPE(t, ew_distill_kernel), a, s);
+    return forward<Distill, false, false>(t, a, s, path);
 }
 
 hipError_t launch_distill_grad(RowType t, const DistillGradArgs &a, int, hipStream_t s,
                                const char **path)
 {
     *path = "a block a row";
-    return go(EW_BY_TYPE(t, ew_distill_grad_kernel), a, s);
+    return go(EW_BY_TYPE(t, ew_distill_grad_kernel), a.rows, s, a);
 }
 
 }  // namespace ew
