@@ -102,6 +102,14 @@ struct Vec {
     }
 };
 
+// Store a vector of T that is only element aligned.
+template <typename T>
+__device__ __forceinline__ void store16_row(char *p, u32x4 v)
+{
+    if constexpr (sizeof(T) == 4) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a4 *>(p));
+    else __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2 *>(p));
+}
+
 // How a row of n elements starting at p splits: `head` elements up to the
 // first 16-byte boundary, `vectors` aligned vectors, `tail` elements.
 template <typename T>

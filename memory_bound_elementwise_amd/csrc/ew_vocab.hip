@@ -571,62 +571,232 @@ __global__ void __launch_bounds__(kVocabBlock) ew_vocab_join_kernel(typename Op:
 // Gradients
 // ---------------------------------------------------------------------------
 
-// p = exp(scale * x - lse), at most 1 (a difference of large numbers may
-// round to above 0).
-__device__ __forceinline__ float log_p(float x, float scale, float lse)
-{
-    return min_or_nan(__builtin_fmaf(x, scale, -lse), 0.0f);
-}
+// A gradient has one block for each kGradLane elements a thread of a row: the
+// tile's loads are all in flight before the row's few numbers have arrived.
+// Tiles start at the row's start, so dlogits is stored with 16-byte stores at
+// whatever alignment the row has: on MI355X that cost less than a scalar head
+// in every tile.
+constexpr int kGradLane = 32;
 
 template <typename T>
-__global__ void __launch_bounds__(kVocabBlock) ew_logprobs_grad_kernel(LogprobsGradArgs a)
+struct GradTile {
+    static constexpr int N = Vec<T>::N, U = kGradLane / N;
+    static constexpr uint32_t kCols = kVocabBlock * kGradLane;
+    const char *in;
+    char *out;
+    uint32_t first, cols;      // the tile's first column and its number of columns
+    u32x4 v[U];
+
+    __device__ GradTile(const T *x, T *dx, uint32_t row_cols, uint32_t tile)
+    {
+        first = tile * kCols;
+        cols = row_cols - first < kCols ? row_cols - first : kCols;
+        in = reinterpret_cast<const char *>(x + first);
+        out = reinterpret_cast<char *>(dx + first);
+        // whole vectors are loaded as such, the row's last elements one by one
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = vector(u);
+            v[u] = u32x4{0, 0, 0, 0};
+            if ((i + 1) * N <= cols) v[u] = load16<false, sizeof(T)>(in + (uint64_t)i * 16);
+        }
+        if (cols % N) {
+            const uint32_t i = cols / N;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (vector(u) == i) v[u] = load_some(i);
+        }
+    }
+    // this thread's u-th vector of the tile
+    __device__ static uint32_t vector(int u) { return threadIdx.x + u * kVocabBlock; }
+
+    __device__ u32x4 load_some(uint32_t i) const
+    {
+        typename Vec<T>::type t{};
+        const T *const p = reinterpret_cast<const T *>(in) + (uint64_t)i * N;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (i * N + j < cols) t[j] = p[j];
+        return __builtin_bit_cast(u32x4, t);
+    }
+    __device__ void store(int u, typename Vec<T>::wide g) const
+    {
+        const uint32_t i = vector(u);
+        const u32x4 w = Vec<T>::narrow(g);
+        if ((i + 1) * N <= cols) {
+            store16_row<T>(out + (uint64_t)i * 16, w);
+        } else if (i * N < cols) {
+            const typename Vec<T>::type t = __builtin_bit_cast(typename Vec<T>::type, w);
+            T *const p = reinterpret_cast<T *>(out) + (uint64_t)i * N;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (i * N + j < cols) p[j] = t[j];
+        }
+    }
+};
+
+// scale * x - lse, at most 0 (a difference of large numbers may round to
+// above it) and finite where x is masked: 2^ of it is 0 there all the same.
+__device__ __forceinline__ float log_p(float x, float scale, float lse)
 {
-    for (uint32_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
-        T *const dx = static_cast<T *>(a.dlogits) + r * a.dlogits_stride;
-        const int64_t t = a.targets[r];
-        const bool given = t >= 0 && t < (int64_t)a.cols;
-        const float lse = a.lse[r], dlogp = given ? a.dlogp[r] : 0.0f;
-        const float dent = a.dentropy ? a.dentropy[r] : 0.0f, ent = a.dentropy ? a.entropy[r] : 0.0f;
-        for (uint32_t c = threadIdx.x; c < a.cols; c += kVocabBlock) {
-            const float v = (float)x[c];
-            float g = 0.0f;
-            if (v * a.scale != -kInf && lse != -kInf) {
-                const float l = log_p(v, a.scale, lse), p = exp_nat(l);
-                g = -p * (dlogp + dent * (l + ent));
-                if (given && c == (uint32_t)t) g += dlogp;
-                g *= a.scale;
+    return __builtin_amdgcn_fmed3f(__builtin_fmaf(x, scale, -lse), kFarBelow, 0.0f);
+}
+
+// dlogits = scale * (dlogp * (hot - p) - dent * p * (l + ent)), l = log p:
+// p * (l * k2 + k1), and dlogp * scale at the target.
+template <typename T>
+__global__ void __launch_bounds__(kVocabBlock) ew_logprobs_grad_kernel(LogprobsGradArgs a,
+                                                                       uint32_t tiles)
+{
+    constexpr int N = Vec<T>::N;
+    const uint64_t items = (uint64_t)a.rows * tiles;
+    for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const uint32_t r = (uint32_t)(item / tiles);
+        GradTile<T> g(static_cast<const T *>(a.logits) + r * a.stride,
+                      static_cast<T *>(a.dlogits) + r * a.dlogits_stride, a.cols,
+                      (uint32_t)(item % tiles));
+        const int64_t target = a.targets[r];
+        const bool given = target >= 0 && target < (int64_t)a.cols;
+        const bool empty = a.lse[r] == -kInf;
+        const float lse = empty ? 0.0f : a.lse[r], dlogp = given ? a.dlogp[r] : 0.0f;
+        const float dent = a.dentropy ? a.dentropy[r] : 0.0f;
+        const float ent = a.dentropy ? a.entropy[r] : 0.0f;
+        const float k1 = empty ? 0.0f : -(dlogp + dent * ent) * a.scale;
+        const float k2 = empty ? 0.0f : -dent * a.scale;
+        // the target's place in the tile, past the tile's end without one
+        const uint32_t hit = given && !empty ? (uint32_t)target - g.first : ~0u;
+#pragma unroll
+        for (int u = 0; u < g.U; ++u) {
+            const typename Vec<T>::wide x = Vec<T>::widen(g.v[u]);
+            typename Vec<T>::wide d;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float l = log_p(x[j], a.scale, lse);
+                d[j] = exp_nat(l) * __builtin_fmaf(l, k2, k1);
             }
-            dx[c] = (T)g;
+            if (hit / N == g.vector(u)) {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (hit % N == j && x[j] * a.scale != -kInf) d[j] += dlogp * a.scale;
+            }
+            if (lse != lse) {          // a NaN in the row: everything but the masked is one
+#pragma unroll
+                for (int j = 0; j < N; ++j) d[j] = x[j] * a.scale == -kInf ? 0.0f : lse;
+            }
+            g.store(u, d);
         }
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGradArgs a)
+// The teacher's distribution in one wave: every wave of a block works it out,
+// which needs no barrier.
+__device__ __forceinline__ Teacher wave_teacher(const float *teacher, const int64_t *ids,
+                                                uint32_t kept, uint32_t cols, float scale)
 {
-    __shared__ float scratch[2][kVocabWaves];
-    for (uint32_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
-        T *const dx = static_cast<T *>(a.dlogits) + r * a.dlogits_stride;
+    Teacher t;
+    float m = -kInf;
+    for (uint32_t k = threadIdx.x % 64; k < kept; k += 64) {
+        const float s = teacher[k] * scale;
+        if (kept_entry(ids[k], s, cols)) m = __builtin_fmaxf(m, s);
+    }
+    t.m = wave_reduce<Max>(m);
+    float z = 0.0f;
+    for (uint32_t k = threadIdx.x % 64; k < kept; k += 64) {
+        const float s = teacher[k] * scale;
+        if (kept_entry(ids[k], s, cols)) z += exp_nat(s - t.m);
+    }
+    t.z = wave_reduce<Sum>(z);
+    return t;
+}
+
+// The kept entries that fall into a tile, in the entries' order, and which of
+// the tile's vectors they fall into.
+constexpr uint32_t kTileEntries = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGradArgs a,
+                                                                      uint32_t tiles)
+{
+    constexpr int N = Vec<T>::N;
+    using Tile = GradTile<T>;
+    __shared__ uint32_t touched[Tile::kCols / N / 32];
+    __shared__ uint32_t at[kTileEntries];
+    __shared__ float weight[kTileEntries];
+    __shared__ uint32_t found;
+    const uint64_t items = (uint64_t)a.rows * tiles;
+    for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const uint32_t r = (uint32_t)(item / tiles);
+        Tile g(static_cast<const T *>(a.logits) + r * a.stride,
+               static_cast<T *>(a.dlogits) + r * a.dlogits_stride, a.cols,
+               (uint32_t)(item % tiles));
         const float *const teacher = a.teacher + (uint64_t)r * a.kept;
         const int64_t *const ids = a.ids + (uint64_t)r * a.kept;
-        const Teacher t = block_teacher(teacher, ids, a.kept, a.cols, a.scale, scratch);
-        const float lse = a.lse[r], g = t.z == 0.0f ? 0.0f : a.dloss[r] * a.scale;
-        for (uint32_t c = threadIdx.x; c < a.cols; c += kVocabBlock) {
-            const float v = (float)x[c];
-            float d = 0.0f;
-            if (v * a.scale != -kInf && lse != -kInf && t.z != 0.0f) {
-                float q = 0.0f;
-                for (uint32_t k = 0; k < a.kept; ++k) {
-                    const float s = teacher[k] * a.scale;
-                    if (ids[k] == (int64_t)c && kept_entry(ids[k], s, a.cols))
-                        q += exp_nat(s - t.m) / t.z;
+        if (threadIdx.x < Tile::kCols / N / 32) touched[threadIdx.x] = 0;
+        const Teacher t = wave_teacher(teacher, ids, a.kept, a.cols, a.scale);
+        __syncthreads();
+        const auto entry = [&](uint32_t k) {      // t of a kept entry
+            return exp_nat(teacher[k] * a.scale - t.m) / t.z;
+        };
+        const auto place = [&](uint32_t k) {      // its place in the tile, or past its end
+            const int64_t id = ids[k];
+            return kept_entry(id, teacher[k] * a.scale, a.cols) &&
+                           (uint64_t)id - g.first < g.cols
+                       ? (uint32_t)id - g.first : ~0u;
+        };
+        if (threadIdx.x < 64) {
+            uint32_t n = 0;
+            for (uint32_t k0 = 0; k0 < a.kept; k0 += 64) {
+                const uint32_t k = k0 + threadIdx.x;
+                const uint32_t p = k < a.kept ? place(k) : ~0u;
+                const uint64_t mask = __ballot(p != ~0u);
+                const uint32_t slot = n + lanes_below(mask);
+                if (p != ~0u) {
+                    atomicOr(&touched[p / N / 32], 1u << p / N % 32);
+                    if (slot < kTileEntries) {
+                        at[slot] = p;
+                        weight[slot] = entry(k);
+                    }
                 }
-                d = g * (exp_nat(log_p(v, a.scale, lse)) - q);
+                n += __builtin_popcountll(mask);
             }
-            dx[c] = (T)d;
+            if (threadIdx.x == 0) found = n;
         }
+        __syncthreads();
+        const uint32_t entries = found;
+        const bool empty = a.lse[r] == -kInf || t.z == 0.0f;
+        const float lse = empty ? 0.0f : a.lse[r], k1 = empty ? 0.0f : a.dloss[r] * a.scale;
+#pragma unroll
+        for (int u = 0; u < g.U; ++u) {
+            const uint32_t i = g.vector(u);
+            const typename Vec<T>::wide x = Vec<T>::widen(g.v[u]);
+            typename Vec<T>::wide d;
+#pragma unroll
+            for (int j = 0; j < N; ++j) d[j] = k1 * exp_nat(log_p(x[j], a.scale, lse));
+            if (touched[i / 32] >> i % 32 & 1) {
+                // the weights of one column are added up in the entries' order
+                float w[N] = {};
+                const auto add = [&](uint32_t p, float v) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (p == i * N + j) w[j] += v;
+                };
+                if (entries <= kTileEntries)
+                    for (uint32_t e = 0; e < entries; ++e) add(at[e], weight[e]);
+                else
+                    for (uint32_t k = 0; k < a.kept; ++k)
+                        if (place(k) / N == i) add(place(k), entry(k));
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (x[j] * a.scale != -kInf) d[j] -= k1 * w[j];
+            }
+            if (lse != lse || t.z != t.z) {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    d[j] = x[j] * a.scale == -kInf ? 0.0f : lse + t.z;
+            }
+            g.store(u, d);
+        }
+        if (item + gridDim.x < items) __syncthreads();
     }
 }
 
@@ -663,7 +833,12 @@ size_t distill_workspace(uint64_t rows, uint64_t cols) { return logprobs_workspa
                       : reinterpret_cast<const void *>(&K<__bf16>))
 
 // Blocks stride over what is beyond this many.
-constexpr uint64_t kMaxGrid = 1 << 20;
+constexpr uint64_t kMaxGrid = 1 << 23;
+
+static uint32_t grad_tiles(uint32_t cols)
+{
+    return (uint32_t)(((uint64_t)cols + kVocabBlock * kGradLane - 1) / (kVocabBlock * kGradLane));
+}
 
 template <class... A>
 static hipError_t go(const void *fn, uint64_t blocks, hipStream_t s, A... args)
@@ -700,8 +875,9 @@ hipError_t launch_logprobs(RowType t, const LogprobsArgs &a, int, hipStream_t s,
 hipError_t launch_logprobs_grad(RowType t, const LogprobsGradArgs &a, int, hipStream_t s,
                                 const char **path)
 {
-    *path = "a block a row";
-    return go(EW_BY_TYPE(t, ew_logprobs_grad_kernel), a.rows, s, a);
+    *path = "a block a tile";
+    const uint32_t tiles = grad_tiles(a.cols);
+    return go(EW_BY_TYPE(t, ew_logprobs_grad_kernel), (uint64_t)a.rows * tiles, s, a, tiles);
 }
 
 hipError_t launch_distill(RowType t, const DistillArgs &a, int, hipStream_t s, const char **path)
@@ -712,8 +888,9 @@ hipError_t launch_distill(RowType t, const DistillArgs &a, int, hipStream_t s, c
 hipError_t launch_distill_grad(RowType t, const DistillGradArgs &a, int, hipStream_t s,
                                const char **path)
 {
-    *path = "a block a row";
-    return go(EW_BY_TYPE(t, ew_distill_grad_kernel), a.rows, s, a);
+    *path = "a block a tile";
+    const uint32_t tiles = grad_tiles(a.cols);
+    return go(EW_BY_TYPE(t, ew_distill_grad_kernel), (uint64_t)a.rows * tiles, s, a, tiles);
 }
 
 }  // namespace ew
