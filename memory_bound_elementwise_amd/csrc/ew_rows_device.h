@@ -24,12 +24,14 @@ __device__ __forceinline__ float min_or_nan(float a, float b)
 }
 
 struct Sum {
-    static constexpr float kNone = 0.0f;
     __device__ static float f(float a, float b) { return a + b; }
 };
 struct Max {        // ignores NaNs
-    static constexpr float kNone = -kInf;
     __device__ static float f(float a, float b) { return __builtin_fmaxf(a, b); }
+};
+
+struct MaxOrNan {
+    __device__ static float f(float a, float b) { return max_or_nan(a, b); }
 };
 
 // The value of another lane of the same 16: dpp control word Ctrl.

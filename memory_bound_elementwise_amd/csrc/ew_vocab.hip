@@ -4,6 +4,8 @@
 
 #include "ew_rows_device.h"
 
+#include <type_traits>
+
 namespace ew {
 
 constexpr int kVocabBlock = 256;
@@ -115,24 +117,31 @@ __device__ __forceinline__ float log_prob(float x, const RowSum &s, const RowSta
 }
 
 // ---------------------------------------------------------------------------
-// The largest of a stream of logits
+// The largest logits of a row
 // ---------------------------------------------------------------------------
 
-// A logit's rank as one number: larger is more likely, ties to the lowest
-// column, a NaN as -inf, -0 as +0.  Never 0.
-__device__ __forceinline__ uint64_t rank_key(float x, uint32_t col)
+// A logit as a number that orders as it does (-0 as +0, a NaN as -inf), and
+// back.
+__device__ __forceinline__ uint32_t order(float x)
 {
     if (x != x) x = -kInf;
     x += 0.0f;
     const uint32_t u = __builtin_bit_cast(uint32_t, x);
-    const uint32_t k = u & 0x80000000u ? ~u : u | 0x80000000u;
-    return (uint64_t)k << 32 | (uint32_t)~col;
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ float key_logit(uint64_t key)
+__device__ __forceinline__ float order_logit(uint32_t k)
 {
-    const uint32_t k = (uint32_t)(key >> 32);
     return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
+constexpr uint32_t kOrderMasked = 0x007fffffu;      // order(-inf)
+
+// A logit's rank as one number: larger is more likely, ties to the lowest
+// column.  Never 0.
+__device__ __forceinline__ uint64_t rank_key(float x, uint32_t col)
+{
+    return (uint64_t)order(x) << 32 | (uint32_t)~col;
+}
+__device__ __forceinline__ float key_logit(uint64_t key) { return order_logit((uint32_t)(key >> 32)); }
 __device__ __forceinline__ uint32_t key_col(uint64_t key) { return ~(uint32_t)key; }
 
 __device__ __forceinline__ uint64_t lane_key(uint64_t k, int lane)
@@ -155,86 +164,70 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The smallest of the lanes' values, in every lane.
-__device__ __forceinline__ uint32_t wave_min(uint32_t x)
+// A number that at least k (1..64) of the lanes' orders are at or above, and
+// hardly below the k-th largest of them: each lane's order with its last six
+// bits replaced by the lane, which makes them different, is counted against
+// all others.
+__device__ __forceinline__ uint32_t lanes_kth(uint32_t own, uint32_t k)
 {
-    const auto step = [](uint32_t v, uint32_t o) { return o < v ? o : v; };
-#define EW_MIN_STEP(ctrl) \
-    x = step(x, (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, ctrl, 0xf, 0xf, true))
-    EW_MIN_STEP(0xB1);
-    EW_MIN_STEP(0x4E);
-    EW_MIN_STEP(0x141);
-    EW_MIN_STEP(0x140);
-#undef EW_MIN_STEP
-    const auto row = [&](int l) { return (uint32_t)__builtin_amdgcn_readlane((int)x, l); };
-    return step(step(row(0), row(16)), step(row(32), row(48)));
+    own = (own & ~63u) | (63 - threadIdx.x % 64);
+    uint32_t above = 0;
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+        above += (uint32_t)__builtin_amdgcn_readlane((int)own, i) > own;
+    const int at = __builtin_ctzll(__ballot(above == k - 1));
+    return (uint32_t)__builtin_amdgcn_readlane((int)own, at) & ~63u;
 }
 
-// One wave's candidates for the k largest keys of what it has seen: an
-// unordered list in LDS that holds at least the k largest (all, while fewer
-// were seen).  A key enters only above the bar; a list that has grown is cut
-// to its k largest, and the smallest of them becomes the bar.  On logits in
-// no special order few pass it: the first full chunk starts it at the k-th
-// largest of the 64 lanes' maxima.
+// One wave's candidates for the k largest keys: an unordered list in LDS that
+// holds every key offered above the bar, at least the k largest of them.  A
+// list that grows too long is cut to its k largest, and the smallest of
+// those becomes the bar.
 constexpr uint32_t kListKeys = 256;
-// A list is cut once it holds this many more than k.
-constexpr uint32_t kListSlack = 32;
 
 struct TopList {
     uint64_t *keys;      // kListKeys of LDS, this wave's
-    uint32_t count, k;   // the same in every lane, as is the rest
+    uint32_t count, k;   // the same in every lane, as is the bar
     uint64_t bar;
-    float bar_logit;     // once closed: no later key with this logit or less enters
-    bool open;           // not yet cut
 
-    __device__ void start(uint64_t *list, uint32_t top)
-    {
-        keys = list;
-        count = 0;
-        k = top;
-        bar = 0;
-        bar_logit = -kInf;
-        open = true;
-    }
-
-    // Cut to the k largest; nothing while there are fewer.  A value with
-    // exactly k keys at or above it is found bit by bit.
+    // A value with exactly k keys at or above it is found bit by bit.
     __device__ void cut()
     {
-        if (count < k) return;
         wave_sync();
         const uint32_t lane = threadIdx.x % 64;
-        if (count > k) {
-            uint64_t own[kListKeys / 64];
+        uint64_t own[kListKeys / 64];
+#pragma unroll
+        for (uint32_t i = 0; i < kListKeys / 64; ++i)
+            own[i] = i * 64 + lane < count ? keys[i * 64 + lane] : 0;
+        uint64_t at = 0;
+        for (int bit = 63; bit >= 0; --bit) {
+            const uint64_t trial = at | (uint64_t)1 << bit;
+            uint32_t n = 0;
 #pragma unroll
             for (uint32_t i = 0; i < kListKeys / 64; ++i)
-                own[i] = i * 64 + lane < count ? keys[i * 64 + lane] : 0;
-            uint64_t at = 0;
-            for (int bit = 63; bit >= 0; --bit) {
-                const uint64_t trial = at | (uint64_t)1 << bit;
-                uint32_t n = 0;
-#pragma unroll
-                for (uint32_t i = 0; i < kListKeys / 64; ++i)
-                    n += __builtin_popcountll(__ballot(own[i] >= trial));
-                if (n >= k) at = trial;
-                if (n == k) break;
-            }
-            count = 0;
-#pragma unroll
-            for (uint32_t i = 0; i < kListKeys / 64; ++i) {
-                const bool stay = own[i] >= at;
-                const uint64_t mask = __ballot(stay);
-                if (stay) keys[count + lanes_below(mask)] = own[i];
-                count += __builtin_popcountll(mask);
-            }
-            wave_sync();
+                n += __builtin_popcountll(__ballot(own[i] >= trial));
+            if (n >= k) at = trial;
+            if (n == k) break;
         }
-        const uint64_t key = lane < count ? keys[lane] : ~(uint64_t)0;
-        const uint32_t hi = wave_min((uint32_t)(key >> 32));
-        const uint32_t lo = wave_min((uint32_t)(key >> 32) == hi ? (uint32_t)key : ~0u);
-        bar = (uint64_t)hi << 32 | lo;
-        bar_logit = key_logit(bar);
-        open = false;
+        count = 0;
+        bar = ~(uint64_t)0;
+#pragma unroll
+        for (uint32_t i = 0; i < kListKeys / 64; ++i) {
+            const bool stay = own[i] >= at;
+            const uint64_t mask = __ballot(stay);
+            if (stay) {
+                keys[count + lanes_below(mask)] = own[i];
+                bar = own[i] < bar ? own[i] : bar;
+            }
+            count += __builtin_popcountll(mask);
+        }
+        wave_sync();
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const uint64_t o = __shfl_xor((unsigned long long)bar, d);
+            bar = o < bar ? o : bar;
+        }
+        bar = lane_key(bar, 0);
     }
 
     // Each lane offers one key (0: none).
@@ -247,46 +240,41 @@ struct TopList {
         count += __builtin_popcountll(mask);
         if (count > kListKeys - 64) cut();
     }
-
-    // The k-th largest of the lanes' values becomes the first bar: at least k
-    // keys are at or above it.
-    __device__ void seed(float lane_top)
-    {
-        if (lane_top != lane_top) lane_top = -kInf;
-        uint32_t rank = 0;
-        const uint32_t lane = threadIdx.x % 64;
-#pragma unroll 8
-        for (uint32_t i = 0; i < 64; ++i) {
-            const float o = lane_value(lane_top, i);
-            rank += o > lane_top || (o == lane_top && i < lane);
-        }
-        const float v = lane_value(lane_top, __builtin_ctzll(__ballot(rank == k - 1)));
-        bar = rank_key(v, ~0u);      // below every key of that logit
-    }
 };
 
-// The k largest keys of all waves' lists, best first: lane i of the first
-// wave returns the i-th (0 past their number).  Every wave calls it; the
-// lists are consecutive.  One barrier.
-__device__ __forceinline__ uint64_t block_top(TopList &list, const uint64_t *lists,
-                                              uint32_t *counts)
+struct TopShared {
+    uint64_t keys[kVocabWaves][kListKeys];
+    uint64_t best[64];
+    uint32_t counts[kVocabWaves], bars[kVocabWaves];
+    uint8_t lanes[kVocabWaves][64];
+};
+
+// The k largest keys of all waves' lists, best first: the first wave's lane i
+// returns the i-th (0 past their number).  Every wave calls it; two barriers.
+// Each key counts the keys above it.
+__device__ __forceinline__ uint64_t block_top(TopList &list, TopShared &sh)
 {
     const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    list.cut();
-    if (lane == 0) counts[wave] = list.count;
+    if (list.count > 63) list.cut();
+    if (lane == 0) {
+        sh.counts[wave] = list.count;
+        list.keys[list.count] = 0;             // pairs are read below
+    }
+    if (wave == 0) sh.best[lane] = 0;
     __syncthreads();
-    if (wave != 0) return 0;
-    for (uint32_t w = 1; w < kVocabWaves; ++w)       // at most k <= 64 keys each
-        list.offer(lane < counts[w] ? lists[w * kListKeys + lane] : 0);
-    list.cut();
-    wave_sync();
     const uint64_t key = lane < list.count ? list.keys[lane] : 0;
-    uint32_t rank = 0;
-    for (uint32_t i = 0; i < list.count; ++i) rank += lane_key(key, i) > key;
-    wave_sync();
-    if (lane < list.count) list.keys[rank] = key;
-    wave_sync();
-    return lane < list.count ? list.keys[lane] : 0;
+    uint32_t above = 0;
+#pragma unroll
+    for (int w = 0; w < kVocabWaves; ++w) {
+        const uint32_t n = sh.counts[w];
+        for (uint32_t i = 0; i < n; i += 2) {
+            const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&sh.keys[w][i]);
+            above += (two.x > key) + (two.y > key);
+        }
+    }
+    if (key != 0 && above < list.k) sh.best[above] = key;
+    __syncthreads();
+    return wave == 0 ? sh.best[lane] : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -314,24 +302,14 @@ struct Part {
     }
 };
 
-template <typename T, bool Ent, bool Top>
+template <typename T, bool Ent>
 __device__ __forceinline__ RowSum stream_part(const T *x, uint32_t cols, const Part &p,
-                                              const RowSplit<T> &split, float c, TopList &list)
+                                              const RowSplit<T> &split, float c)
 {
     constexpr int U = kPerLane / Vec<T>::N;
     constexpr uint32_t kStep = kVocabBlock * U;
-    const uint32_t lane = threadIdx.x % 64;
     const char *const body = reinterpret_cast<const char *>(x + split.head);
     RowSum s{-kInf, 0.0f, 0.0f};
-
-    // up to a vector's elements before or after the aligned body: one lane each
-    const auto edge = [&](uint32_t start, uint32_t n) {
-        const bool live = lane < n;
-        const float v[1] = {live ? (float)x[start + lane] : -kInf};
-        absorb<Ent>(s, v, c);
-        if constexpr (Top) list.offer(live ? rank_key(v[0], start + lane) : 0);
-    };
-    if (p.first && threadIdx.x < 64 && split.head) edge(0, split.head);
 
     u32x4 next[U];
     const auto fetch = [&](uint32_t v) {       // v: the block's first vector
@@ -348,6 +326,15 @@ __device__ __forceinline__ RowSum stream_part(const T *x, uint32_t cols, const P
         }
     };
     if (p.lo < p.hi) fetch(p.lo);
+    // up to a vector's elements before and after the aligned body: one lane each
+    if (threadIdx.x < split.head && p.first) {
+        const float v[1] = {(float)x[threadIdx.x]};
+        absorb<Ent>(s, v, c);
+    }
+    if (threadIdx.x < split.tail && p.last) {
+        const float v[1] = {(float)x[cols - split.tail + threadIdx.x]};
+        absorb<Ent>(s, v, c);
+    }
     for (uint32_t v = p.lo; v < p.hi;) {
         float f[kPerLane];
 #pragma unroll
@@ -356,26 +343,77 @@ __device__ __forceinline__ RowSum stream_part(const T *x, uint32_t cols, const P
 #pragma unroll
             for (int j = 0; j < Vec<T>::N; ++j) f[u * Vec<T>::N + j] = w[j];
         }
-        const uint32_t at = v;
         v = p.hi - v > kStep ? v + kStep : p.hi;
         if (v < p.hi) fetch(v);
-        const float top = absorb<Ent>(s, f, c);
-        if constexpr (Top) {
-            if (list.open || __ballot(top > list.bar_logit) != 0) {
-                if (list.open && list.bar == 0 && p.hi - at >= kStep) list.seed(top);
+        absorb<Ent>(s, f, c);
+    }
+    return s;
+}
+
+// The part's `top` largest logits.  The stream has left each lane the largest
+// of its own (lane_top); at least `top` logits are at or above the top-th
+// largest of a wave's 64, so that the highest of the waves' is a bar that few
+// more than `top` logits pass, and only lanes whose largest passes it hold
+// any: their vectors, one in a few hundred, are read again.  Where fewer
+// lanes than that have a logit that is not masked the bar is -inf: then every
+// such logit is taken, and the lowest masked columns after them.
+template <typename T>
+__device__ __forceinline__ uint64_t part_top(const T *x, uint32_t cols, const Part &p,
+                                             const RowSplit<T> &split, float lane_top,
+                                             uint32_t top, TopShared &sh)
+{
+    constexpr uint32_t N = Vec<T>::N;
+    const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const uint32_t kth = lanes_kth(order(lane_top), top);
+    if (lane == 0) sh.bars[wave] = kth;
+    __syncthreads();
+    uint32_t bar = sh.bars[0];
 #pragma unroll
-                for (int k = 0; k < kPerLane; ++k) {
-                    const uint32_t i = at + threadIdx.x + k / Vec<T>::N * kVocabBlock;
-                    if (__ballot(!(f[k] < key_logit(list.bar))) != 0)
-                        list.offer(i < p.hi ? rank_key(f[k], split.head + i * Vec<T>::N + k % Vec<T>::N)
-                                            : 0);
-                }
-                if (list.open || list.count > list.k + kListSlack) list.cut();
+    for (int w = 1; w < kVocabWaves; ++w) bar = sh.bars[w] > bar ? sh.bars[w] : bar;
+    bar = __builtin_amdgcn_readfirstlane(bar);
+    const bool masked = bar <= kOrderMasked;
+    TopList list{sh.keys[wave], 0, top, masked ? (uint64_t)kOrderMasked << 32 | ~0u
+                                               : (uint64_t)bar << 32};
+    // lanes to read again, and the vectors each took
+    const bool again = masked ? lane_top > -kInf : order(lane_top) >= bar;
+    const uint64_t mask = __ballot(again);
+    if (again) sh.lanes[wave][lanes_below(mask)] = (uint8_t)lane;
+    wave_sync();
+    const uint32_t count = __builtin_popcountll(mask);
+    const uint32_t each = (p.hi - p.lo + kVocabBlock - 1) / kVocabBlock;
+    const char *const body = reinterpret_cast<const char *>(x + split.head);
+    for (uint32_t i0 = 0; i0 < count * each; i0 += 64) {
+        const uint32_t i = i0 + lane;
+        // the lowest columns first
+        const uint32_t v = i < count * each
+                               ? p.lo + i / count * kVocabBlock + wave * 64 + sh.lanes[wave][i % count]
+                               : p.hi;
+        const typename Vec<T>::wide f = Vec<T>::widen(
+            v < p.hi ? load16<true, sizeof(T)>(body + (uint64_t)v * 16) : Vec<T>::masked());
+#pragma unroll
+        for (uint32_t j = 0; j < N; ++j)
+            list.offer(v < p.hi ? rank_key(f[j], split.head + v * N + j) : 0);
+    }
+    if (wave == 0) {
+        if (p.first && split.head) list.offer(lane < split.head ? rank_key((float)x[lane], lane) : 0);
+        if (p.last && split.tail) {
+            const uint32_t at = cols - split.tail + lane;
+            list.offer(lane < split.tail ? rank_key((float)x[at], at) : 0);
+        }
+        if (masked) {
+            // fewer than `top` (or the list has them all): masked columns, of
+            // which the first 128 hold enough
+            list.bar = 0;
+            const uint32_t from = p.first ? 0 : split.head + p.lo * N;
+            const uint32_t to = p.last ? cols : split.head + p.hi * N;
+            for (uint32_t k = 0; k < 2; ++k) {
+                const uint32_t at = from + k * 64 + lane;
+                const float f = at < to ? (float)x[at] : 0.0f;
+                list.offer(order(f) == kOrderMasked ? rank_key(f, at) : 0);
             }
         }
     }
-    if (p.last && threadIdx.x < 64 && split.tail) edge(cols - split.tail, split.tail);
-    return s;
+    return block_top(list, sh);
 }
 
 // ---------------------------------------------------------------------------
@@ -491,19 +529,20 @@ __device__ __forceinline__ uint64_t *part_keys(void *ws, uint32_t rows, uint32_t
     return reinterpret_cast<uint64_t *>(part_sums(ws) + (uint64_t)rows * parts);
 }
 
+struct Nothing {};
+
 template <bool Top>
 struct ForwardShared {
+    std::conditional_t<Top, TopShared, Nothing> top;
     RowSum part[kVocabWaves];
     float scratch[3][kVocabWaves];
-    uint32_t counts[kVocabWaves];
-    uint64_t keys[Top ? kVocabWaves * kListKeys : 1];
 };
 
 template <typename T, class Op, bool Ent, bool Top>
 __global__ void __launch_bounds__(kVocabBlock) ew_vocab_forward_kernel(typename Op::Args a,
                                                                        uint32_t parts)
 {
-    __shared__ ForwardShared<Top> sh;
+    __shared__ __align__(16) ForwardShared<Top> sh;
     const uint64_t items = (uint64_t)a.rows * parts;
     const float c = a.scale * kLog2e;
     for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
@@ -512,12 +551,11 @@ __global__ void __launch_bounds__(kVocabBlock) ew_vocab_forward_kernel(typename 
         typename Op::Ahead h{};
         if (parts == 1) h = Op::ahead(a, r, x);
         const RowSplit<T> split(x, a.cols);
-        TopList list;
-        if constexpr (Top) list.start(sh.keys + threadIdx.x / 64 * kListKeys, Op::top(a));
-        RowSum s = stream_part<T, Ent, Top>(x, a.cols, Part(split.vectors, part, parts), split, c, list);
-        block_join<Ent>(s, c, sh.part);
+        const Part p(split.vectors, part, parts);
+        RowSum s = stream_part<T, Ent>(x, a.cols, p, split, c);
         uint64_t key = 0;
-        if constexpr (Top) key = block_top(list, sh.keys, sh.counts);
+        if constexpr (Top) key = part_top(x, a.cols, p, split, s.m, Op::top(a), sh.top);
+        block_join<Ent>(s, c, sh.part);
         if (parts == 1) {
             Op::finish(a, r, x, h, s, key, sh.scratch);
         } else {
@@ -534,7 +572,7 @@ template <typename T, class Op, bool Ent, bool Top>
 __global__ void __launch_bounds__(kVocabBlock) ew_vocab_join_kernel(typename Op::Args a,
                                                                     uint32_t parts)
 {
-    __shared__ ForwardShared<Top> sh;
+    __shared__ __align__(16) ForwardShared<Top> sh;
     const float c = a.scale * kLog2e;
     for (uint64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
@@ -549,19 +587,23 @@ __global__ void __launch_bounds__(kVocabBlock) ew_vocab_join_kernel(typename Op:
             s.z += o.z;
             s.b += o.b;
         }
-        block_join<Ent>(s, c, sh.part);
         uint64_t key = 0;
         if constexpr (Top) {
-            TopList list;
-            list.start(sh.keys + threadIdx.x / 64 * kListKeys, Op::top(a));
-            const uint32_t n = parts * Op::top(a);
+            // the parts' lists are in order: the top-th largest of 64 keys
+            // from their heads is a bar for all
+            const uint32_t top = Op::top(a), n = parts * top, lane = threadIdx.x % 64;
             const uint64_t *const keys = part_keys(a.workspace, a.rows, parts) + r * n;
+            const uint32_t from = lane % parts * top + lane / parts;
+            const uint32_t head = lane / parts < top ? (uint32_t)(keys[from] >> 32) : 0;
+            const uint32_t bar = lanes_kth(head, top);
+            TopList list{sh.top.keys[threadIdx.x / 64], 0, top, (uint64_t)bar << 32};
             for (uint32_t i = threadIdx.x / 64 * 64; i < n; i += kVocabBlock) {
                 const uint32_t at = i + threadIdx.x % 64;
                 list.offer(at < n ? keys[at] : 0);
             }
-            key = block_top(list, sh.keys, sh.counts);
+            key = block_top(list, sh.top);
         }
+        block_join<Ent>(s, c, sh.part);
         Op::finish(a, (uint32_t)r, x, h, s, key, sh.scratch);
         if (r + gridDim.x < a.rows) __syncthreads();
     }
