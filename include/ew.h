@@ -559,7 +559,7 @@ ew_status_t ew_logprobs_grad_bf16(const uint16_t *logits, size_t stride, const i
  *   loss = sum t * (log t - (s[id] - lse))
  * per row: 0 if no entry remains; entries whose t underflows (below 2^-126)
  * add nothing; +inf if another entry meets a masked logit.  A column named twice counts twice.
- * lse is optional.  scale is finite and > 0, kept <= 2^20. */
+ * lse is optional.  scale is finite and > 0, kept <= 1024. */
 size_t ew_distill_workspace(size_t rows, size_t cols);
 ew_status_t ew_distill_f32(const float *logits, size_t stride, const float *teacher,
                            const int64_t *ids, size_t kept, float *loss, float *lse, float scale,

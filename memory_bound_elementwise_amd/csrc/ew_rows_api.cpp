@@ -276,8 +276,6 @@ ew_status_t logprobs_grad(RowType t, const void *logits, size_t stride, const in
     return launch("logprobs_grad", t, a, stream, launch_logprobs_grad);
 }
 
-constexpr size_t kMaxKept = (size_t)1 << 20;
-
 ew_status_t distill(RowType t, const void *logits, size_t stride, const float *teacher,
                     const int64_t *ids, size_t kept, float *loss, float *lse, float scale,
                     void *workspace, size_t workspace_bytes, size_t rows, size_t cols,

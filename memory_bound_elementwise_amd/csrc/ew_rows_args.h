@@ -79,6 +79,9 @@ struct DistillGradArgs {
 // Most alternatives a call ranks: one per lane of a wave.
 constexpr uint32_t kTopMax = 64;
 
+// Most kept entries of a row: the distillation's gradient holds a row's in LDS.
+constexpr uint32_t kMaxKept = 1024;
+
 // Workspace bytes: a function of the sizes alone.
 size_t norm_grad_workspace(uint64_t rows, uint64_t cols);
 size_t logprobs_workspace(uint64_t rows, uint64_t cols, uint64_t top);

@@ -15,10 +15,9 @@ constexpr int kVocabWaves = kVocabBlock / 64;
 // Softmax statistics of a row
 // ---------------------------------------------------------------------------
 
-// With m the largest logit seen (NaNs ignored), c = scale * log2(e) and
-// d = c * (x - m): z = sum 2^d, b = sum 2^d * d.  The difference is taken
-// before the product so that d is exactly 0 at the largest logit, whatever
-// its size.  Masked logits (-inf) add nothing; a NaN or +inf makes z a NaN.
+// With m the largest logit seen (NaNs ignored), c = scale * log2(e) and d(x)
+// the distance of x from m in powers of two (below): z = sum 2^d, b = sum
+// 2^d * d.  Masked logits (-inf) add nothing; a NaN or +inf makes z a NaN.
 struct RowSum {
     float m, z, b;
 };
@@ -27,36 +26,83 @@ struct RowSum {
 // keeps 0 * d from being a NaN, and 2^d is 0 all the same.
 constexpr float kFarBelow = -1e30f;
 
+// d(x) is c * x - t with t = c * m rounded: the product and difference in one
+// fma, rounded once, and the sums are exact relative to 2^t whatever t is.
+// Where |t| is past kNear its rounding would be larger than the differences
+// that matter (a row of one large number must give d = 0, not the error of
+// t), so there d(x) is c * (x - m).  t is the same number wherever it is
+// used: the functions that form it leave its product alone (contract off).
+constexpr float kNear = 0x1p16f;
+
 __device__ __forceinline__ float finite_base(float m) { return m == -kInf ? 0.0f : m; }
+
+__device__ __forceinline__ float distance(float x, float m, float c)
+{
+#pragma clang fp contract(off)
+    m = finite_base(m);
+    const float t = m * c;
+    return __builtin_fabsf(t) <= kNear ? __builtin_fmaf(x, c, -t) : (x - m) * c;
+}
 
 // s re-based from s.m to m >= s.m.
 template <bool Ent>
 __device__ __forceinline__ void rebase(RowSum &s, float m, float c)
 {
-    const float shift = __builtin_fmaxf((s.m - finite_base(m)) * c, kFarBelow);
-    const float f = __builtin_amdgcn_exp2f(shift);
+#pragma clang fp contract(off)
+    const float from = s.m * c, to = finite_base(m) * c;
+    const bool near = __builtin_fabsf(from) <= kNear && __builtin_fabsf(to) <= kNear;
+    const float d = near ? from - to : (s.m - finite_base(m)) * c;
+    const float shift = __builtin_fmaxf(d, kFarBelow), f = __builtin_amdgcn_exp2f(shift);
     if constexpr (Ent) s.b = f * __builtin_fmaf(shift, s.z, s.b);
     s.z *= f;
     s.m = m;
 }
 
-// N more logits of this lane.  One re-basing for N terms; the maximum costs
-// half an instruction a logit (three operands each).
-template <bool Ent, int N>
-__device__ __forceinline__ float absorb(RowSum &s, const float (&v)[N], float c)
+template <int N>
+__device__ __forceinline__ float largest(const float (&v)[N])
 {
     float top = v[0];
 #pragma unroll
-    for (int k = 1; k < N; ++k) top = __builtin_fmaxf(top, v[k]);
-    rebase<Ent>(s, __builtin_fmaxf(s.m, top), c);
-    const float base = finite_base(s.m);
+    for (int k = 1; k < N; ++k) top = __builtin_fmaxf(top, v[k]);   // three operands each
+    return top;
+}
+
+// N more logits of this lane, whatever they are.
+template <bool Ent, int N>
+__device__ __forceinline__ void absorb_any(RowSum &s, const float (&v)[N], float c)
+{
+    rebase<Ent>(s, __builtin_fmaxf(s.m, largest(v)), c);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const float d = (v[k] - base) * c, e = __builtin_amdgcn_exp2f(d);
+        const float d = distance(v[k], s.m, c), e = __builtin_amdgcn_exp2f(d);
         s.z += e;
         if constexpr (Ent) s.b = __builtin_fmaf(e, __builtin_fmaxf(d, kFarBelow), s.b);
     }
-    return top;
+}
+
+// The same in fewer instructions, for logits of ordinary size and, with
+// entropy, none masked: returns whether that was so for this lane (s is of no
+// use otherwise).  16-bit rows are bound by the vector unit: an element costs
+// its widening, half a maximum, an fma, a power, an addition and, with
+// entropy, another fma.
+template <bool Ent, int N>
+__device__ __forceinline__ bool absorb_plain(RowSum &s, const float (&v)[N], float c)
+{
+#pragma clang fp contract(off)
+    const float m = __builtin_fmaxf(s.m, largest(v));
+    const float t = finite_base(m) * c;
+    const float shift = __builtin_fmaxf(s.m * c - t, kFarBelow);
+    const float f = __builtin_amdgcn_exp2f(shift);
+    if constexpr (Ent) s.b = f * __builtin_fmaf(shift, s.z, s.b);
+    s.z *= f;
+    s.m = m;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float d = __builtin_fmaf(v[k], c, -t), e = __builtin_amdgcn_exp2f(d);
+        s.z += e;
+        if constexpr (Ent) s.b = __builtin_fmaf(e, d, s.b);
+    }
+    return __builtin_fabsf(t) <= kNear && (!Ent || s.b == s.b);
 }
 
 // The sums of the wave's lanes, in every lane.
@@ -113,7 +159,10 @@ __device__ __forceinline__ float log_prob(float x, const RowSum &s, const RowSta
 {
     if (st.empty) return -kInf;
     if (st.lse != st.lse) return st.lse;
-    return (x - s.m) * scale - st.log_z;
+    const float d = distance(x, s.m, scale * kLog2e);
+    // far away (where d may overflow though its natural logarithm does not)
+    // the rounding of t no longer matters
+    return d < -kNear ? (x - s.m) * scale - st.log_z : __builtin_fmaf(d, kLn2, -st.log_z);
 }
 
 // ---------------------------------------------------------------------------
@@ -267,6 +316,7 @@ __device__ __forceinline__ uint64_t block_top(TopList &list, TopShared &sh)
 #pragma unroll
     for (int w = 0; w < kVocabWaves; ++w) {
         const uint32_t n = sh.counts[w];
+#pragma unroll 4
         for (uint32_t i = 0; i < n; i += 2) {
             const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&sh.keys[w][i]);
             above += (two.x > key) + (two.y > key);
@@ -302,50 +352,64 @@ struct Part {
     }
 };
 
+// The next vectors are on their way while the lane's last ones are added up.
+// 4096 x 131072 bf16: reading alone, in this pattern, takes 157 us (151 at
+// best, with blocks of 1024 threads, whose few rows at a time leave the ends
+// of rows uncovered).
 template <typename T, bool Ent>
 __device__ __forceinline__ RowSum stream_part(const T *x, uint32_t cols, const Part &p,
                                               const RowSplit<T> &split, float c)
 {
-    constexpr int U = kPerLane / Vec<T>::N;
+    constexpr int N = Vec<T>::N, U = kPerLane / N;
     constexpr uint32_t kStep = kVocabBlock * U;
     const char *const body = reinterpret_cast<const char *>(x + split.head);
     RowSum s{-kInf, 0.0f, 0.0f};
 
     u32x4 next[U];
     const auto fetch = [&](uint32_t v) {       // v: the block's first vector
-        if (p.hi - v >= kStep) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                next[u] = load16<true, sizeof(T)>(body + (uint64_t)(v + threadIdx.x + u * kVocabBlock) * 16);
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t i = v + threadIdx.x + u * kVocabBlock;
-                next[u] = i < p.hi ? load16<true, sizeof(T)>(body + (uint64_t)i * 16) : Vec<T>::masked();
-            }
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = v + threadIdx.x + u * kVocabBlock;
+            if (i < p.hi) next[u] = load16<true, sizeof(T)>(body + (uint64_t)i * 16);
         }
     };
-    if (p.lo < p.hi) fetch(p.lo);
+    fetch(p.lo);
     // up to a vector's elements before and after the aligned body: one lane each
     if (threadIdx.x < split.head && p.first) {
         const float v[1] = {(float)x[threadIdx.x]};
-        absorb<Ent>(s, v, c);
+        absorb_any<Ent>(s, v, c);
     }
     if (threadIdx.x < split.tail && p.last) {
         const float v[1] = {(float)x[cols - split.tail + threadIdx.x]};
-        absorb<Ent>(s, v, c);
+        absorb_any<Ent>(s, v, c);
     }
-    for (uint32_t v = p.lo; v < p.hi;) {
+    bool plain = true;       // until the wave meets logits that are not
+    uint32_t v = p.lo;
+    for (; p.hi - v >= kStep; v += kStep) {
         float f[kPerLane];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const typename Vec<T>::wide w = Vec<T>::widen(next[u]);
 #pragma unroll
-            for (int j = 0; j < Vec<T>::N; ++j) f[u * Vec<T>::N + j] = w[j];
+            for (int j = 0; j < N; ++j) f[u * N + j] = w[j];
         }
-        v = p.hi - v > kStep ? v + kStep : p.hi;
-        if (v < p.hi) fetch(v);
-        absorb<Ent>(s, f, c);
+        fetch(v + kStep);
+        if (plain) {
+            RowSum more = s;
+            plain = __ballot(!absorb_plain<Ent>(more, f, c)) == 0;
+            if (plain) s = more;
+        }
+        if (!plain) absorb_any<Ent>(s, f, c);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (v + threadIdx.x + u * kVocabBlock < p.hi) {
+            const typename Vec<T>::wide w = Vec<T>::widen(next[u]);
+            float f[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) f[j] = w[j];
+            absorb_any<Ent>(s, f, c);
+        }
     }
     return s;
 }
@@ -432,27 +496,6 @@ __device__ __forceinline__ bool kept_entry(int64_t id, float scaled, uint32_t co
     return id >= 0 && id < (int64_t)cols && scaled != -kInf;
 }
 
-__device__ Teacher block_teacher(const float *teacher, const int64_t *ids, uint32_t kept,
-                                 uint32_t cols, float scale, float (*scratch)[kVocabWaves])
-{
-    Teacher t;
-    float m = -kInf;
-    for (uint32_t k = threadIdx.x; k < kept; k += kVocabBlock) {
-        const float s = teacher[k] * scale;
-        if (kept_entry(ids[k], s, cols)) m = __builtin_fmaxf(m, s);
-    }
-    t.m = block_reduce<Max, kVocabWaves>(m, scratch[0]);
-    float z = 0.0f;
-    for (uint32_t k = threadIdx.x; k < kept; k += kVocabBlock) {
-        const float s = teacher[k] * scale;
-        if (kept_entry(ids[k], s, cols)) z += exp_nat(s - t.m);
-    }
-    t.z = block_reduce<Sum, kVocabWaves>(z, scratch[1]);
-    __syncthreads();
-    return t;
-}
-
-
 // What a forward call does with a row's sums, for all threads of a block.
 struct Logprobs {
     using Args = LogprobsArgs;
@@ -484,41 +527,61 @@ struct Logprobs {
             a.top_logp[i] = log_prob(key_logit(key), s, st, a.scale);
         }
     }
-    __device__ static uint32_t top(const Args &a) { return a.top; }
+    __host__ __device__ static uint32_t top(const Args &a) { return a.top; }
 };
 
 struct Distill {
     using Args = DistillArgs;
-    struct Ahead {};
+    struct Ahead {              // thread k's entry k: loaded before the row is streamed
+        float teacher, logit;   // scaled teacher logit, -inf if there is none
+    };
     template <typename T>
-    __device__ static Ahead ahead(const Args &, uint32_t, const T *)
+    __device__ static Ahead entry(const Args &a, uint32_t r, const T *x, uint32_t k)
     {
-        return Ahead{};
+        Ahead h{-kInf, 0.0f};
+        if (k < a.kept) {
+            const int64_t id = a.ids[(uint64_t)r * a.kept + k];
+            const float t = a.teacher[(uint64_t)r * a.kept + k] * a.scale;
+            if (kept_entry(id, t, a.cols)) h = Ahead{t, (float)x[id]};
+        }
+        return h;
     }
     template <typename T>
-    __device__ static void finish(const Args &a, uint32_t r, const T *x, const Ahead &,
+    __device__ static Ahead ahead(const Args &a, uint32_t r, const T *x)
+    {
+        return entry(a, r, x, threadIdx.x);
+    }
+    template <typename T>
+    __device__ static void finish(const Args &a, uint32_t r, const T *x, const Ahead &h,
                                   const RowSum &s, uint64_t, float (*scratch)[kVocabWaves])
     {
-        const float *const teacher = a.teacher + (uint64_t)r * a.kept;
-        const int64_t *const ids = a.ids + (uint64_t)r * a.kept;
         const RowStat st = row_stat(s, a.scale);
-        const Teacher t = block_teacher(teacher, ids, a.kept, a.cols, a.scale, scratch);
-        const float log_tz = __builtin_logf(t.z);
+        // the entries past the block's size are read where they are needed
+        const auto each = [&](const auto &f) {
+            f(h);
+            for (uint32_t k = threadIdx.x + kVocabBlock; k < a.kept; k += kVocabBlock)
+                f(entry(a, r, x, k));
+        };
+        float m = -kInf;
+        each([&](const Ahead &e) { m = __builtin_fmaxf(m, e.teacher); });
+        m = block_reduce<Max, kVocabWaves>(m, scratch[0]);
+        float z = 0.0f;
+        each([&](const Ahead &e) { z += e.teacher == -kInf ? 0.0f : exp_nat(e.teacher - m); });
+        z = block_reduce<Sum, kVocabWaves>(z, scratch[1]);
+        const float log_z = __builtin_logf(z);
         float loss = 0.0f;
-        for (uint32_t k = threadIdx.x; k < a.kept; k += kVocabBlock) {
-            const float v = teacher[k] * a.scale;
-            if (!kept_entry(ids[k], v, a.cols)) continue;
-            const float l = v - t.m - log_tz, p = exp_nat(v - t.m) / t.z;
-            if (p >= 0x1p-126f || p != p)
-                loss += p * (l - log_prob((float)x[ids[k]], s, st, a.scale));
-        }
+        each([&](const Ahead &e) {
+            if (e.teacher == -kInf) return;
+            const float l = e.teacher - m - log_z, p = exp_nat(e.teacher - m) / z;
+            if (p >= 0x1p-126f || p != p) loss += p * (l - log_prob(e.logit, s, st, a.scale));
+        });
         loss = block_reduce<Sum, kVocabWaves>(loss, scratch[2]);
         if (threadIdx.x == 0) {
             a.loss[r] = loss;
             if (a.lse) a.lse[r] = st.lse;
         }
     }
-    __device__ static uint32_t top(const Args &) { return 0; }
+    __host__ __device__ static uint32_t top(const Args &) { return 0; }
 };
 
 // The workspace of a call that splits rows: a RowSum padded to 16 bytes for
@@ -538,8 +601,12 @@ struct ForwardShared {
     float scratch[3][kVocabWaves];
 };
 
+// Eight waves a SIMD for 16-bit logits: with the 74 registers the compiler
+// would take, the 2048 blocks of as many rows need a second round on 256 CUs
+// (2048 x 50257 bf16, 5 alternatives: 54.6 us; 50.6 with 64).  32-bit rows,
+// twice as long in bytes, would spill.
 template <typename T, class Op, bool Ent, bool Top>
-__global__ void __launch_bounds__(kVocabBlock) ew_vocab_forward_kernel(typename Op::Args a,
+__global__ void __launch_bounds__(kVocabBlock, sizeof(T) == 2 ? 8 : 4) ew_vocab_forward_kernel(typename Op::Args a,
                                                                        uint32_t parts)
 {
     __shared__ __align__(16) ForwardShared<Top> sh;
@@ -593,14 +660,19 @@ __global__ void __launch_bounds__(kVocabBlock) ew_vocab_join_kernel(typename Op:
             // from their heads is a bar for all
             const uint32_t top = Op::top(a), n = parts * top, lane = threadIdx.x % 64;
             const uint64_t *const keys = part_keys(a.workspace, a.rows, parts) + r * n;
+            constexpr int kEarly = 4;      // keys loaded before the bar is known
+            uint64_t early[kEarly];
+#pragma unroll
+            for (int k = 0; k < kEarly; ++k)
+                early[k] = k * kVocabBlock + threadIdx.x < n ? keys[k * kVocabBlock + threadIdx.x] : 0;
             const uint32_t from = lane % parts * top + lane / parts;
             const uint32_t head = lane / parts < top ? (uint32_t)(keys[from] >> 32) : 0;
             const uint32_t bar = lanes_kth(head, top);
             TopList list{sh.top.keys[threadIdx.x / 64], 0, top, (uint64_t)bar << 32};
-            for (uint32_t i = threadIdx.x / 64 * 64; i < n; i += kVocabBlock) {
-                const uint32_t at = i + threadIdx.x % 64;
-                list.offer(at < n ? keys[at] : 0);
-            }
+#pragma unroll
+            for (int k = 0; k < kEarly; ++k) list.offer(early[k]);
+            for (uint32_t i = kEarly * kVocabBlock + threadIdx.x / 64 * 64; i < n; i += kVocabBlock)
+                list.offer(i + lane < n ? keys[i + lane] : 0);
             key = block_top(list, sh.top);
         }
         block_join<Ent>(s, c, sh.part);
@@ -613,20 +685,24 @@ __global__ void __launch_bounds__(kVocabBlock) ew_vocab_join_kernel(typename Op:
 // Gradients
 // ---------------------------------------------------------------------------
 
-// A gradient has one block for each kGradLane elements a thread of a row: the
-// tile's loads are all in flight before the row's few numbers have arrived.
-// Tiles start at the row's start, so dlogits is stored with 16-byte stores at
-// whatever alignment the row has: on MI355X that cost less than a scalar head
-// in every tile.
-constexpr int kGradLane = 32;
+// A gradient's rows are cut into tiles of kGradSteps steps, a block each; a
+// step is kGradLane elements a thread.  The first step's loads are in flight
+// while the block works out what it needs of the row, each later one's while
+// the step before is worked on.  Vectors start at the row's start, whatever
+// alignment it has.  4096 x 131072 bf16, log probabilities: two steps of 16
+// elements 348 us, one 353-365, four 359, one of 32 354, two of 32 358; the
+// distillation's 2048 x 131072: 182, 203, 186, 189, 185.
+constexpr int kGradLane = 16, kGradSteps = 2;
 
 template <typename T>
 struct GradTile {
     static constexpr int N = Vec<T>::N, U = kGradLane / N;
-    static constexpr uint32_t kCols = kVocabBlock * kGradLane;
+    static constexpr uint32_t kStepVectors = kVocabBlock * U;
+    static constexpr uint32_t kCols = kStepVectors * N * kGradSteps;
     const char *in;
     char *out;
     uint32_t first, cols;      // the tile's first column and its number of columns
+    bool aligned;              // dlogits on 16-byte boundaries: stored at device scope (1 % faster)
     u32x4 v[U];
 
     __device__ GradTile(const T *x, T *dx, uint32_t row_cols, uint32_t tile)
@@ -635,44 +711,63 @@ struct GradTile {
         cols = row_cols - first < kCols ? row_cols - first : kCols;
         in = reinterpret_cast<const char *>(x + first);
         out = reinterpret_cast<char *>(dx + first);
-        // whole vectors are loaded as such, the row's last elements one by one
+        aligned = reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    }
+    // this thread's u-th vector of a step, as one of the tile's
+    __device__ static uint32_t vector(uint32_t step, int u)
+    {
+        return step * kStepVectors + threadIdx.x + u * kVocabBlock;
+    }
+    // whole vectors are loaded as such, the row's last elements one by one
+    __device__ void fetch(uint32_t step)
+    {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t i = vector(u);
+            const uint32_t i = vector(step, u);
             v[u] = u32x4{0, 0, 0, 0};
-            if ((i + 1) * N <= cols) v[u] = load16<false, sizeof(T)>(in + (uint64_t)i * 16);
+            if ((i + 1) * N <= cols) v[u] = load16<false, sizeof(T)>(in + i * 16);
         }
         if (cols % N) {
-            const uint32_t i = cols / N;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (vector(u) == i) v[u] = load_some(i);
+                if (vector(step, u) == cols / N) v[u] = load_some(cols / N);
         }
     }
-    // this thread's u-th vector of the tile
-    __device__ static uint32_t vector(int u) { return threadIdx.x + u * kVocabBlock; }
-
     __device__ u32x4 load_some(uint32_t i) const
     {
         typename Vec<T>::type t{};
-        const T *const p = reinterpret_cast<const T *>(in) + (uint64_t)i * N;
+        const T *const p = reinterpret_cast<const T *>(in) + i * N;
 #pragma unroll
         for (int j = 0; j < N; ++j)
             if (i * N + j < cols) t[j] = p[j];
         return __builtin_bit_cast(u32x4, t);
     }
-    __device__ void store(int u, typename Vec<T>::wide g) const
+    __device__ void store(uint32_t i, typename Vec<T>::wide g) const
     {
-        const uint32_t i = vector(u);
         const u32x4 w = Vec<T>::narrow(g);
         if ((i + 1) * N <= cols) {
-            store16_row<T>(out + (uint64_t)i * 16, w);
+            if (aligned) store16_device(out, kCols * sizeof(T), i * 16, w);
+            else store16_row<T>(out + i * 16, w);
         } else if (i * N < cols) {
             const typename Vec<T>::type t = __builtin_bit_cast(typename Vec<T>::type, w);
-            T *const p = reinterpret_cast<T *>(out) + (uint64_t)i * N;
+            T *const p = reinterpret_cast<T *>(out) + i * N;
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 if (i * N + j < cols) p[j] = t[j];
+        }
+    }
+    // f(vector of the tile, its widened elements) for each step's vectors;
+    // the first step has been fetched
+    template <class F>
+    __device__ void each(const F &f)
+    {
+        for (uint32_t step = 0; step * kStepVectors * N < cols; ++step) {
+            u32x4 own[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) own[u] = v[u];
+            if ((step + 1) * kStepVectors * N < cols) fetch(step + 1);
+#pragma unroll
+            for (int u = 0; u < U; ++u) store(vector(step, u), f(vector(step, u), Vec<T>::widen(own[u])));
         }
     }
 };
@@ -697,6 +792,7 @@ __global__ void __launch_bounds__(kVocabBlock) ew_logprobs_grad_kernel(LogprobsG
         GradTile<T> g(static_cast<const T *>(a.logits) + r * a.stride,
                       static_cast<T *>(a.dlogits) + r * a.dlogits_stride, a.cols,
                       (uint32_t)(item % tiles));
+        g.fetch(0);
         const int64_t target = a.targets[r];
         const bool given = target >= 0 && target < (int64_t)a.cols;
         const bool empty = a.lse[r] == -kInf;
@@ -707,16 +803,14 @@ __global__ void __launch_bounds__(kVocabBlock) ew_logprobs_grad_kernel(LogprobsG
         const float k2 = empty ? 0.0f : -dent * a.scale;
         // the target's place in the tile, past the tile's end without one
         const uint32_t hit = given && !empty ? (uint32_t)target - g.first : ~0u;
-#pragma unroll
-        for (int u = 0; u < g.U; ++u) {
-            const typename Vec<T>::wide x = Vec<T>::widen(g.v[u]);
+        g.each([&](uint32_t i, typename Vec<T>::wide x) {
             typename Vec<T>::wide d;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const float l = log_p(x[j], a.scale, lse);
                 d[j] = exp_nat(l) * __builtin_fmaf(l, k2, k1);
             }
-            if (hit / N == g.vector(u)) {
+            if (hit / N == i) {
 #pragma unroll
                 for (int j = 0; j < N; ++j)
                     if (hit % N == j && x[j] * a.scale != -kInf) d[j] += dlogp * a.scale;
@@ -725,13 +819,12 @@ __global__ void __launch_bounds__(kVocabBlock) ew_logprobs_grad_kernel(LogprobsG
 #pragma unroll
                 for (int j = 0; j < N; ++j) d[j] = x[j] * a.scale == -kInf ? 0.0f : lse;
             }
-            g.store(u, d);
-        }
+            return d;
+        });
     }
 }
 
-// The teacher's distribution in one wave: every wave of a block works it out,
-// which needs no barrier.
+// The teacher's distribution, in one wave.
 __device__ __forceinline__ Teacher wave_teacher(const float *teacher, const int64_t *ids,
                                                 uint32_t kept, uint32_t cols, float scale)
 {
@@ -751,92 +844,85 @@ __device__ __forceinline__ Teacher wave_teacher(const float *teacher, const int6
     return t;
 }
 
-// The kept entries that fall into a tile, in the entries' order, and which of
-// the tile's vectors they fall into.
-constexpr uint32_t kTileEntries = 256;
-
+// dlogits = k1 * (p - w), w the weight of the entries that name the column.
+// The tile is written as if w were 0; the few columns that entries name are
+// written again after it, one thread each, from the logits that the first
+// wave set aside (dlogits may be logits).  Looking for the entries while
+// streaming took more instructions than the softmax: 220 us for 2048 rows of
+// 131072 bf16 with 64 entries, where this takes 182.
 template <typename T>
 __global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGradArgs a,
                                                                       uint32_t tiles)
 {
     constexpr int N = Vec<T>::N;
-    using Tile = GradTile<T>;
-    __shared__ uint32_t touched[Tile::kCols / N / 32];
-    __shared__ uint32_t at[kTileEntries];
-    __shared__ float weight[kTileEntries];
+    // the kept entries that fall into the tile, in their order: place,
+    // weight, logit
+    __shared__ uint32_t at[kMaxKept];
+    __shared__ float weight[kMaxKept], logit[kMaxKept];
     __shared__ uint32_t found;
+    __shared__ float teacher_sum;
     const uint64_t items = (uint64_t)a.rows * tiles;
     for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const uint32_t r = (uint32_t)(item / tiles);
-        Tile g(static_cast<const T *>(a.logits) + r * a.stride,
-               static_cast<T *>(a.dlogits) + r * a.dlogits_stride, a.cols,
-               (uint32_t)(item % tiles));
-        const float *const teacher = a.teacher + (uint64_t)r * a.kept;
-        const int64_t *const ids = a.ids + (uint64_t)r * a.kept;
-        if (threadIdx.x < Tile::kCols / N / 32) touched[threadIdx.x] = 0;
-        const Teacher t = wave_teacher(teacher, ids, a.kept, a.cols, a.scale);
-        __syncthreads();
-        const auto entry = [&](uint32_t k) {      // t of a kept entry
-            return exp_nat(teacher[k] * a.scale - t.m) / t.z;
-        };
-        const auto place = [&](uint32_t k) {      // its place in the tile, or past its end
-            const int64_t id = ids[k];
-            return kept_entry(id, teacher[k] * a.scale, a.cols) &&
-                           (uint64_t)id - g.first < g.cols
-                       ? (uint32_t)id - g.first : ~0u;
-        };
+        const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
+        GradTile<T> g(x, static_cast<T *>(a.dlogits) + r * a.dlogits_stride, a.cols,
+                      (uint32_t)(item % tiles));
+        g.fetch(0);
         if (threadIdx.x < 64) {
+            const float *const teacher = a.teacher + (uint64_t)r * a.kept;
+            const int64_t *const ids = a.ids + (uint64_t)r * a.kept;
+            const Teacher t = wave_teacher(teacher, ids, a.kept, a.cols, a.scale);
             uint32_t n = 0;
             for (uint32_t k0 = 0; k0 < a.kept; k0 += 64) {
                 const uint32_t k = k0 + threadIdx.x;
-                const uint32_t p = k < a.kept ? place(k) : ~0u;
-                const uint64_t mask = __ballot(p != ~0u);
-                const uint32_t slot = n + lanes_below(mask);
-                if (p != ~0u) {
-                    atomicOr(&touched[p / N / 32], 1u << p / N % 32);
-                    if (slot < kTileEntries) {
-                        at[slot] = p;
-                        weight[slot] = entry(k);
-                    }
+                const int64_t id = k < a.kept ? ids[k] : -1;
+                const float s = k < a.kept ? teacher[k] * a.scale : -kInf;
+                const bool here = kept_entry(id, s, a.cols) && (uint64_t)id - g.first < g.cols;
+                const uint64_t mask = __ballot(here);
+                if (here) {
+                    const uint32_t slot = n + lanes_below(mask);
+                    at[slot] = (uint32_t)id - g.first;
+                    weight[slot] = exp_nat(s - t.m) / t.z;
+                    logit[slot] = (float)x[id];
                 }
                 n += __builtin_popcountll(mask);
             }
-            if (threadIdx.x == 0) found = n;
+            if (threadIdx.x == 0) {
+                found = n;
+                teacher_sum = t.z;
+            }
         }
         __syncthreads();
         const uint32_t entries = found;
-        const bool empty = a.lse[r] == -kInf || t.z == 0.0f;
+        const float tz = teacher_sum;
+        const bool empty = a.lse[r] == -kInf || tz == 0.0f, nan = a.lse[r] != a.lse[r] || tz != tz;
         const float lse = empty ? 0.0f : a.lse[r], k1 = empty ? 0.0f : a.dloss[r] * a.scale;
-#pragma unroll
-        for (int u = 0; u < g.U; ++u) {
-            const uint32_t i = g.vector(u);
-            const typename Vec<T>::wide x = Vec<T>::widen(g.v[u]);
+        g.each([&](uint32_t, typename Vec<T>::wide v) {
             typename Vec<T>::wide d;
 #pragma unroll
-            for (int j = 0; j < N; ++j) d[j] = k1 * exp_nat(log_p(x[j], a.scale, lse));
-            if (touched[i / 32] >> i % 32 & 1) {
-                // the weights of one column are added up in the entries' order
-                float w[N] = {};
-                const auto add = [&](uint32_t p, float v) {
+            for (int j = 0; j < N; ++j) d[j] = k1 * exp_nat(log_p(v[j], a.scale, lse));
+            if (nan) {
 #pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        if (p == i * N + j) w[j] += v;
-                };
-                if (entries <= kTileEntries)
-                    for (uint32_t e = 0; e < entries; ++e) add(at[e], weight[e]);
-                else
-                    for (uint32_t k = 0; k < a.kept; ++k)
-                        if (place(k) / N == i) add(place(k), entry(k));
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (x[j] * a.scale != -kInf) d[j] -= k1 * w[j];
+                for (int j = 0; j < N; ++j) d[j] = v[j] * a.scale == -kInf ? 0.0f : lse + tz;
             }
-            if (lse != lse || t.z != t.z) {
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    d[j] = x[j] * a.scale == -kInf ? 0.0f : lse + t.z;
+            return d;
+        });
+        __syncthreads();       // the tile is stored
+        if (!nan) {
+            for (uint32_t e = threadIdx.x; e < entries; e += kVocabBlock) {
+                // the first entry of a column adds up all of them, in order
+                const uint32_t place = at[e];
+                bool first = logit[e] * a.scale != -kInf;
+                float w = 0.0f;
+                for (uint32_t o = 0; o < entries; ++o) {
+                    const bool same = at[o] == place;
+                    first = first && !(same && o < e);
+                    w += same ? weight[o] : 0.0f;
+                }
+                if (first)
+                    reinterpret_cast<T *>(g.out)[place] =
+                        (T)(k1 * (exp_nat(log_p(logit[e], a.scale, lse)) - w));
             }
-            g.store(u, d);
         }
         if (item + gridDim.x < items) __syncthreads();
     }
@@ -846,25 +932,30 @@ __global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGra
 // Dispatch
 // ---------------------------------------------------------------------------
 
-// Blocks a forward call should have, and the fewest columns of a part.  A
+// A row is split where there are too few to fill the GPU and it is long enough
+// to pay for the second launch, which costs the host 3.5 us and the GPU about
+// 3 (one block a row against parts, GPU time in us, bf16: distillation of 37
+// rows of 32001 7.1 / 6.9, 1 of 131072 19.3 / 6.1; log probabilities of 256
+// rows of 8000 4.9 / 7.0, 256 of 131072 24.3 / 16.9, 512 28.4 / 28.4).
+// Ranking makes a block's row dearer (5 of 64 rows of 50257 15.7 / 13.1, 20 of
+// 32 rows of 32000 f32 20.2 / 12.3, 5 of 1 row of 4000 6.0 / 6.0).  A
 // function of the sizes alone, so that the workspace is too.
-constexpr uint64_t kWantBlocks = 1024;
-constexpr uint64_t kPartCols = 4096;
-constexpr uint64_t kMaxParts = 256;
+constexpr uint64_t kWholeRows = 512;                            // from here on no row is split
+constexpr uint64_t kWholeCols = 49152, kWholeTopCols = 16384;   // nor up to here
+constexpr uint64_t kWantBlocks = 1024, kPartCols = 4096, kMaxParts = 256;
 
-static uint32_t row_parts(uint64_t rows, uint64_t cols)
+static uint32_t row_parts(uint64_t rows, uint64_t cols, uint64_t top)
 {
-    if (rows == 0) return 1;
-    const uint64_t most = (cols + kPartCols - 1) / kPartCols;
+    if (rows == 0 || rows >= kWholeRows || cols <= (top ? kWholeTopCols : kWholeCols)) return 1;
     uint64_t parts = (kWantBlocks + rows - 1) / rows;
+    const uint64_t most = (cols + kPartCols - 1) / kPartCols;
     if (parts > most) parts = most;
-    if (parts > kMaxParts) parts = kMaxParts;
-    return parts ? (uint32_t)parts : 1;
+    return (uint32_t)(parts < kMaxParts ? parts : kMaxParts);
 }
 
 size_t logprobs_workspace(uint64_t rows, uint64_t cols, uint64_t top)
 {
-    const uint64_t parts = row_parts(rows, cols);
+    const uint64_t parts = row_parts(rows, cols, top);
     return parts == 1 ? 0 : rows * parts * (sizeof(float4) + top * sizeof(uint64_t));
 }
 size_t distill_workspace(uint64_t rows, uint64_t cols) { return logprobs_workspace(rows, cols, 0); }
@@ -879,7 +970,8 @@ constexpr uint64_t kMaxGrid = 1 << 23;
 
 static uint32_t grad_tiles(uint32_t cols)
 {
-    return (uint32_t)(((uint64_t)cols + kVocabBlock * kGradLane - 1) / (kVocabBlock * kGradLane));
+    constexpr uint64_t tile = (uint64_t)kVocabBlock * kGradLane * kGradSteps;
+    return (uint32_t)((cols + tile - 1) / tile);
 }
 
 template <class... A>
@@ -893,7 +985,7 @@ static hipError_t go(const void *fn, uint64_t blocks, hipStream_t s, A... args)
 template <class Op, bool Ent, bool Top>
 static hipError_t forward(RowType t, const typename Op::Args &a, hipStream_t s, const char **path)
 {
-    const uint32_t parts = row_parts(a.rows, a.cols);
+    const uint32_t parts = row_parts(a.rows, a.cols, Op::top(a));
 #define EW_FORWARD(K)                                                                      \
     (t == kRowF32 ? reinterpret_cast<const void *>(&K<float, Op, Ent, Top>)                \
      : t == kRowF16 ? reinterpret_cast<const void *>(&K<_Float16, Op, Ent, Top>)           \
