@@ -309,21 +309,24 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_norm_grad_kernel(NormG
     __shared__ float sums[2][Waves * Groups];
     __shared__ float joined[Groups > 1 ? kThreads * V * N : 1];
     const uint32_t group = threadIdx.x / kThreads, i = threadIdx.x % kThreads;
+    // the next row is on its way while this one is worked on, and the weight
+    // stays, unless they would not fit in registers
+    constexpr bool kAhead = V < 4;
     u32x4 wv[V];
-    load_row<T, V, false>(wv, static_cast<const T *>(a.weight), a.cols, i, kThreads);
+    const auto fetch_weight = [&] {
+        load_row<T, V, false>(wv, static_cast<const T *>(a.weight), a.cols, i, kThreads);
+    };
+    if constexpr (kAhead) fetch_weight();
     Wide dw[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) dw[k] = Wide(0.0f);
-    // the next row is on its way while this one is worked on (unless it would
-    // not fit in registers)
-    constexpr bool kAhead = V < 4;
     u32x4 dy[V], x[V], dt[V];
     float rstd = 0.0f;
     const auto fetch = [&](uint64_t r0) {
         const uint64_t r = r0 + group < a.rows ? r0 + group : r0;
         load_row<T, V, true>(dy, static_cast<const T *>(a.dy) + r * a.dy_stride, a.cols, i, kThreads);
         load_row<T, V, true>(x, static_cast<const T *>(a.x) + r * a.x_stride, a.cols, i, kThreads);
-        if (a.dtotal)
+        if (kAhead && a.dtotal)
             load_row<T, V, true>(dt, static_cast<const T *>(a.dtotal) + r * a.dtotal_stride, a.cols,
                                  i, kThreads);
         rstd = a.rstd[r];
@@ -333,7 +336,10 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_norm_grad_kernel(NormG
     if (kAhead && r0 < a.rows) fetch(r0);
     for (int set = 0; r0 < a.rows; r0 += step, set ^= 1) {
         const bool live = r0 + group < a.rows;
-        if constexpr (!kAhead) fetch(r0);
+        if constexpr (!kAhead) {
+            fetch(r0);
+            fetch_weight();
+        }
         const float rs = rstd;
         u32x4 dyv[V], xv[V], dtv[V];
 #pragma unroll
@@ -355,7 +361,12 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_norm_grad_kernel(NormG
         // has loaded
         dot = row_reduce<Sum, Waves>(dot, sums[set] + group * Waves);
         const float c = dot / (float)a.cols * rs * rs * rs;
-        T *const dx = static_cast<T *>(a.dx) + (live ? r0 + group : r0) * a.dx_stride;
+        const uint64_t r = live ? r0 + group : r0;
+        if constexpr (!kAhead) fetch_weight();
+        if (!kAhead && a.dtotal)
+            load_row<T, V, true>(dtv, static_cast<const T *>(a.dtotal) + r * a.dtotal_stride, a.cols,
+                                 i, kThreads);
+        T *const dx = static_cast<T *>(a.dx) + r * a.dx_stride;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             Wide g = rs * (Vec<T>::widen(dyv[k]) * Vec<T>::widen(wv[k])) - c * Vec<T>::widen(xv[k]);
@@ -537,7 +548,7 @@ hipError_t launch_norm(RowType t, const NormArgs &a, int, hipStream_t s, const c
 
 // The gradient's rows: one vector a lane as long as they fit, eight waves a
 // block or a row's (1024 vectors of bf16: sixteen waves of one vector 52.5 us,
-// eight of two 53.7).  Two vectors of 16-bit data a lane are what the
+// eight of two 53.7).  Two vectors of 16-bit data a lane are what the 128
 // registers of sixteen waves hold; of 32-bit data, whose sums take half as
 // many, four.
 template <typename T>
