@@ -134,8 +134,8 @@ __device__ __forceinline__ void store_e4m3(uint8_t *row, uint32_t cols, uint32_t
     }
 }
 
-// Threads of a block: a row's waves, at least four waves in all.
-constexpr int norm_block(int waves) { return waves < 4 ? 256 : waves * 64; }
+// Threads of a block: a row's waves, or four waves of short rows.
+constexpr int norm_block(int waves) { return waves < 3 ? 256 : waves * 64; }
 
 template <typename T, int Waves, int V, bool E4M3>
 __global__ void __launch_bounds__(norm_block(Waves)) ew_norm_row_kernel(NormArgs a)
@@ -505,7 +505,11 @@ static uint32_t row_vectors(RowType t, uint32_t cols)
 // Beyond 512 vectors rows of 16 waves leave a CU with one or two blocks that
 // all load or all store: eight waves of two vectors took 46.6 us on rows of
 // 1024 vectors, sixteen of one 49-67.  For the longest rows sixteen waves win
-// (2048 vectors: 50 us as eight of four; 16 rows: 4.6 us against 5.5).
+// (2048 vectors: 50 us as eight of four; 16 rows: 4.6 us against 5.5).  Three
+// waves, five, and ten and twelve of two vectors are there because rows just
+// past a power of two leave a larger block's lanes idle (e4m3, 1536 vectors of
+// bf16: 46 us with twelve, 54 with sixteen; 300 of f32: 44 with five, 53 with
+// eight); six, seven and fourteen gained nothing or lost up to 18 %.
 template <typename T, bool E4M3>
 static hipError_t norm_rows(const NormArgs &a, uint32_t vectors, hipStream_t s)
 {
@@ -516,9 +520,13 @@ static hipError_t norm_rows(const NormArgs &a, uint32_t vectors, hipStream_t s)
                   norm_block(W), s, a);
     EW_NORM_ROWS(1, 1)
     EW_NORM_ROWS(2, 1)
+    EW_NORM_ROWS(3, 1)
     EW_NORM_ROWS(4, 1)
+    EW_NORM_ROWS(5, 1)
     EW_NORM_ROWS(8, 1)
     EW_NORM_ROWS(8, 2)
+    EW_NORM_ROWS(10, 2)
+    EW_NORM_ROWS(12, 2)
     EW_NORM_ROWS(16, 2)
     EW_NORM_ROWS(16, 4)
 #undef EW_NORM_ROWS
