@@ -509,7 +509,8 @@ static uint32_t row_vectors(RowType t, uint32_t cols)
 // waves, five, and ten and twelve of two vectors are there because rows just
 // past a power of two leave a larger block's lanes idle (e4m3, 1536 vectors of
 // bf16: 46 us with twelve, 54 with sixteen; 300 of f32: 44 with five, 53 with
-// eight); six, seven and fourteen gained nothing or lost up to 18 %.
+// eight); six, seven and fourteen gained nothing or lost up to 18 %, and plain
+// 32-bit rows of 1251 and 1536 vectors lost 3-8 % to ten and twelve.
 template <typename T, bool E4M3>
 static hipError_t norm_rows(const NormArgs &a, uint32_t vectors, hipStream_t s)
 {
@@ -525,8 +526,10 @@ static hipError_t norm_rows(const NormArgs &a, uint32_t vectors, hipStream_t s)
     EW_NORM_ROWS(5, 1)
     EW_NORM_ROWS(8, 1)
     EW_NORM_ROWS(8, 2)
-    EW_NORM_ROWS(10, 2)
-    EW_NORM_ROWS(12, 2)
+    if constexpr (E4M3 || sizeof(T) == 2) {
+        EW_NORM_ROWS(10, 2)
+        EW_NORM_ROWS(12, 2)
+    }
     EW_NORM_ROWS(16, 2)
     EW_NORM_ROWS(16, 4)
 #undef EW_NORM_ROWS
