@@ -137,6 +137,13 @@ __device__ __forceinline__ void store_e4m3(uint8_t *row, uint32_t cols, uint32_t
 // Threads of a block: a row's waves, or four waves of short rows.
 constexpr int norm_block(int waves) { return waves < 3 ? 256 : waves * 64; }
 
+// total = round(x + residual), y = total * rstd * weight in one pass: the row's
+// vectors stay in registers between the sum of squares and the product, and
+// the sum costs one barrier.  Bound by memory: 8192 x 4096 bf16 with residual
+// and total 42.5 us, 6.3 TB/s (a copy of 2^28 floats: 6.64); e4m3, 4096 x 8192
+// bf16 41 us, 5.8 TB/s (8-byte stores); 1021 x 5003 f32, rows 4 bytes off,
+// 17.7 us, 4.6 TB/s (two rounds of blocks that load, then store); one row of
+// 4096 2.3 us on the GPU.
 template <typename T, int Waves, int V, bool E4M3>
 __global__ void __launch_bounds__(norm_block(Waves)) ew_norm_row_kernel(NormArgs a)
 {
@@ -299,7 +306,9 @@ constexpr uint32_t kGradParts = 256;
 __host__ __device__ constexpr uint64_t part_pitch(uint64_t cols) { return (cols + 7) & ~(uint64_t)7; }
 
 // Rows that fit in registers: Waves waves a row, V vectors a lane, Groups rows
-// at a time in a block, which adds up dweight over its rows.
+// at a time in a block, which adds up dweight over its rows.  Bound by memory:
+// 8192 x 4096 bf16 45 us, 6.0 TB/s, and 4.7 us for the sum of the parts;
+// without the next row's loads ahead 51 us.
 
 template <typename T, int Waves, int V, int Groups>
 __global__ void __launch_bounds__(Waves * 64 * Groups) ew_norm_grad_kernel(NormGradArgs a)

@@ -601,6 +601,13 @@ struct ForwardShared {
     float scratch[3][kVocabWaves];
 };
 
+// One pass over the logits: each lane keeps a running maximum and sums, joined
+// at the row's end.  4096 x 131072 bf16 with entropy 165-170 us, 6.3-6.5 TB/s
+// (reading alone in this pattern: 157 us); distillation 2048 x 131072 bf16 84
+// us, 6.4 TB/s; 2048 x 50257 with 5 alternatives 48 us, 4.3 TB/s, of which the
+// blocks' starts and ends, all at the same time, are a third; 8 x 131072 f32
+// with 20 alternatives 8.6 us and 4.8 for the join, latency.
+//
 // Eight waves a SIMD for 16-bit logits: with the 74 registers the compiler
 // would take, the 2048 blocks of as many rows need a second round on 256 CUs
 // (2048 x 50257 bf16, 5 alternatives: 54.6 us; 50.6 with 64).  32-bit rows,
@@ -779,6 +786,7 @@ __device__ __forceinline__ float log_p(float x, float scale, float lse)
     return __builtin_amdgcn_fmed3f(__builtin_fmaf(x, scale, -lse), kFarBelow, 0.0f);
 }
 
+// Bound by memory: 4096 x 131072 bf16 340 us, 6.3 TB/s (copy 6.64).
 // dlogits = scale * (dlogp * (hot - p) - dent * p * (l + ent)), l = log p:
 // p * (l * k2 + k1), and dlogp * scale at the target.
 template <typename T>
