@@ -426,16 +426,19 @@ __global__ void __launch_bounds__(kSumCols * kSumParts) ew_norm_dweight_sum_kern
 {
     __shared__ float sums[kSumParts][kSumCols];
     const uint32_t col = threadIdx.x % kSumCols, p0 = threadIdx.x / kSumCols;
-    const uint32_t c = blockIdx.x * kSumCols + col;
-    float sum = 0.0f;
-    if (c < a.cols)
-        for (uint32_t p = p0; p < parts; p += kSumParts) sum += a.partial[p * part_pitch(a.cols) + c];
-    sums[p0][col] = sum;
-    __syncthreads();
-    if (p0 == 0 && c < a.cols) {
+    for (uint64_t c0 = (uint64_t)blockIdx.x * kSumCols; c0 < a.cols; c0 += (uint64_t)gridDim.x * kSumCols) {
+        const uint64_t c = c0 + col;
+        float sum = 0.0f;
+        if (c < a.cols)
+            for (uint32_t p = p0; p < parts; p += kSumParts) sum += a.partial[p * part_pitch(a.cols) + c];
+        sums[p0][col] = sum;
+        __syncthreads();
+        if (p0 == 0 && c < a.cols) {
 #pragma unroll
-        for (uint32_t p = 1; p < kSumParts; ++p) sum += sums[p][col];
-        a.dweight[c] = sum;
+            for (uint32_t p = 1; p < kSumParts; ++p) sum += sums[p][col];
+            a.dweight[c] = sum;
+        }
+        __syncthreads();
     }
 }
 
@@ -553,7 +556,7 @@ static hipError_t norm_rows(const NormArgs &a, uint32_t vectors, hipStream_t s)
 }
 constexpr uint32_t kNormVectors = 16 * 64 * 4;       // the longest row it takes
 
-hipError_t launch_norm(RowType t, const NormArgs &a, int, hipStream_t s, const char **path)
+hipError_t launch_norm(RowType t, const NormArgs &a, hipStream_t s, const char **path)
 {
     const uint32_t vectors = row_vectors(t, a.cols);
     if (vectors <= kNormVectors) {
@@ -608,11 +611,12 @@ static hipError_t norm_grad_rows(const NormGradArgs &a, uint32_t vectors, hipStr
 }
 static uint32_t grad_vectors(RowType t) { return t == kRowF32 ? 16 * 64 * 4 : 16 * 64 * 2; }
 
-hipError_t launch_norm_grad(RowType t, const NormGradArgs &a, int, hipStream_t s, const char **path)
+hipError_t launch_norm_grad(RowType t, const NormGradArgs &a, hipStream_t s, const char **path)
 {
     const auto sum = [&](uint32_t parts) {
         return go(reinterpret_cast<const void *>(&ew_norm_dweight_sum_kernel),
-                  dim3((a.cols + kSumCols - 1) / kSumCols), kSumCols * kSumParts, s, a, parts);
+                  dim3(row_grid(((uint64_t)a.cols + kSumCols - 1) / kSumCols)), kSumCols * kSumParts, s, a,
+                  parts);
     };
     if (a.rows == 0) return sum(0);
     const uint32_t vectors = row_vectors(t, a.cols);

@@ -103,13 +103,13 @@ bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.0f; }
 
 template <class Args>
 ew_status_t launch(const char *op, RowType t, const Args &a, hipStream_t s,
-                   hipError_t (*fn)(RowType, const Args &, int, hipStream_t, const char **))
+                   hipError_t (*fn)(RowType, const Args &, hipStream_t, const char **))
 {
     int cus = 0;
     const ew_status_t st = host_device(&cus);
     if (st != EW_OK) return st;
     const char *path = "";
-    const hipError_t e = fn(t, a, cus, s, &path);
+    const hipError_t e = fn(t, a, s, &path);
     if (host_log_enabled()) {
         static const char *const names[] = {"f32", "f16", "bf16"};
         std::fprintf(stderr, "[ew] %s_%s rows=%u cols=%u path=%s\n", op, names[t], a.rows, a.cols,

@@ -88,16 +88,16 @@ size_t logprobs_workspace(uint64_t rows, uint64_t cols, uint64_t top);
 size_t distill_workspace(uint64_t rows, uint64_t cols);
 
 // Each launches its kernels on s; *path names what ran (for the log).
-hipError_t launch_norm(RowType t, const NormArgs &a, int cus, hipStream_t s, const char **path);
-hipError_t launch_norm_grad(RowType t, const NormGradArgs &a, int cus, hipStream_t s,
+hipError_t launch_norm(RowType t, const NormArgs &a, hipStream_t s, const char **path);
+hipError_t launch_norm_grad(RowType t, const NormGradArgs &a, hipStream_t s,
                             const char **path);
-hipError_t launch_logprobs(RowType t, const LogprobsArgs &a, int cus, hipStream_t s,
+hipError_t launch_logprobs(RowType t, const LogprobsArgs &a, hipStream_t s,
                            const char **path);
-hipError_t launch_logprobs_grad(RowType t, const LogprobsGradArgs &a, int cus, hipStream_t s,
+hipError_t launch_logprobs_grad(RowType t, const LogprobsGradArgs &a, hipStream_t s,
                                 const char **path);
-hipError_t launch_distill(RowType t, const DistillArgs &a, int cus, hipStream_t s,
+hipError_t launch_distill(RowType t, const DistillArgs &a, hipStream_t s,
                           const char **path);
-hipError_t launch_distill_grad(RowType t, const DistillGradArgs &a, int cus, hipStream_t s,
+hipError_t launch_distill_grad(RowType t, const DistillGradArgs &a, hipStream_t s,
                                const char **path);
 
 }  // namespace ew

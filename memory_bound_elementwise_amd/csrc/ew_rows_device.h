@@ -18,10 +18,6 @@ __device__ __forceinline__ float max_or_nan(float a, float b)
 {
     return __builtin_elementwise_maximum(a, b);
 }
-__device__ __forceinline__ float min_or_nan(float a, float b)
-{
-    return __builtin_elementwise_minimum(a, b);
-}
 
 struct Sum {
     __device__ static float f(float a, float b) { return a + b; }

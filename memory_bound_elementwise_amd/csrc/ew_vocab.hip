@@ -1005,7 +1005,7 @@ static hipError_t forward(RowType t, const typename Op::Args &a, hipStream_t s, 
 #undef EW_FORWARD
 }
 
-hipError_t launch_logprobs(RowType t, const LogprobsArgs &a, int, hipStream_t s, const char **path)
+hipError_t launch_logprobs(RowType t, const LogprobsArgs &a, hipStream_t s, const char **path)
 {
     if (a.top)
         return a.entropy ? forward<Logprobs, true, true>(t, a, s, path)
@@ -1014,7 +1014,7 @@ hipError_t launch_logprobs(RowType t, const LogprobsArgs &a, int, hipStream_t s,
                      : forward<Logprobs, false, false>(t, a, s, path);
 }
 
-hipError_t launch_logprobs_grad(RowType t, const LogprobsGradArgs &a, int, hipStream_t s,
+hipError_t launch_logprobs_grad(RowType t, const LogprobsGradArgs &a, hipStream_t s,
                                 const char **path)
 {
     *path = "a block a tile";
@@ -1022,12 +1022,12 @@ hipError_t launch_logprobs_grad(RowType t, const LogprobsGradArgs &a, int, hipSt
     return go(EW_BY_TYPE(t, ew_logprobs_grad_kernel), (uint64_t)a.rows * tiles, s, a, tiles);
 }
 
-hipError_t launch_distill(RowType t, const DistillArgs &a, int, hipStream_t s, const char **path)
+hipError_t launch_distill(RowType t, const DistillArgs &a, hipStream_t s, const char **path)
 {
     return forward<Distill, false, false>(t, a, s, path);
 }
 
-hipError_t launch_distill_grad(RowType t, const DistillGradArgs &a, int, hipStream_t s,
+hipError_t launch_distill_grad(RowType t, const DistillGradArgs &a, hipStream_t s,
                                const char **path)
 {
     *path = "a block a tile";

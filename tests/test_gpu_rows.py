@@ -734,3 +734,23 @@ def test_offsets_past_32_bits():
     ew.ew_logprobs_grad_bf16(x, t, got["lse"], dlogp, x)
     g, tol = ref.logprobs_grad(data, targets, got["lse"][-tail:], dlogp[-tail:], 1.0)
     close(x[-tail:], g, tol + (g.abs() + tol) * 2.0 ** -8 + ref.tiny(torch.bfloat16), "dlogits")
+
+
+def test_norm_offsets_past_32_bits():
+    """The last rows of matrices of more than 2^32 elements, and dweight, to
+    which only they contribute."""
+    rows, cols, tail = 263000, 16400, 3            # 4.3e9 elements, 8.6 GB in bf16
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    y = torch.empty_like(x)
+    data, res, w = norm_inputs("bf16", tail, cols, 0, 0, 95)
+    x[-tail:].copy_(data)
+    rstd = torch.empty(rows, device=DEV)
+    ew.ew_rmsnorm_bf16(x, w, y, rstd=rstd)
+    check_norm("bf16", x[-tail:], None, w, y[-tail:], None, rstd[-tail:], 1e-5)
+    assert bool((y[:-tail].view(torch.int16) == 0).all())
+    y[-tail:].copy_(res)                           # as dy
+    dw = torch.empty(cols, device=DEV)
+    ew.ew_rmsnorm_grad_bf16(y, x, w, rstd, y, dw, grad_space(rows, cols))
+    want, want_w, tol, tol_w = ref.norm_grad(res, data, w, rstd[-tail:], None)
+    close(y[-tail:], want, tol + (want.abs() + tol) * 2.0 ** -8 + ref.tiny(torch.bfloat16), "dx")
+    close(dw, want_w, tol_w, "dweight")            # every other row adds an exact 0
