@@ -534,9 +534,10 @@ ew_status_t ew_logprobs_bf16(const uint16_t *logits, size_t stride, const int64_
 /* Their gradient, from the forward call's lse (and entropy):
  *   dlogits[c] = round(scale * (dlogp * (1[c == target] - p)
  *                               - dentropy * p * (s - lse + entropy)))
- * with no dlogp term in a row without a target; 0 where s is -inf and in a
- * row whose mask leaves nothing (lse = -inf).  dentropy is optional, entropy
- * required with it.  dlogits may be exactly logits. */
+ * with no dlogp term in a row without a target; 0 where s is -inf (whatever
+ * dlogp and dentropy are, infinite or NaN too) and in a row whose mask leaves
+ * nothing (lse = -inf).  A p below 2^-126 counts as 0.  dentropy is optional,
+ * entropy required with it.  dlogits may be exactly logits. */
 ew_status_t ew_logprobs_grad_f32(const float *logits, size_t stride, const int64_t *targets,
                                  const float *lse, const float *entropy, const float *dlogp,
                                  const float *dentropy, float *dlogits, size_t dlogits_stride,
@@ -576,8 +577,9 @@ ew_status_t ew_distill_bf16(const uint16_t *logits, size_t stride, const float *
 
 /* Its gradient, from the forward call's lse:
  *   dlogits[c] = round(scale * dloss * (p - sum of t over entries naming c))
- * and 0 where s is -inf, in a row without a kept entry and in a row whose
- * mask leaves nothing.  dlogits may be exactly logits. */
+ * and 0 where s is -inf (whatever dloss is), in a row without a kept entry
+ * and in a row whose mask leaves nothing.  A p below 2^-126 counts as 0.
+ * dlogits may be exactly logits. */
 ew_status_t ew_distill_grad_f32(const float *logits, size_t stride, const float *teacher,
                                 const int64_t *ids, size_t kept, const float *lse,
                                 const float *dloss, float *dlogits, size_t dlogits_stride,

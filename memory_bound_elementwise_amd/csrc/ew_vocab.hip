@@ -777,18 +777,51 @@ struct GradTile {
             for (int u = 0; u < U; ++u) store(vector(step, u), f(vector(step, u), Vec<T>::widen(own[u])));
         }
     }
+    // the same, a vector at a time: for rare rows beside the loop above,
+    // whose registers it must not add to (the log probabilities' 16-bit
+    // gradient 173-174 us with it, 178-180 with a second loop like the first;
+    // the distillation's, with fewer registers, gains nothing)
+    template <class F>
+    __device__ void each_in_turn(const F &f) const
+    {
+        for (uint32_t i = threadIdx.x; i * N < cols; i += kVocabBlock) {
+            const u32x4 w = (i + 1) * N <= cols ? load16<false, sizeof(T)>(in + i * 16) : load_some(i);
+            store(i, f(i, Vec<T>::widen(w)));
+        }
+    }
 };
 
 // scale * x - lse, at most 0 (a difference of large numbers may round to
-// above it) and finite where x is masked: 2^ of it is 0 there all the same.
+// above it) and at least kLeast, below which its exponential is 0 anyway
+// (from -88 on): what it is multiplied by stays small where x is masked or far
+// below the rest.
+constexpr float kLeast = -1e4f;
+
 __device__ __forceinline__ float log_p(float x, float scale, float lse)
 {
-    return __builtin_amdgcn_fmed3f(__builtin_fmaf(x, scale, -lse), kFarBelow, 0.0f);
+    return __builtin_amdgcn_fmed3f(__builtin_fmaf(x, scale, -lse), kLeast, 0.0f);
 }
+
+// A row's gradient is scale times factors times terms of p.  Where factor and
+// scale together pass kLargeFactor the product with p might still be ordinary
+// (and infinite times a p of 0 a NaN), so there the factors come in 2^-40 times
+// as large and without a scale above 1, and the terms are multiplied by both
+// once they are whole.
+constexpr float kLargeFactor = 1e38f, kShrink = 0x1p-40f;
+
+struct Factors {
+    float shrink, scale;       // before: (1, the scale), or of a large row (2^-40, at most 1)
+    float above;               // after, in a large row: with 2^40
+    __device__ Factors(bool large, float s)
+        : shrink(large ? kShrink : 1.0f), scale(large ? __builtin_fminf(s, 1.0f) : s),
+          above(large ? __builtin_fmaxf(s, 1.0f) : 1.0f) {}
+    __device__ float whole(float d) const { return shrink == 1.0f ? d : d * (1.0f / kShrink) * above; }
+};
 
 // Bound by memory: 4096 x 131072 bf16 340 us, 6.3 TB/s (copy 6.64).
 // dlogits = scale * (dlogp * (hot - p) - dent * p * (l + ent)), l = log p:
-// p * (l * k2 + k1), and dlogp * scale at the target.
+// p * (l * k2 + k1), and dlogp * scale at the target.  Masked logits get their
+// 0 whatever the factors are; everything else in a row with a NaN is one.
 template <typename T>
 __global__ void __launch_bounds__(kVocabBlock) ew_logprobs_grad_kernel(LogprobsGradArgs a,
                                                                        uint32_t tiles)
@@ -803,15 +836,20 @@ __global__ void __launch_bounds__(kVocabBlock) ew_logprobs_grad_kernel(LogprobsG
         g.fetch(0);
         const int64_t target = a.targets[r];
         const bool given = target >= 0 && target < (int64_t)a.cols;
-        const bool empty = a.lse[r] == -kInf;
-        const float lse = empty ? 0.0f : a.lse[r], dlogp = given ? a.dlogp[r] : 0.0f;
+        const float row_lse = a.lse[r], row_dlogp = a.dlogp[r];
+        const bool empty = row_lse == -kInf;
+        const float lse = empty ? 0.0f : row_lse, dlogp = given ? row_dlogp : 0.0f;
         const float dent = a.dentropy ? a.dentropy[r] : 0.0f;
         const float ent = a.dentropy ? a.entropy[r] : 0.0f;
-        const float k1 = empty ? 0.0f : -(dlogp + dent * ent) * a.scale;
-        const float k2 = empty ? 0.0f : -dent * a.scale;
+        const bool large = !((__builtin_fabsf(dlogp) + __builtin_fabsf(dent) * -kLeast) * a.scale <
+                             kLargeFactor);
+        const Factors f(large, a.scale);
+        const float k1 = empty ? 0.0f : -(dlogp * f.shrink + dent * f.shrink * ent) * f.scale;
+        const float k2 = empty ? 0.0f : -(dent * f.shrink) * f.scale;
+        const float hot = dlogp * f.shrink * f.scale;
         // the target's place in the tile, past the tile's end without one
         const uint32_t hit = given && !empty ? (uint32_t)target - g.first : ~0u;
-        g.each([&](uint32_t i, typename Vec<T>::wide x) {
+        const auto gradient = [&](uint32_t i, typename Vec<T>::wide x) {
             typename Vec<T>::wide d;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
@@ -821,14 +859,21 @@ __global__ void __launch_bounds__(kVocabBlock) ew_logprobs_grad_kernel(LogprobsG
             if (hit / N == i) {
 #pragma unroll
                 for (int j = 0; j < N; ++j)
-                    if (hit % N == j && x[j] * a.scale != -kInf) d[j] += dlogp * a.scale;
-            }
-            if (lse != lse) {          // a NaN in the row: everything but the masked is one
-#pragma unroll
-                for (int j = 0; j < N; ++j) d[j] = x[j] * a.scale == -kInf ? 0.0f : lse;
+                    if (hit % N == j && x[j] * a.scale != -kInf) d[j] += hot;
             }
             return d;
-        });
+        };
+        if (large || lse != lse) {
+            g.each_in_turn([&](uint32_t i, typename Vec<T>::wide x) {
+                typename Vec<T>::wide d = gradient(i, x);
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    d[j] = empty || x[j] * a.scale == -kInf ? 0.0f : lse != lse ? lse : f.whole(d[j]);
+                return d;
+            });
+        } else {
+            g.each(gradient);
+        }
     }
 }
 
@@ -876,6 +921,7 @@ __global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGra
         GradTile<T> g(x, static_cast<T *>(a.dlogits) + r * a.dlogits_stride, a.cols,
                       (uint32_t)(item % tiles));
         g.fetch(0);
+        const float row_lse = a.lse[r], row_dloss = a.dloss[r];
         if (threadIdx.x < 64) {
             const float *const teacher = a.teacher + (uint64_t)r * a.kept;
             const int64_t *const ids = a.ids + (uint64_t)r * a.kept;
@@ -903,18 +949,28 @@ __global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGra
         __syncthreads();
         const uint32_t entries = found;
         const float tz = teacher_sum;
-        const bool empty = a.lse[r] == -kInf || tz == 0.0f, nan = a.lse[r] != a.lse[r] || tz != tz;
-        const float lse = empty ? 0.0f : a.lse[r], k1 = empty ? 0.0f : a.dloss[r] * a.scale;
-        g.each([&](uint32_t, typename Vec<T>::wide v) {
+        const bool empty = row_lse == -kInf || tz == 0.0f, nan = row_lse != row_lse || tz != tz;
+        const float lse = empty ? 0.0f : row_lse, dloss = empty ? 0.0f : row_dloss;
+        const bool large = !(__builtin_fabsf(dloss) * a.scale < kLargeFactor);
+        const Factors f(large, a.scale);
+        const float k1 = dloss * f.shrink * f.scale;
+        const auto gradient = [&](uint32_t, typename Vec<T>::wide v) {
             typename Vec<T>::wide d;
 #pragma unroll
             for (int j = 0; j < N; ++j) d[j] = k1 * exp_nat(log_p(v[j], a.scale, lse));
-            if (nan) {
-#pragma unroll
-                for (int j = 0; j < N; ++j) d[j] = v[j] * a.scale == -kInf ? 0.0f : lse + tz;
-            }
             return d;
-        });
+        };
+        if (large || nan) {
+            g.each([&](uint32_t i, typename Vec<T>::wide v) {
+                typename Vec<T>::wide d = gradient(i, v);
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    d[j] = v[j] * a.scale == -kInf ? 0.0f : nan ? lse + tz : f.whole(d[j]);
+                return d;
+            });
+        } else {
+            g.each(gradient);
+        }
         __syncthreads();       // the tile is stored
         if (!nan) {
             for (uint32_t e = threadIdx.x; e < entries; e += kVocabBlock) {
@@ -929,7 +985,7 @@ __global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGra
                 }
                 if (first)
                     reinterpret_cast<T *>(g.out)[place] =
-                        (T)(k1 * (exp_nat(log_p(logit[e], a.scale, lse)) - w));
+                        (T)f.whole(k1 * (exp_nat(log_p(logit[e], a.scale, lse)) - w));
             }
         }
         if (item + gridDim.x < items) __syncthreads();

@@ -1,0 +1,111 @@
+"""The row operators on the GPU at the ends of their ranges: gradients and
+scales that overflow, logits of any size, rows of 2^31 columns, workspaces at
+their documented alignment, more rows than a grid holds.  Against the 64-bit
+definitions and tolerances of tests/rows_ref.py."""
+import math
+
+import pytest
+import torch
+
+import memory_bound_elementwise_amd as ew
+from tests import rows_ref as ref
+from tests.rows_ref import TYPES, U, close
+from tests.test_gpu_rows import (DEV, check_logprobs, check_norm, check_norm8, check_norm_grad, gen,
+                                 grad_space, logits_of, norm_inputs, randn, run_distill,
+                                 run_logprobs, teacher_of)
+
+pytestmark = pytest.mark.gpu
+
+every_type = pytest.mark.parametrize("t", TYPES)
+FLUSH = 2.0 ** -126            # a probability below it counts as 0
+
+
+def close_rounded(got, want, tol, dt, what):
+    """got is `want` rounded to dt: infinite past its largest value (elements
+    within 2 % of it may fall either way), NaN nowhere."""
+    most = torch.finfo(dt).max
+    edge = (want.abs() > 0.98 * most) & (want.abs() < 1.02 * most)
+    want = torch.where(want.abs() >= 1.02 * most, want.sign() * math.inf, want)
+    assert not bool(torch.isnan(got).any()), f"{what}: a NaN"
+    got = torch.where(edge, 0.0, got.double())
+    want = torch.where(edge, 0.0, want)
+    close(got, want, tol + (want.abs().nan_to_num(posinf=0.0) + tol) * ref.half_ulp(dt) + ref.tiny(dt),
+          what)
+
+
+# ---------------------------------------------------------------------------
+# Gradients of any size beside masked logits
+# ---------------------------------------------------------------------------
+
+def masked_logits(t, rows, cols, seed):
+    """Logits of which a third are -inf and some the type's lowest value."""
+    x, targets = logits_of(t, rows, cols, 0, 0, seed, 0.33)
+    x[:, 3::17] = torch.finfo(TYPES[t]).min
+    targets[:] = (x.float() * torch.rand(x.shape, generator=gen(seed), device=DEV)).argmax(1)
+    return x, targets
+
+
+@every_type
+@pytest.mark.parametrize("cols", (70, 3000, 20001))
+@pytest.mark.parametrize("scale", (0.5, 1.0, 2.0))
+@pytest.mark.parametrize("slope", (1e9, 1e30, 3e38))
+def test_logprobs_grad_of_large_slopes(t, cols, scale, slope):
+    """Large gradients of logp and entropy: exactly 0 where masked, the
+    definition elsewhere (infinite only where that passes the type)."""
+    rows = 6
+    x, targets = masked_logits(t, rows, cols, 200 + cols)
+    stat = ref.logprobs(x, targets, scale)
+    lse, ent = stat.lse.float(), stat.entropy.float()
+    dlogp = torch.tensor([slope, -slope, 1.0, 0.0, slope, 1.0], device=DEV)
+    dent = torch.tensor([0.0, 1.0, slope, -slope, slope / 4, 1.0], device=DEV)
+    masked = x.float() * scale == -math.inf
+    for more in ({}, {"entropy": ent, "dentropy": dent}):
+        dx = torch.empty_like(x)
+        getattr(ew, "ew_logprobs_grad_" + t)(x, targets, lse, dlogp, dx, scale=scale, **more)
+        want, tol = ref.logprobs_grad(x, targets, lse, dlogp, scale, **more)
+        # a probability that is flushed, times what it is multiplied by (its
+        # logarithm is at most 104 in magnitude where its square root is not 0)
+        lost = dlogp.double().abs() + (dent.double().abs() * (104 + ent.double().abs()) if more else 0)
+        tol = tol + (lost * scale * FLUSH)[:, None]
+        assert bool((dx[masked] == 0).all())
+        close_rounded(dx, want, torch.where(masked, 0.0, tol), TYPES[t], "dlogits")
+
+
+@every_type
+@pytest.mark.parametrize("cols", (70, 20001))
+def test_masked_logits_have_no_gradient_whatever_the_slope(t, cols):
+    rows, kept = 6, 5
+    x, targets = masked_logits(t, rows, cols, 300 + cols)
+    got = run_logprobs(t, x, targets, 0, 1.0)
+    odd = torch.tensor([math.inf, -math.inf, math.nan, 1.0, 1.0, math.inf], device=DEV)
+    dent = torch.tensor([0.0, 1.0, 0.0, math.inf, math.nan, -math.inf], device=DEV)
+    masked = x == -math.inf
+    for more in ({}, {"entropy": got["entropy"], "dentropy": dent}):
+        dx = torch.empty_like(x)
+        getattr(ew, "ew_logprobs_grad_" + t)(x, targets, got["lse"], odd, dx, **more)
+        assert bool((dx[masked] == 0).all())
+        dx = dx[torch.arange(rows, device=DEV), targets][:3]
+        assert not bool(torch.isfinite(dx.float()).any())      # the slopes reach the target
+    z, ids = teacher_of(rows, cols, kept, 301)
+    _, lse = run_distill(t, x, z, ids, 1.0)
+    dx = torch.empty_like(x)
+    getattr(ew, "ew_distill_grad_" + t)(x, z, ids, lse, odd, dx)
+    assert bool((dx[masked] == 0).all())
+
+
+@every_type
+@pytest.mark.parametrize("cols,kept", [(70, 4), (3000, 40), (20001, 100)])
+@pytest.mark.parametrize("scale", (0.5, 2.0))
+def test_distill_grad_of_large_slopes(t, cols, kept, scale):
+    rows = 6
+    x, _ = masked_logits(t, rows, cols, 400 + cols)
+    z, ids = teacher_of(rows, cols, kept, 401 + kept)
+    _, lse = run_distill(t, x, z, ids, scale)
+    dloss = torch.tensor([1e9, 1e30, 3e38, -3e38, 2e38, 0.0], device=DEV)
+    dx = torch.empty_like(x)
+    getattr(ew, "ew_distill_grad_" + t)(x, z, ids, lse, dloss, dx, scale=scale)
+    want, tol = ref.distill_grad(x, z, ids, lse, dloss, scale)
+    masked = x.float() * scale == -math.inf
+    assert bool((dx[masked] == 0).all())
+    tol = torch.where(masked, 0.0, tol + (dloss.double().abs() * scale * FLUSH)[:, None])
+    close_rounded(dx, want, tol, TYPES[t], "dlogits")
