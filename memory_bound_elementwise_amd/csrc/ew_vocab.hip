@@ -23,8 +23,9 @@ struct RowSum {
 };
 
 // Where a difference of exponents is -inf its term is 0; this finite stand-in
-// keeps 0 * d from being a NaN, and 2^d is 0 all the same.
-constexpr float kFarBelow = -1e30f;
+// keeps 0 * d from being a NaN, times a sum of 2^31 terms too, and 2^d is 0
+// all the same.
+constexpr float kFarBelow = -1e4f;
 
 // d(x) is c * x - t with t = c * m rounded: the product and difference in one
 // fma, rounded once, and the sums are exact relative to 2^t whatever t is.

@@ -109,3 +109,22 @@ def test_distill_grad_of_large_slopes(t, cols, kept, scale):
     assert bool((dx[masked] == 0).all())
     tol = torch.where(masked, 0.0, tol + (dloss.double().abs() * scale * FLUSH)[:, None])
     close_rounded(dx, want, tol, TYPES[t], "dlogits")
+
+
+def test_entropy_of_the_longest_row():
+    """2^31 - 1 equal logits and one that is larger by 3e38: a sum of 2^31
+    terms is re-based by a difference that no power of two holds."""
+    cols = (1 << 31) - 1
+    x = torch.zeros(1, cols, dtype=torch.bfloat16, device=DEV)
+    targets = torch.tensor([cols - 1], device=DEV)
+    even = run_logprobs("bf16", x, targets, 0, 1.0)
+    # lanes count exactly; then at most 16 roundings of the joins, and of the logarithm
+    tol = (16 + 4 * math.log(cols)) * U
+    for k in ("lse", "entropy"):
+        assert abs(float(even[k]) - math.log(cols)) <= tol, k
+    x[0, cols - 1] = 3e38
+    got = run_logprobs("bf16", x, targets, 2, 1.0)
+    assert float(got["lse"]) == float(x[0, cols - 1]) and float(got["logp"]) == 0.0
+    assert float(got["entropy"]) == 0.0
+    assert got["top_ids"].tolist() == [[cols - 1, 0]]
+    assert float(got["top_logp"][0, 0]) == 0.0
