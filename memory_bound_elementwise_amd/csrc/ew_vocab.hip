@@ -28,11 +28,13 @@ struct RowSum {
 constexpr float kFarBelow = -1e4f;
 
 // d(x) is c * x - t with t = c * m rounded: the product and difference in one
-// fma, rounded once, and the sums are exact relative to 2^t whatever t is.
-// Where |t| is past kNear its rounding would be larger than the differences
-// that matter (a row of one large number must give d = 0, not the error of
-// t), so there d(x) is c * (x - m).  t is the same number wherever it is
-// used: the functions that form it leave its product alone (contract off).
+// fma, rounded once, and the sums are relative to 2^t, whatever the rounding
+// of t.  Where |t| is past kNear its rounding would be larger than the
+// differences that matter (a row of one large number must give d = 0, not the
+// error of t), so there d(x) is c * (x - m) and the sums are relative to c * m
+// itself.  A sum that moves from one base to another takes the roundings of
+// both along.  t is the same number wherever it is used: the functions that
+// form it leave its product alone (contract off).
 constexpr float kNear = 0x1p16f;
 
 __device__ __forceinline__ float finite_base(float m) { return m == -kInf ? 0.0f : m; }
@@ -45,14 +47,21 @@ __device__ __forceinline__ float distance(float x, float m, float c)
     return __builtin_fabsf(t) <= kNear ? __builtin_fmaf(x, c, -t) : (x - m) * c;
 }
 
+// c * m minus the base of sums whose largest logit is m.
+__device__ __forceinline__ float base_rounding(float m, float c)
+{
+#pragma clang fp contract(off)
+    const float t = m * c;
+    return __builtin_fabsf(t) <= kNear ? __builtin_fmaf(m, c, -t) : 0.0f;
+}
+
 // s re-based from s.m to m >= s.m.
 template <bool Ent>
 __device__ __forceinline__ void rebase(RowSum &s, float m, float c)
 {
 #pragma clang fp contract(off)
-    const float from = s.m * c, to = finite_base(m) * c;
-    const bool near = __builtin_fabsf(from) <= kNear && __builtin_fabsf(to) <= kNear;
-    const float d = near ? from - to : (s.m - finite_base(m)) * c;
+    const float base = finite_base(m);
+    const float d = (s.m - base) * c + (base_rounding(base, c) - base_rounding(s.m, c));
     const float shift = __builtin_fmaxf(d, kFarBelow), f = __builtin_amdgcn_exp2f(shift);
     if constexpr (Ent) s.b = f * __builtin_fmaf(shift, s.z, s.b);
     s.z *= f;
@@ -81,9 +90,9 @@ __device__ __forceinline__ void absorb_any(RowSum &s, const float (&v)[N], float
     }
 }
 
-// The same in fewer instructions, for logits of ordinary size and, with
-// entropy, none masked: returns whether that was so for this lane (s is of no
-// use otherwise).  16-bit rows are bound by the vector unit: an element costs
+// The same in fewer instructions, for logits and an s of ordinary size (or an
+// empty s) and, with entropy, none masked: returns whether the logits were so
+// for this lane (s is of no use otherwise).  16-bit rows are bound by the vector unit: an element costs
 // its widening, half a maximum, an fma, a power, an addition and, with
 // entropy, another fma.
 template <bool Ent, int N>
@@ -384,7 +393,8 @@ __device__ __forceinline__ RowSum stream_part(const T *x, uint32_t cols, const P
         const float v[1] = {(float)x[cols - split.tail + threadIdx.x]};
         absorb_any<Ent>(s, v, c);
     }
-    bool plain = true;       // until the wave meets logits that are not
+    // until the wave meets logits that are not (the head's and tail's first)
+    bool plain = __ballot(s.m != -kInf && __builtin_fabsf(s.m * c) > kNear) == 0;
     uint32_t v = p.lo;
     for (; p.hi - v >= kStep; v += kStep) {
         float f[kPerLane];

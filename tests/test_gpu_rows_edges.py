@@ -128,3 +128,43 @@ def test_entropy_of_the_longest_row():
     assert float(got["entropy"]) == 0.0
     assert got["top_ids"].tolist() == [[cols - 1, 0]]
     assert float(got["top_logp"][0, 0]) == 0.0
+
+
+# ---------------------------------------------------------------------------
+# Logits of any size
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("scale", (0.3, 1.0, 1.7))
+@pytest.mark.parametrize("sign", (1, -1))
+@pytest.mark.parametrize("rows,cols,top", [(2, 64, 0), (3, 300, 5), (5, 3001, 3), (2, 150000, 0),
+                                           (2, 150000, 20), (600, 9001, 0)])
+def test_logits_around_the_change_of_base(rows, cols, top, sign, scale):
+    """Logits whose exponents (in powers of two) lie on both sides of +-2^16,
+    a few steps of binary32 apart."""
+    at = sign * 65536.0 * math.log(2.0) / scale
+    step = 2.0 ** (math.floor(math.log2(abs(at))) - 23)
+    g = gen(int(cols + top + 10 * scale))
+    for spread in (3, 200):
+        x = (at + step * torch.randint(-spread, spread + 1, (rows, cols), generator=g, device=DEV)).float()
+        targets = torch.randint(cols, (rows,), generator=g, device=DEV)
+        check_logprobs("f32", x, targets, top, scale)
+    # one logit past the change of base, the rest a step before it
+    x = torch.full((rows, cols), at - 5 * step, device=DEV).float()
+    x[:, cols // 3] = at + 4 * step
+    check_logprobs("f32", x, torch.full((rows,), cols // 3, device=DEV), top, scale)
+    # rows that start far below it (as masks by a low number do) and rise past it
+    x[:, : cols // 2] = -3e38
+    check_logprobs("f32", x, torch.full((rows,), cols - 1, device=DEV), top, scale)
+
+
+@pytest.mark.parametrize("offset", (1, 2, 3))
+def test_a_large_negative_head_before_ordinary_logits(offset):
+    """Rows off 16-byte boundaries, whose first logits are added up apart."""
+    rows, cols = 4, 5000
+    at = -65536.0 * math.log(2.0)
+    whole = torch.empty(rows, cols + 4, device=DEV)
+    x = whole[:, offset:offset + cols]
+    x.copy_(at + randn(gen(7), rows, cols) * 0.02)
+    x[:, :4 - offset] = at - 0.05
+    x[:, -3:] = at - 0.04
+    check_logprobs("f32", x, torch.arange(rows, device=DEV), 3, 1.0)
