@@ -37,31 +37,53 @@ constexpr float kFarBelow = -1e4f;
 // form it leave its product alone (contract off).
 constexpr float kNear = 0x1p16f;
 
+// c, in two factors where it is infinite itself (scales above 2.36e38): c * x is
+// unit * x, exact, times c.
+struct Rate {
+    float c, unit;
+    __device__ explicit Rate(float scale)
+        : c(scale * kLog2e), unit(1.0f)
+    {
+        if (c == kInf) c = 0.5f * scale * kLog2e, unit = 2.0f;
+    }
+};
+
 __device__ __forceinline__ float finite_base(float m) { return m == -kInf ? 0.0f : m; }
 
-__device__ __forceinline__ float distance(float x, float m, float c)
-{
+// What d(x) = c * (unit * x - far) - near is formed with, for a largest logit m:
+// near is t, or far is unit * m.
+struct Base {
+    float near, far;
+    __device__ Base(float m, Rate k)
+    {
 #pragma clang fp contract(off)
-    m = finite_base(m);
-    const float t = m * c;
-    return __builtin_fabsf(t) <= kNear ? __builtin_fmaf(x, c, -t) : (x - m) * c;
-}
+        const float u = finite_base(m) * k.unit, t = u * k.c;
+        const bool is_near = __builtin_fabsf(t) <= kNear;
+        near = is_near ? t : 0.0f;
+        far = is_near ? 0.0f : u;
+    }
+    __device__ float distance(float x, Rate k) const
+    {
+        return __builtin_fmaf(__builtin_fmaf(x, k.unit, -far), k.c, -near);
+    }
+};
 
 // c * m minus the base of sums whose largest logit is m.
-__device__ __forceinline__ float base_rounding(float m, float c)
+__device__ __forceinline__ float base_rounding(float m, Rate k)
 {
 #pragma clang fp contract(off)
-    const float t = m * c;
-    return __builtin_fabsf(t) <= kNear ? __builtin_fmaf(m, c, -t) : 0.0f;
+    const float u = m * k.unit, t = u * k.c;
+    return __builtin_fabsf(t) <= kNear ? __builtin_fmaf(u, k.c, -t) : 0.0f;
 }
 
 // s re-based from s.m to m >= s.m.
 template <bool Ent>
-__device__ __forceinline__ void rebase(RowSum &s, float m, float c)
+__device__ __forceinline__ void rebase(RowSum &s, float m, Rate k)
 {
 #pragma clang fp contract(off)
     const float base = finite_base(m);
-    const float d = (s.m - base) * c + (base_rounding(base, c) - base_rounding(s.m, c));
+    const float d = __builtin_fmaf(s.m, k.unit, -(base * k.unit)) * k.c +
+                    (base_rounding(base, k) - base_rounding(s.m, k));
     const float shift = __builtin_fmaxf(d, kFarBelow), f = __builtin_amdgcn_exp2f(shift);
     if constexpr (Ent) s.b = f * __builtin_fmaf(shift, s.z, s.b);
     s.z *= f;
@@ -79,12 +101,13 @@ __device__ __forceinline__ float largest(const float (&v)[N])
 
 // N more logits of this lane, whatever they are.
 template <bool Ent, int N>
-__device__ __forceinline__ void absorb_any(RowSum &s, const float (&v)[N], float c)
+__device__ __forceinline__ void absorb_any(RowSum &s, const float (&v)[N], Rate rate)
 {
-    rebase<Ent>(s, __builtin_fmaxf(s.m, largest(v)), c);
+    rebase<Ent>(s, __builtin_fmaxf(s.m, largest(v)), rate);
+    const Base base(s.m, rate);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const float d = distance(v[k], s.m, c), e = __builtin_amdgcn_exp2f(d);
+        const float d = base.distance(v[k], rate), e = __builtin_amdgcn_exp2f(d);
         s.z += e;
         if constexpr (Ent) s.b = __builtin_fmaf(e, __builtin_fmaxf(d, kFarBelow), s.b);
     }
@@ -117,18 +140,18 @@ __device__ __forceinline__ bool absorb_plain(RowSum &s, const float (&v)[N], flo
 
 // The sums of the wave's lanes, in every lane.
 template <bool Ent>
-__device__ __forceinline__ void wave_join(RowSum &s, float c)
+__device__ __forceinline__ void wave_join(RowSum &s, Rate k)
 {
-    rebase<Ent>(s, wave_reduce<Max>(s.m), c);
+    rebase<Ent>(s, wave_reduce<Max>(s.m), k);
     s.z = wave_reduce<Sum>(s.z);
     if constexpr (Ent) s.b = wave_reduce<Sum>(s.b);
 }
 
 // The sums of the block's threads, in every thread; one barrier.
 template <bool Ent>
-__device__ __forceinline__ void block_join(RowSum &s, float c, RowSum *part)
+__device__ __forceinline__ void block_join(RowSum &s, Rate k, RowSum *part)
 {
-    wave_join<Ent>(s, c);
+    wave_join<Ent>(s, k);
     if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = s;
     __syncthreads();
     float m = part[0].m;
@@ -138,7 +161,7 @@ __device__ __forceinline__ void block_join(RowSum &s, float c, RowSum *part)
 #pragma unroll
     for (int w = 0; w < kVocabWaves; ++w) {
         RowSum p = part[w];
-        rebase<Ent>(p, m, c);
+        rebase<Ent>(p, m, k);
         all.z += p.z;
         all.b += p.b;
     }
@@ -169,7 +192,8 @@ __device__ __forceinline__ float log_prob(float x, const RowSum &s, const RowSta
 {
     if (st.empty) return -kInf;
     if (st.lse != st.lse) return st.lse;
-    const float d = distance(x, s.m, scale * kLog2e);
+    const Rate k(scale);
+    const float d = Base(s.m, k).distance(x, k);
     // far away (where d may overflow though its natural logarithm does not)
     // the rounding of t no longer matters
     return d < -kNear ? (x - s.m) * scale - st.log_z : __builtin_fmaf(d, kLn2, -st.log_z);
@@ -368,7 +392,7 @@ struct Part {
 // of rows uncovered).
 template <typename T, bool Ent>
 __device__ __forceinline__ RowSum stream_part(const T *x, uint32_t cols, const Part &p,
-                                              const RowSplit<T> &split, float c)
+                                              const RowSplit<T> &split, Rate k)
 {
     constexpr int N = Vec<T>::N, U = kPerLane / N;
     constexpr uint32_t kStep = kVocabBlock * U;
@@ -387,14 +411,14 @@ __device__ __forceinline__ RowSum stream_part(const T *x, uint32_t cols, const P
     // up to a vector's elements before and after the aligned body: one lane each
     if (threadIdx.x < split.head && p.first) {
         const float v[1] = {(float)x[threadIdx.x]};
-        absorb_any<Ent>(s, v, c);
+        absorb_any<Ent>(s, v, k);
     }
     if (threadIdx.x < split.tail && p.last) {
         const float v[1] = {(float)x[cols - split.tail + threadIdx.x]};
-        absorb_any<Ent>(s, v, c);
+        absorb_any<Ent>(s, v, k);
     }
     // until the wave meets logits that are not (the head's and tail's first)
-    bool plain = __ballot(s.m != -kInf && __builtin_fabsf(s.m * c) > kNear) == 0;
+    bool plain = k.unit == 1.0f && __ballot(s.m != -kInf && __builtin_fabsf(s.m * k.c) > kNear) == 0;
     uint32_t v = p.lo;
     for (; p.hi - v >= kStep; v += kStep) {
         float f[kPerLane];
@@ -407,10 +431,10 @@ __device__ __forceinline__ RowSum stream_part(const T *x, uint32_t cols, const P
         fetch(v + kStep);
         if (plain) {
             RowSum more = s;
-            plain = __ballot(!absorb_plain<Ent>(more, f, c)) == 0;
+            plain = __ballot(!absorb_plain<Ent>(more, f, k.c)) == 0;
             if (plain) s = more;
         }
-        if (!plain) absorb_any<Ent>(s, f, c);
+        if (!plain) absorb_any<Ent>(s, f, k);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -419,7 +443,7 @@ __device__ __forceinline__ RowSum stream_part(const T *x, uint32_t cols, const P
             float f[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) f[j] = w[j];
-            absorb_any<Ent>(s, f, c);
+            absorb_any<Ent>(s, f, k);
         }
     }
     return s;
@@ -629,7 +653,7 @@ __global__ void __launch_bounds__(kVocabBlock, sizeof(T) == 2 ? 8 : 4) ew_vocab_
 {
     __shared__ __align__(16) ForwardShared<Top> sh;
     const uint64_t items = (uint64_t)a.rows * parts;
-    const float c = a.scale * kLog2e;
+    const Rate rate(a.scale);
     for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const uint32_t r = (uint32_t)(item / parts), part = (uint32_t)(item % parts);
         const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
@@ -637,10 +661,10 @@ __global__ void __launch_bounds__(kVocabBlock, sizeof(T) == 2 ? 8 : 4) ew_vocab_
         if (parts == 1) h = Op::ahead(a, r, x);
         const RowSplit<T> split(x, a.cols);
         const Part p(split.vectors, part, parts);
-        RowSum s = stream_part<T, Ent>(x, a.cols, p, split, c);
+        RowSum s = stream_part<T, Ent>(x, a.cols, p, split, rate);
         uint64_t key = 0;
         if constexpr (Top) key = part_top(x, a.cols, p, split, s.m, Op::top(a), sh.top);
-        block_join<Ent>(s, c, sh.part);
+        block_join<Ent>(s, rate, sh.part);
         if (parts == 1) {
             Op::finish(a, r, x, h, s, key, sh.scratch);
         } else {
@@ -658,7 +682,7 @@ __global__ void __launch_bounds__(kVocabBlock) ew_vocab_join_kernel(typename Op:
                                                                     uint32_t parts)
 {
     __shared__ __align__(16) ForwardShared<Top> sh;
-    const float c = a.scale * kLog2e;
+    const Rate rate(a.scale);
     for (uint64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
         const typename Op::Ahead h = Op::ahead(a, (uint32_t)r, x);
@@ -667,8 +691,8 @@ __global__ void __launch_bounds__(kVocabBlock) ew_vocab_join_kernel(typename Op:
             const float4 q = part_sums(a.workspace)[r * parts + p];
             RowSum o{q.x, q.y, q.z};
             const float m = __builtin_fmaxf(s.m, o.m);
-            rebase<Ent>(s, m, c);
-            rebase<Ent>(o, m, c);
+            rebase<Ent>(s, m, rate);
+            rebase<Ent>(o, m, rate);
             s.z += o.z;
             s.b += o.b;
         }
@@ -693,7 +717,7 @@ __global__ void __launch_bounds__(kVocabBlock) ew_vocab_join_kernel(typename Op:
                 list.offer(i + lane < n ? keys[i + lane] : 0);
             key = block_top(list, sh.top);
         }
-        block_join<Ent>(s, c, sh.part);
+        block_join<Ent>(s, rate, sh.part);
         Op::finish(a, (uint32_t)r, x, h, s, key, sh.scratch);
         if (r + gridDim.x < a.rows) __syncthreads();
     }

@@ -168,3 +168,40 @@ def test_a_large_negative_head_before_ordinary_logits(offset):
     x[:, :4 - offset] = at - 0.05
     x[:, -3:] = at - 0.04
     check_logprobs("f32", x, torch.arange(rows, device=DEV), 3, 1.0)
+
+
+@every_type
+@pytest.mark.parametrize("cols", (5, 70, 3000, 60000))
+@pytest.mark.parametrize("scale", (2.3e38, 2.4e38, 3.4e38, 1e-38))
+def test_the_largest_and_smallest_scales(t, cols, scale):
+    """Scales whose product with log2(e) overflows: rows of zeros and masked
+    logits, and of logits so small that their scaled values are ordinary."""
+    rows, kept = 6, 3
+    scale = float(torch.tensor(scale))                # as the call receives it
+    g = gen(500 + cols)
+    x = torch.zeros(rows, cols, device=DEV)
+    x[1, ::2] = -math.inf
+    x[2] = -math.inf
+    x[2, cols - 1] = 0.0
+    x[3:] = randn(g, 3, cols) * (3 / scale if scale > 1 else 3)
+    x[4, 1::3] = -math.inf
+    x = x.to(TYPES[t])
+    targets = torch.tensor([0, 1, cols - 1, 2, 3, -1], device=DEV)
+    got = check_logprobs(t, x, targets, min(cols, 5), scale)
+    z, ids = torch.zeros(rows, kept, device=DEV), torch.arange(kept, device=DEV).repeat(rows, 1)
+    z[3:] = randn(g, 3, kept) / max(scale, 1.0)
+    loss, lse = run_distill(t, x, z, ids, scale)
+    want, tol, _ = ref.distill(x, z, ids, scale)
+    close(loss, want, tol, "loss")
+    close(lse, ref.Rows(x, scale).lse, ref.Rows(x, scale).lse_tol, "lse")
+    slope = torch.full((rows,), 0.25, device=DEV)
+    small = 6 * 2.0 ** -150                           # roundings to binary32's subnormals
+    dx = torch.empty_like(x)
+    getattr(ew, "ew_distill_grad_" + t)(x, z, ids, lse, slope, dx, scale=scale)
+    want, tol = ref.distill_grad(x, z, ids, lse, slope, scale)
+    close_rounded(dx, want, tol + small, TYPES[t], "distill dlogits")
+    getattr(ew, "ew_logprobs_grad_" + t)(x, targets, lse, slope, dx, entropy=got["entropy"],
+                                         dentropy=slope, scale=scale)
+    want, tol = ref.logprobs_grad(x, targets, lse, slope, scale, entropy=got["entropy"],
+                                  dentropy=slope)
+    close_rounded(dx, want, tol + small, TYPES[t], "logprobs dlogits")
