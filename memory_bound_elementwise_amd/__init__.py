@@ -607,17 +607,17 @@ def ew_batch(op, items, alpha=0.0, stream=None):
 # ---------------------------------------------------------------------------
 
 def _shape(x, rows, cols, role):
-    """(rows, cols) of the call: as given, or of the matrix argument x."""
+    """(rows, cols) of the call: each as given, or that of the matrix argument x."""
     if rows is None or cols is None:
         if isinstance(x, int):
             raise ValueError("rows and cols are required when buffers are raw pointers")
         shape = x.shape
-        if len(shape) == 2:
-            return shape
         if not shape:
             raise ValueError(f"{role}: a scalar has no rows")
-        cols = shape[-1]
-        rows = math.prod(shape[:-1])
+        if rows is None:
+            rows = shape[0] if len(shape) == 2 else math.prod(shape[:-1])
+        if cols is None:
+            cols = shape[-1]
     return int(rows), int(cols)
 
 
