@@ -798,6 +798,8 @@ def ew_logprobs_workspace(rows, cols, top=0):
 def _logprobs(name, es, logits, targets, logp, entropy, lse, top_logp, top_ids, scale, workspace,
               rows, cols, top, stream):
     rows, cols = _shape(logits, rows, cols, "logits")
+    if (top_logp is None) != (top_ids is None):
+        raise ValueError("top_logp and top_ids: both or neither")
     if top is None:
         if isinstance(top_ids, int):
             raise ValueError("top is required when top_ids is a raw pointer")

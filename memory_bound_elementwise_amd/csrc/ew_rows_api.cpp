@@ -213,6 +213,7 @@ ew_status_t logprobs(RowType t, const void *logits, size_t stride, const int64_t
     if (rows == 0) return EW_OK;
     if (!dims_ok(rows, cols) || !stride_ok(stride) || !scale_ok(scale)) return EW_ERR_INVALID_ARG;
     if (top > kTopMax || top > cols) return EW_ERR_INVALID_ARG;
+    if (!top_logp != !top_ids) return EW_ERR_INVALID_ARG;
     const size_t need = logprobs_workspace(rows, cols, top);
     if (workspace_bytes < need) return EW_ERR_INVALID_ARG;
     const Span ins[] = {matrix(logits, row_elem_size(t), stride, rows, cols),

@@ -34,3 +34,21 @@ def test_rows_or_cols_given_alone_count():
         ew.ew_rmsnorm_f32(x.view(2, 4, 16), w, y, cols=16)
     with pytest.raises(ValueError, match="covers 7 rows of 16"):
         ew.ew_rmsnorm_f32(x.view(2, 4, 16), w, y, rows=7)
+
+
+@pytest.mark.parametrize("t", ("f32", "f16", "bf16"))
+def test_top_logp_and_top_ids_come_together(t):
+    """One without the other would be left unwritten."""
+    def call(top_logp, top_ids, top):
+        return ew._c["ew_logprobs_" + t](BASE, 64, BASE + (1 << 20), BASE + (2 << 20), None, None,
+                                         top_logp, top_ids, top, 1.0, None, 0, 8, 64, 0)
+
+    for top in (0, 5):
+        assert call(BASE + (3 << 20), None, top) == -1
+        assert call(None, BASE + (4 << 20), top) == -1
+    ids = torch.zeros(8, 5, dtype=torch.int64)
+    fn = getattr(ew, "ew_logprobs_" + t)
+    for more in ({"top_logp": torch.zeros(8, 5)}, {"top_ids": ids}, {"top_ids": ids, "top": 5},
+                 {"top_logp": BASE, "top": 5}):
+        with pytest.raises(ValueError, match="both or neither"):
+            fn(BASE, BASE, BASE, rows=8, cols=64, stream=0, **more)
