@@ -658,6 +658,15 @@ def _ids64(x, n, role):
     return _buf(x, 8, n, role)
 
 
+def _table(x, rows, k, role):
+    """A rows x k argument's shape: a larger tensor whose rows hold another
+    number of values would be read or written as if they held k."""
+    if x is None or isinstance(x, int):
+        return
+    if x.numel() != rows * k and x.dim() > 1 and x.shape[-1] != k:
+        raise ValueError(f"{role}: shape {tuple(x.shape)}, the call covers {rows} rows of {k}")
+
+
 def _space(x, need):
     """(address, bytes) of a workspace; an integer address is taken to hold
     the bytes the call needs."""
@@ -719,6 +728,7 @@ def _rmsnorm_e4m3(name, es, x, weight, q, scales, group, residual, total, rstd, 
     if group < 0:
         raise ValueError(f"group: {group}")
     groups = -(-cols // group) if group else 1
+    _table(scales, rows, groups, "scales")
     _check(_c[name](px, sx, _buf(weight, es, cols, "weight"), pr, sr, pq, sq,
                     _buf(scales, 4, rows * groups, "scales"), group, pt, st,
                     _buf(rstd, 4, rows, "rstd"), rows, cols, eps, _stream(q, stream)), name)
@@ -805,6 +815,8 @@ def _logprobs(name, es, logits, targets, logp, entropy, lse, top_logp, top_ids, 
             raise ValueError("top is required when top_ids is a raw pointer")
         top = top_ids.shape[-1] if top_ids is not None and top_ids.dim() else 0
     top = int(top)
+    _table(top_logp, rows, top, "top_logp")
+    _table(top_ids, rows, top, "top_ids")
     p, stride = _mat(logits, es, rows, cols, "logits")
     ws, size = _space(workspace, _c["ew_logprobs_workspace"](rows, cols, top))
     _check(_c[name](p, stride, _ids64(targets, rows, "targets"), _buf(logp, 4, rows, "logp"),
@@ -877,18 +889,23 @@ def ew_distill_workspace(rows, cols):
     return _c["ew_distill_workspace"](int(rows), int(cols))
 
 
-def _kept(ids, kept):
-    if kept is not None:
-        return int(kept)
-    if isinstance(ids, int):
-        raise ValueError("kept is required when ids is a raw pointer")
-    return ids.shape[-1]
+def _kept(teacher, ids, rows, kept):
+    if kept is None:
+        if isinstance(ids, int):
+            raise ValueError("kept is required when ids is a raw pointer")
+        if not ids.dim():
+            raise ValueError("ids: a scalar has no rows")
+        kept = ids.shape[-1]
+    kept = int(kept)
+    _table(teacher, rows, kept, "teacher")
+    _table(ids, rows, kept, "ids")
+    return kept
 
 
 def _distill(name, es, logits, teacher, ids, loss, lse, scale, workspace, rows, cols, kept,
              stream):
     rows, cols = _shape(logits, rows, cols, "logits")
-    kept = _kept(ids, kept)
+    kept = _kept(teacher, ids, rows, kept)
     p, stride = _mat(logits, es, rows, cols, "logits")
     ws, size = _space(workspace, _c["ew_distill_workspace"](rows, cols))
     _check(_c[name](p, stride, _buf(teacher, 4, rows * kept, "teacher"),
@@ -923,7 +940,7 @@ def ew_distill_bf16(logits, teacher, ids, loss, lse=None, scale=1.0, workspace=N
 def _distill_grad(name, es, logits, teacher, ids, lse, dloss, dlogits, scale, rows, cols, kept,
                   stream):
     rows, cols = _shape(logits, rows, cols, "logits")
-    kept = _kept(ids, kept)
+    kept = _kept(teacher, ids, rows, kept)
     p, stride = _mat(logits, es, rows, cols, "logits")
     pd, sd = _mat(dlogits, es, rows, cols, "dlogits")
     _check(_c[name](p, stride, _buf(teacher, 4, rows * kept, "teacher"),

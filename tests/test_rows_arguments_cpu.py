@@ -52,3 +52,33 @@ def test_top_logp_and_top_ids_come_together(t):
                  {"top_logp": BASE, "top": 5}):
         with pytest.raises(ValueError, match="both or neither"):
             fn(BASE, BASE, BASE, rows=8, cols=64, stream=0, **more)
+
+
+def test_tables_of_other_widths():
+    """teacher, ids, top_logp, top_ids and scales hold a row of values per row
+    of the matrix: a wider tensor's rows are not taken for narrower ones."""
+    x, r, targets = torch.zeros(4, 64), torch.zeros(4), torch.zeros(4, dtype=torch.int64)
+    narrow, wide = (torch.zeros(4, k, dtype=torch.int64) for k in (3, 6))
+    for teacher, ids, kept, role in ((torch.zeros(4, 6), narrow, None, "teacher"),
+                                     (torch.zeros(4, 3), wide, 3, "ids"),
+                                     (torch.zeros(2, 4, 6), narrow, None, "teacher")):
+        with pytest.raises(ValueError, match=f"{role}: shape .* covers 4 rows of 3"):
+            ew.ew_distill_f32(x, teacher, ids, r, kept=kept)
+        with pytest.raises(ValueError, match=f"{role}: shape .* covers 4 rows of 3"):
+            ew.ew_distill_grad_f32(x, teacher, ids, r, r, x, kept=kept)
+    with pytest.raises(ValueError, match="top_logp: shape .* covers 4 rows of 3"):
+        ew.ew_logprobs_f32(x, targets, r, top_logp=torch.zeros(4, 6), top_ids=narrow)
+    with pytest.raises(ValueError, match="top_ids: shape .* covers 4 rows of 3"):
+        ew.ew_logprobs_f32(x, targets, r, top_logp=torch.zeros(4, 3), top_ids=wide, top=3)
+    with pytest.raises(ValueError, match="scales: shape .* covers 4 rows of 2"):
+        ew.ew_rmsnorm_e4m3_f32(BASE, BASE, BASE, torch.zeros(4, 4), group=32, rows=4, cols=64,
+                               stream=0)
+    with pytest.raises(ValueError, match="ids: a scalar"):
+        ew.ew_distill_f32(x, r, torch.zeros((), dtype=torch.int64), r)
+    # as many values in another arrangement of the rows, and flat buffers
+    flat = torch.zeros(64, dtype=torch.int64)
+    for teacher, ids, kept in ((torch.zeros(2, 2, 3), narrow, None), (torch.zeros(64), flat, 3),
+                               (torch.zeros(4, 1), torch.zeros(4, 1, 1, dtype=torch.int64), None),
+                               (torch.zeros(2, 2), torch.zeros(2, 2, 1, dtype=torch.int64), None)):
+        with pytest.raises(ValueError, match="logits: .* not on a GPU"):
+            ew.ew_distill_f32(x, teacher, ids, r, kept=kept)
