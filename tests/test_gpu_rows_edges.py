@@ -205,3 +205,73 @@ def test_the_largest_and_smallest_scales(t, cols, scale):
     want, tol = ref.logprobs_grad(x, targets, lse, slope, scale, entropy=got["entropy"],
                                   dentropy=slope)
     close_rounded(dx, want, tol + small, TYPES[t], "logprobs dlogits")
+
+
+# ---------------------------------------------------------------------------
+# 8-bit norm: the bytes themselves
+# ---------------------------------------------------------------------------
+
+def e4m3_of(x, w, total, rstd, group):
+    """q and scales by their definition in binary32 on the CPU (whose division
+    by a tensor is a division), from the rstd that the call returned."""
+    y = (total.float().cpu() * rstd.cpu()[:, None] * w.float().cpu())
+    rows, cols = y.shape
+    size = group or cols
+    a = torch.zeros(rows, -(-cols // size) * size)
+    a[:, :cols] = y.abs()
+    top = a.view(rows, -1, size).amax(2)
+    scales = (top / torch.full_like(top, ref.E4M3_MAX)).clamp_min(ref.SCALE_MIN)
+    each = scales.repeat_interleave(size, 1)[:, :cols]
+    return (y / each).to(torch.float8_e4m3fn), scales
+
+
+def e4m3_call(t, x, w, group, pad=0, eps=1e-5):
+    rows, cols = x.shape
+    groups = -(-cols // group) if group else 1
+    q = torch.empty(rows, cols + pad, dtype=torch.float8_e4m3fn, device=DEV)[:, :cols]
+    scales, rstd = torch.empty(rows, groups, device=DEV), torch.empty(rows, device=DEV)
+    getattr(ew, "ew_rmsnorm_e4m3_" + t)(x, w, q, scales, group=group, rstd=rstd, eps=eps)
+    return q, scales, rstd
+
+
+@every_type
+@pytest.mark.parametrize("group", (0, 16, 64, 256))
+@pytest.mark.parametrize("cols", (17, 1000, 4096, 40000))
+def test_e4m3_bytes_are_those_of_the_quotient(t, group, cols):
+    """Integer rows, whose quotients by the scale often lie halfway between
+    two e4m3 values, and random ones: every byte and every scale."""
+    rows = 24
+    g = gen(600 + cols + group)
+    whole = torch.randint(-40, 41, (rows, cols), generator=g, device=DEV).float()
+    for x in (whole, randn(g, rows, cols), whole * 2.0 ** torch.arange(-14, 10, device=DEV)[:, None]):
+        x = x.to(TYPES[t])
+        for w in (torch.ones(cols, device=DEV), 1 + 0.2 * randn(g, cols)):
+            w = w.to(TYPES[t])
+            q, scales, rstd = e4m3_call(t, x, w, group, pad=3)
+            want, want_scales = e4m3_of(x, w, x, rstd, group)
+            assert torch.equal(scales.cpu(), want_scales)
+            off = int((q.cpu().view(torch.uint8) != want.view(torch.uint8)).sum())
+            assert off == 0, f"{off} of {q.numel()} bytes differ"
+
+
+@pytest.mark.parametrize("group", (0, 32))
+def test_e4m3_bytes_at_the_ends_of_the_scales(group):
+    """y near 2^-126 (scales at and around the smallest), near binary32's
+    largest, infinite in one column, and all zero."""
+    rows, cols = 8, 256
+    g = gen(610)
+    x = torch.randint(-40, 41, (rows, cols), generator=g, device=DEV).float()
+    x[6] = 0.0
+    for size in (2.0 ** -126, 2.0 ** -124, 2.0 ** -118, 2.0 ** -100, 2.0 ** 60, 2.0 ** 125):
+        w = torch.full((cols,), size, device=DEV)
+        q, scales, rstd = e4m3_call("f32", x, w, group)
+        want, want_scales = e4m3_of(x, w, x, rstd, group)
+        assert torch.equal(scales.cpu(), want_scales)
+        assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8)), size
+    w[37] = math.inf                        # y there is infinite, or NaN where x is 0
+    q, scales, rstd = e4m3_call("f32", x, w, group)
+    want, want_scales = e4m3_of(x, w, x, rstd, group)
+    assert torch.equal(scales.cpu().nan_to_num(7.0), want_scales.nan_to_num(7.0))
+    # the conversion of torch and the hardware's write different NaNs
+    a, b = q.cpu().float(), want.float()
+    assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
