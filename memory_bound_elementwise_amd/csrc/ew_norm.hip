@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kNormBlock) ew_norm_kernel(NormArgs a)
 // 55 us).
 constexpr uint32_t kGradParts = 256;
 
-// Floats from one part's sums to the next: whole 32-byte pieces.
+// Floats from one part's sums to the next: whole vectors of sums.
 __host__ __device__ constexpr uint64_t part_pitch(uint64_t cols) { return (cols + 7) & ~(uint64_t)7; }
 
 // Rows that fit in registers: Waves waves a row, V vectors a lane, Groups rows
@@ -432,6 +432,8 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_norm_grad_kernel(NormG
     }
     if (group != 0) return;
     const bool only = gridDim.x == 1;      // the one part is the sum
+    // the workspace is 16-byte aligned, a vector of sums of 16-bit data is 32 bytes
+    typedef float Sums __attribute__((ext_vector_type(N), aligned(16)));
     float *const part = a.partial + blockIdx.x * part_pitch(a.cols);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_norm_grad_kernel(NormG
             for (uint32_t j = 0; j < N; ++j)
                 if (c + j < a.cols) a.dweight[c + j] = dw[k][j];
         } else if (c < a.cols) {
-            *reinterpret_cast<Wide *>(part + c) = dw[k];
+            *reinterpret_cast<Sums *>(part + c) = dw[k];
         }
     }
 }

@@ -275,3 +275,39 @@ def test_e4m3_bytes_at_the_ends_of_the_scales(group):
     # the conversion of torch and the hardware's write different NaNs
     a, b = q.cpu().float(), want.float()
     assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
+
+
+# ---------------------------------------------------------------------------
+# Workspaces at their documented alignment, more rows than a grid's blocks
+# ---------------------------------------------------------------------------
+
+@every_type
+@pytest.mark.parametrize("rows,cols", [(40, 260), (70, 4096), (9, 5003), (6, 33000)])
+def test_a_workspace_16_bytes_off(t, rows, cols):
+    x, _, w = norm_inputs(t, rows, cols, 0, 0, 700, residual=False)
+    dy = (0.1 * randn(gen(701), rows, cols)).to(TYPES[t])
+    rstd = (x.double().square().mean(1) + 1e-5).rsqrt().float()
+    need = ew.ew_rmsnorm_grad_workspace(rows, cols)
+    space = torch.full((need + 32,), 0xff, dtype=torch.uint8, device=DEV)
+    assert space.data_ptr() % 32 == 0
+    dx, dw = torch.empty_like(x), torch.empty(cols, device=DEV)
+    getattr(ew, "ew_rmsnorm_grad_" + t)(dy, x, w, rstd, dx, dw, space[16:16 + need])
+    check_norm_grad(t, dy, x, w, rstd, None, dx, dw)
+    assert bool((space[:16] == 0xff).all()) and bool((space[16 + need:] == 0xff).all())
+
+
+def test_logits_workspaces_16_bytes_off():
+    rows, cols, top = 3, 131072, 20
+    x, targets = logits_of("bf16", rows, cols, 0, 0, 702)
+    want = run_logprobs("bf16", x, targets, top, 1.0)
+    z, ids = teacher_of(rows, cols, 8, 703)
+    want_loss, _ = run_distill("bf16", x, z, ids, 1.0)
+    need = max(ew.ew_logprobs_workspace(rows, cols, top), ew.ew_distill_workspace(rows, cols))
+    assert need
+    space = torch.full((need + 32,), 0xff, dtype=torch.uint8, device=DEV)[16:16 + need]
+    got = {k: torch.empty_like(v) for k, v in want.items()}
+    ew.ew_logprobs_bf16(x, targets, got["logp"], entropy=got["entropy"], lse=got["lse"],
+                        top_logp=got["top_logp"], top_ids=got["top_ids"], workspace=space)
+    loss = torch.empty(rows, device=DEV)
+    ew.ew_distill_bf16(x, z, ids, loss, workspace=space)
+    assert all(torch.equal(got[k], want[k]) for k in want) and torch.equal(loss, want_loss)
