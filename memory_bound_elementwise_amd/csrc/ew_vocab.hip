@@ -683,44 +683,37 @@ __global__ void __launch_bounds__(kVocabBlock) ew_vocab_join_kernel(typename Op:
 {
     __shared__ __align__(16) ForwardShared<Top> sh;
     const Rate rate(a.scale);
-    for (uint64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
-        const typename Op::Ahead h = Op::ahead(a, (uint32_t)r, x);
-        RowSum s{-kInf, 0.0f, 0.0f};
-        for (uint32_t p = threadIdx.x; p < parts; p += kVocabBlock) {
-            const float4 q = part_sums(a.workspace)[r * parts + p];
-            RowSum o{q.x, q.y, q.z};
-            const float m = __builtin_fmaxf(s.m, o.m);
-            rebase<Ent>(s, m, rate);
-            rebase<Ent>(o, m, rate);
-            s.z += o.z;
-            s.b += o.b;
-        }
-        uint64_t key = 0;
-        if constexpr (Top) {
-            // the parts' lists are in order: the top-th largest of 64 keys
-            // from their heads is a bar for all
-            const uint32_t top = Op::top(a), n = parts * top, lane = threadIdx.x % 64;
-            const uint64_t *const keys = part_keys(a.workspace, a.rows, parts) + r * n;
-            constexpr int kEarly = 4;      // keys loaded before the bar is known
-            uint64_t early[kEarly];
-#pragma unroll
-            for (int k = 0; k < kEarly; ++k)
-                early[k] = k * kVocabBlock + threadIdx.x < n ? keys[k * kVocabBlock + threadIdx.x] : 0;
-            const uint32_t from = lane % parts * top + lane / parts;
-            const uint32_t head = lane / parts < top ? (uint32_t)(keys[from] >> 32) : 0;
-            const uint32_t bar = lanes_kth(head, top);
-            TopList list{sh.top.keys[threadIdx.x / 64], 0, top, (uint64_t)bar << 32};
-#pragma unroll
-            for (int k = 0; k < kEarly; ++k) list.offer(early[k]);
-            for (uint32_t i = kEarly * kVocabBlock + threadIdx.x / 64 * 64; i < n; i += kVocabBlock)
-                list.offer(i + lane < n ? keys[i + lane] : 0);
-            key = block_top(list, sh.top);
-        }
-        block_join<Ent>(s, rate, sh.part);
-        Op::finish(a, (uint32_t)r, x, h, s, key, sh.scratch);
-        if (r + gridDim.x < a.rows) __syncthreads();
+    const uint64_t r = blockIdx.x;       // rows that are split are fewer than a grid's blocks
+    const T *const x = static_cast<const T *>(a.logits) + r * a.stride;
+    const typename Op::Ahead h = Op::ahead(a, (uint32_t)r, x);
+    RowSum s{-kInf, 0.0f, 0.0f};
+    if (threadIdx.x < parts) {
+        const float4 q = part_sums(a.workspace)[r * parts + threadIdx.x];
+        s = RowSum{q.x, q.y, q.z};
     }
+    uint64_t key = 0;
+    if constexpr (Top) {
+        // the parts' lists are in order: the top-th largest of 64 keys
+        // from their heads is a bar for all
+        const uint32_t top = Op::top(a), n = parts * top, lane = threadIdx.x % 64;
+        const uint64_t *const keys = part_keys(a.workspace, a.rows, parts) + r * n;
+        constexpr int kEarly = 4;      // keys loaded before the bar is known
+        uint64_t early[kEarly];
+#pragma unroll
+        for (int k = 0; k < kEarly; ++k)
+            early[k] = k * kVocabBlock + threadIdx.x < n ? keys[k * kVocabBlock + threadIdx.x] : 0;
+        const uint32_t from = lane % parts * top + lane / parts;
+        const uint32_t head = lane / parts < top ? (uint32_t)(keys[from] >> 32) : 0;
+        const uint32_t bar = lanes_kth(head, top);
+        TopList list{sh.top.keys[threadIdx.x / 64], 0, top, (uint64_t)bar << 32};
+#pragma unroll
+        for (int k = 0; k < kEarly; ++k) list.offer(early[k]);
+        for (uint32_t i = kEarly * kVocabBlock + threadIdx.x / 64 * 64; i < n; i += kVocabBlock)
+            list.offer(i + lane < n ? keys[i + lane] : 0);
+        key = block_top(list, sh.top);
+    }
+    block_join<Ent>(s, rate, sh.part);
+    Op::finish(a, (uint32_t)r, x, h, s, key, sh.scratch);
 }
 
 // ---------------------------------------------------------------------------
@@ -1042,6 +1035,7 @@ __global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGra
 constexpr uint64_t kWholeRows = 512;                            // from here on no row is split
 constexpr uint64_t kWholeCols = 49152, kWholeTopCols = 16384;   // nor up to here
 constexpr uint64_t kWantBlocks = 1024, kPartCols = 4096, kMaxParts = 256;
+static_assert(kMaxParts <= kVocabBlock, "the join takes a part a thread");
 
 static uint32_t row_parts(uint64_t rows, uint64_t cols, uint64_t top)
 {
