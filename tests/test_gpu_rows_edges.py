@@ -10,8 +10,8 @@ import torch
 import memory_bound_elementwise_amd as ew
 from tests import rows_ref as ref
 from tests.rows_ref import TYPES, U, close
-from tests.test_gpu_rows import (DEV, check_logprobs, check_norm, check_norm8, check_norm_grad, gen,
-                                 grad_space, logits_of, norm_inputs, randn, run_distill,
+from tests.test_gpu_rows import (DEV, check_logprobs, check_norm, check_norm_grad, gen, grad_space,
+                                 logits_of, norm_inputs, randn, run_distill,
                                  run_logprobs, teacher_of)
 
 pytestmark = pytest.mark.gpu
@@ -311,3 +311,130 @@ def test_logits_workspaces_16_bytes_off():
     loss = torch.empty(rows, device=DEV)
     ew.ew_distill_bf16(x, z, ids, loss, workspace=space)
     assert all(torch.equal(got[k], want[k]) for k in want) and torch.equal(loss, want_loss)
+
+
+GRID_LOGITS = 1 << 23          # blocks of the logits' kernels: the rest are strided over
+GRID_NORM = 1 << 20            # and of the norm's
+
+
+def in_parts(rows, step=1 << 21):
+    return [slice(i, min(i + step, rows)) for i in range(0, rows, step)]
+
+
+def near(got, want, tol, what):
+    """rows_ref.close where the tensors are."""
+    got, want = got.double(), want.double()
+    same = (got == want) | (got.isnan() & want.isnan()) | ((got - want).abs() <= tol)
+    assert bool(same.all()), f"{what}: {int((~same).sum())} off"
+
+
+def near_rounded(got, want, tol, t, what):
+    dt = TYPES[t]
+    near(got, want, tol + (want.abs() + tol) * ref.half_ulp(dt) + ref.tiny(dt), what)
+
+
+@pytest.mark.parametrize("t,cols,top", [("f32", 9, 3), ("bf16", 12, 0), ("f16", 40, 5)])
+def test_logprobs_of_more_rows_than_a_grid(t, cols, top):
+    rows = GRID_LOGITS + 70001
+    x = randn(gen(800 + cols), rows, cols).mul_(3).to(TYPES[t])
+    x[::97, 1] = -math.inf
+    targets = torch.randint(-1, cols, (rows,), generator=gen(801), device=DEV)
+    got = run_logprobs(t, x, targets, top, 1.25)
+    slope = randn(gen(802), rows)
+    dx = torch.empty_like(x)
+    getattr(ew, "ew_logprobs_grad_" + t)(x, targets, got["lse"], slope, dx, entropy=got["entropy"],
+                                         dentropy=slope, scale=1.25)
+    for p in in_parts(rows):
+        want = ref.logprobs(x[p], targets[p], 1.25)
+        near(got["lse"][p], want.lse, want.lse_tol, "lse")
+        near(got["entropy"][p], want.entropy, want.entropy_tol, "entropy")
+        near(got["logp"][p], want.target_logp, want.target_tol, "logp")
+        if top:
+            assert torch.equal(got["top_ids"][p], want.top(top))
+            v, tol = want.logp(got["top_ids"][p])
+            near(got["top_logp"][p], v, tol, "top_logp")
+        g, tol = ref.logprobs_grad(x[p], targets[p], got["lse"][p], slope[p], 1.25,
+                                   entropy=got["entropy"][p], dentropy=slope[p])
+        near_rounded(dx[p], g, tol, t, "dlogits")
+
+
+@pytest.mark.parametrize("t,cols,kept", [("f32", 7, 2), ("bf16", 24, 5)])
+def test_distillation_of_more_rows_than_a_grid(t, cols, kept):
+    rows = GRID_LOGITS + 70001
+    x = randn(gen(810), rows, cols).mul_(3).to(TYPES[t])
+    z, ids = teacher_of(rows, cols, kept, 811)
+    loss, lse = run_distill(t, x, z, ids, 0.5)
+    slope = torch.rand(rows, generator=gen(812), device=DEV)
+    dx = torch.empty_like(x)
+    getattr(ew, "ew_distill_grad_" + t)(x, z, ids, lse, slope, dx, scale=0.5)
+    for p in in_parts(rows):
+        want, tol, stat = ref.distill(x[p], z[p], ids[p], 0.5)
+        near(loss[p], want, tol, "loss")
+        near(lse[p], stat.lse, stat.lse_tol, "lse")
+        g, tol = ref.distill_grad(x[p], z[p], ids[p], lse[p], slope[p], 0.5)
+        near_rounded(dx[p], g, tol, t, "dlogits")
+
+
+# rows a block's waves share: four of one wave, two of two, one of three and of four
+@pytest.mark.parametrize("t,cols,per_block", [("f32", 5, 4), ("bf16", 600, 2), ("bf16", 1100, 1),
+                                              ("f16", 2048, 1)])
+def test_norm_of_more_rows_than_a_grid(t, cols, per_block):
+    """Plain, and to 8 bits with one scale a row (two reductions a row) and
+    several."""
+    rows = per_block * GRID_NORM + 1001
+    x = torch.empty(rows, cols, dtype=TYPES[t], device=DEV)
+    for p in in_parts(rows, 1 << 18):
+        x[p] = randn(gen(820 + p.start), p.stop - p.start, cols)
+    w = (1 + 0.2 * randn(gen(821), cols)).to(TYPES[t])
+    y, rstd = torch.empty_like(x), torch.empty(rows, device=DEV)
+    getattr(ew, "ew_rmsnorm_" + t)(x, w, y, rstd=rstd)
+    for p in in_parts(rows, 1 << 18):
+        want, r, tol, tol_r = ref.norm(x[p], w, 1e-5)
+        near(rstd[p], r, tol_r, "rstd")
+        near_rounded(y[p], want, tol, t, "y")
+    del y
+    q = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=DEV)
+    rel = (ref.adds(cols) / 2 + 10) * U
+    for group in (0, 16):
+        scales = torch.empty(rows, -(-cols // group) if group else 1, device=DEV)
+        again = torch.empty_like(rstd)
+        getattr(ew, "ew_rmsnorm_e4m3_" + t)(x, w, q, scales, group=group, rstd=again)
+        assert torch.equal(again, rstd)
+        for p in in_parts(rows, 1 << 18):
+            want, _, tol, _ = ref.norm(x[p], w, 1e-5)
+            s, each = ref.group_scales(want, group)
+            near(scales[p], s, s * rel, "scales")
+            # as for the 8-bit norm of fewer rows
+            got = q[p].double() * scales[p].double().repeat_interleave(group or cols, 1)[:, :cols]
+            near(got, want, want.abs() * (2.0 ** -4 * (1 + rel) + 4 * rel)
+                 + each * 2.0 ** -10 * (1 + 4 * rel) + tol, "q * scale")
+
+
+def test_long_rows_of_more_than_a_grid():
+    """The norm's and the gradient's kernels for rows past the registers, in
+    place: rows of zeros but for those at the ends of both rounds."""
+    rows, cols = GRID_NORM + 5, 32776                    # 69 GB in bf16
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    at = (0, 1, 4, 5, 6, GRID_NORM - 1, GRID_NORM, GRID_NORM + 4)
+    data, _, w = norm_inputs("bf16", len(at), cols, 0, 0, 830)
+
+    def put():
+        for k, r in enumerate(at):
+            x[r].copy_(data[k])
+
+    def take():
+        return torch.stack([x[r] for r in at])
+
+    put()
+    rstd = torch.empty(rows, device=DEV)
+    ew.ew_rmsnorm_bf16(x, w, x, rstd=rstd)
+    mine = torch.stack([rstd[r] for r in at])
+    check_norm("bf16", data, None, w, take(), None, mine, 1e-5)
+    assert bool((rstd[7:1000] == rstd[7]).all()) and not bool(x[7:1000].any())
+    put()
+    # one buffer holds both the normed rows and dy, and receives dx
+    ew.ew_rmsnorm_grad_bf16(x, x, w, rstd, x)
+    check_norm_grad("bf16", None, None, w, mine, None, take(), None, inputs=(data, data, None))
+    assert not bool(x[7:1000].any())
+    del x
+    torch.cuda.empty_cache()
