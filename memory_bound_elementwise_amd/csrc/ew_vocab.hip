@@ -99,11 +99,17 @@ __device__ __forceinline__ float largest(const float (&v)[N])
     return top;
 }
 
-// N more logits of this lane, whatever they are.
+// N more logits of this lane, whatever they are.  Their largest is found by
+// comparisons: the hardware's maximum ignores a quiet NaN but drops its other
+// operand for a signalling one (which widening 16-bit data does not quiet).
 template <bool Ent, int N>
 __device__ __forceinline__ void absorb_any(RowSum &s, const float (&v)[N], Rate rate)
 {
-    rebase<Ent>(s, __builtin_fmaxf(s.m, largest(v)), rate);
+    float m = s.m;
+    asm("" : "+v"(m));       // no value the compiler knows, or it makes a maximum of these
+#pragma unroll
+    for (int k = 0; k < N; ++k) m = v[k] > m ? v[k] : m;
+    rebase<Ent>(s, m, rate);
     const Base base(s.m, rate);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -114,7 +120,7 @@ __device__ __forceinline__ void absorb_any(RowSum &s, const float (&v)[N], Rate 
 }
 
 // The same in fewer instructions, for logits and an s of ordinary size (or an
-// empty s) and, with entropy, none masked: returns whether the logits were so
+// empty s), no NaN among them and, with entropy, none masked: returns whether the logits were so
 // for this lane (s is of no use otherwise).  16-bit rows are bound by the vector unit: an element costs
 // its widening, half a maximum, an fma, a power, an addition and, with
 // entropy, another fma.
@@ -135,7 +141,8 @@ __device__ __forceinline__ bool absorb_plain(RowSum &s, const float (&v)[N], flo
         s.z += e;
         if constexpr (Ent) s.b = __builtin_fmaf(e, d, s.b);
     }
-    return __builtin_fabsf(t) <= kNear && (!Ent || s.b == s.b);
+    const float sum = Ent ? s.b : s.z;
+    return __builtin_fabsf(t) <= kNear && sum == sum;
 }
 
 // The sums of the wave's lanes, in every lane.

@@ -207,6 +207,35 @@ def test_the_largest_and_smallest_scales(t, cols, scale):
     close_rounded(dx, want, tol + small, TYPES[t], "logprobs dlogits")
 
 
+@every_type
+@pytest.mark.parametrize("cols", (70, 5000, 60000))
+def test_signalling_nans_count_as_nans(t, cols):
+    """Bit patterns that arithmetic never leaves, but memory may hold."""
+    rows, top = 5, 9
+    x, targets = logits_of(t, rows, cols, 0, 0, 900)
+    bits, word = {"f32": (0x7fa00000, torch.int32), "f16": (0x7d00, torch.int16),
+                  "bf16": (0x7fa0, torch.int16)}[t]
+    targets[:] = 5
+    raw = x.view(word)
+    raw[0, cols // 2] = bits
+    raw[1, 0] = bits
+    raw[2, cols - 1] = bits
+    raw[3, ::2] = bits
+    got = run_logprobs(t, x, targets, top, 1.0)
+    for k in ("lse", "entropy", "top_logp", "logp"):
+        assert bool(torch.isnan(got[k][:4]).all()), k
+    plain = x.float()
+    assert torch.equal(got["top_ids"], ref.Rows(plain, 1.0).top(top))
+    want = ref.logprobs(x[4:], targets[4:], 1.0)
+    close(got["lse"][4:], want.lse, want.lse_tol, "lse")
+    y, w = torch.empty_like(x), torch.ones(cols, dtype=TYPES[t], device=DEV)
+    getattr(ew, "ew_rmsnorm_" + t)(x, w, y)
+    assert bool(y[:4].isnan().all()) and not bool(y[4].isnan().any())
+    q, s = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=DEV), torch.empty(rows, 1, device=DEV)
+    getattr(ew, "ew_rmsnorm_e4m3_" + t)(x, w, q, s, group=0)
+    assert bool(s[:4].isnan().all()) and not bool(s[4].isnan().any())
+
+
 # ---------------------------------------------------------------------------
 # 8-bit norm: the bytes themselves
 # ---------------------------------------------------------------------------
