@@ -43,6 +43,14 @@ __device__ __forceinline__ float lane_value(float x, int lane)
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
 
+// R over each four neighbouring lanes, in each of them.
+template <class R>
+__device__ __forceinline__ float quad_reduce(float x)
+{
+    x = R::f(x, dpp<0xB1>(x));
+    return R::f(x, dpp<0x4E>(x));
+}
+
 // R over the 64 lanes of a wave, in every lane; all lanes must be active.
 // Within each row of 16 by lane exchanges (xor 1, xor 2, then mirrors of 8
 // and 16, which after the first two steps hold the other half's value), then
@@ -50,8 +58,7 @@ __device__ __forceinline__ float lane_value(float x, int lane)
 template <class R>
 __device__ __forceinline__ float wave_reduce(float x)
 {
-    x = R::f(x, dpp<0xB1>(x));
-    x = R::f(x, dpp<0x4E>(x));
+    x = quad_reduce<R>(x);
     x = R::f(x, dpp<0x141>(x));
     x = R::f(x, dpp<0x140>(x));
     return R::f(R::f(lane_value(x, 0), lane_value(x, 16)),

@@ -161,21 +161,17 @@ __device__ __forceinline__ void block_join(RowSum &s, Rate k, RowSum *part)
     wave_join<Ent>(s, k);
     if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = s;
     __syncthreads();
-    float m = part[0].m;
-#pragma unroll
-    for (int w = 1; w < kVocabWaves; ++w) m = __builtin_fmaxf(m, part[w].m);
-    RowSum all{m, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < kVocabWaves; ++w) {
-        RowSum p = part[w];
-        rebase<Ent>(p, m, k);
-        all.z += p.z;
-        all.b += p.b;
-    }
-    s = all;
+    // each four lanes hold the four waves' sums: one re-basing in all
+    static_assert(kVocabWaves == 4, "the exchanges below are within four lanes");
+    s = part[threadIdx.x % kVocabWaves];
+    rebase<Ent>(s, quad_reduce<Max>(s.m), k);
+    s.z = quad_reduce<Sum>(s.z);
+    if constexpr (Ent) s.b = quad_reduce<Sum>(s.b);
 }
 
 // lse and entropy from a row's sums.  empty: the scaled logits are all -inf.
+// log_z is relative to the sums' base, lse rounded once from the largest logit
+// itself.
 struct RowStat {
     float lse, entropy, log_z;
     bool empty;
@@ -188,7 +184,8 @@ __device__ __forceinline__ RowStat row_stat(const RowSum &s, float scale)
     // all NaN: m stays -inf while z is a NaN
     st.empty = top == -kInf && s.z == s.z;
     st.log_z = __builtin_logf(s.z);
-    st.lse = st.empty ? -kInf : top == kInf ? __builtin_nanf("") : top + st.log_z;
+    const float past = __builtin_fmaf(-kLn2, base_rounding(s.m, Rate(scale)), st.log_z);
+    st.lse = st.empty ? -kInf : top == kInf ? __builtin_nanf("") : __builtin_fmaf(s.m, scale, past);
     st.entropy = st.empty ? 0.0f
                  : st.lse != st.lse ? st.lse : __builtin_fmaf(-kLn2, s.b / s.z, st.log_z);
     return st;

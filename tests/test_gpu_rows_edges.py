@@ -171,6 +171,23 @@ def test_a_large_negative_head_before_ordinary_logits(offset):
 
 
 @every_type
+@pytest.mark.parametrize("rows,cols,top", [(40, 300, 0), (9, 3001, 3), (3, 150000, 0), (600, 1000, 0)])
+@pytest.mark.parametrize("scale", (1.0, 1.25, 0.7))
+def test_lse_of_large_logits_is_rounded_once(t, rows, cols, top, scale):
+    """Logits that share a large offset: lse is off by its own rounding and by
+    what the sum and its logarithm are off, not by the offset's products."""
+    g = gen(910 + cols)
+    x = torch.randint(-3, 4, (rows, cols), generator=g, device=DEV).float()
+    scale = float(torch.tensor(scale))
+    for offset in (1000.0, -1000.0, 1840.0, -2000.0):
+        y = ((x + offset) if t == "f16" else x * 8 + offset).to(TYPES[t])
+        got = run_logprobs(t, y, torch.zeros(rows, dtype=torch.int64, device=DEV), top, scale)
+        want = ref.Rows(y, scale)
+        tol = want.z_tol + (4 * want.log_z.abs() + want.lse.abs()) * U
+        close(got["lse"], want.lse, tol, "lse")
+
+
+@every_type
 @pytest.mark.parametrize("cols", (5, 70, 3000, 60000))
 @pytest.mark.parametrize("scale", (2.3e38, 2.4e38, 3.4e38, 1e-38))
 def test_the_largest_and_smallest_scales(t, cols, scale):
