@@ -499,8 +499,8 @@ ew_status_t ew_rmsnorm_grad_bf16(const uint16_t *dy, size_t dy_stride, const uin
                                  size_t workspace_bytes, size_t rows, size_t cols,
                                  hipStream_t stream);
 
-/* Log probabilities of given tokens.  With s = scale * logits (scale finite
- * and > 0: the reciprocal of a temperature), per row
+/* Log probabilities of given tokens.  With s = scale * logits in binary32
+ * (scale finite and > 0: the reciprocal of a temperature), per row
  *   lse     = log(sum exp(s))                           (optional)
  *   logp    = s[target] - lse; 0 where target is outside [0, cols), as for
  *             the padding positions of a batch
@@ -508,12 +508,13 @@ ew_status_t ew_rmsnorm_grad_bf16(const uint16_t *dy, size_t dy_stride, const uin
  *   top_ids, top_logp: the `top` most likely columns, most likely first,
  *             ties to the lowest column, and their s - lse; rows x top
  *             values, both or neither; top <= min(64, cols).
- * A logit of -inf is masked: p = 0 and nothing of it enters the sums.  A row
- * whose mask leaves nothing has lse = -inf, entropy 0, logp -inf (0 without
- * a target) and top_logp -inf.  A row that holds a NaN or a scaled logit of
- * +inf has NaN in lse, entropy, top_logp and the logp of a given target.  For
- * the ranking a NaN counts as -inf, so top_ids always holds `top` different
- * columns. */
+ * A logit whose s is -inf is masked: p = 0 and nothing of it enters the sums.
+ * (A type's lowest value is a number: where its s is finite a row of nothing
+ * else is an even one.)  A row whose mask leaves nothing has lse = -inf,
+ * entropy 0, logp -inf (0 without a target) and top_logp -inf.  A row that
+ * holds a NaN or a scaled logit of +inf has NaN in lse, entropy, top_logp and
+ * the logp of a given target.  For the ranking a NaN counts as -inf, so
+ * top_ids always holds `top` different columns. */
 size_t ew_logprobs_workspace(size_t rows, size_t cols, size_t top);
 ew_status_t ew_logprobs_f32(const float *logits, size_t stride, const int64_t *targets,
                             float *logp, float *entropy, float *lse, float *top_logp,
@@ -556,7 +557,8 @@ ew_status_t ew_logprobs_grad_bf16(const uint16_t *logits, size_t stride, const i
 /* Distillation from a teacher's `kept` top logits: teacher and ids are
  * rows x kept.  An entry whose id is outside [0, cols), or whose scaled
  * teacher logit is -inf, is dropped; t is the softmax of scale * teacher over
- * the entries that remain, and with s and lse as for the log probabilities
+ * the entries that remain (NaN if one of them is a NaN or +inf when scaled),
+ * and with s and lse as for the log probabilities
  *   loss = sum t * (log t - (s[id] - lse))
  * per row: 0 if no entry remains; entries whose t underflows (below 2^-126)
  * add nothing; +inf if another entry meets a masked logit.  A column named twice counts twice.

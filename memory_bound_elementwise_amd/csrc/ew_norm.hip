@@ -16,8 +16,8 @@ constexpr float kScaleMin = 0x1p-126f;
 // it could only round otherwise where the quotient lies that close to the
 // middle of two binary32 numbers, and only matter where one of them lies
 // halfway between two e4m3 values; in none of the mantissas for which both
-// hold does it.  (The product alone falls on the other side of 0.1-2 % of the
-// ties; a division costs 3-8 % more time.)  Small scales are worked with 2^64
+// hold does it.  (The product alone puts 0.1-1.5 % of the bytes one step off,
+// at ties; a division costs 3-8 % more time.)  Small scales are worked with 2^64
 // times as large, so that the residual is exact; a scale of +inf (a norm that
 // overflowed) divides finite y to 0.
 struct Quotient {
@@ -166,10 +166,12 @@ constexpr int norm_block(int waves) { return waves < 3 ? 256 : waves * 64; }
 // total = round(x + residual), y = total * rstd * weight in one pass: the row's
 // vectors stay in registers between the sum of squares and the product, and
 // the sum costs one barrier.  Bound by memory: 8192 x 4096 bf16 with residual
-// and total 42.5 us, 6.3 TB/s (a copy of 2^28 floats: 6.64); e4m3, 4096 x 8192
-// bf16 41 us, 5.8 TB/s (8-byte stores); 1021 x 5003 f32, rows 4 bytes off,
-// 17.7 us, 4.6 TB/s (two rounds of blocks that load, then store); one row of
-// 4096 2.3 us on the GPU.
+// and total 42.4 us, 6.3 TB/s (a copy of 2^28 floats: 6.64); e4m3, 4096 x 8192
+// bf16 42.3 us, 5.6 TB/s (8-byte stores; the vector unit is busy 72 %).  A
+// row whose columns fill no whole vectors is bound by latency: the last
+// vector's elements are loaded one after another while the block waits, and
+// the weight, x and the residual are waited for in turn (1021 x 5003 f32 17.8
+// us, 4.6 TB/s; 8192 x 4097 bf16 65).  One row of 4096 2.4 us on the GPU.
 template <typename T, int Waves, int V, bool E4M3>
 __global__ void __launch_bounds__(norm_block(Waves)) ew_norm_row_kernel(NormArgs a)
 {

@@ -457,9 +457,11 @@ __device__ __forceinline__ RowSum stream_part(const T *x, uint32_t cols, const P
 // of its own (lane_top); at least `top` logits are at or above the top-th
 // largest of a wave's 64, so that the highest of the waves' is a bar that few
 // more than `top` logits pass, and only lanes whose largest passes it hold
-// any: their vectors, one in a few hundred, are read again.  Where fewer
-// lanes than that have a logit that is not masked the bar is -inf: then every
-// such logit is taken, and the lowest masked columns after them.
+// any: all their vectors are read again.  Eight lanes share a cache line, so
+// that is a third of the row at 5 alternatives, nearly all of it from 20 on
+// (2048 x 50257 bf16, of 206 MB: 276 MB read at 5, 390 at 20, 411 at 32).
+// Where fewer lanes than that have a logit that is not masked the bar is -inf:
+// then every such logit is taken, and the lowest masked columns after them.
 template <typename T>
 __device__ __forceinline__ uint64_t part_top(const T *x, uint32_t cols, const Part &p,
                                              const RowSplit<T> &split, float lane_top,
@@ -641,11 +643,12 @@ struct ForwardShared {
 };
 
 // One pass over the logits: each lane keeps a running maximum and sums, joined
-// at the row's end.  4096 x 131072 bf16 with entropy 165-170 us, 6.3-6.5 TB/s
-// (reading alone in this pattern: 157 us); distillation 2048 x 131072 bf16 84
-// us, 6.4 TB/s; 2048 x 50257 with 5 alternatives 48 us, 4.3 TB/s, of which the
-// blocks' starts and ends, all at the same time, are a third; 8 x 131072 f32
-// with 20 alternatives 8.6 us and 4.8 for the join, latency.
+// at the row's end.  4096 x 131072 bf16 with entropy 167-171 us, 6.3-6.4 TB/s
+// (reading alone in this pattern: 157 us); distillation 2048 x 131072 bf16 85
+// us, 6.3 TB/s; 2048 x 50257 49 us with 5 alternatives, 39 without, the floor
+// is 29: the blocks' starts and ends come all at the same time; 20
+// alternatives 73 us, 32 81, 64 120 (read again: part_top); 8 x 131072 f32
+// with 20 alternatives 8.5 us and 4.7 for the join, latency.
 //
 // Eight waves a SIMD for 16-bit logits: with the 74 registers the compiler
 // would take, the 2048 blocks of as many rows need a second round on 256 CUs
