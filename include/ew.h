@@ -557,7 +557,7 @@ ew_status_t ew_logprobs_grad_bf16(const uint16_t *logits, size_t stride, const i
 /* Distillation from a teacher's `kept` top logits: teacher and ids are
  * rows x kept.  An entry whose id is outside [0, cols), or whose scaled
  * teacher logit is -inf, is dropped; t is the softmax of scale * teacher over
- * the entries that remain (NaN if one of them is a NaN or +inf when scaled),
+ * the entries that remain (NaN if one of them is a NaN or +inf),
  * and with s and lse as for the log probabilities
  *   loss = sum t * (log t - (s[id] - lse))
  * per row: 0 if no entry remains; entries whose t underflows (below 2^-126)

@@ -526,8 +526,9 @@ __device__ __forceinline__ uint64_t part_top(const T *x, uint32_t cols, const Pa
 // joins the parts
 // ---------------------------------------------------------------------------
 
-// The teacher's distribution over its kept entries: the scaled logits'
-// maximum and sum, in every thread.
+// The teacher's distribution over its kept entries: the largest logit and the
+// sum of exp((logit - m) * scale), in every thread.  The difference comes
+// first: scaled logits would each bring a rounding of their own size along.
 struct Teacher {
     float m, z;
 };
@@ -574,7 +575,7 @@ struct Logprobs {
 struct Distill {
     using Args = DistillArgs;
     struct Ahead {              // thread k's entry k: loaded before the row is streamed
-        float teacher, logit;   // scaled teacher logit, -inf if there is none
+        float teacher, logit;   // the teacher's logit, -inf if there is none
     };
     template <typename T>
     __device__ static Ahead entry(const Args &a, uint32_t r, const T *x, uint32_t k)
@@ -582,8 +583,8 @@ struct Distill {
         Ahead h{-kInf, 0.0f};
         if (k < a.kept) {
             const int64_t id = a.ids[(uint64_t)r * a.kept + k];
-            const float t = a.teacher[(uint64_t)r * a.kept + k] * a.scale;
-            if (kept_entry(id, t, a.cols)) h = Ahead{t, (float)x[id]};
+            const float t = a.teacher[(uint64_t)r * a.kept + k];
+            if (kept_entry(id, t * a.scale, a.cols)) h = Ahead{t, (float)x[id]};
         }
         return h;
     }
@@ -607,13 +608,15 @@ struct Distill {
         each([&](const Ahead &e) { m = __builtin_fmaxf(m, e.teacher); });
         m = block_reduce<Max, kVocabWaves>(m, scratch[0]);
         float z = 0.0f;
-        each([&](const Ahead &e) { z += e.teacher == -kInf ? 0.0f : exp_nat(e.teacher - m); });
+        each([&](const Ahead &e) {
+            z += e.teacher == -kInf ? 0.0f : exp_nat((e.teacher - m) * a.scale);
+        });
         z = block_reduce<Sum, kVocabWaves>(z, scratch[1]);
         const float log_z = __builtin_logf(z);
         float loss = 0.0f;
         each([&](const Ahead &e) {
             if (e.teacher == -kInf) return;
-            const float l = e.teacher - m - log_z, p = exp_nat(e.teacher - m) / z;
+            const float d = (e.teacher - m) * a.scale, l = d - log_z, p = exp_nat(d) / z;
             if (p >= 0x1p-126f || p != p) loss += p * (l - log_prob(e.logit, s, st, a.scale));
         });
         loss = block_reduce<Sum, kVocabWaves>(loss, scratch[2]);
@@ -919,14 +922,12 @@ __device__ __forceinline__ Teacher wave_teacher(const float *teacher, const int6
     Teacher t;
     float m = -kInf;
     for (uint32_t k = threadIdx.x % 64; k < kept; k += 64) {
-        const float s = teacher[k] * scale;
-        if (kept_entry(ids[k], s, cols)) m = __builtin_fmaxf(m, s);
+        if (kept_entry(ids[k], teacher[k] * scale, cols)) m = __builtin_fmaxf(m, teacher[k]);
     }
     t.m = wave_reduce<Max>(m);
     float z = 0.0f;
     for (uint32_t k = threadIdx.x % 64; k < kept; k += 64) {
-        const float s = teacher[k] * scale;
-        if (kept_entry(ids[k], s, cols)) z += exp_nat(s - t.m);
+        if (kept_entry(ids[k], teacher[k] * scale, cols)) z += exp_nat((teacher[k] - t.m) * scale);
     }
     t.z = wave_reduce<Sum>(z);
     return t;
@@ -965,13 +966,14 @@ __global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGra
             for (uint32_t k0 = 0; k0 < a.kept; k0 += 64) {
                 const uint32_t k = k0 + threadIdx.x;
                 const int64_t id = k < a.kept ? ids[k] : -1;
-                const float s = k < a.kept ? teacher[k] * a.scale : -kInf;
-                const bool here = kept_entry(id, s, a.cols) && (uint64_t)id - g.first < g.cols;
+                const float own = k < a.kept ? teacher[k] : -kInf;
+                const bool here =
+                    kept_entry(id, own * a.scale, a.cols) && (uint64_t)id - g.first < g.cols;
                 const uint64_t mask = __ballot(here);
                 if (here) {
                     const uint32_t slot = n + lanes_below(mask);
                     at[slot] = (uint32_t)id - g.first;
-                    weight[slot] = exp_nat(s - t.m) / t.z;
+                    weight[slot] = exp_nat((own - t.m) * a.scale) / t.z;
                     logit[slot] = (float)x[id];
                 }
                 n += __builtin_popcountll(mask);

@@ -254,6 +254,46 @@ def test_signalling_nans_count_as_nans(t, cols):
 
 
 # ---------------------------------------------------------------------------
+# Teachers of any size
+# ---------------------------------------------------------------------------
+
+@every_type
+@pytest.mark.parametrize("rows,cols,kept", [(9, 40, 1), (30, 300, 5), (4, 5000, 300), (3, 60000, 1024)])
+@pytest.mark.parametrize("scale", (0.1, 1.0, 0.7))
+def test_teacher_logits_that_share_a_large_offset(t, rows, cols, kept, scale):
+    """t depends on the differences of the teacher's logits: a single entry's
+    is 1, however large its logit."""
+    scale = float(torch.tensor(scale))
+    g = gen(920 + cols)
+    x = (3 * randn(g, rows, cols)).to(TYPES[t])
+    ids = torch.stack([torch.randperm(cols, generator=g, device=DEV)[:kept] for _ in range(rows)])
+    slope = randn(g, rows)
+    for offset in (0.0, 100.0, -3000.0, 1e5, -1e7, 1e30):
+        z = (offset + 8 * randn(g, rows, kept) / scale).float()
+        loss, lse = run_distill(t, x, z, ids, scale)
+        want, tol, _ = ref.distill(x, z, ids, scale)
+        close(loss, want, tol, f"loss {offset}")
+        dx = torch.empty_like(x)
+        getattr(ew, "ew_distill_grad_" + t)(x, z, ids, lse, slope, dx, scale=scale)
+        want, tol = ref.distill_grad(x, z, ids, lse, slope, scale)
+        close_rounded(dx, want, tol, TYPES[t], f"dlogits {offset}")
+
+
+def test_teacher_logits_whose_scaled_values_overflow():
+    """Only their differences count; an infinite one makes a NaN."""
+    x, ids = randn(gen(930), 3, 50), torch.tensor([[3, 4], [5, 6], [7, 8]], device=DEV)
+    z = torch.tensor([[3e38, 3e38], [3e38, -3e38], [math.inf, 0.0]], device=DEV)
+    loss, lse = run_distill("f32", x, z, ids, 2.0)
+    want, tol, _ = ref.distill(x[:2], z[:2], ids[:2], 2.0)
+    close(loss[:2], want, tol, "loss")
+    dx, one = torch.empty_like(x), torch.ones(3, device=DEV)
+    ew.ew_distill_grad_f32(x, z, ids, lse, one, dx, scale=2.0)
+    want, tol = ref.distill_grad(x, z, ids, lse, one, 2.0)
+    close_rounded(dx[:2], want[:2], tol[:2], torch.float32, "dlogits")
+    assert math.isnan(float(loss[2])) and bool(dx[2].isnan().all())
+
+
+# ---------------------------------------------------------------------------
 # 8-bit norm: the bytes themselves
 # ---------------------------------------------------------------------------
 
