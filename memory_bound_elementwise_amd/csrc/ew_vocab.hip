@@ -48,7 +48,12 @@ struct Rate {
     }
 };
 
-__device__ __forceinline__ float finite_base(float m) { return m == -kInf ? 0.0f : m; }
+// unit * m, kept finite from below: where m is -inf, or times c is anyway, all
+// distances come out as -inf.
+__device__ __forceinline__ float unit_base(float m, Rate k)
+{
+    return __builtin_fmaxf(m * k.unit, -__FLT_MAX__);
+}
 
 // What d(x) = c * (unit * x - far) - near is formed with, for a largest logit m:
 // near is t, or far is unit * m.
@@ -57,7 +62,7 @@ struct Base {
     __device__ Base(float m, Rate k)
     {
 #pragma clang fp contract(off)
-        const float u = finite_base(m) * k.unit, t = u * k.c;
+        const float u = unit_base(m, k), t = u * k.c;
         const bool is_near = __builtin_fabsf(t) <= kNear;
         near = is_near ? t : 0.0f;
         far = is_near ? 0.0f : u;
@@ -72,7 +77,7 @@ struct Base {
 __device__ __forceinline__ float base_rounding(float m, Rate k)
 {
 #pragma clang fp contract(off)
-    const float u = m * k.unit, t = u * k.c;
+    const float u = unit_base(m, k), t = u * k.c;
     return __builtin_fabsf(t) <= kNear ? __builtin_fmaf(u, k.c, -t) : 0.0f;
 }
 
@@ -81,9 +86,8 @@ template <bool Ent>
 __device__ __forceinline__ void rebase(RowSum &s, float m, Rate k)
 {
 #pragma clang fp contract(off)
-    const float base = finite_base(m);
-    const float d = __builtin_fmaf(s.m, k.unit, -(base * k.unit)) * k.c +
-                    (base_rounding(base, k) - base_rounding(s.m, k));
+    const float d = __builtin_fmaf(s.m, k.unit, -unit_base(m, k)) * k.c +
+                    (base_rounding(m, k) - base_rounding(s.m, k));
     const float shift = __builtin_fmaxf(d, kFarBelow), f = __builtin_amdgcn_exp2f(shift);
     if constexpr (Ent) s.b = f * __builtin_fmaf(shift, s.z, s.b);
     s.z *= f;
@@ -129,7 +133,7 @@ __device__ __forceinline__ bool absorb_plain(RowSum &s, const float (&v)[N], flo
 {
 #pragma clang fp contract(off)
     const float m = __builtin_fmaxf(s.m, largest(v));
-    const float t = finite_base(m) * c;
+    const float t = m == -kInf ? 0.0f : m * c;
     const float shift = __builtin_fmaxf(s.m * c - t, kFarBelow);
     const float f = __builtin_amdgcn_exp2f(shift);
     if constexpr (Ent) s.b = f * __builtin_fmaf(shift, s.z, s.b);

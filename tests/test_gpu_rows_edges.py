@@ -224,6 +224,31 @@ def test_the_largest_and_smallest_scales(t, cols, scale):
     close_rounded(dx, want, tol + small, TYPES[t], "logprobs dlogits")
 
 
+@pytest.mark.parametrize("t", ("f32", "bf16"))
+@pytest.mark.parametrize("cols", (6, 3000, 60000))
+@pytest.mark.parametrize("scale", (1.5, 2.3e38, 2.5e38, 3.4e38))
+def test_rows_whose_scaled_logits_all_overflow_downwards(t, cols, scale):
+    """Every scaled logit is -inf in binary32: a row whose mask leaves nothing,
+    whatever the logits; one that is not is the row's."""
+    scale = float(torch.tensor(scale))
+    x = torch.full((5, cols), -3e38, device=DEV)
+    x[1] = -3.3e38 + 3e37 * torch.rand(cols, generator=gen(940), device=DEV)
+    x[2, : cols // 2] = -math.inf
+    x[3, cols // 3] = -1e38 / scale
+    x[4, cols // 3], x[4, cols // 2] = 0.0, -0.5 / scale
+    x = x.to(TYPES[t])
+    targets = torch.full((5,), cols // 3, device=DEV)
+    got = check_logprobs(t, x, targets, 3, scale)
+    assert bool((got["lse"][:3] == -math.inf).all()) and bool((got["entropy"][:3] == 0).all())
+    z, ids = torch.zeros(5, 2, device=DEV), torch.full((5, 2), cols // 3, device=DEV)
+    loss, lse = run_distill(t, x, z, ids, scale)
+    assert bool((loss[:3] == math.inf).all()) and bool((lse[:3] == -math.inf).all())
+    one, dx = torch.ones(5, device=DEV), torch.empty_like(x)
+    getattr(ew, "ew_logprobs_grad_" + t)(x, targets, got["lse"], one, dx, entropy=got["entropy"],
+                                         dentropy=one, scale=scale)
+    assert not bool(dx[:3].any())
+
+
 @every_type
 @pytest.mark.parametrize("cols", (70, 5000, 60000))
 def test_signalling_nans_count_as_nans(t, cols):
