@@ -202,9 +202,10 @@ __device__ __forceinline__ float log_prob(float x, const RowSum &s, const RowSta
     if (st.lse != st.lse) return st.lse;
     const Rate k(scale);
     const float d = Base(s.m, k).distance(x, k);
-    // far away (where d may overflow though its natural logarithm does not)
-    // the rounding of t no longer matters
-    return d < -kNear ? (x - s.m) * scale - st.log_z : __builtin_fmaf(d, kLn2, -st.log_z);
+    // far away (where d, and x - m, may overflow though their product with
+    // scale does not) the rounding of t no longer matters
+    return d < -kNear ? (0.5f * x - 0.5f * s.m) * scale * 2.0f - st.log_z
+                      : __builtin_fmaf(d, kLn2, -st.log_z);
 }
 
 // ---------------------------------------------------------------------------

@@ -226,6 +226,23 @@ def test_the_largest_and_smallest_scales(t, cols, scale):
 
 @pytest.mark.parametrize("t", ("f32", "bf16"))
 @pytest.mark.parametrize("cols", (6, 3000, 60000))
+@pytest.mark.parametrize("scale", (1e-30, 0.3, 1e-3))
+def test_log_probabilities_of_logits_farther_apart_than_a_number(t, cols, scale):
+    """x - m overflows, scale * (x - m) does not."""
+    scale = float(torch.tensor(scale))
+    x = torch.full((3, cols), -3e38, device=DEV)
+    x[:, 1] = torch.tensor([3e38, 2e38, 1e38], device=DEV)
+    x[:, 4] = -1.5e38
+    x = x.to(TYPES[t])
+    check_logprobs(t, x, torch.tensor([0, 4, cols - 1], device=DEV), 3, scale)
+    z, ids = torch.zeros(3, 2, device=DEV), torch.tensor([[0, 1], [4, 0], [1, 1]], device=DEV)
+    loss, _ = run_distill(t, x, z, ids, scale)
+    want, tol, _ = ref.distill(x, z, ids, scale)
+    close(loss, want, tol, "loss")
+
+
+@pytest.mark.parametrize("t", ("f32", "bf16"))
+@pytest.mark.parametrize("cols", (6, 3000, 60000))
 @pytest.mark.parametrize("scale", (1.5, 2.3e38, 2.5e38, 3.4e38))
 def test_rows_whose_scaled_logits_all_overflow_downwards(t, cols, scale):
     """Every scaled logit is -inf in binary32: a row whose mask leaves nothing,
