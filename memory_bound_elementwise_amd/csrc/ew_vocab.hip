@@ -838,23 +838,23 @@ struct GradTile {
 // above it) and at least kLeast, below which its exponential is 0 anyway
 // (from -88 on): what it is multiplied by stays small where x is masked or far
 // below the rest.
-constexpr float kLeast = -1e4f;
+constexpr float kLeast = -110.0f;
 
 __device__ __forceinline__ float log_p(float x, float scale, float lse)
 {
     return __builtin_amdgcn_fmed3f(__builtin_fmaf(x, scale, -lse), kLeast, 0.0f);
 }
 
-// A row's gradient is scale times factors times terms of p.  Where factor and
-// scale together pass kLargeFactor the product with p might still be ordinary
-// (and infinite times a p of 0 a NaN), so there the factors come in 2^-40 times
-// as large and without a scale above 1, and the terms are multiplied by both
-// once they are whole.
-constexpr float kLargeFactor = 1e38f, kShrink = 0x1p-40f;
+// A row's gradient is scale times slopes times terms of p.  Where a slope and
+// scale together pass kLargeFactor the product with p may still be ordinary
+// (and infinite times a p of 0 a NaN), so there the slopes come in 2^-8 times
+// as large, enough for their terms (a logarithm is at most 110) to stay finite,
+// and without a scale above 1; both are made up for once the terms are whole.
+constexpr float kLargeFactor = 1e38f, kShrink = 0x1p-8f;
 
 struct Factors {
-    float shrink, scale;       // before: (1, the scale), or of a large row (2^-40, at most 1)
-    float above;               // after, in a large row: with 2^40
+    float shrink, scale;       // before: (1, the scale), or of a large row (2^-8, at most 1)
+    float above;               // after, in a large row: with 2^8
     __device__ Factors(bool large, float s)
         : shrink(large ? kShrink : 1.0f), scale(large ? __builtin_fminf(s, 1.0f) : s),
           above(large ? __builtin_fmaxf(s, 1.0f) : 1.0f) {}

@@ -111,6 +111,45 @@ def test_distill_grad_of_large_slopes(t, cols, kept, scale):
     close_rounded(dx, want, tol, TYPES[t], "dlogits")
 
 
+@every_type
+@pytest.mark.parametrize("cols", (70, 20001))
+@pytest.mark.parametrize("scale", (1e10, 2e30, 2.5e38))
+def test_gradients_of_small_probabilities_at_large_scales(t, cols, scale):
+    """scale times p is an ordinary number for p of 1e-35 too."""
+    rows, kept = 5, 4
+    scale = float(torch.tensor(scale))
+    g = gen(950 + cols)
+    # scaled logits of 0 to -80, in values that 16-bit types hold
+    step = 2.0 ** math.ceil(math.log2(80 / 64 / scale))
+    steps = torch.randint(0, 64, (rows, cols), generator=g, device=DEV)
+    x = (-step * steps.float()).to(TYPES[t])
+    x[:, 0] = 0.0
+    targets = torch.tensor([0, 1, 2, -1, 3], device=DEV)
+    lse = ref.Rows(x, scale).lse.float()
+    ent = ref.Rows(x, scale).entropy.float()
+    slope = torch.tensor([1.0, -0.3, 1e-3, 1e20, 3e38], device=DEV)
+    for more in ({}, {"entropy": ent, "dentropy": torch.flip(slope, (0,)) * 0.01}):
+        dx = torch.empty_like(x)
+        getattr(ew, "ew_logprobs_grad_" + t)(x, targets, lse, slope, dx, scale=scale, **more)
+        want, tol = ref.logprobs_grad(x, targets, lse, slope, scale, **more)
+        lost = slope.double().abs()
+        if more:
+            lost = lost + more["dentropy"].double().abs() * (104 + ent.double())
+        tol = tol + (lost * scale * FLUSH)[:, None]
+        # elsewhere roundings, or p that count as 0, pass the type
+        fine = tol < 0.01 * torch.finfo(TYPES[t]).max
+        close_rounded(torch.where(fine, dx.double(), 0.0), torch.where(fine, want, 0.0), tol, TYPES[t],
+                      "logprobs")
+    z, ids = randn(g, rows, kept) / scale, torch.randint(1, cols, (rows, kept), generator=g, device=DEV)
+    dx = torch.empty_like(x)
+    getattr(ew, "ew_distill_grad_" + t)(x, z, ids, lse, slope, dx, scale=scale)
+    want, tol = ref.distill_grad(x, z, ids, lse, slope, scale)
+    tol = tol + (slope.double().abs() * scale * FLUSH)[:, None]
+    fine = tol < 0.01 * torch.finfo(TYPES[t]).max
+    close_rounded(torch.where(fine, dx.double(), 0.0), torch.where(fine, want, 0.0), tol, TYPES[t],
+                  "distill")
+
+
 def test_entropy_of_the_longest_row():
     """2^31 - 1 equal logits and one that is larger by 3e38: a sum of 2^31
     terms is re-based by a difference that no power of two holds."""
