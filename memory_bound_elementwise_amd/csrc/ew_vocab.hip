@@ -37,14 +37,19 @@ constexpr float kFarBelow = -1e4f;
 // form it leave its product alone (contract off).
 constexpr float kNear = 0x1p16f;
 
-// c, in two factors where it is infinite itself (scales above 2.36e38): c * x is
-// unit * x, exact, times c.
+// c * x is unit * x, exact, times c: in two factors where the product of scale
+// and log2(e) overflows (scales above 2.36e38), and of halves where the
+// difference of two logits may overflow though c times it does not come to
+// -infinity (scales below kTiny).
+constexpr float kTiny = 0x1p-64f;
+
 struct Rate {
     float c, unit;
     __device__ explicit Rate(float scale)
         : c(scale * kLog2e), unit(1.0f)
     {
         if (c == kInf) c = 0.5f * scale * kLog2e, unit = 2.0f;
+        if (scale < kTiny) c *= 2.0f, unit = 0.5f;
     }
 };
 

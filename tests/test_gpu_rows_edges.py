@@ -305,6 +305,32 @@ def test_rows_whose_scaled_logits_all_overflow_downwards(t, cols, scale):
     assert not bool(dx[:3].any())
 
 
+@pytest.mark.parametrize("t", ("f32", "bf16"))
+@pytest.mark.parametrize("cols", (9, 3000, 60000))
+@pytest.mark.parametrize("scale", (1e-38, 1e-37, 3e-36, 1e-25))
+def test_logits_of_every_size_at_tiny_scales(t, cols, scale):
+    """Sums of lanes whose largest logits are farther apart than a number is
+    large, though not when scaled."""
+    rows = 4
+    scale = float(torch.tensor(scale))
+    g = gen(970 + cols)
+    x = 3.3e38 * (2 * torch.rand(rows, cols, generator=g, device=DEV) - 1)
+    x[1] = torch.where(x[1] > 0, 3.3e38, -3.3e38)
+    x[2, 1:] = -3.3e38
+    x[2, 0] = 3.3e38
+    x = x.to(TYPES[t])
+    targets = torch.randint(cols, (rows,), generator=g, device=DEV)
+    got = check_logprobs(t, x, targets, 5, scale)
+    slope = torch.full((rows,), 1e30, device=DEV)
+    dx = torch.empty_like(x)
+    getattr(ew, "ew_logprobs_grad_" + t)(x, targets, got["lse"], slope, dx, entropy=got["entropy"],
+                                         dentropy=slope, scale=scale)
+    want, tol = ref.logprobs_grad(x, targets, got["lse"], slope, scale, entropy=got["entropy"],
+                                  dentropy=slope)
+    tol = tol + 1e30 * (1 + 104 + got["entropy"].double())[:, None] * scale * FLUSH
+    close_rounded(dx, want, tol, TYPES[t], "dlogits")
+
+
 @every_type
 @pytest.mark.parametrize("cols", (70, 5000, 60000))
 def test_signalling_nans_count_as_nans(t, cols):
