@@ -307,6 +307,7 @@ ew_status_t distill(RowType t, const void *logits, size_t stride, const float *t
     a.cols = (uint32_t)cols;
     a.kept = (uint32_t)kept;
     a.scale = scale;
+    a.by = teacher_scale(scale);
     return launch("distill", t, a, stream, launch_distill);
 }
 
@@ -339,6 +340,7 @@ ew_status_t distill_grad(RowType t, const void *logits, size_t stride, const flo
     a.cols = (uint32_t)cols;
     a.kept = (uint32_t)kept;
     a.scale = scale;
+    a.by = teacher_scale(scale);
     return launch("distill_grad", t, a, stream, launch_distill_grad);
 }
 

@@ -54,6 +54,20 @@ struct LogprobsGradArgs {
     float scale;
 };
 
+// Below it the difference of two logits may overflow though scale times it is
+// an ordinary number.
+constexpr float kTinyScale = 0x1p-64f;
+
+// scale in two factors: the exact part that logits take before their
+// difference is formed, and what the difference takes.
+struct TeacherScale {
+    float part, whole;
+};
+constexpr TeacherScale teacher_scale(float scale)
+{
+    return scale < kTinyScale ? TeacherScale{0.5f, 2.0f * scale} : TeacherScale{1.0f, scale};
+}
+
 struct DistillArgs {
     const void *logits;
     const float *teacher;
@@ -63,6 +77,7 @@ struct DistillArgs {
     uint64_t stride;
     uint32_t rows, cols, kept;
     float scale;
+    TeacherScale by;
 };
 
 struct DistillGradArgs {
@@ -74,6 +89,7 @@ struct DistillGradArgs {
     uint64_t stride, dlogits_stride;
     uint32_t rows, cols, kept;
     float scale;
+    TeacherScale by;
 };
 
 // Most alternatives a call ranks: one per lane of a wave.

@@ -40,16 +40,14 @@ constexpr float kNear = 0x1p16f;
 // c * x is unit * x, exact, times c: in two factors where the product of scale
 // and log2(e) overflows (scales above 2.36e38), and of halves where the
 // difference of two logits may overflow though c times it does not come to
-// -infinity (scales below kTiny).
-constexpr float kTiny = 0x1p-64f;
-
+// -infinity (scales below kTinyScale).
 struct Rate {
     float c, unit;
     __device__ explicit Rate(float scale)
         : c(scale * kLog2e), unit(1.0f)
     {
         if (c == kInf) c = 0.5f * scale * kLog2e, unit = 2.0f;
-        if (scale < kTiny) c *= 2.0f, unit = 0.5f;
+        if (scale < kTinyScale) c *= 2.0f, unit = 0.5f;
     }
 };
 
@@ -537,11 +535,18 @@ __device__ __forceinline__ uint64_t part_top(const T *x, uint32_t cols, const Pa
 // ---------------------------------------------------------------------------
 
 // The teacher's distribution over its kept entries: the largest logit and the
-// sum of exp((logit - m) * scale), in every thread.  The difference comes
-// first: scaled logits would each bring a rounding of their own size along.
+// sum of exp((logit - m) * scale), in every thread.
 struct Teacher {
     float m, z;
 };
+
+// (t - m) * scale.  The difference comes first: scaled logits would each bring
+// a rounding of their own size along.  Of halves (by.part) where it may
+// overflow though scale times it does not come to -infinity.
+__device__ __forceinline__ float teacher_distance(float t, float m, const TeacherScale &by)
+{
+    return __builtin_fmaf(t, by.part, -(m * by.part)) * by.whole;
+}
 
 __device__ __forceinline__ bool kept_entry(int64_t id, float scaled, uint32_t cols)
 {
@@ -619,14 +624,15 @@ struct Distill {
         m = block_reduce<Max, kVocabWaves>(m, scratch[0]);
         float z = 0.0f;
         each([&](const Ahead &e) {
-            z += e.teacher == -kInf ? 0.0f : exp_nat((e.teacher - m) * a.scale);
+            z += e.teacher == -kInf ? 0.0f : exp_nat(teacher_distance(e.teacher, m, a.by));
         });
         z = block_reduce<Sum, kVocabWaves>(z, scratch[1]);
         const float log_z = __builtin_logf(z);
         float loss = 0.0f;
         each([&](const Ahead &e) {
             if (e.teacher == -kInf) return;
-            const float d = (e.teacher - m) * a.scale, l = d - log_z, p = exp_nat(d) / z;
+            const float d = teacher_distance(e.teacher, m, a.by);
+            const float l = d - log_z, p = exp_nat(d) / z;
             if (p >= 0x1p-126f || p != p) loss += p * (l - log_prob(e.logit, s, st, a.scale));
         });
         loss = block_reduce<Sum, kVocabWaves>(loss, scratch[2]);
@@ -927,17 +933,20 @@ __global__ void __launch_bounds__(kVocabBlock) ew_logprobs_grad_kernel(LogprobsG
 
 // The teacher's distribution, in one wave.
 __device__ __forceinline__ Teacher wave_teacher(const float *teacher, const int64_t *ids,
-                                                uint32_t kept, uint32_t cols, float scale)
+                                                uint32_t kept, uint32_t cols, float scale,
+                                                const TeacherScale &by)
 {
     Teacher t;
     float m = -kInf;
     for (uint32_t k = threadIdx.x % 64; k < kept; k += 64) {
-        if (kept_entry(ids[k], teacher[k] * scale, cols)) m = __builtin_fmaxf(m, teacher[k]);
+        const float own = teacher[k];
+        if (kept_entry(ids[k], own * scale, cols)) m = __builtin_fmaxf(m, own);
     }
     t.m = wave_reduce<Max>(m);
     float z = 0.0f;
     for (uint32_t k = threadIdx.x % 64; k < kept; k += 64) {
-        if (kept_entry(ids[k], teacher[k] * scale, cols)) z += exp_nat((teacher[k] - t.m) * scale);
+        const float own = teacher[k];
+        if (kept_entry(ids[k], own * scale, cols)) z += exp_nat(teacher_distance(own, t.m, by));
     }
     t.z = wave_reduce<Sum>(z);
     return t;
@@ -971,7 +980,7 @@ __global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGra
         if (threadIdx.x < 64) {
             const float *const teacher = a.teacher + (uint64_t)r * a.kept;
             const int64_t *const ids = a.ids + (uint64_t)r * a.kept;
-            const Teacher t = wave_teacher(teacher, ids, a.kept, a.cols, a.scale);
+            const Teacher t = wave_teacher(teacher, ids, a.kept, a.cols, a.scale, a.by);
             uint32_t n = 0;
             for (uint32_t k0 = 0; k0 < a.kept; k0 += 64) {
                 const uint32_t k = k0 + threadIdx.x;
@@ -983,7 +992,7 @@ __global__ void __launch_bounds__(kVocabBlock) ew_distill_grad_kernel(DistillGra
                 if (here) {
                     const uint32_t slot = n + lanes_below(mask);
                     at[slot] = (uint32_t)id - g.first;
-                    weight[slot] = exp_nat((own - t.m) * a.scale) / t.z;
+                    weight[slot] = exp_nat(teacher_distance(own, t.m, a.by)) / t.z;
                     logit[slot] = (float)x[id];
                 }
                 n += __builtin_popcountll(mask);

@@ -400,6 +400,25 @@ def test_teacher_logits_whose_scaled_values_overflow():
     assert math.isnan(float(loss[2])) and bool(dx[2].isnan().all())
 
 
+@pytest.mark.parametrize("scale", (1e-37, 1e-38, 0.5))
+def test_teacher_logits_farther_apart_than_a_number(scale):
+    """t - m overflows, scale * (t - m) does not: such entries have their
+    weight."""
+    rows, cols, kept = 4, 500, 6
+    scale = float(torch.tensor(scale))
+    g = gen(960)
+    x, ids = randn(g, rows, cols) * 1e37, torch.randint(cols, (rows, kept), generator=g, device=DEV)
+    z = 3e38 * (2 * torch.rand(rows, kept, generator=g, device=DEV) - 1)
+    z[:, 0], z[:, 1] = 3e38, -3e38
+    loss, lse = run_distill("f32", x, z, ids, scale)
+    want, tol, _ = ref.distill(x, z, ids, scale)
+    close(loss, want, tol, "loss")
+    dx, one = torch.empty_like(x), torch.full((rows,), 1e10, device=DEV)
+    ew.ew_distill_grad_f32(x, z, ids, lse, one, dx, scale=scale)
+    want, tol = ref.distill_grad(x, z, ids, lse, one, scale)
+    close_rounded(dx, want, tol, torch.float32, "dlogits")
+
+
 # ---------------------------------------------------------------------------
 # 8-bit norm: the bytes themselves
 # ---------------------------------------------------------------------------
