@@ -580,7 +580,7 @@ ew_status_t ew_distill_bf16(const uint16_t *logits, size_t stride, const float *
 /* Its gradient, from the forward call's lse:
  *   dlogits[c] = round(scale * dloss * (p - sum of t over entries naming c))
  * and 0 where s is -inf (whatever dloss is), in a row without a kept entry
- * and in a row whose mask leaves nothing.  A p below 2^-126 counts as 0.
+ * and in a row whose mask leaves nothing.  A p or t below 2^-126 counts as 0.
  * dlogits may be exactly logits. */
 ew_status_t ew_distill_grad_f32(const float *logits, size_t stride, const float *teacher,
                                 const int64_t *ids, size_t kept, const float *lse,

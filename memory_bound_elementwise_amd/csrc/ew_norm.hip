@@ -166,8 +166,8 @@ constexpr int norm_block(int waves) { return waves < 3 ? 256 : waves * 64; }
 // total = round(x + residual), y = total * rstd * weight in one pass: the row's
 // vectors stay in registers between the sum of squares and the product, and
 // the sum costs one barrier.  Bound by memory: 8192 x 4096 bf16 with residual
-// and total 42.4 us, 6.3 TB/s (a copy of 2^28 floats: 6.64); e4m3, 4096 x 8192
-// bf16 42.3 us, 5.6 TB/s (8-byte stores; the vector unit is busy 72 %).  A
+// and total 42.5 us, 6.3 TB/s (a copy of 2^28 floats: 6.64); e4m3, 4096 x 8192
+// bf16 41-42 us, 5.6-5.8 TB/s (8-byte stores; the vector unit is busy 72 %).  A
 // row whose columns fill no whole vectors is bound by latency: the last
 // vector's elements are loaded one after another while the block waits, and
 // the weight, x and the residual are waited for in turn (1021 x 5003 f32 17.8

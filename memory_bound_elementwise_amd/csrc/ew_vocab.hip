@@ -662,11 +662,11 @@ struct ForwardShared {
 };
 
 // One pass over the logits: each lane keeps a running maximum and sums, joined
-// at the row's end.  4096 x 131072 bf16 with entropy 167-171 us, 6.3-6.4 TB/s
+// at the row's end.  4096 x 131072 bf16 with entropy 162-171 us, 6.3-6.6 TB/s
 // (reading alone in this pattern: 157 us); distillation 2048 x 131072 bf16 85
-// us, 6.3 TB/s; 2048 x 50257 49 us with 5 alternatives, 39 without, the floor
+// us, 6.3 TB/s; 2048 x 50257 49 us with 5 alternatives, 38 without, the floor
 // is 29: the blocks' starts and ends come all at the same time; 20
-// alternatives 73 us, 32 81, 64 120 (read again: part_top); 8 x 131072 f32
+// alternatives 73 us, 32 80, 64 119 (read again: part_top); 8 x 131072 f32
 // with 20 alternatives 8.5 us and 4.7 for the join, latency.
 //
 // Eight waves a SIMD for 16-bit logits: with the 74 registers the compiler
