@@ -127,10 +127,10 @@ __device__ __forceinline__ void absorb_any(RowSum &s, const float (&v)[N], Rate 
 }
 
 // The same in fewer instructions, for logits and an s of ordinary size (or an
-// empty s), no NaN among them and, with entropy, none masked: returns whether the logits were so
-// for this lane (s is of no use otherwise).  16-bit rows are bound by the vector unit: an element costs
-// its widening, half a maximum, an fma, a power, an addition and, with
-// entropy, another fma.
+// empty s), no NaN among them and, with entropy, none masked: returns whether
+// the logits were so for this lane (s is of no use otherwise).  16-bit rows
+// are bound by the vector unit: an element costs its widening, half a maximum,
+// an fma, a power, an addition and, with entropy, another fma.
 template <bool Ent, int N>
 __device__ __forceinline__ bool absorb_plain(RowSum &s, const float (&v)[N], float c)
 {
