@@ -392,9 +392,12 @@ ew_status_t ew_bias_relu_f32(const float *x, const float *bias, float *y,
 /* ------------------------------------------------------------------------ */
 /* Operations that reduce along the rows of a matrix: the RMS norm with the
  * residual's addition (plain and 8-bit output, gradient), log probabilities
- * of given tokens (entropy, top alternatives, gradient) and distillation from
- * a teacher's top logits (gradient).  Each has an f32, an f16 and a bf16
- * form; 16-bit data are raw uint16_t bit patterns.
+ * of given tokens (entropy, top alternatives, gradient), distillation from
+ * a teacher's top logits (gradient), the layer norm (gradient) and a clipped
+ * policy loss (gradient); and the movement of rows to the experts that their
+ * tokens are sent to, and back (gradient).  Each has an f32, an f16 and a bf16
+ * form, but the policy loss, whose log probabilities are binary32, and the
+ * sorting; 16-bit data are raw uint16_t bit patterns.
  *
  * Matrices    rows x cols, row-major, columns contiguous; row r starts
  *             r * stride elements after the pointer (stride in elements, at
@@ -403,10 +406,12 @@ ew_status_t ew_bias_relu_f32(const float *x, const float *bias, float *y,
  *             boundaries are fastest.  Vectors and per-row outputs are
  *             contiguous.
  * Sizes       rows and cols below 2^31; offsets are 64-bit.  rows == 0
- *             returns EW_OK without a launch (the gradient of the norm
- *             still clears dweight).  cols == 0 returns EW_OK without a
- *             launch for the norm; a row of logits without columns is a row
- *             whose mask leaves nothing.
+ *             returns EW_OK without a launch (the gradients of the norms
+ *             still clear dweight and dbias, the policy loss and the sorting
+ *             write their results).  cols == 0 returns EW_OK without a
+ *             launch for the norms and the movement of rows; a row of logits
+ *             or of log probabilities without columns is a row whose mask
+ *             leaves nothing.
  * Optional    A pointer documented as optional may be NULL.
  * Workspace   Device memory of the caller's, 16-byte aligned, of at least the
  *             bytes the _workspace function gives (EW_ERR_INVALID_ARG if
@@ -594,6 +599,208 @@ ew_status_t ew_distill_grad_bf16(const uint16_t *logits, size_t stride, const fl
                                  const int64_t *ids, size_t kept, const float *lse,
                                  const float *dloss, uint16_t *dlogits, size_t dlogits_stride,
                                  float scale, size_t rows, size_t cols, hipStream_t stream);
+
+/* Layer norm, row by row, with n = cols:
+ *   total = round(x + residual), mean = sum(total) / n,
+ *   rstd = 1 / sqrt(sum((total - mean)^2) / n + eps),
+ *   y = round((total - mean) * rstd * weight + bias).
+ * The mean is summed in binary64, so that rows far from 0 keep their
+ * differences: a row of equal values has y = bias exactly (for eps > 0).
+ * weight, bias  each optional: 1 and 0 where absent
+ * residual      optional: without it total is x itself
+ * total         optional, requires residual: the rounded sum
+ * mean, rstd    optional, rows values each: what the gradient needs
+ * eps           >= 0 and finite
+ * total may be exactly x or residual; y may be exactly x or residual unless
+ * total is that one. */
+ew_status_t ew_layernorm_f32(const float *x, size_t x_stride, const float *weight,
+                             const float *bias, const float *residual, size_t residual_stride,
+                             float *y, size_t y_stride, float *total, size_t total_stride,
+                             float *mean, float *rstd, size_t rows, size_t cols, float eps,
+                             hipStream_t stream);
+ew_status_t ew_layernorm_f16(const uint16_t *x, size_t x_stride, const uint16_t *weight,
+                             const uint16_t *bias, const uint16_t *residual, size_t residual_stride,
+                             uint16_t *y, size_t y_stride, uint16_t *total, size_t total_stride,
+                             float *mean, float *rstd, size_t rows, size_t cols, float eps,
+                             hipStream_t stream);
+ew_status_t ew_layernorm_bf16(const uint16_t *x, size_t x_stride, const uint16_t *weight,
+                              const uint16_t *bias, const uint16_t *residual,
+                              size_t residual_stride, uint16_t *y, size_t y_stride, uint16_t *total,
+                              size_t total_stride, float *mean, float *rstd, size_t rows,
+                              size_t cols, float eps, hipStream_t stream);
+
+/* The layer norm's gradient.  x is the normed matrix (the forward call's
+ * total), mean and rstd its statistics, dy the gradient of y and dtotal
+ * (optional) that of total; with h = (x - mean) * rstd and g = dy * weight
+ * (weight optional), per row
+ *   dx = round(rstd * (g - sum(g) / n - h * sum(g * h) / n) + dtotal)
+ * (the gradient of the forward call's x and of its residual alike), and
+ *   dweight[c] = sum over rows of dy * h, dbias[c] = sum over rows of dy,
+ * in binary32, each optional.  dx may be exactly dy, x or dtotal.  The
+ * workspace is needed for dweight and dbias only (without both it may be
+ * NULL). */
+size_t ew_layernorm_grad_workspace(size_t rows, size_t cols);
+ew_status_t ew_layernorm_grad_f32(const float *dy, size_t dy_stride, const float *x,
+                                  size_t x_stride, const float *weight, const float *mean,
+                                  const float *rstd, const float *dtotal, size_t dtotal_stride,
+                                  float *dx, size_t dx_stride, float *dweight, float *dbias,
+                                  void *workspace, size_t workspace_bytes, size_t rows, size_t cols,
+                                  hipStream_t stream);
+ew_status_t ew_layernorm_grad_f16(const uint16_t *dy, size_t dy_stride, const uint16_t *x,
+                                  size_t x_stride, const uint16_t *weight, const float *mean,
+                                  const float *rstd, const uint16_t *dtotal, size_t dtotal_stride,
+                                  uint16_t *dx, size_t dx_stride, float *dweight, float *dbias,
+                                  void *workspace, size_t workspace_bytes, size_t rows, size_t cols,
+                                  hipStream_t stream);
+ew_status_t ew_layernorm_grad_bf16(const uint16_t *dy, size_t dy_stride, const uint16_t *x,
+                                   size_t x_stride, const uint16_t *weight, const float *mean,
+                                   const float *rstd, const uint16_t *dtotal, size_t dtotal_stride,
+                                   uint16_t *dx, size_t dx_stride, float *dweight, float *dbias,
+                                   void *workspace, size_t workspace_bytes, size_t rows,
+                                   size_t cols, hipStream_t stream);
+
+/* How the policy loss weighs its tokens: by the number of counted tokens of
+ * the batch; by that of each sequence, and the number of sequences that have
+ * any; or not at all. */
+typedef enum ew_mean {
+    EW_MEAN_TOKENS = 0,
+    EW_MEAN_SEQUENCES = 1,
+    EW_MEAN_NONE = 2
+} ew_mean_t;
+
+/* Clipped policy loss with a KL term, over the tokens of `rows` sequences of
+ * at most `cols`.  Of a counted token, with x = logp - old_logp, r = exp(x),
+ * a its advantage and d = ref_logp - logp,
+ *   gain = min(r * a, clip(r, 1 - clip_low, 1 + clip_high) * a)
+ *   k    = exp(d) - d - 1       (0 without ref_logp)
+ * and, w being the weight of its sequence's tokens (scale / number of counted
+ * tokens of the batch, scale / (number of counted tokens of the sequence *
+ * number of sequences that have any), or scale),
+ *   loss = sum w * (kl * k - gain).
+ * Which side of a border r lies on is decided exactly (x against the border's
+ * logarithm, in binary64); sums are binary64.  A batch or sequence whose mask
+ * leaves nothing adds nothing, whatever lies in its masked places: its weights
+ * are 0, and a loss of no tokens is 0.
+ * ref_logp    optional; kl weighs its term, which is left out where kl is 0
+ * advantage   a matrix, or with advantage_stride 0 one value a sequence
+ * mask        optional, rows x cols bytes with a stride of its own: tokens
+ *             whose byte is not 0 count; without it all do
+ * loss        one value
+ * stats       optional, four values: -sum w * gain, sum w * k, the fraction
+ *             of counted tokens whose gain is the clipped one, and the mean of
+ *             old_logp - logp over counted tokens
+ * weights     optional, rows values: w (0 for a sequence of no counted
+ *             tokens), which the gradient needs
+ * clip_low, clip_high   >= 0, infinity for no clip on that side
+ * kl          >= 0 and finite; scale finite
+ * mean        an ew_mean_t */
+size_t ew_policy_loss_workspace(size_t rows, size_t cols);
+ew_status_t ew_policy_loss_f32(const float *logp, size_t logp_stride, const float *old_logp,
+                               size_t old_stride, const float *ref_logp, size_t ref_stride,
+                               const float *advantage, size_t advantage_stride,
+                               const uint8_t *mask, size_t mask_stride, float *loss, float *stats,
+                               float *weights, float clip_low, float clip_high, float kl,
+                               float scale, int mean, void *workspace,
+                               size_t workspace_bytes, size_t rows, size_t cols,
+                               hipStream_t stream);
+
+/* Its gradient by logp, from the forward call's weights:
+ *   dlogp = dloss * w * (-(clipped ? 0 : r * a) - kl * (exp(d) - 1))
+ * for counted tokens, 0 for the others.  dloss is one value on the device
+ * (optional: 1).  dlogp may be exactly one of the matrices it is computed
+ * from. */
+ew_status_t ew_policy_loss_grad_f32(const float *logp, size_t logp_stride, const float *old_logp,
+                                    size_t old_stride, const float *ref_logp, size_t ref_stride,
+                                    const float *advantage, size_t advantage_stride,
+                                    const uint8_t *mask, size_t mask_stride,
+                                    const float *weights, const float *dloss, float *dlogp,
+                                    size_t dlogp_stride, float clip_low, float clip_high,
+                                    float kl, size_t rows, size_t cols, hipStream_t stream);
+
+/* Sorting of entries (a token's choices of experts, in the tokens' order) by
+ * expert: entries of expert e get consecutive rows from offsets[e] on, in
+ * their own order; offsets[e] is a multiple of align.  An entry whose id is
+ * outside [0, experts) is dropped.
+ * slot        entries values: the row of each entry, -1 for a dropped one
+ * offsets     experts + 1 values: each expert's first row, and the end of the
+ *             last expert's rows
+ * counts      optional, experts values: entries of each expert (the rows from
+ *             offsets[e] + counts[e] to offsets[e + 1] are padding)
+ * source      optional, ew_experts_rows() values: the entry of each row, -1
+ *             for a row without one
+ * experts and align in [1, 1024], ew_experts_rows() < 2^31 (it is the rows
+ * that any ids of these sizes fit in: entries + min(entries, experts) *
+ * (align - 1), rounded up to a multiple of align; SIZE_MAX for sizes no call
+ * accepts). */
+size_t ew_experts_rows(size_t entries, size_t experts, size_t align);
+size_t ew_experts_sort_workspace(size_t entries, size_t experts);
+ew_status_t ew_experts_sort(const int64_t *ids, size_t entries, size_t experts, size_t align,
+                            int32_t *slot, int32_t *offsets, int32_t *counts, int32_t *source,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Rows of x to the places of their entries: out[slot[t * top + j]] = x[t] for
+ * t < rows, j < top.  Entries whose slot is outside [0, out_rows) are dropped;
+ * the others' slots differ.  With offsets and counts (both or neither) the
+ * padding rows of each of `experts` experts become 0; all other rows of out
+ * stay as they are.  top in [1, 64].  The gradient of x is
+ * ew_experts_combine_* of that of out, without weights. */
+ew_status_t ew_experts_gather_f32(const float *x, size_t x_stride, const int32_t *slot, size_t top,
+                                  const int32_t *offsets, const int32_t *counts, size_t experts,
+                                  float *out, size_t out_stride, size_t out_rows, size_t rows,
+                                  size_t cols, hipStream_t stream);
+ew_status_t ew_experts_gather_f16(const uint16_t *x, size_t x_stride, const int32_t *slot,
+                                  size_t top, const int32_t *offsets, const int32_t *counts,
+                                  size_t experts, uint16_t *out, size_t out_stride, size_t out_rows,
+                                  size_t rows, size_t cols, hipStream_t stream);
+ew_status_t ew_experts_gather_bf16(const uint16_t *x, size_t x_stride, const int32_t *slot,
+                                   size_t top, const int32_t *offsets, const int32_t *counts,
+                                   size_t experts, uint16_t *out, size_t out_stride,
+                                   size_t out_rows, size_t rows, size_t cols, hipStream_t stream);
+
+/* Rows of z back to their tokens, weighed:
+ *   y[t] = round(residual[t] + sum over j of weights[t * top + j] *
+ *                z[slot[t * top + j]])
+ * in the order of j, without the entries whose slot is outside [0, z_rows).
+ * weights (rows x top values) are 1 where absent, residual is 0.  y may be
+ * exactly residual. */
+ew_status_t ew_experts_combine_f32(const float *z, size_t z_stride, size_t z_rows,
+                                   const int32_t *slot, size_t top, const float *weights,
+                                   const float *residual, size_t residual_stride, float *y,
+                                   size_t y_stride, size_t rows, size_t cols, hipStream_t stream);
+ew_status_t ew_experts_combine_f16(const uint16_t *z, size_t z_stride, size_t z_rows,
+                                   const int32_t *slot, size_t top, const float *weights,
+                                   const uint16_t *residual, size_t residual_stride, uint16_t *y,
+                                   size_t y_stride, size_t rows, size_t cols, hipStream_t stream);
+ew_status_t ew_experts_combine_bf16(const uint16_t *z, size_t z_stride, size_t z_rows,
+                                    const int32_t *slot, size_t top, const float *weights,
+                                    const uint16_t *residual, size_t residual_stride, uint16_t *y,
+                                    size_t y_stride, size_t rows, size_t cols, hipStream_t stream);
+
+/* The gradient of that by z and the weights, from the gradient dy of y (which
+ * is that of residual too):
+ *   dz[slot[t * top + j]] = round(weights[t * top + j] * dy[t])
+ *   dweights[t * top + j] = sum over columns of dy[t] * z[slot[t * top + j]]
+ * (0 where the entry is dropped).  The kept entries' slots differ.  Padding
+ * rows and other rows of dz (z_rows, as z) are treated as ew_experts_gather_*
+ * treats out's.  dz may be exactly z. */
+ew_status_t ew_experts_combine_grad_f32(const float *dy, size_t dy_stride, const float *z,
+                                        size_t z_stride, size_t z_rows, const int32_t *slot,
+                                        size_t top, const float *weights, const int32_t *offsets,
+                                        const int32_t *counts, size_t experts, float *dz,
+                                        size_t dz_stride, float *dweights, size_t rows, size_t cols,
+                                        hipStream_t stream);
+ew_status_t ew_experts_combine_grad_f16(const uint16_t *dy, size_t dy_stride, const uint16_t *z,
+                                        size_t z_stride, size_t z_rows, const int32_t *slot,
+                                        size_t top, const float *weights, const int32_t *offsets,
+                                        const int32_t *counts, size_t experts, uint16_t *dz,
+                                        size_t dz_stride, float *dweights, size_t rows, size_t cols,
+                                        hipStream_t stream);
+ew_status_t ew_experts_combine_grad_bf16(const uint16_t *dy, size_t dy_stride, const uint16_t *z,
+                                         size_t z_stride, size_t z_rows, const int32_t *slot,
+                                         size_t top, const float *weights, const int32_t *offsets,
+                                         const int32_t *counts, size_t experts, uint16_t *dz,
+                                         size_t dz_stride, float *dweights, size_t rows,
+                                         size_t cols, hipStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Status, launch configuration and planning                                */

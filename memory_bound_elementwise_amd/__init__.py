@@ -41,6 +41,13 @@ __all__ = [
     "ew_logprobs_grad_f32", "ew_logprobs_grad_f16", "ew_logprobs_grad_bf16",
     "ew_logprobs_workspace", "ew_distill_f32", "ew_distill_f16", "ew_distill_bf16",
     "ew_distill_grad_f32", "ew_distill_grad_f16", "ew_distill_grad_bf16", "ew_distill_workspace",
+    "ew_layernorm_f32", "ew_layernorm_f16", "ew_layernorm_bf16", "ew_layernorm_grad_f32",
+    "ew_layernorm_grad_f16", "ew_layernorm_grad_bf16", "ew_layernorm_grad_workspace",
+    "ew_policy_loss_f32", "ew_policy_loss_grad_f32", "ew_policy_loss_workspace", "MEANS",
+    "ew_experts_sort", "ew_experts_rows", "ew_experts_sort_workspace", "ew_experts_gather_f32",
+    "ew_experts_gather_f16", "ew_experts_gather_bf16", "ew_experts_combine_f32",
+    "ew_experts_combine_f16", "ew_experts_combine_bf16", "ew_experts_combine_grad_f32",
+    "ew_experts_combine_grad_f16", "ew_experts_combine_grad_bf16",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -188,6 +195,33 @@ _c = {
     **{f"ew_distill_grad_{d}": _proto(f"ew_distill_grad_{d}", _int, _vp, _sz, _vp, _vp, _sz, _vp,
                                       _vp, _vp, _sz, ctypes.c_float, _sz, _sz, _vp)
        for d in MAP_DTYPES},
+    **{f"ew_layernorm_{d}": _proto(f"ew_layernorm_{d}", _int, _vp, _sz, _vp, _vp, _vp, _sz, _vp,
+                                   _sz, _vp, _sz, _vp, _vp, _sz, _sz, ctypes.c_float, _vp)
+       for d in MAP_DTYPES},
+    **{f"ew_layernorm_grad_{d}": _proto(f"ew_layernorm_grad_{d}", _int, _vp, _sz, _vp, _sz, _vp,
+                                        _vp, _vp, _vp, _sz, _vp, _sz, _vp, _vp, _vp, _sz, _sz,
+                                        _sz, _vp) for d in MAP_DTYPES},
+    **{f"ew_experts_gather_{d}": _proto(f"ew_experts_gather_{d}", _int, _vp, _sz, _vp, _sz, _vp,
+                                        _vp, _sz, _vp, _sz, _sz, _sz, _sz, _vp)
+       for d in MAP_DTYPES},
+    **{f"ew_experts_combine_{d}": _proto(f"ew_experts_combine_{d}", _int, _vp, _sz, _sz, _vp, _sz,
+                                         _vp, _vp, _sz, _vp, _sz, _sz, _sz, _vp)
+       for d in MAP_DTYPES},
+    **{f"ew_experts_combine_grad_{d}": _proto(f"ew_experts_combine_grad_{d}", _int, _vp, _sz, _vp,
+                                              _sz, _sz, _vp, _sz, _vp, _vp, _vp, _sz, _vp, _sz,
+                                              _vp, _sz, _sz, _vp) for d in MAP_DTYPES},
+    "ew_policy_loss_f32": _proto("ew_policy_loss_f32", _int, _vp, _sz, _vp, _sz, _vp, _sz, _vp,
+                                 _sz, _vp, _sz, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float,
+                                 ctypes.c_float, ctypes.c_float, _int, _vp, _sz, _sz, _sz, _vp),
+    "ew_policy_loss_grad_f32": _proto("ew_policy_loss_grad_f32", _int, _vp, _sz, _vp, _sz, _vp,
+                                      _sz, _vp, _sz, _vp, _sz, _vp, _vp, _vp, _sz, ctypes.c_float,
+                                      ctypes.c_float, ctypes.c_float, _sz, _sz, _vp),
+    "ew_experts_sort": _proto("ew_experts_sort", _int, _vp, _sz, _sz, _sz, _vp, _vp, _vp, _vp, _vp,
+                              _sz, _vp),
+    "ew_experts_rows": _proto("ew_experts_rows", _sz, _sz, _sz, _sz),
+    "ew_experts_sort_workspace": _proto("ew_experts_sort_workspace", _sz, _sz, _sz),
+    "ew_layernorm_grad_workspace": _proto("ew_layernorm_grad_workspace", _sz, _sz, _sz),
+    "ew_policy_loss_workspace": _proto("ew_policy_loss_workspace", _sz, _sz, _sz),
     "ew_rmsnorm_grad_workspace": _proto("ew_rmsnorm_grad_workspace", _sz, _sz, _sz),
     "ew_logprobs_workspace": _proto("ew_logprobs_workspace", _sz, _sz, _sz, _sz),
     "ew_distill_workspace": _proto("ew_distill_workspace", _sz, _sz, _sz),
@@ -969,6 +1003,357 @@ def ew_distill_grad_bf16(logits, teacher, ids, lse, dloss, dlogits, scale=1.0, r
     """ew_distill_grad_f32 on bfloat16 logits."""
     _distill_grad("ew_distill_grad_bf16", 2, logits, teacher, ids, lse, dloss, dlogits, scale,
                   rows, cols, kept, stream)
+
+
+def _layernorm(name, es, x, weight, bias, y, residual, total, mean, rstd, eps, rows, cols, stream):
+    rows, cols = _shape(x, rows, cols, "x")
+    px, sx = _mat(x, es, rows, cols, "x")
+    pr, sr = _mat(residual, es, rows, cols, "residual")
+    py, sy = _mat(y, es, rows, cols, "y")
+    pt, st = _mat(total, es, rows, cols, "total")
+    _check(_c[name](px, sx, _buf(weight, es, cols, "weight"), _buf(bias, es, cols, "bias"), pr, sr,
+                    py, sy, pt, st, _buf(mean, 4, rows, "mean"), _buf(rstd, 4, rows, "rstd"), rows,
+                    cols, eps, _stream(y, stream)), name)
+
+
+def ew_layernorm_f32(x, weight, bias, y, residual=None, total=None, mean=None, rstd=None, eps=1e-5,
+                     rows=None, cols=None, stream=None):
+    """total = x + residual, y = (total - mean) / sqrt(variance + eps) * weight + bias, row by
+    row (binary32, the mean summed in binary64); mean and rstd receive the
+    row's mean and 1 / sqrt(variance + eps).  weight and bias may be None (1
+    and 0).  Without a residual the norm is x's.  total may be x or residual,
+    y whichever of them total is not."""
+    _layernorm("ew_layernorm_f32", 4, x, weight, bias, y, residual, total, mean, rstd, eps, rows,
+               cols, stream)
+
+
+def ew_layernorm_f16(x, weight, bias, y, residual=None, total=None, mean=None, rstd=None, eps=1e-5,
+                     rows=None, cols=None, stream=None):
+    """ew_layernorm_f32 on binary16 data: total and y rounded once each."""
+    _layernorm("ew_layernorm_f16", 2, x, weight, bias, y, residual, total, mean, rstd, eps, rows,
+               cols, stream)
+
+
+def ew_layernorm_bf16(x, weight, bias, y, residual=None, total=None, mean=None, rstd=None,
+                      eps=1e-5, rows=None, cols=None, stream=None):
+    """ew_layernorm_f32 on bfloat16 data: total and y rounded once each."""
+    _layernorm("ew_layernorm_bf16", 2, x, weight, bias, y, residual, total, mean, rstd, eps, rows,
+               cols, stream)
+
+
+def ew_layernorm_grad_workspace(rows, cols):
+    """Bytes of workspace ew_layernorm_grad_* needs for dweight and dbias."""
+    return _c["ew_layernorm_grad_workspace"](int(rows), int(cols))
+
+
+def _layernorm_grad(name, es, dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, dtotal,
+                    rows, cols, stream):
+    rows, cols = _shape(dy, rows, cols, "dy")
+    pdy, sdy = _mat(dy, es, rows, cols, "dy")
+    px, sx = _mat(x, es, rows, cols, "x")
+    pdt, sdt = _mat(dtotal, es, rows, cols, "dtotal")
+    pdx, sdx = _mat(dx, es, rows, cols, "dx")
+    need = 0
+    if dweight is not None or dbias is not None:
+        need = _c["ew_layernorm_grad_workspace"](rows, cols)
+    ws, size = _space(workspace, need)
+    _check(_c[name](pdy, sdy, px, sx, _buf(weight, es, cols, "weight"),
+                    _buf(mean, 4, rows, "mean"), _buf(rstd, 4, rows, "rstd"), pdt, sdt, pdx, sdx,
+                    _buf(dweight, 4, cols, "dweight"), _buf(dbias, 4, cols, "dbias"), ws, size,
+                    rows, cols, _stream(dx, stream)), name)
+
+
+def ew_layernorm_grad_f32(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, workspace=None,
+                          dtotal=None, rows=None, cols=None, stream=None):
+    """Gradient of the layer norm: x is the normed matrix (the forward call's
+    total); with h = (x - mean) * rstd and g = dy * weight,
+    dx = rstd * (g - mean(g) - h * mean(g * h)) + dtotal, dweight and dbias
+    are the sums over rows of dy * h and of dy (binary32).  weight may be None
+    (1); dx may be dy, x or dtotal."""
+    _layernorm_grad("ew_layernorm_grad_f32", 4, dy, x, weight, mean, rstd, dx, dweight, dbias,
+                    workspace, dtotal, rows, cols, stream)
+
+
+def ew_layernorm_grad_f16(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, workspace=None,
+                          dtotal=None, rows=None, cols=None, stream=None):
+    """ew_layernorm_grad_f32 on binary16 data (dweight and dbias in binary32)."""
+    _layernorm_grad("ew_layernorm_grad_f16", 2, dy, x, weight, mean, rstd, dx, dweight, dbias,
+                    workspace, dtotal, rows, cols, stream)
+
+
+def ew_layernorm_grad_bf16(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, workspace=None,
+                           dtotal=None, rows=None, cols=None, stream=None):
+    """ew_layernorm_grad_f32 on bfloat16 data (dweight and dbias in binary32)."""
+    _layernorm_grad("ew_layernorm_grad_bf16", 2, dy, x, weight, mean, rstd, dx, dweight, dbias,
+                    workspace, dtotal, rows, cols, stream)
+
+
+# ew_mean_t: how the policy loss weighs its tokens
+MEANS = {"tokens": 0, "sequences": 1, "none": 2}
+
+
+def _advantage(x, rows, cols, per_token):
+    """(address, row stride) of advantages: a value a token (a matrix), or a
+    value a sequence (stride 0)."""
+    if per_token is None:
+        if isinstance(x, int):
+            raise ValueError("per_token is required when advantage is a raw pointer")
+        per_token = x.numel() == rows * cols and (x.dim() != 1 or rows == 1)
+    if per_token:
+        return _mat(x, 4, rows, cols, "advantage")
+    if not isinstance(x, int) and x.numel() != rows:
+        raise ValueError(f"advantage: shape {tuple(x.shape)}, the call covers {rows} sequences of "
+                         f"{cols} tokens")
+    return _buf(x, 4, rows, "advantage"), 0
+
+
+def ew_policy_loss_workspace(rows, cols):
+    """Bytes of workspace ew_policy_loss_f32 needs."""
+    return _c["ew_policy_loss_workspace"](int(rows), int(cols))
+
+
+def ew_policy_loss_f32(logp, old_logp, advantage, loss, weights=None, ref_logp=None, mask=None,
+                       stats=None, clip_low=0.2, clip_high=0.2, kl=0.0, mean="tokens", scale=1.0,
+                       workspace=None, rows=None, cols=None, per_token=None, stream=None):
+    """Clipped policy loss over rows sequences of up to cols tokens: the mean
+    over "tokens" or "sequences" (or, with "none", the sum) of
+    -min(r * a, clip(r, 1 - clip_low, 1 + clip_high) * a) + kl * (exp(d) - d - 1),
+    r = exp(logp - old_logp), d = ref_logp - logp, times scale.  advantage
+    holds a value a token or a value a sequence; tokens whose mask (bool or
+    uint8) is 0 do not count.  weights (a value a sequence) is what the
+    gradient needs; stats receives the policy term, the mean of
+    exp(d) - d - 1, the fraction of tokens clipped and the mean of
+    old_logp - logp."""
+    rows, cols = _shape(logp, rows, cols, "logp")
+    if mean not in MEANS:
+        raise ValueError(f"mean: {mean!r}, not one of {', '.join(MEANS)}")
+    pl, sl = _mat(logp, 4, rows, cols, "logp")
+    po, so = _mat(old_logp, 4, rows, cols, "old_logp")
+    pr, sr = _mat(ref_logp, 4, rows, cols, "ref_logp")
+    pa, sa = _advantage(advantage, rows, cols, per_token)
+    pm, sm = _mat(mask, 1, rows, cols, "mask")
+    ws, size = _space(workspace, _c["ew_policy_loss_workspace"](rows, cols))
+    _check(_c["ew_policy_loss_f32"](pl, sl, po, so, pr, sr, pa, sa, pm, sm,
+                                    _buf(loss, 4, 1, "loss"), _buf(stats, 4, 4, "stats"),
+                                    _buf(weights, 4, rows, "weights"), clip_low, clip_high, kl,
+                                    scale, MEANS[mean], ws, size, rows, cols,
+                                    _stream(loss, stream)), "ew_policy_loss_f32")
+
+
+def ew_policy_loss_grad_f32(logp, old_logp, advantage, weights, dlogp, ref_logp=None, mask=None,
+                            dloss=None, clip_low=0.2, clip_high=0.2, kl=0.0, rows=None, cols=None,
+                            per_token=None, stream=None):
+    """Gradient of the policy loss by logp, from the forward call's weights
+    and the gradient dloss of the loss (one value on the device, None for 1);
+    0 for tokens that do not count.  dlogp may be logp, old_logp, ref_logp or
+    a matrix of advantages."""
+    rows, cols = _shape(logp, rows, cols, "logp")
+    pl, sl = _mat(logp, 4, rows, cols, "logp")
+    po, so = _mat(old_logp, 4, rows, cols, "old_logp")
+    pr, sr = _mat(ref_logp, 4, rows, cols, "ref_logp")
+    pa, sa = _advantage(advantage, rows, cols, per_token)
+    pm, sm = _mat(mask, 1, rows, cols, "mask")
+    pd, sd = _mat(dlogp, 4, rows, cols, "dlogp")
+    _check(_c["ew_policy_loss_grad_f32"](pl, sl, po, so, pr, sr, pa, sa, pm, sm,
+                                         _buf(weights, 4, rows, "weights"),
+                                         _buf(dloss, 4, 1, "dloss"), pd, sd, clip_low, clip_high,
+                                         kl, rows, cols, _stream(dlogp, stream)),
+           "ew_policy_loss_grad_f32")
+
+
+def _ids32(x, n, role):
+    """Address of n 32-bit row numbers."""
+    if x is not None and not isinstance(x, int) and x.dtype is not torch.int32:
+        raise TypeError(f"{role}: {x.dtype}, the operation takes int32 rows")
+    return _buf(x, 4, n, role)
+
+
+def ew_experts_rows(entries, experts, align=1):
+    """Rows that any sorting of so many entries fits in."""
+    entries, experts, align = int(entries), int(experts), int(align)
+    if min(entries, experts, align) < 0:
+        raise ValueError(f"entries {entries}, experts {experts}, align {align}")
+    rows = _c["ew_experts_rows"](entries, experts, align)
+    if rows >= 1 << 31:
+        raise ValueError(f"entries {entries}, experts {experts}, align {align}: no call accepts "
+                         "these sizes")
+    return rows
+
+
+def ew_experts_sort_workspace(entries, experts):
+    """Bytes of workspace ew_experts_sort needs."""
+    return _c["ew_experts_sort_workspace"](int(entries), int(experts))
+
+
+def ew_experts_sort(ids, experts, slot, offsets, counts=None, source=None, align=1, workspace=None,
+                    entries=None, stream=None):
+    """Sort entries (ids: int64 experts of tokens x choices) by expert, in
+    their order within each: slot receives the row of each entry (-1 where its
+    id is outside [0, experts)), offsets (experts + 1 values) each expert's
+    first row, a multiple of align, and the end; counts the entries of each
+    expert; source (ew_experts_rows() values) the entry of each row, or -1.
+    All but ids are int32."""
+    n = _numel(ids, entries)
+    experts, align = int(experts), int(align)
+    rows = ew_experts_rows(n, experts, align)
+    ws, size = _space(workspace, _c["ew_experts_sort_workspace"](n, experts))
+    _check(_c["ew_experts_sort"](_ids64(ids, n, "ids"), n, experts, align,
+                                 _ids32(slot, n, "slot"), _ids32(offsets, experts + 1, "offsets"),
+                                 _ids32(counts, experts, "counts"),
+                                 _ids32(source, rows, "source"), ws, size,
+                                 _stream(offsets, stream)), "ew_experts_sort")
+
+
+def _choices(slot, rows, top):
+    """Choices a token, from slot's last dimension."""
+    if top is None:
+        if isinstance(slot, int):
+            raise ValueError("top is required when slot is a raw pointer")
+        if not slot.dim():
+            raise ValueError("slot: a scalar has no rows")
+        top = slot.shape[-1] if slot.dim() > 1 else 1
+    top = int(top)
+    if not isinstance(slot, int) and slot.numel() != rows * top:
+        raise ValueError(f"slot: shape {tuple(slot.shape)}, the call covers {rows} rows of {top}")
+    return top
+
+
+def _places(x, rows, cols, role):
+    """Rows of the matrix that slots name."""
+    if rows is not None:
+        return int(rows)
+    if isinstance(x, int):
+        raise ValueError(f"{role} is required when buffers are raw pointers")
+    return x.numel() // cols if cols else 0
+
+
+def _padding(offsets, counts, experts):
+    """Number of experts whose padding rows the call clears."""
+    if (offsets is None) != (counts is None):
+        raise ValueError("offsets and counts: both or neither")
+    if experts is None:
+        if isinstance(counts, int):
+            raise ValueError("experts is required when counts is a raw pointer")
+        experts = counts.numel() if counts is not None else 0
+    return int(experts)
+
+
+def _experts_gather(name, es, x, slot, out, offsets, counts, rows, cols, top, out_rows, experts,
+                    stream):
+    rows, cols = _shape(x, rows, cols, "x")
+    top = _choices(slot, rows, top)
+    experts = _padding(offsets, counts, experts)
+    px, sx = _mat(x, es, rows, cols, "x")
+    out_rows = _places(out, out_rows, cols, "out_rows")
+    po, so = _mat(out, es, out_rows, cols, "out")
+    _check(_c[name](px, sx, _ids32(slot, rows * top, "slot"), top,
+                    _ids32(offsets, experts + 1, "offsets"), _ids32(counts, experts, "counts"),
+                    experts, po, so, out_rows, rows, cols, _stream(out, stream)), name)
+
+
+def ew_experts_gather_f32(x, slot, out, offsets=None, counts=None, rows=None, cols=None, top=None,
+                          out_rows=None, experts=None, stream=None):
+    """out[slot[t, j]] = x[t] for every token t and choice j whose slot names a
+    row of out; with offsets and counts the experts' padding rows become 0.
+    Other rows of out stay.  x's gradient is ew_experts_combine_f32 of out's,
+    without weights."""
+    _experts_gather("ew_experts_gather_f32", 4, x, slot, out, offsets, counts, rows, cols, top,
+                    out_rows, experts, stream)
+
+
+def ew_experts_gather_f16(x, slot, out, offsets=None, counts=None, rows=None, cols=None, top=None,
+                          out_rows=None, experts=None, stream=None):
+    """ew_experts_gather_f32 on binary16 data."""
+    _experts_gather("ew_experts_gather_f16", 2, x, slot, out, offsets, counts, rows, cols, top,
+                    out_rows, experts, stream)
+
+
+def ew_experts_gather_bf16(x, slot, out, offsets=None, counts=None, rows=None, cols=None, top=None,
+                           out_rows=None, experts=None, stream=None):
+    """ew_experts_gather_f32 on bfloat16 data."""
+    _experts_gather("ew_experts_gather_bf16", 2, x, slot, out, offsets, counts, rows, cols, top,
+                    out_rows, experts, stream)
+
+
+def _experts_combine(name, es, z, slot, y, weights, residual, rows, cols, top, z_rows, stream):
+    rows, cols = _shape(y, rows, cols, "y")
+    top = _choices(slot, rows, top)
+    _table(weights, rows, top, "weights")
+    z_rows = _places(z, z_rows, cols, "z_rows")
+    pz, sz = _mat(z, es, z_rows, cols, "z")
+    pr, sr = _mat(residual, es, rows, cols, "residual")
+    py, sy = _mat(y, es, rows, cols, "y")
+    _check(_c[name](pz, sz, z_rows, _ids32(slot, rows * top, "slot"), top,
+                    _buf(weights, 4, rows * top, "weights"), pr, sr, py, sy, rows, cols,
+                    _stream(y, stream)), name)
+
+
+def ew_experts_combine_f32(z, slot, y, weights=None, residual=None, rows=None, cols=None, top=None,
+                           z_rows=None, stream=None):
+    """y[t] = residual[t] + sum over j of weights[t, j] * z[slot[t, j]], without
+    the choices whose slot names no row of z (weights None: 1, residual None:
+    0).  y may be residual."""
+    _experts_combine("ew_experts_combine_f32", 4, z, slot, y, weights, residual, rows, cols, top,
+                     z_rows, stream)
+
+
+def ew_experts_combine_f16(z, slot, y, weights=None, residual=None, rows=None, cols=None, top=None,
+                           z_rows=None, stream=None):
+    """ew_experts_combine_f32 on binary16 data: summed in binary32, rounded once."""
+    _experts_combine("ew_experts_combine_f16", 2, z, slot, y, weights, residual, rows, cols, top,
+                     z_rows, stream)
+
+
+def ew_experts_combine_bf16(z, slot, y, weights=None, residual=None, rows=None, cols=None,
+                            top=None, z_rows=None, stream=None):
+    """ew_experts_combine_f32 on bfloat16 data: summed in binary32, rounded once."""
+    _experts_combine("ew_experts_combine_bf16", 2, z, slot, y, weights, residual, rows, cols, top,
+                     z_rows, stream)
+
+
+def _experts_combine_grad(name, es, dy, z, slot, weights, dz, dweights, offsets, counts, rows,
+                          cols, top, z_rows, experts, stream):
+    rows, cols = _shape(dy, rows, cols, "dy")
+    top = _choices(slot, rows, top)
+    experts = _padding(offsets, counts, experts)
+    _table(weights, rows, top, "weights")
+    _table(dweights, rows, top, "dweights")
+    pdy, sdy = _mat(dy, es, rows, cols, "dy")
+    z_rows = _places(z, z_rows, cols, "z_rows")
+    pz, sz = _mat(z, es, z_rows, cols, "z")
+    pdz, sdz = _mat(dz, es, z_rows, cols, "dz")
+    _check(_c[name](pdy, sdy, pz, sz, z_rows, _ids32(slot, rows * top, "slot"), top,
+                    _buf(weights, 4, rows * top, "weights"),
+                    _ids32(offsets, experts + 1, "offsets"), _ids32(counts, experts, "counts"),
+                    experts, pdz, sdz, _buf(dweights, 4, rows * top, "dweights"), rows, cols,
+                    _stream(dz, stream)), name)
+
+
+def ew_experts_combine_grad_f32(dy, z, slot, weights, dz, dweights, offsets=None, counts=None,
+                                rows=None, cols=None, top=None, z_rows=None, experts=None,
+                                stream=None):
+    """Gradient of ew_experts_combine_f32 by z and the weights:
+    dz[slot[t, j]] = weights[t, j] * dy[t] and dweights[t, j] = dy[t] .
+    z[slot[t, j]] (0 for a dropped choice); with offsets and counts the
+    experts' padding rows of dz become 0.  dz may be z."""
+    _experts_combine_grad("ew_experts_combine_grad_f32", 4, dy, z, slot, weights, dz, dweights,
+                          offsets, counts, rows, cols, top, z_rows, experts, stream)
+
+
+def ew_experts_combine_grad_f16(dy, z, slot, weights, dz, dweights, offsets=None, counts=None,
+                                rows=None, cols=None, top=None, z_rows=None, experts=None,
+                                stream=None):
+    """ew_experts_combine_grad_f32 on binary16 data (dweights in binary32)."""
+    _experts_combine_grad("ew_experts_combine_grad_f16", 2, dy, z, slot, weights, dz, dweights,
+                          offsets, counts, rows, cols, top, z_rows, experts, stream)
+
+
+def ew_experts_combine_grad_bf16(dy, z, slot, weights, dz, dweights, offsets=None, counts=None,
+                                 rows=None, cols=None, top=None, z_rows=None, experts=None,
+                                 stream=None):
+    """ew_experts_combine_grad_f32 on bfloat16 data (dweights in binary32)."""
+    _experts_combine_grad("ew_experts_combine_grad_bf16", 2, dy, z, slot, weights, dz, dweights,
+                          offsets, counts, rows, cols, top, z_rows, experts, stream)
 
 
 def ew_status_string(status: int) -> str:

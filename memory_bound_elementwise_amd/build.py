@@ -25,10 +25,12 @@ ARCH = "gfx950"
 
 KERNEL_SOURCES = [os.path.join(CSRC, f) for f in
                   ("ew_stream.hip", "ew_batch.hip", "ew_gather.hip", "ew_view.hip")]
-# the row operators, whose kernels reduce along rows through LDS
-ROW_KERNEL_SOURCES = [os.path.join(CSRC, f) for f in ("ew_norm.hip", "ew_vocab.hip")]
+# the row operators, whose kernels reduce along rows through LDS or move rows
+ROW_KERNEL_SOURCES = [os.path.join(CSRC, f) for f in
+                      ("ew_norm.hip", "ew_vocab.hip", "ew_layernorm.hip", "ew_policy.hip",
+                       "ew_experts.hip")]
 SOURCES = [os.path.join(CSRC, "ew_api.cpp"), os.path.join(CSRC, "ew_rows_api.cpp"),
-           *KERNEL_SOURCES, *ROW_KERNEL_SOURCES]
+           os.path.join(CSRC, "ew_train_api.cpp"), *KERNEL_SOURCES, *ROW_KERNEL_SOURCES]
 
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 COMMON_FLAGS = [

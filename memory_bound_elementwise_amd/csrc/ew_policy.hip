@@ -1,0 +1,493 @@
+// ew_policy.hip -- the clipped policy loss with a KL term, and its gradient,
+// for CDNA4 (gfx950).
+
+#include "ew.h"
+#include "ew_rows_vec.h"
+
+namespace ew {
+
+// exp(d) - 1 and exp(d) - 1 - d, which are of the order of d and d^2: for
+// |d| < 1 by the series (the first term left out is below 2^-26 of the sum),
+// beyond from exp(d), where less than two bits cancel.
+struct Growth {
+    float one, line;
+    __device__ explicit Growth(float d)
+    {
+        float p = 1.0f / 479001600.0f;                       // 1 / 12!
+        p = __builtin_fmaf(p, d, 1.0f / 39916800.0f);
+        p = __builtin_fmaf(p, d, 1.0f / 3628800.0f);
+        p = __builtin_fmaf(p, d, 1.0f / 362880.0f);
+        p = __builtin_fmaf(p, d, 1.0f / 40320.0f);
+        p = __builtin_fmaf(p, d, 1.0f / 5040.0f);
+        p = __builtin_fmaf(p, d, 1.0f / 720.0f);
+        p = __builtin_fmaf(p, d, 1.0f / 120.0f);
+        p = __builtin_fmaf(p, d, 1.0f / 24.0f);
+        p = __builtin_fmaf(p, d, 1.0f / 6.0f);
+        p = __builtin_fmaf(p, d, 0.5f);
+        const bool near = __builtin_fabsf(d) < 1.0f;
+        const float bend = p * d * d, e = exp_nat(d) - 1.0f;
+        one = near ? d + bend : e;
+        line = near ? bend : e == kInf ? e : e - d;          // (not inf - inf)
+    }
+};
+
+// What a token adds.
+struct Token {
+    float x;           // logp - old_logp
+    float ratio;       // exp(x)
+    bool clipped;      // the gain is that of the border
+    float one, line;   // of d = ref_logp - logp: exp(d) - 1, exp(d) - 1 - d
+};
+
+template <bool Ref>
+__device__ __forceinline__ Token token(const PolicyTokens &in, float logp, float old, float ref, float a)
+{
+    Token t;
+    const double x = (double)logp - (double)old;        // exact
+    t.clipped = (a > 0.0f && x > in.above) || (a < 0.0f && x < in.below);
+    t.x = (float)x;
+    t.ratio = exp_nat(t.x);
+    t.one = 0.0f;
+    t.line = 0.0f;
+    if constexpr (Ref) {
+        const Growth g(ref - logp);
+        t.one = g.one;
+        t.line = g.line;
+    }
+    return t;
+}
+
+// Four neighbouring tokens of a row, and which of them count.
+struct Four {
+    f32x4 logp, old, ref, a;
+    uint32_t counted;          // bits
+};
+
+// A row's pointers.
+struct PolicyRow {
+    const float *logp, *old, *ref, *advantage;
+    const uint8_t *mask;
+    float each;                // the advantage of all its tokens, if one
+    __device__ PolicyRow(const PolicyTokens &in, uint64_t r)
+        : logp(in.logp + r * in.logp_stride), old(in.old + r * in.old_stride),
+          ref(in.ref + r * in.ref_stride), advantage(in.advantage + r * in.advantage_stride),
+          mask(in.mask + r * in.mask_stride),
+          each(in.advantage_stride ? 0.0f : in.advantage[r])
+    {
+    }
+};
+
+__device__ __forceinline__ f32x4 load4(const float *row, uint32_t cols, uint32_t at)
+{
+    return __builtin_bit_cast(f32x4, load_vec<float, true>(row, cols, at));
+}
+
+// Four tokens from `at` on (at < cols).
+template <bool Ref>
+__device__ __forceinline__ Four load_four(const PolicyTokens &in, const PolicyRow &row, uint32_t cols,
+                                          uint32_t at)
+{
+    typedef uint32_t word __attribute__((aligned(1)));
+    Four f;
+    f.logp = load4(row.logp, cols, at);
+    f.old = load4(row.old, cols, at);
+    f.ref = Ref ? load4(row.ref, cols, at) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    f.a = in.advantage_stride ? load4(row.advantage, cols, at)
+                              : f32x4{row.each, row.each, row.each, row.each};
+    f.counted = 0;
+    uint32_t bytes = 0x01010101u;
+    if (in.mask) {
+        if (cols >= 4) {
+            bytes = __builtin_nontemporal_load(
+                reinterpret_cast<const word *>(row.mask + (at + 4 <= cols ? at : cols - 4)));
+        } else {
+            bytes = 0;
+            for (uint32_t j = 0; j < cols; ++j) bytes |= (uint32_t)row.mask[j] << 8 * j;
+        }
+    }
+    if (at + 4 > cols) {
+        const uint32_t past = at + 4 - cols;
+        if (cols >= 4) {
+            const auto shift = [&](f32x4 v) {
+                return __builtin_bit_cast(f32x4, drop_first<float>(__builtin_bit_cast(u32x4, v), past));
+            };
+            f.logp = shift(f.logp);
+            f.old = shift(f.old);
+            if constexpr (Ref) f.ref = shift(f.ref);
+            if (in.advantage_stride) f.a = shift(f.a);
+            bytes >>= 8 * past;
+        } else {
+            bytes &= (1u << 8 * cols) - 1;
+        }
+        if (!in.mask) bytes = (1u << 8 * (4 - past)) - 1;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.counted |= (bytes >> 8 * j & 0xffu ? 1u : 0u) << j;
+    return f;
+}
+
+// ---------------------------------------------------------------------------
+// Forward: sums over parts of the batch, then their join.  Both in one block
+// for few tokens.
+// ---------------------------------------------------------------------------
+
+// Sums over tokens: of -gain, of exp(d) - 1 - d (both weighed within their
+// sequence where the mean is over sequences), of old_logp - logp, and counts.
+struct PolicySums {
+    double policy, kl, fall;
+    uint64_t clipped, tokens, rows;     // rows: sequences with counted tokens
+};
+
+constexpr int kPolicyBlock = 256;
+constexpr int kSmallBlock = 1024;
+
+// Lanes join: sums in a fixed order.
+__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t x)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) x += (uint64_t)__shfl_xor((unsigned long long)x, d);
+    return x;
+}
+
+// The sums of a block in its thread 0.
+template <int Waves>
+__device__ __forceinline__ PolicySums block_sums(PolicySums s, PolicySums *scratch)
+{
+    s.policy = wave_sum64(s.policy);
+    s.kl = wave_sum64(s.kl);
+    s.fall = wave_sum64(s.fall);
+    s.clipped = wave_sum_u64(s.clipped);
+    s.tokens = wave_sum_u64(s.tokens);
+    s.rows = wave_sum_u64(s.rows);
+    __syncthreads();
+    if (threadIdx.x % 64 == 0) scratch[threadIdx.x / 64] = s;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int w = 1; w < Waves; ++w) {
+            s.policy += scratch[w].policy;
+            s.kl += scratch[w].kl;
+            s.fall += scratch[w].fall;
+            s.clipped += scratch[w].clipped;
+            s.tokens += scratch[w].tokens;
+            s.rows += scratch[w].rows;
+        }
+    return s;
+}
+
+// What a thread sums of a row's tokens [from, to): steps of `step` tokens.
+template <bool Ref>
+__device__ __forceinline__ void sum_tokens(const PolicyTokens &in, uint64_t r, uint32_t cols,
+                                           uint64_t from, uint64_t to, uint32_t step, PolicySums &s)
+{
+    if (from >= to) return;        // (the advantage of no tokens may be absent)
+    const PolicyRow row(in, r);
+    for (uint64_t at = from; at < to; at += step) {
+        const Four f = load_four<Ref>(in, row, cols, (uint32_t)at);
+        float policy = 0.0f, kl = 0.0f, fall = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const Token t = token<Ref>(in, f.logp[j], f.old[j], f.ref[j], f.a[j]);
+            const bool counted = f.counted >> j & 1u;
+            const float bound = f.a[j] > 0.0f ? in.most : in.least;
+            const float loss = -f.a[j] * (t.clipped ? bound : t.ratio);
+            policy += counted ? loss : 0.0f;
+            kl += counted ? t.line : 0.0f;
+            fall -= counted ? t.x : 0.0f;
+            s.clipped += counted && t.clipped;
+        }
+        s.policy += (double)policy;
+        s.kl += (double)kl;
+        s.fall += (double)fall;
+        s.tokens += (uint64_t)__builtin_popcount(f.counted);
+    }
+}
+
+// Loss, stats and the weights of rows [first, last) from the batch's sums.
+__device__ __forceinline__ void write_loss(const PolicyLossArgs &a, const PolicySums &s)
+{
+    const double n = a.mean == EW_MEAN_TOKENS ? (double)s.tokens
+                     : a.mean == EW_MEAN_SEQUENCES ? (double)s.rows : 1.0;
+    const double w = s.tokens ? (double)a.scale / n : 0.0;
+    const double policy = s.tokens ? s.policy * w : 0.0, kl = s.tokens ? s.kl * w : 0.0;
+    // (a KL term that does not count may be infinite)
+    a.loss[0] = (float)(a.in.kl != 0.0f ? policy + (double)a.in.kl * kl : policy);
+    if (a.stats) {
+        a.stats[0] = (float)policy;
+        a.stats[1] = (float)kl;
+        a.stats[2] = s.tokens ? (float)((double)s.clipped / (double)s.tokens) : 0.0f;
+        a.stats[3] = s.tokens ? (float)(s.fall / (double)s.tokens) : 0.0f;
+    }
+}
+
+// Weight of a counted token of a sequence that has n of them.
+__device__ __forceinline__ float token_weight(const PolicyLossArgs &a, const PolicySums &s, uint32_t n)
+{
+    if (n == 0) return 0.0f;
+    if (a.mean == EW_MEAN_TOKENS) return (float)((double)a.scale / (double)s.tokens);
+    if (a.mean == EW_MEAN_NONE) return a.scale;
+    return (float)((double)a.scale / ((double)n * (double)s.rows));
+}
+
+// Sum over `lanes` neighbouring lanes (a power of two), in each of them.
+__device__ __forceinline__ uint32_t lanes_sum(uint32_t x, uint32_t lanes)
+{
+    for (uint32_t d = 1; d < lanes; d *= 2) x += (uint32_t)__shfl_xor((int)x, (int)d);
+    return x;
+}
+
+// A sequence's sums as the batch counts them: divided by its tokens where the
+// mean is over sequences.  Lane 0 of its lanes counts the sequence.
+__device__ __forceinline__ void add_sequence(PolicySums &all, const PolicySums &s, bool by_sequence,
+                                             uint32_t tokens, bool first)
+{
+    const double w = by_sequence && tokens ? 1.0 / (double)tokens : 1.0;
+    all.policy += s.policy * w;
+    all.kl += s.kl * w;
+    all.fall += s.fall;
+    all.clipped += s.clipped;
+    all.tokens += s.tokens;
+    all.rows += first && tokens;
+}
+
+// Few tokens: one block, `lanes` lanes a sequence at a time.
+template <bool Ref>
+__global__ void __launch_bounds__(kSmallBlock) ew_policy_small_kernel(PolicyLossArgs a, uint32_t lanes)
+{
+    __shared__ PolicySums scratch[kSmallBlock / 64];
+    uint32_t *const counts = static_cast<uint32_t *>(a.workspace);
+    PolicySums all{};
+    const uint32_t lane = threadIdx.x % lanes;
+    // (whole waves go round together: lanes_sum)
+    for (uint32_t r0 = 0; r0 < a.rows; r0 += kSmallBlock / lanes) {
+        const uint32_t r = r0 + threadIdx.x / lanes;
+        PolicySums s{};
+        if (r < a.rows)
+            sum_tokens<Ref>(a.in, r, a.cols, (uint64_t)lane * 4, a.cols, lanes * 4, s);
+        const uint32_t tokens = lanes_sum((uint32_t)s.tokens, lanes);
+        add_sequence(all, s, a.mean == EW_MEAN_SEQUENCES, tokens, lane == 0);
+        if (r < a.rows && lane == 0) counts[r] = tokens;
+    }
+    all = block_sums<kSmallBlock / 64>(all, scratch);
+    if (threadIdx.x == 0) {
+        scratch[0] = all;
+        write_loss(a, all);
+    }
+    __syncthreads();
+    all = scratch[0];
+    if (a.weights)
+        for (uint32_t r = threadIdx.x; r < a.rows; r += kSmallBlock)
+            a.weights[r] = token_weight(a, all, counts[r]);
+}
+
+// Whole sequences: `lanes` lanes each; a record of sums a block, a count of
+// tokens a sequence.
+template <bool Ref>
+__global__ void __launch_bounds__(kPolicyBlock) ew_policy_rows_kernel(PolicyLossArgs a, uint32_t lanes,
+                                                                     PolicySums *records,
+                                                                     uint32_t *counts)
+{
+    __shared__ PolicySums scratch[kPolicyBlock / 64];
+    PolicySums all{};
+    const uint32_t lane = threadIdx.x % lanes, per = kPolicyBlock / lanes;
+    for (uint64_t r0 = (uint64_t)blockIdx.x * per; r0 < a.rows; r0 += (uint64_t)gridDim.x * per) {
+        const uint64_t r = r0 + threadIdx.x / lanes;
+        PolicySums s{};
+        if (r < a.rows)
+            sum_tokens<Ref>(a.in, r, a.cols, (uint64_t)lane * 4, a.cols, lanes * 4, s);
+        const uint32_t tokens = lanes_sum((uint32_t)s.tokens, lanes);
+        add_sequence(all, s, a.mean == EW_MEAN_SEQUENCES, tokens, lane == 0);
+        if (r < a.rows && lane == 0) counts[r] = tokens;
+    }
+    all = block_sums<kPolicyBlock / 64>(all, scratch);
+    if (threadIdx.x == 0) records[blockIdx.x] = all;
+}
+
+// Parts of few long sequences: block (part, sequence), a record each.
+template <bool Ref>
+__global__ void __launch_bounds__(kPolicyBlock) ew_policy_parts_kernel(PolicyLossArgs a,
+                                                                      uint64_t part_tokens,
+                                                                      PolicySums *records)
+{
+    __shared__ PolicySums scratch[kPolicyBlock / 64];
+    PolicySums s{};
+    const uint64_t from = blockIdx.x * part_tokens, to = from + part_tokens;
+    sum_tokens<Ref>(a.in, blockIdx.y, a.cols, from + threadIdx.x * 4, to < a.cols ? to : a.cols,
+                    kPolicyBlock * 4, s);
+    s = block_sums<kPolicyBlock / 64>(s, scratch);
+    if (threadIdx.x == 0) records[(uint64_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
+}
+
+// Sequences that are cut into parts: fewer than this.
+constexpr uint32_t kCutRows = 256;
+
+// The join: every block adds up all records; the first writes loss and stats,
+// each the weights of its sequences.  parts > 0: records are of parts of
+// sequences, and a sequence's tokens are counted here.
+__global__ void __launch_bounds__(kSmallBlock) ew_policy_join_kernel(PolicyLossArgs a,
+                                                                    const PolicySums *records,
+                                                                    uint32_t n, uint32_t parts,
+                                                                    const uint32_t *counts)
+{
+    __shared__ PolicySums scratch[kSmallBlock / 64];
+    PolicySums all{};
+    __shared__ uint32_t tokens_of[kCutRows];
+    if (parts) {
+        for (uint32_t r = threadIdx.x / 64; r < a.rows; r += kSmallBlock / 64) {
+            uint32_t tokens = 0;
+            for (uint32_t p = threadIdx.x % 64; p < parts; p += 64)
+                tokens += (uint32_t)records[(uint64_t)r * parts + p].tokens;
+            tokens = lanes_sum(tokens, 64);
+            if (threadIdx.x % 64 == 0) tokens_of[r] = tokens;
+        }
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < n; i += kSmallBlock)
+            add_sequence(all, records[i], a.mean == EW_MEAN_SEQUENCES, tokens_of[i / parts],
+                         i % parts == 0);
+    } else {
+        for (uint32_t i = threadIdx.x; i < n; i += kSmallBlock) {
+            const PolicySums &s = records[i];
+            all.policy += s.policy;
+            all.kl += s.kl;
+            all.fall += s.fall;
+            all.clipped += s.clipped;
+            all.tokens += s.tokens;
+            all.rows += s.rows;
+        }
+    }
+    all = block_sums<kSmallBlock / 64>(all, scratch);
+    if (threadIdx.x == 0) {
+        scratch[0] = all;
+        if (blockIdx.x == 0) write_loss(a, all);
+    }
+    __syncthreads();
+    all = scratch[0];
+    if (!a.weights) return;
+    for (uint64_t r = (uint64_t)blockIdx.x * kSmallBlock + threadIdx.x; r < a.rows;
+         r += (uint64_t)gridDim.x * kSmallBlock)
+        a.weights[r] = token_weight(a, all, parts ? tokens_of[r] : counts[r]);
+}
+
+// ---------------------------------------------------------------------------
+// Gradient: `lanes` lanes a sequence (or a part of one)
+// ---------------------------------------------------------------------------
+
+template <bool Ref>
+__global__ void __launch_bounds__(kPolicyBlock) ew_policy_grad_kernel(PolicyGradArgs a, uint32_t lanes,
+                                                                     uint64_t part_tokens)
+{
+    const uint32_t lane = threadIdx.x % lanes, per = kPolicyBlock / lanes;
+    const float dloss = a.dloss ? a.dloss[0] : 1.0f;
+    const uint64_t from = blockIdx.y * part_tokens, end = from + part_tokens;
+    const uint64_t to = end < a.cols ? end : a.cols;
+    for (uint64_t r0 = (uint64_t)blockIdx.x * per; r0 < a.rows; r0 += (uint64_t)gridDim.x * per) {
+        const uint64_t r = r0 + threadIdx.x / lanes;
+        if (r >= a.rows) break;
+        const PolicyRow row(a.in, r);
+        float *const out = a.dlogp + r * a.dlogp_stride;
+        const float w = a.weights[r] * dloss;
+        for (uint64_t at = from + (uint64_t)lane * 4; at < to; at += (uint64_t)lanes * 4) {
+            const Four f = load_four<Ref>(a.in, row, a.cols, (uint32_t)at);
+            f32x4 g;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const Token t = token<Ref>(a.in, f.logp[j], f.old[j], f.ref[j], f.a[j]);
+                float slope = t.clipped ? 0.0f : -f.a[j] * t.ratio;
+                if constexpr (Ref) slope -= a.in.kl * t.one;
+                g[j] = f.counted >> j & 1u ? w * slope : 0.0f;
+            }
+            store_vec(out, a.cols, (uint32_t)at, __builtin_bit_cast(u32x4, g));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch
+// ---------------------------------------------------------------------------
+
+// One block sums up to this many tokens.
+constexpr uint64_t kSmallTokens = 16384;
+// Records of sums: at most this many blocks.
+constexpr uint64_t kRecords = 1024;
+
+// Lanes that share a sequence: each takes four tokens at a time.
+static uint32_t lanes_for(uint64_t cols, uint32_t most)
+{
+    uint32_t lanes = 1;
+    while (lanes < most && lanes * 4 < cols) lanes *= 2;
+    return lanes;
+}
+
+// Few long sequences are cut into parts of whole steps of a block.
+static uint64_t parts_of(uint64_t rows, uint64_t cols)
+{
+    constexpr uint64_t kStep = kPolicyBlock * 4;
+    if (rows == 0 || rows >= kCutRows) return 1;
+    const uint64_t most = (cols + kStep - 1) / kStep, want = kRecords / rows;
+    return most < want ? most : want;
+}
+
+size_t policy_loss_workspace(uint64_t rows, uint64_t cols)
+{
+    return kRecords * sizeof(PolicySums) + (rows * sizeof(uint32_t) + 15) / 16 * 16;
+}
+
+hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, const char **path)
+{
+    const bool ref = a.in.ref;
+    if ((uint64_t)a.rows * (a.cols ? a.cols : 1) <= kSmallTokens) {
+        *path = "one block";
+        const uint32_t lanes = lanes_for(a.cols, 64);
+        return start(ref ? reinterpret_cast<const void *>(&ew_policy_small_kernel<true>)
+                         : reinterpret_cast<const void *>(&ew_policy_small_kernel<false>),
+                     dim3(1), kSmallBlock, 0, s, a, lanes);
+    }
+    PolicySums *const records = static_cast<PolicySums *>(a.workspace);
+    uint32_t *const counts = reinterpret_cast<uint32_t *>(records + kRecords);
+    const uint64_t parts = parts_of(a.rows, a.cols);
+    uint32_t n;
+    hipError_t e;
+    if (parts > 1) {
+        *path = "parts of sequences";
+        constexpr uint64_t kStep = kPolicyBlock * 4;
+        const uint64_t tokens = ((a.cols + parts - 1) / parts + kStep - 1) / kStep * kStep;
+        const uint32_t used = (uint32_t)((a.cols + tokens - 1) / tokens);
+        n = a.rows * used;
+        e = start(ref ? reinterpret_cast<const void *>(&ew_policy_parts_kernel<true>)
+                      : reinterpret_cast<const void *>(&ew_policy_parts_kernel<false>),
+                  dim3(used, a.rows), kPolicyBlock, 0, s, a, tokens, records);
+        if (e != hipSuccess) return e;
+        return start(reinterpret_cast<const void *>(&ew_policy_join_kernel), dim3(1), kSmallBlock, 0, s,
+                     a, (const PolicySums *)records, n, used, (const uint32_t *)counts);
+    }
+    *path = "whole sequences";
+    const uint32_t lanes = lanes_for(a.cols, 64);
+    const uint64_t blocks = ((uint64_t)a.rows * lanes + kPolicyBlock - 1) / kPolicyBlock;
+    n = (uint32_t)(blocks < kRecords ? blocks : kRecords);
+    e = start(ref ? reinterpret_cast<const void *>(&ew_policy_rows_kernel<true>)
+                  : reinterpret_cast<const void *>(&ew_policy_rows_kernel<false>),
+              dim3(n), kPolicyBlock, 0, s, a, lanes, records, counts);
+    if (e != hipSuccess) return e;
+    const uint64_t joins = a.weights ? ((uint64_t)a.rows + kSmallBlock - 1) / kSmallBlock : 1;
+    return start(reinterpret_cast<const void *>(&ew_policy_join_kernel),
+                 dim3((uint32_t)(joins < kRecords ? joins : kRecords)), kSmallBlock, 0, s, a,
+                 (const PolicySums *)records, n, (uint32_t)0, (const uint32_t *)counts);
+}
+
+hipError_t launch_policy_grad(RowType, const PolicyGradArgs &a, hipStream_t s, const char **path)
+{
+    const uint32_t lanes = lanes_for(a.cols, kPolicyBlock);
+    const uint64_t blocks = ((uint64_t)a.rows * lanes + kPolicyBlock - 1) / kPolicyBlock;
+    constexpr uint64_t kStep = kPolicyBlock * 4;
+    const uint64_t parts = lanes == kPolicyBlock ? parts_of(a.rows, a.cols) : 1;
+    const uint64_t tokens = parts > 1 ? ((a.cols + parts - 1) / parts + kStep - 1) / kStep * kStep
+                                      : (uint64_t)a.cols;
+    const uint32_t used = (uint32_t)((a.cols + tokens - 1) / tokens);
+    *path = used > 1 ? "parts of sequences" : "whole sequences";
+    // a KL term that does not count is not read
+    return start(a.in.ref && a.in.kl != 0.0f
+                     ? reinterpret_cast<const void *>(&ew_policy_grad_kernel<true>)
+                     : reinterpret_cast<const void *>(&ew_policy_grad_kernel<false>),
+                 dim3(row_blocks(blocks), used), kPolicyBlock, 0, s, a, lanes, tokens);
+}
+
+}  // namespace ew
