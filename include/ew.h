@@ -604,8 +604,10 @@ ew_status_t ew_distill_grad_bf16(const uint16_t *logits, size_t stride, const fl
  *   total = round(x + residual), mean = sum(total) / n,
  *   rstd = 1 / sqrt(sum((total - mean)^2) / n + eps),
  *   y = round((total - mean) * rstd * weight + bias).
- * The mean is summed in binary64, so that rows far from 0 keep their
- * differences: a row of equal values has y = bias exactly (for eps > 0).
+ * Differences are taken from the row's mean to 24 bits of the difference,
+ * however far the row lies from 0: a row of equal values has y = bias exactly
+ * (for eps > 0).  A row that holds a NaN or an infinity has NaN in mean, rstd
+ * and y.
  * weight, bias  each optional: 1 and 0 where absent
  * residual      optional: without it total is x itself
  * total         optional, requires residual: the rounded sum

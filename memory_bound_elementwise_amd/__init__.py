@@ -1019,8 +1019,8 @@ def _layernorm(name, es, x, weight, bias, y, residual, total, mean, rstd, eps, r
 def ew_layernorm_f32(x, weight, bias, y, residual=None, total=None, mean=None, rstd=None, eps=1e-5,
                      rows=None, cols=None, stream=None):
     """total = x + residual, y = (total - mean) / sqrt(variance + eps) * weight + bias, row by
-    row (binary32, the mean summed in binary64); mean and rstd receive the
-    row's mean and 1 / sqrt(variance + eps).  weight and bias may be None (1
+    row (binary32); mean and rstd receive the row's mean and
+    1 / sqrt(variance + eps).  weight and bias may be None (1
     and 0).  Without a residual the norm is x's.  total may be x or residual,
     y whichever of them total is not."""
     _layernorm("ew_layernorm_f32", 4, x, weight, bias, y, residual, total, mean, rstd, eps, rows,

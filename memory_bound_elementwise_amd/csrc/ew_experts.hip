@@ -13,8 +13,6 @@ namespace ew {
 // function of the entries before it.
 // ---------------------------------------------------------------------------
 
-constexpr uint32_t kSortWaves = 4, kSortBlock = kSortWaves * 64;
-
 // Lanes whose key equals this lane's; keys below 2^bits, live lanes only.
 __device__ __forceinline__ uint64_t lanes_of(uint32_t key, bool live, uint32_t bits)
 {
@@ -35,44 +33,70 @@ __device__ __forceinline__ uint32_t expert_of(const ExpertsSortArgs &a, uint64_t
     return id >= 0 && id < (int64_t)a.cols ? (uint32_t)id : a.cols;
 }
 
-// Counts of a wave's entries [from, end) by expert, added to its counters.
-__device__ __forceinline__ void count_entries(const ExpertsSortArgs &a, uint64_t from, uint64_t end,
-                                              uint32_t bits, uint32_t *counter)
+// A wave's entries, 64 at a time: it holds this many rounds of them in
+// registers from the counting to the placing (their loads are on their way
+// together), and reads longer ones twice.
+constexpr uint32_t kHeld = 8;
+
+// How a sorting is split: `chunk` entries a block, `per` (a multiple of 64) a
+// counting wave.
+struct SortSplit {
+    uint32_t chunk, per, waves;      // waves: of a block that count
+    uint32_t bits;                   // of an expert's number
+};
+
+// The entries [from, end) of a wave.
+struct WaveEntries {
+    uint64_t from, end;
+    __device__ WaveEntries(const ExpertsSortArgs &a, const SortSplit &split)
+    {
+        const uint32_t wave = threadIdx.x / 64;
+        const uint64_t first = (uint64_t)blockIdx.x * split.chunk;
+        const uint64_t last = first + split.chunk < a.rows ? first + split.chunk : a.rows;
+        from = wave < split.waves ? first + (uint64_t)wave * split.per : last;
+        from = from < last ? from : last;
+        end = from + split.per < last ? from + split.per : last;
+    }
+};
+
+// Calls f(expert, entry) for a wave's entries, round by round.
+template <bool Held, class F>
+__device__ __forceinline__ void each_entry(const ExpertsSortArgs &a, const WaveEntries &own,
+                                           const uint32_t (&held)[kHeld], F f)
 {
     const uint32_t lane = threadIdx.x % 64;
-    for (uint64_t i = from; i < end; i += 64) {
-        const uint32_t e = expert_of(a, i + lane, end);
-        const uint64_t same = lanes_of(e, e < a.cols, bits);
-        if (e < a.cols && (uint32_t)__builtin_ctzll(same) == lane)
-            counter[e] += (uint32_t)__builtin_popcountll(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if constexpr (Held) {
+#pragma unroll
+        for (uint32_t k = 0; k < kHeld; ++k)
+            if (own.from + 64 * k < own.end) f(held[k], own.from + 64 * k + lane);
+    } else {
+        for (uint64_t i = own.from; i < own.end; i += 64) f(expert_of(a, i + lane, own.end), i + lane);
     }
 }
 
-// Rows of a wave's entries: counter[e] is the row of its next one of expert e.
-__device__ __forceinline__ void place_entries(const ExpertsSortArgs &a, uint64_t from, uint64_t end,
-                                              uint32_t bits, uint32_t *counter)
+// The waves' counters of a block's entries by expert (and `held`).
+template <bool Held>
+__device__ __forceinline__ void count_entries(const ExpertsSortArgs &a, const SortSplit &split,
+                                              const WaveEntries &own, uint32_t (&held)[kHeld],
+                                              uint32_t *counters)
 {
-    const uint32_t lane = threadIdx.x % 64;
-    for (uint64_t i = from; i < end; i += 64) {
-        const uint32_t e = expert_of(a, i + lane, end);
-        const bool live = e < a.cols;
-        const uint64_t same = lanes_of(e, live, bits);
-        const uint32_t first = live ? counter[e] : 0;
+    const uint32_t experts = a.cols, lane = threadIdx.x % 64;
+    uint32_t *const mine = counters + threadIdx.x / 64 * experts;
+    if constexpr (Held)
+#pragma unroll
+        for (uint32_t k = 0; k < kHeld; ++k) held[k] = expert_of(a, own.from + 64 * k + lane, own.end);
+    for (uint32_t i = threadIdx.x; i < split.waves * experts; i += blockDim.x) counters[i] = 0;
+    __syncthreads();
+    each_entry<Held>(a, own, held, [&](uint32_t e, uint64_t) {
+        const uint64_t same = lanes_of(e, e < experts, split.bits);
+        if (e < experts && (uint32_t)__builtin_ctzll(same) == lane)
+            mine[e] += (uint32_t)__builtin_popcountll(same);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (live && (uint32_t)__builtin_ctzll(same) == lane)
-            counter[e] = first + (uint32_t)__builtin_popcountll(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const uint32_t row = first + (uint32_t)__builtin_popcountll(same & (((uint64_t)1 << lane) - 1));
-        if (i + lane < end) {
-            a.slot[i + lane] = live ? (int32_t)row : -1;
-            if (live && a.source) a.source[row] = (int32_t)(i + lane);
-        }
-    }
+    });
+    __syncthreads();
 }
 
 // Inclusive sum over a block's threads; scratch: a value a wave.
-template <uint32_t Waves>
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *scratch)
 {
     const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -88,53 +112,60 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *scratch)
     return x;
 }
 
-// One launch sorts what a block can (kOne), else every block adds up the
-// counts of those before it (`totals`: a row of counts a block, by
-// ew_experts_count_kernel).
-// LDS: Waves counters an expert, then the experts' first rows.
-template <uint32_t Waves, bool One>
-__global__ void __launch_bounds__(Waves * 64) ew_experts_sort_kernel(ExpertsSortArgs a, uint32_t chunk,
-                                                                    uint32_t bits,
-                                                                    const uint32_t *totals)
+// The first row of each expert and the places of a block's entries.  One: all
+// entries are the block's; else every block adds up the counts of all blocks
+// (totals: a row of them each, by ew_experts_count_kernel).
+// LDS: the waves' counters, then (not One) the threads' sums.
+template <bool One, bool Held>
+__global__ void __launch_bounds__(1024) ew_experts_sort_kernel(ExpertsSortArgs a, SortSplit split,
+                                                               const uint32_t *totals)
 {
-    constexpr uint32_t kThreads = Waves * 64;
     extern __shared__ uint32_t counters[];
-    __shared__ uint32_t scratch[Waves];
-    const uint32_t experts = a.cols, wave = threadIdx.x / 64;
+    __shared__ uint32_t scratch[16];
+    const uint32_t experts = a.cols, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const WaveEntries own(a, split);
     uint32_t *const mine = counters + wave * experts;
-    // the wave's own entries
-    const uint64_t block_from = (uint64_t)blockIdx.x * chunk;
-    const uint64_t block_end = block_from + chunk < a.rows ? block_from + chunk : a.rows;
-    uint64_t from = block_from + (uint64_t)wave * (chunk / Waves);
-    uint64_t end = from + chunk / Waves;
-    from = from < block_end ? from : block_end;
-    end = end < block_end ? end : block_end;
-    for (uint32_t i = threadIdx.x; i < Waves * experts; i += kThreads) counters[i] = 0;
-    __syncthreads();
-    count_entries(a, from, end, bits, mine);
-    __syncthreads();
-    // the experts' rows: kThreads of them at a time
+    uint32_t held[kHeld];
+    count_entries<Held>(a, split, own, held, counters);
+    // the experts' rows, a tile of them at a time
+    const uint32_t tile = experts < blockDim.x ? 1u << split.bits : blockDim.x;
     uint32_t start = 0;
-    for (uint32_t e0 = 0; e0 < experts; e0 += kThreads) {
-        const uint32_t e = e0 + threadIdx.x;
+    for (uint32_t e0 = 0; e0 < experts; e0 += tile) {
         uint32_t before = 0, all = 0;
-        if (e < experts) {
-            if constexpr (One) {
-                for (uint32_t w = 0; w < Waves; ++w) all += counters[w * experts + e];
-            } else {
-                for (uint32_t b = 0; b < gridDim.x; ++b) {
-                    const uint32_t n = totals[(uint64_t)b * experts + e];
+        if constexpr (!One) {
+            // threads of the same expert share the blocks
+            uint32_t *const sums = counters + split.waves * experts;
+            const uint32_t e = e0 + threadIdx.x % tile, part = threadIdx.x / tile;
+            const uint32_t parts = blockDim.x / tile;
+            if (e < experts) {
+#pragma unroll 8
+                for (uint32_t b = part; b < gridDim.x; b += parts) {
+                    const uint32_t n = totals[b * experts + e];
                     all += n;
                     before += b < blockIdx.x ? n : 0;
                 }
             }
+            __syncthreads();
+            sums[threadIdx.x] = before;
+            sums[blockDim.x + threadIdx.x] = all;
+            __syncthreads();
+            before = all = 0;
+            if (threadIdx.x < tile)
+                for (uint32_t q = 0; q < parts; ++q) {
+                    before += sums[q * tile + threadIdx.x];
+                    all += sums[blockDim.x + q * tile + threadIdx.x];
+                }
         }
-        const uint32_t room = (all + a.align - 1) / a.align * a.align;
-        const uint32_t after = start + block_scan<Waves>(room, scratch);
-        if (e < experts) {
+        const uint32_t e = e0 + threadIdx.x;
+        const bool live = threadIdx.x < tile && e < experts;
+        if (One && live)
+            for (uint32_t w = 0; w < split.waves; ++w) all += counters[w * experts + e];
+        const uint32_t room = live ? (all + a.align - 1) / a.align * a.align : 0;
+        const uint32_t after = start + block_scan(room, scratch);
+        if (live) {
             const uint32_t first = after - room;
             uint32_t next = first + before;
-            for (uint32_t w = 0; w < Waves; ++w) {
+            for (uint32_t w = 0; w < split.waves; ++w) {
                 const uint32_t n = counters[w * experts + e];
                 counters[w * experts + e] = next;
                 next += n;
@@ -148,165 +179,307 @@ __global__ void __launch_bounds__(Waves * 64) ew_experts_sort_kernel(ExpertsSort
             if (a.source && e % gridDim.x == blockIdx.x)
                 for (uint32_t r = first + all; r < after; ++r) a.source[r] = -1;
         }
-        for (uint32_t w = 0; w < Waves; ++w) start += scratch[w];
+        for (uint32_t w = 0; w < blockDim.x / 64; ++w) start += scratch[w];
         __syncthreads();
     }
     if (a.source)
-        for (uint64_t r = start + (uint64_t)blockIdx.x * kThreads + threadIdx.x; r < a.source_rows;
-             r += (uint64_t)gridDim.x * kThreads)
+        for (uint64_t r = start + (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.source_rows;
+             r += (uint64_t)gridDim.x * blockDim.x)
             a.source[r] = -1;
-    place_entries(a, from, end, bits, mine);
+    each_entry<Held>(a, own, held, [&](uint32_t e, uint64_t i) {
+        const bool live = e < experts;
+        const uint64_t same = lanes_of(e, live, split.bits);
+        const uint32_t first = live ? mine[e] : 0;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (live && (uint32_t)__builtin_ctzll(same) == lane)
+            mine[e] = first + (uint32_t)__builtin_popcountll(same);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const uint32_t row = first + (uint32_t)__builtin_popcountll(same & (((uint64_t)1 << lane) - 1));
+        if (i < own.end) {
+            a.slot[i] = live ? (int32_t)row : -1;
+            if (live && a.source) a.source[row] = (int32_t)i;
+        }
+    });
 }
 
 // Counts of each block's entries by expert.
-__global__ void __launch_bounds__(kSortBlock) ew_experts_count_kernel(ExpertsSortArgs a, uint32_t chunk,
-                                                                     uint32_t bits, uint32_t *totals)
+template <bool Held>
+__global__ void __launch_bounds__(1024) ew_experts_count_kernel(ExpertsSortArgs a, SortSplit split,
+                                                                uint32_t *totals)
 {
     extern __shared__ uint32_t counters[];
-    const uint32_t experts = a.cols, wave = threadIdx.x / 64;
-    const uint64_t block_from = (uint64_t)blockIdx.x * chunk;
-    const uint64_t block_end = block_from + chunk < a.rows ? block_from + chunk : a.rows;
-    uint64_t from = block_from + (uint64_t)wave * (chunk / kSortWaves);
-    uint64_t end = from + chunk / kSortWaves;
-    from = from < block_end ? from : block_end;
-    end = end < block_end ? end : block_end;
-    for (uint32_t i = threadIdx.x; i < kSortWaves * experts; i += kSortBlock) counters[i] = 0;
-    __syncthreads();
-    count_entries(a, from, end, bits, counters + wave * experts);
-    __syncthreads();
-    for (uint32_t e = threadIdx.x; e < experts; e += kSortBlock) {
+    const uint32_t experts = a.cols;
+    uint32_t held[kHeld];
+    count_entries<Held>(a, split, WaveEntries(a, split), held, counters);
+    for (uint32_t e = threadIdx.x; e < experts; e += blockDim.x) {
         uint32_t n = 0;
-        for (uint32_t w = 0; w < kSortWaves; ++w) n += counters[w * experts + e];
-        totals[(uint64_t)blockIdx.x * experts + e] = n;
+        for (uint32_t w = 0; w < split.waves; ++w) n += counters[w * experts + e];
+        totals[blockIdx.x * experts + e] = n;
     }
 }
 
 // ---------------------------------------------------------------------------
-// Movement of rows.  Lanes threads of a block share a token and go along its
-// columns 16 bytes at a time; the token's row is read once.
+// Movement of rows.  Waves waves share a token (a wave each for short rows, the
+// block for long ones) and go along its columns a stretch at a time, 16 bytes a
+// lane and vector; the token's own row is read once.  A token's slots lie in
+// the lanes of each of its waves.
 // ---------------------------------------------------------------------------
 
-constexpr uint32_t kMoveBlock = 256;
+constexpr uint32_t kMoveBlock = 256, kMoveWaves = kMoveBlock / 64;
+
+// Which token of a round a thread's wave works on, the same in all its lanes,
+// and the thread's place among the token's.
+template <uint32_t Waves>
+struct Worker {
+    static constexpr uint32_t kTokens = kMoveWaves / Waves, kLanes = Waves * 64;
+    uint32_t token, place;
+    __device__ Worker()
+        : token(Waves == kMoveWaves
+                    ? 0 : (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / kLanes))),
+          place(threadIdx.x % kLanes)
+    {
+    }
+};
+
+// A token's slots, choice j's in lane j: -1 where it names no row.
+struct Slots {
+    int32_t mine;
+    __device__ Slots(const ExpertsMoveArgs &a, uint64_t t) : mine(-1)
+    {
+        const uint32_t lane = threadIdx.x % 64;
+        if (lane < a.top) mine = a.slot[t * a.top + lane];
+        if ((uint32_t)mine >= a.places) mine = -1;
+    }
+    __device__ int32_t of(uint32_t j) const { return __builtin_amdgcn_readlane(mine, (int)j); }
+};
+
+// A token's weights, choice j's in lane j.
+struct Weights {
+    float mine;
+    __device__ Weights(const ExpertsMoveArgs &a, uint64_t t) : mine(1.0f)
+    {
+        const uint32_t lane = threadIdx.x % 64;
+        if (a.weights && lane < a.top) mine = a.weights[t * a.top + lane];
+    }
+    __device__ float of(uint32_t j) const { return lane_value(mine, (int)j); }
+};
+
+// A lane's vectors of a stretch of columns, from column `from` on: pieces of
+// the stretch, whose row starts `back` elements before it (the last piece of a
+// stretch shorter than a vector does).
+template <typename T, uint32_t Lanes, uint32_t U, bool Tiny>
+struct Stretch {
+    static constexpr uint32_t N = Vec<T>::N, kCols = Lanes * U * N;
+    uint64_t from;
+    uint32_t cols, place, back;
+    __device__ Stretch(uint64_t from_, uint32_t all, uint32_t place_)
+        : from(from_), cols(all - from_ < kCols ? (uint32_t)(all - from_) : kCols), place(place_),
+          back(from_ ? N : 0)
+    {
+    }
+    __device__ Piece<T, Tiny> piece(uint32_t u) const
+    {
+        return Piece<T, Tiny>((place + u * Lanes) * N, cols, back);
+    }
+    __device__ const T *row(const void *base, uint64_t r, uint64_t stride) const
+    {
+        return static_cast<const T *>(base) + r * stride + from - back;
+    }
+    __device__ T *row(void *base, uint64_t r, uint64_t stride) const
+    {
+        return static_cast<T *>(base) + r * stride + from - back;
+    }
+    template <bool Nt>
+    __device__ u32x4 load(const void *base, uint64_t r, uint64_t stride, uint32_t u) const
+    {
+        return load_piece<T, Nt>(row(base, r, stride), cols, piece(u));
+    }
+};
 
 // Zeros in the padding rows of expert e, by a block.
-template <typename T>
+template <typename T, bool Tiny>
 __device__ __forceinline__ void clear_padding(const ExpertsMoveArgs &a, uint32_t e)
 {
-    constexpr uint32_t N = Vec<T>::N;
+    using Cols = Stretch<T, kMoveBlock, 1, Tiny>;
     const int64_t first = (int64_t)a.offsets[e] + a.counts[e], after = a.offsets[e + 1];
     const int64_t from = first < 0 ? 0 : first, to = after < a.places ? after : a.places;
     for (int64_t r = from; r < to; ++r) {
-        T *const row = static_cast<T *>(a.out) + (uint64_t)r * a.out_stride;
-        for (uint64_t at = threadIdx.x * N; at < a.cols; at += kMoveBlock * N)
-            store_vec(row, a.cols, (uint32_t)at, u32x4{0, 0, 0, 0});
+        for (uint64_t first = 0; first < a.cols; first += Cols::kCols) {
+            const Cols part(first, a.cols, threadIdx.x);
+            store_piece(part.row(a.out, (uint64_t)r, a.out_stride), part.cols, part.piece(0),
+                           u32x4{0, 0, 0, 0});
+        }
     }
 }
 
-// A token's slot j, or -1 where it names no row.
-__device__ __forceinline__ int32_t place_of(const ExpertsMoveArgs &a, uint64_t t, uint32_t j)
-{
-    const int32_t s = a.slot[t * a.top + j];
-    return (uint32_t)s < a.places ? s : -1;
-}
-
-template <typename T, uint32_t Lanes>
+template <typename T, uint32_t Waves, bool Tiny>
 __global__ void __launch_bounds__(kMoveBlock) ew_experts_gather_kernel(ExpertsMoveArgs a, uint32_t blocks)
 {
-    constexpr uint32_t N = Vec<T>::N, kTokens = kMoveBlock / Lanes;
+    constexpr uint32_t U = 4;
+    using Cols = Stretch<T, Waves * 64, U, Tiny>;
     if (blockIdx.x >= blocks) {
-        if (blockIdx.y == 0) clear_padding<T>(a, blockIdx.x - blocks);
+        clear_padding<T, Tiny>(a, blockIdx.x - blocks);
         return;
     }
-    const uint32_t lane = threadIdx.x % Lanes;
-    for (uint64_t t0 = (uint64_t)blockIdx.x * kTokens; t0 < a.rows; t0 += (uint64_t)blocks * kTokens) {
-        const uint64_t t = t0 + threadIdx.x / Lanes;
+    const Worker<Waves> worker;
+    for (uint64_t t0 = (uint64_t)blockIdx.x * worker.kTokens; t0 < a.rows;
+         t0 += (uint64_t)blocks * worker.kTokens) {
+        const uint64_t t = t0 + worker.token;
         if (t >= a.rows) break;
-        const T *const x = static_cast<const T *>(a.in) + t * a.in_stride;
-        for (uint64_t at = (blockIdx.y * (uint64_t)Lanes + lane) * N; at < a.cols;
-             at += (uint64_t)gridDim.y * Lanes * N) {
-            const u32x4 v = settle<T>(load_vec<T, true>(x, a.cols, (uint32_t)at), a.cols, (uint32_t)at);
+        const Slots slots(a, t);
+        for (uint64_t first = 0; first < a.cols; first += Cols::kCols) {
+            const Cols part(first, a.cols, worker.place);
+            u32x4 v[U];
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u) v[u] = part.template load<true>(a.in, t, a.in_stride, u);
             for (uint32_t j = 0; j < a.top; ++j) {
-                const int32_t s = place_of(a, t, j);
-                if (s >= 0)
-                    store_vec(static_cast<T *>(a.out) + (uint64_t)(uint32_t)s * a.out_stride, a.cols,
-                              (uint32_t)at, v);
+                const int32_t s = slots.of(j);
+                if (s < 0) continue;
+                T *const row = part.row(a.out, (uint32_t)s, a.out_stride);
+#pragma unroll
+                for (uint32_t u = 0; u < U; ++u) store_piece(row, part.cols, part.piece(u), v[u]);
             }
         }
     }
 }
 
-template <typename T, uint32_t Lanes>
+// C choices of U vectors are on their way together.
+template <typename T, uint32_t Waves, uint32_t C, uint32_t U, bool Tiny>
 __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_kernel(ExpertsMoveArgs a, uint32_t blocks)
 {
-    constexpr uint32_t N = Vec<T>::N, kTokens = kMoveBlock / Lanes;
+    using Cols = Stretch<T, Waves * 64, U, Tiny>;
     using Wide = typename Vec<T>::wide;
-    const uint32_t lane = threadIdx.x % Lanes;
-    for (uint64_t t0 = (uint64_t)blockIdx.x * kTokens; t0 < a.rows; t0 += (uint64_t)blocks * kTokens) {
-        const uint64_t t = t0 + threadIdx.x / Lanes;
+    const Worker<Waves> worker;
+    for (uint64_t t0 = (uint64_t)blockIdx.x * worker.kTokens; t0 < a.rows;
+         t0 += (uint64_t)blocks * worker.kTokens) {
+        const uint64_t t = t0 + worker.token;
         if (t >= a.rows) break;
-        T *const y = static_cast<T *>(a.out) + t * a.out_stride;
-        const T *const res = static_cast<const T *>(a.residual) + t * a.residual_stride;
-        for (uint64_t at64 = (blockIdx.y * (uint64_t)Lanes + lane) * N; at64 < a.cols;
-             at64 += (uint64_t)gridDim.y * Lanes * N) {
-            const uint32_t at = (uint32_t)at64;
-            Wide sum(0.0f);
-            if (a.residual) sum = Vec<T>::widen(settle<T>(load_vec<T, true>(res, a.cols, at), a.cols, at));
-            for (uint32_t j = 0; j < a.top; ++j) {
-                const int32_t s = place_of(a, t, j);
-                if (s < 0) continue;
-                const T *const z = static_cast<const T *>(a.z) + (uint64_t)(uint32_t)s * a.z_stride;
-                const Wide v = Vec<T>::widen(settle<T>(load_vec<T, true>(z, a.cols, at), a.cols, at));
-                const float w = a.weights ? a.weights[t * a.top + j] : 1.0f;
+        const Slots slots(a, t);
+        const Weights weights(a, t);
+        for (uint64_t first = 0; first < a.cols; first += Cols::kCols) {
+            const Cols part(first, a.cols, worker.place);
+            u32x4 r[U];
+            if (a.residual)
 #pragma unroll
-                for (uint32_t k = 0; k < N; ++k) sum[k] = __builtin_fmaf(w, v[k], sum[k]);
+                for (uint32_t u = 0; u < U; ++u)
+                    r[u] = part.template load<true>(a.residual, t, a.residual_stride, u);
+            Wide sum[U];
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u) sum[u] = Wide(0.0f);
+            for (uint32_t j0 = 0; j0 < a.top; j0 += C) {
+                u32x4 v[C][U];
+#pragma unroll
+                for (uint32_t c = 0; c < C; ++c)
+                    if (slots.of(j0 + c) >= 0)
+#pragma unroll
+                        for (uint32_t u = 0; u < U; ++u)
+                            v[c][u] = part.template load<true>(a.z, (uint32_t)slots.of(j0 + c),
+                                                               a.z_stride, u);
+#pragma unroll
+                for (uint32_t c = 0; c < C; ++c)
+                    if (slots.of(j0 + c) >= 0) {
+                        const float w = weights.of(j0 + c);
+#pragma unroll
+                        for (uint32_t u = 0; u < U; ++u) {
+                            const Wide z = Vec<T>::widen(v[c][u]);
+#pragma unroll
+                            for (uint32_t k = 0; k < Cols::N; ++k)
+                                sum[u][k] = __builtin_fmaf(w, z[k], sum[u][k]);
+                        }
+                    }
             }
-            store_vec(y, a.cols, at, Vec<T>::narrow(sum));
+            if (a.residual)
+#pragma unroll
+                for (uint32_t u = 0; u < U; ++u) sum[u] += Vec<T>::widen(r[u]);
+            // (y may be the residual: a piece's other elements may hold sums)
+            T *const y = part.row(a.out, t, a.out_stride);
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u)
+                store_own(y, part.cols, part.piece(u), Vec<T>::narrow(sum[u]));
         }
     }
 }
 
-// dz and the weights' gradients: one choice after another, the token's dy
-// again for each (from the caches).
-template <typename T, uint32_t Lanes>
+// dz and the weights' gradients, C choices of U vectors at a time; dy is read
+// again for each C choices.
+template <typename T, uint32_t Waves, uint32_t C, uint32_t U, bool Tiny>
 __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_grad_kernel(ExpertsMoveArgs a,
                                                                             uint32_t blocks)
 {
-    constexpr uint32_t N = Vec<T>::N, kTokens = kMoveBlock / Lanes;
+    using Cols = Stretch<T, Waves * 64, U, Tiny>;
     using Wide = typename Vec<T>::wide;
-    __shared__ float scratch[2][kMoveBlock / 64];
+    // two sets, used in turn: a wave is at most one barrier ahead of another
+    __shared__ float scratch[2][kMoveWaves][C];
     if (blockIdx.x >= blocks) {
-        clear_padding<T>(a, blockIdx.x - blocks);
+        clear_padding<T, Tiny>(a, blockIdx.x - blocks);
         return;
     }
-    const uint32_t lane = threadIdx.x % Lanes;
+    const Worker<Waves> worker;
+    const uint32_t lane = threadIdx.x % 64;
     int set = 0;
-    for (uint64_t t0 = (uint64_t)blockIdx.x * kTokens; t0 < a.rows; t0 += (uint64_t)blocks * kTokens) {
-        const uint64_t t = t0 + threadIdx.x / Lanes;
-        const bool live = t < a.rows;
-        const T *const dy = static_cast<const T *>(a.in) + t * a.in_stride;
-        for (uint32_t j = 0; j < a.top; ++j, set ^= 1) {
-            const int32_t s = live ? place_of(a, t, j) : -1;
-            float dot = 0.0f;
-            if (s >= 0) {
-                const T *const z = static_cast<const T *>(a.z) + (uint64_t)(uint32_t)s * a.z_stride;
-                T *const dz = static_cast<T *>(a.out) + (uint64_t)(uint32_t)s * a.out_stride;
-                const float w = a.weights[t * a.top + j];
-                for (uint64_t at64 = lane * N; at64 < a.cols; at64 += Lanes * N) {
-                    const uint32_t at = (uint32_t)at64;
-                    const Wide g = Vec<T>::widen(settle<T>(load_vec<T, false>(dy, a.cols, at), a.cols, at));
-                    const Wide v = Vec<T>::widen(settle<T>(load_vec<T, true>(z, a.cols, at), a.cols, at));
+    // (a token that a block's waves share is the same in all of them: the barrier)
+    for (uint64_t t0 = (uint64_t)blockIdx.x * worker.kTokens; t0 < a.rows;
+         t0 += (uint64_t)blocks * worker.kTokens) {
+        const uint64_t t = t0 + worker.token;
+        if (t >= a.rows) break;
+        const Slots slots(a, t);
+        const Weights weights(a, t);
+        for (uint32_t j0 = 0; j0 < a.top; j0 += C, set ^= 1) {
+            float dots[C];
 #pragma unroll
-                    for (uint32_t k = 0; k < N; ++k) dot = __builtin_fmaf(g[k], v[k], dot);
-                    store_vec(dz, a.cols, at, Vec<T>::narrow(w * g));
+            for (uint32_t c = 0; c < C; ++c) dots[c] = 0.0f;
+            for (uint64_t first = 0; first < a.cols; first += Cols::kCols) {
+                const Cols part(first, a.cols, worker.place);
+                u32x4 d[U], v[C][U];
+#pragma unroll
+                for (uint32_t u = 0; u < U; ++u) d[u] = part.template load<false>(a.in, t, a.in_stride, u);
+#pragma unroll
+                for (uint32_t c = 0; c < C; ++c) {
+                    const int32_t s = slots.of(j0 + c);
+                    if (s >= 0)
+#pragma unroll
+                        for (uint32_t u = 0; u < U; ++u)
+                            v[c][u] = part.template load<true>(a.z, (uint32_t)s, a.z_stride, u);
+                }
+                Wide g[U];
+                u32x4 own[U];
+#pragma unroll
+                for (uint32_t u = 0; u < U; ++u) {
+                    g[u] = Vec<T>::widen(d[u]);
+                    own[u] = own_bits(part.cols, part.piece(u));
+                }
+#pragma unroll
+                for (uint32_t c = 0; c < C; ++c) {
+                    const int32_t s = slots.of(j0 + c);
+                    if (s < 0) continue;
+                    const float w = weights.of(j0 + c);
+                    T *const dz = part.row(a.out, (uint32_t)s, a.out_stride);
+#pragma unroll
+                    for (uint32_t u = 0; u < U; ++u) {
+                        const Wide z = Vec<T>::widen(v[c][u] & own[u]);
+#pragma unroll
+                        for (uint32_t k = 0; k < Cols::N; ++k) dots[c] = __builtin_fmaf(g[u][k], z[k], dots[c]);
+                        store_piece(dz, part.cols, part.piece(u), Vec<T>::narrow(w * g[u]));
+                    }
                 }
             }
-            if constexpr (Lanes <= 64) {
+            float mine = 0.0f;             // choice j0 + c in lane c
 #pragma unroll
-                for (uint32_t d = 1; d < Lanes; d *= 2) dot += __shfl_xor(dot, (int)d);
-            } else {
-                dot = block_reduce<Sum, kMoveBlock / 64>(dot, scratch[set]);
+            for (uint32_t c = 0; c < C; ++c) {
+                const float dot = wave_reduce<Sum>(dots[c]);
+                if (lane == c) mine = dot;
             }
-            if (live && lane == 0) a.dweights[t * a.top + j] = dot;
+            if constexpr (Waves > 1) {
+                if (lane < C) scratch[set][threadIdx.x / 64][lane] = mine;
+                __syncthreads();
+                if (threadIdx.x < C) {
+                    mine = scratch[set][0][lane];
+#pragma unroll
+                    for (uint32_t w = 1; w < Waves; ++w) mine += scratch[set][w][lane];
+                }
+            }
+            if (worker.place < C && j0 + worker.place < a.top)
+                a.dweights[t * a.top + j0 + worker.place] = mine;
         }
     }
 }
@@ -316,9 +489,11 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_grad_kernel(Exp
 // ---------------------------------------------------------------------------
 
 // One block sorts up to this many entries.
-constexpr uint64_t kOneSort = 8192;
+constexpr uint32_t kOneSort = 8192;
 // Blocks of a larger sorting: each adds up all the others' counts.
-constexpr uint64_t kSortBlocks = 128;
+constexpr uint32_t kSortBlocks = 64;
+// Counters of a block's waves: 32 KB of LDS.
+constexpr uint32_t kCounters = 8192;
 
 size_t experts_sort_workspace(uint64_t entries, uint64_t experts)
 {
@@ -327,74 +502,98 @@ size_t experts_sort_workspace(uint64_t entries, uint64_t experts)
 
 hipError_t launch_experts_sort(RowType, const ExpertsSortArgs &a, hipStream_t s, const char **path)
 {
-    uint32_t bits = 0;
-    while ((1u << bits) < a.cols) ++bits;
+    const uint32_t experts = a.cols;
+    SortSplit split{};
+    while ((1u << split.bits) < experts) ++split.bits;
+    const uint32_t most = kCounters / experts < 16 ? kCounters / experts : 16;    // 8 or more
+    const auto waves_for = [&](uint32_t entries) {
+        const uint32_t n = (entries + 63) / 64;
+        split.waves = n < 1 ? 1 : n < most ? n : most;
+        split.per = ((entries + split.waves - 1) / split.waves + 63) / 64 * 64;
+        split.chunk = entries;
+        // threads enough for an expert each, in whole waves, a power of two
+        uint32_t threads = 64;
+        while (threads < 1024 && (threads < split.waves * 64 || threads < experts)) threads *= 2;
+        return threads;
+    };
     if (a.rows <= kOneSort) {
         *path = "one block";
-        // 32 KB of counters at most
-        const uint32_t waves = a.cols <= 512 ? 16 : 8, block = waves * 64;
-        const uint32_t chunk = (a.rows + block - 1) / block * block;
-        return start(waves == 16 ? reinterpret_cast<const void *>(&ew_experts_sort_kernel<16, true>)
-                                 : reinterpret_cast<const void *>(&ew_experts_sort_kernel<8, true>),
-                     dim3(1), block, waves * a.cols * sizeof(uint32_t), s, a, chunk, bits,
+        const uint32_t threads = waves_for(a.rows);
+        return start(split.per <= kHeld * 64
+                         ? reinterpret_cast<const void *>(&ew_experts_sort_kernel<true, true>)
+                         : reinterpret_cast<const void *>(&ew_experts_sort_kernel<true, false>),
+                     dim3(1), threads, split.waves * experts * sizeof(uint32_t), s, a, split,
                      (const uint32_t *)nullptr);
     }
     *path = "counts, then places";
-    const uint64_t per = ((uint64_t)a.rows + kSortBlocks - 1) / kSortBlocks;
-    const uint32_t chunk = (uint32_t)((per + kSortBlock - 1) / kSortBlock * kSortBlock);
-    const uint32_t blocks = (a.rows + chunk - 1) / chunk;
-    const size_t lds = kSortWaves * a.cols * sizeof(uint32_t);
+    const uint32_t chunk = ((a.rows + kSortBlocks - 1) / kSortBlocks + 1023) / 1024 * 1024;
+    const uint32_t blocks = (a.rows + chunk - 1) / chunk, threads = waves_for(chunk);
+    const bool held = split.per <= kHeld * 64;
+    const size_t lds = split.waves * experts * sizeof(uint32_t);
     uint32_t *const totals = static_cast<uint32_t *>(a.workspace);
-    const hipError_t e = start(reinterpret_cast<const void *>(&ew_experts_count_kernel), dim3(blocks),
-                               kSortBlock, lds, s, a, chunk, bits, totals);
+    const hipError_t e =
+        start(held ? reinterpret_cast<const void *>(&ew_experts_count_kernel<true>)
+                   : reinterpret_cast<const void *>(&ew_experts_count_kernel<false>),
+              dim3(blocks), threads, lds, s, a, split, totals);
     if (e != hipSuccess) return e;
-    return start(reinterpret_cast<const void *>(&ew_experts_sort_kernel<kSortWaves, false>), dim3(blocks),
-                 kSortBlock, lds, s, a, chunk, bits, (const uint32_t *)totals);
+    return start(held ? reinterpret_cast<const void *>(&ew_experts_sort_kernel<false, true>)
+                      : reinterpret_cast<const void *>(&ew_experts_sort_kernel<false, false>),
+                 dim3(blocks), threads, lds + 2 * threads * sizeof(uint32_t), s, a, split,
+                 (const uint32_t *)totals);
 }
 
-// Lanes of a token: 16, 64 or the block.
-#define EW_MOVE_KERNEL(t, K, lanes)                                                             \
-    ((lanes) == 16   ? ((t) == kRowF32   ? reinterpret_cast<const void *>(&K<float, 16>)        \
-                        : (t) == kRowF16 ? reinterpret_cast<const void *>(&K<_Float16, 16>)     \
-                                         : reinterpret_cast<const void *>(&K<__bf16, 16>))      \
-     : (lanes) == 64 ? ((t) == kRowF32   ? reinterpret_cast<const void *>(&K<float, 64>)        \
-                        : (t) == kRowF16 ? reinterpret_cast<const void *>(&K<_Float16, 64>)     \
-                                         : reinterpret_cast<const void *>(&K<__bf16, 64>))      \
-                     : ((t) == kRowF32   ? reinterpret_cast<const void *>(&K<float, 256>)       \
-                        : (t) == kRowF16 ? reinterpret_cast<const void *>(&K<_Float16, 256>)    \
-                                         : reinterpret_cast<const void *>(&K<__bf16, 256>)))
+// The kernel of a type for rows that a block shares (each), those that a wave
+// takes, and those shorter than a vector.
+#define EW_MOVE_OF(T, K, W, TINY, ...) K<T, W, ##__VA_ARGS__, TINY>
+#define EW_MOVE_BY_TYPE(t, K, W, TINY, ...)                                                            \
+    ((t) == kRowF32   ? reinterpret_cast<const void *>(&EW_MOVE_OF(float, K, W, TINY, ##__VA_ARGS__))    \
+     : (t) == kRowF16 ? reinterpret_cast<const void *>(&EW_MOVE_OF(_Float16, K, W, TINY, ##__VA_ARGS__)) \
+                      : reinterpret_cast<const void *>(&EW_MOVE_OF(__bf16, K, W, TINY, ##__VA_ARGS__)))
+#define EW_MOVE_KERNEL(t, split, K, ...)                                      \
+    ((split).each   ? EW_MOVE_BY_TYPE(t, K, kMoveWaves, false, ##__VA_ARGS__) \
+     : (split).tiny ? EW_MOVE_BY_TYPE(t, K, 1, true, ##__VA_ARGS__)           \
+                    : EW_MOVE_BY_TYPE(t, K, 1, false, ##__VA_ARGS__))
 
-static uint32_t move_lanes(uint32_t vectors) { return vectors <= 16 ? 16 : vectors <= 64 ? 64 : kMoveBlock; }
+struct MoveSplit {
+    bool each, tiny;      // a block a token; rows shorter than a vector
+    uint32_t blocks;      // of tokens
+};
 
-static uint32_t token_blocks(uint64_t rows, uint32_t lanes)
+// A block shares a token where its row has more than four vectors a lane of a
+// wave; of few tokens, more than one.
+static MoveSplit move_split(RowType t, const ExpertsMoveArgs &a, const char **path)
 {
-    const uint64_t per = kMoveBlock / lanes;
-    return row_blocks((rows + per - 1) / per);
+    const uint32_t vectors = vectors_of(t, a.cols);
+    MoveSplit m;
+    m.each = vectors > (a.rows < 1024 ? 64u : 256u);
+    m.tiny = a.cols < 16 / (uint32_t)row_elem_size(t);
+    m.blocks = row_blocks(m.each ? a.rows : ((uint64_t)a.rows + kMoveWaves - 1) / kMoveWaves);
+    *path = m.each ? "a block a token" : m.tiny ? "short rows" : "a wave a token";
+    return m;
 }
 
 hipError_t launch_experts_gather(RowType t, const ExpertsMoveArgs &a, hipStream_t s, const char **path)
 {
-    *path = "by tokens";
-    const uint32_t lanes = move_lanes(vectors_of(t, a.cols)), blocks = token_blocks(a.rows, lanes);
-    return start(EW_MOVE_KERNEL(t, ew_experts_gather_kernel, lanes), dim3(blocks + a.experts), kMoveBlock,
-                 0, s, a, blocks);
+    const MoveSplit m = move_split(t, a, path);
+    return start(EW_MOVE_KERNEL(t, m, ew_experts_gather_kernel), dim3(m.blocks + a.experts), kMoveBlock,
+                 0, s, a, m.blocks);
 }
 
 hipError_t launch_experts_combine(RowType t, const ExpertsMoveArgs &a, hipStream_t s, const char **path)
 {
-    *path = "by tokens";
-    const uint32_t lanes = move_lanes(vectors_of(t, a.cols)), blocks = token_blocks(a.rows, lanes);
-    return start(EW_MOVE_KERNEL(t, ew_experts_combine_kernel, lanes), dim3(blocks), kMoveBlock, 0, s, a,
-                 blocks);
+    const MoveSplit m = move_split(t, a, path);
+    return start(a.top <= 2 ? EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 2, 4)
+                            : EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 8, 1),
+                 dim3(m.blocks), kMoveBlock, 0, s, a, m.blocks);
 }
 
 hipError_t launch_experts_combine_grad(RowType t, const ExpertsMoveArgs &a, hipStream_t s,
                                        const char **path)
 {
-    *path = "by tokens";
-    const uint32_t lanes = move_lanes(vectors_of(t, a.cols)), blocks = token_blocks(a.rows, lanes);
-    return start(EW_MOVE_KERNEL(t, ew_experts_combine_grad_kernel, lanes), dim3(blocks + a.experts),
-                 kMoveBlock, 0, s, a, blocks);
+    const MoveSplit m = move_split(t, a, path);
+    return start(a.top <= 2 ? EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 2, 4)
+                            : EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 8, 1),
+                 dim3(m.blocks + a.experts), kMoveBlock, 0, s, a, m.blocks);
 }
 
 }  // namespace ew

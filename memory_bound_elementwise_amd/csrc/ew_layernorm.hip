@@ -30,96 +30,93 @@ struct Mean {
     __device__ explicit Mean(double m) : hi((float)m), lo((float)(m - (double)(float)m)) {}
 };
 
-// Sum of one value a wave (scratch[0 .. Waves)) in all lanes: of eight or
-// sixteen by lane exchanges, which hold one of them in a register, not all.
-template <int Waves>
-__device__ __forceinline__ double join_waves(const double *scratch)
+// sum / n, by = 1 / n: exact where the quotient is a binary64 number (a row of
+// equal values), without the steps of a division.
+__device__ __forceinline__ double divide(double sum, uint32_t n, double by)
 {
-    if constexpr (Waves == 8 || Waves == 16) {
-        double x = scratch[threadIdx.x % Waves];
-        x += dpp64<0xB1>(x);
-        x += dpp64<0x4E>(x);
-        x += dpp64<0x141>(x);
-        if constexpr (Waves == 16) x += dpp64<0x140>(x);
-        return x;
-    }
-    double x = scratch[0];
-#pragma unroll
-    for (int w = 1; w < Waves; ++w) x += scratch[w];
+    const double q = sum * by;
+    return __builtin_fma(__builtin_fma(-q, (double)n, sum), by, q);
+}
+
+// Sum of one value a wave (x in lanes w, w + Waves, ...) in all lanes: of a
+// power of two of them by lane exchanges.
+template <int Waves>
+__device__ __forceinline__ double sum_of_waves(double x)
+{
+    if constexpr (Waves > 1) x += dpp64<0xB1>(x);
+    if constexpr (Waves > 2) x += dpp64<0x4E>(x);
+    if constexpr (Waves > 4) x += dpp64<0x141>(x);
+    if constexpr (Waves > 8) x += dpp64<0x140>(x);
     return x;
 }
-
 template <int Waves>
-__device__ __forceinline__ float join_waves(const float *scratch)
+__device__ __forceinline__ float sum_of_waves(float x)
 {
-    if constexpr (Waves == 8 || Waves == 16) {
-        float x = quad_reduce<Sum>(scratch[threadIdx.x % Waves]);
-        x += dpp<0x141>(x);
-        if constexpr (Waves == 16) x += dpp<0x140>(x);
-        return x;
-    }
-    float x = scratch[0];
-#pragma unroll
-    for (int w = 1; w < Waves; ++w) x += scratch[w];
+    if constexpr (Waves > 1) x += dpp<0xB1>(x);
+    if constexpr (Waves > 2) x += dpp<0x4E>(x);
+    if constexpr (Waves > 4) x += dpp<0x141>(x);
+    if constexpr (Waves > 8) x += dpp<0x140>(x);
     return x;
 }
+// Lanes that hold the values of so many waves: the power of two above.
+constexpr uint32_t lanes_of_waves(int waves) { return waves > 8 ? 16 : waves > 4 ? 8 : waves > 2 ? 4 : waves; }
 
-// Sum over a row's Waves waves in all of them.  scratch: the row's own.
-template <int Waves>
-__device__ __forceinline__ double row_sum(double x, double *scratch)
-{
-    x = wave_sum64(x);
-    if constexpr (Waves > 1) {
-        if (threadIdx.x % 64 == 0) scratch[threadIdx.x / 64 % Waves] = x;
-        __syncthreads();
-        x = join_waves<Waves>(scratch);
-    }
-    return x;
-}
+// What a wave knows of its elements of a row: a number near them, and the sums
+// of the differences from it and of their squares.  The number is the wave's
+// own mean, taken from its first element, so that neither rows far from 0 nor
+// an outlier cost bits, and a row of equal values gives differences of 0.
+struct WaveSums {
+    float near, sum, squares;
+};
 
-template <int Waves>
-__device__ __forceinline__ float row_sum(float x, float *scratch)
-{
-    x = wave_reduce<Sum>(x);
-    if constexpr (Waves > 1) {
-        if (threadIdx.x % 64 == 0) scratch[threadIdx.x / 64 % Waves] = x;
-        __syncthreads();
-        x = join_waves<Waves>(scratch);
-    }
-    return x;
-}
-
-// Sum of a vector's elements in binary64.
-template <typename T>
-__device__ __forceinline__ double sum64(u32x4 v)
-{
-    const typename Vec<T>::wide f = Vec<T>::widen(v);
-    double a = f[0], b = f[1];
-#pragma unroll
-    for (int j = 2; j < Vec<T>::N; j += 2) {
-        a += (double)f[j];
-        b += (double)f[j + 1];
-    }
-    return a + b;
-}
-
-// Sum of the squares of a vector's differences from the mean, of those of its
-// elements that lie in the row.
-template <typename T>
-__device__ __forceinline__ float squares(u32x4 v, const Mean &m, uint32_t cols, uint32_t at)
+template <typename T, int V, bool Tiny, class At>
+__device__ __forceinline__ WaveSums wave_sums(const u32x4 (&h)[V], uint32_t cols, uint32_t n, At piece)
 {
     constexpr uint32_t N = Vec<T>::N;
-    if (at >= cols) return 0.0f;
-    typename Vec<T>::wide d = (Vec<T>::widen(v) - m.hi) - m.lo;
-    if (at + N > cols) {
+    using Wide = typename Vec<T>::wide;
+    const float start = lane_value(Vec<T>::widen(h[0])[0], 0);
+    const float by = n ? 1.0f / (float)n : 0.0f;
+    // differences from x of a lane's own elements, 0 for others
+    const auto own = [&](int k, float x) {
+        Wide d = Vec<T>::widen(h[k]) - x;
+        const Piece<T, Tiny> p = piece(k);
+        if (Tiny || !p.live || p.skip) {
 #pragma unroll
-        for (uint32_t j = 0; j < N; ++j)
-            if (at + j >= cols) d[j] = 0.0f;
-    }
+            for (uint32_t j = 0; j < N; ++j)
+                if (!p.live || !p.own(j, cols)) d[j] = 0.0f;
+        }
+        return d;
+    };
     float sum = 0.0f;
 #pragma unroll
-    for (uint32_t j = 0; j < N; ++j) sum = __builtin_fmaf(d[j], d[j], sum);
-    return sum;
+    for (int k = 0; k < V; ++k) {
+        const Wide d = own(k, start);
+#pragma unroll
+        for (uint32_t j = 0; j < N; ++j) sum += d[j];
+    }
+    WaveSums w;
+    w.near = __builtin_fmaf(wave_reduce<Sum>(sum), by, start);
+    w.sum = 0.0f;
+    w.squares = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const Wide d = own(k, w.near);
+#pragma unroll
+        for (uint32_t j = 0; j < N; ++j) {
+            w.sum += d[j];
+            w.squares = __builtin_fmaf(d[j], d[j], w.squares);
+        }
+    }
+    w.sum = wave_reduce<Sum>(w.sum);
+    w.squares = wave_reduce<Sum>(w.squares);
+    return w;
+}
+
+// The squares about the row's mean of a wave of n elements.
+__device__ __forceinline__ float squares_about(const WaveSums &w, uint32_t n, double mean)
+{
+    const float off = (float)((double)w.near - mean);
+    return __builtin_fmaf(off, __builtin_fmaf(off, (float)n, 2.0f * w.sum), w.squares);
 }
 
 template <typename T>
@@ -143,7 +140,7 @@ __device__ __forceinline__ typename Vec<T>::wide affine(const void *p, u32x4 v, 
 // Forward, rows that fit in registers: Waves waves a row, V vectors a lane
 // ---------------------------------------------------------------------------
 
-template <typename T, int Waves, int V>
+template <typename T, int Waves, int V, bool Tiny = false>
 __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kernel(LayerNormArgs a)
 {
     constexpr uint32_t N = Vec<T>::N, kThreads = Waves * 64;
@@ -152,11 +149,20 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kerne
     // in registers
     constexpr bool kEarly = V < 3;
     // two sets, used in turn: a wave is at most one barrier ahead of another
-    __shared__ double sums[2][layernorm_block(Waves) / 64];
-    __shared__ float sqs[2][layernorm_block(Waves) / 64];
+    __shared__ WaveSums shared[2][layernorm_block(Waves) / 64];
     const uint32_t group = row_of_thread<kThreads, kRows>(), i = place_in_row<kThreads, kRows>();
     const T *const weight = static_cast<const T *>(a.weight), *const bias = static_cast<const T *>(a.bias);
-    const auto at = [&](int k) { return (i + k * kThreads) * N; };
+    const auto piece = [&](int k) { return Piece<T, Tiny>((i + k * kThreads) * N, a.cols); };
+    // elements of wave w of a row
+    const auto elements = [&](uint32_t w) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const uint32_t from = (w * 64 + k * kThreads) * N;
+            n += from >= a.cols ? 0 : a.cols - from < 64 * N ? a.cols - from : 64 * N;
+        }
+        return n;
+    };
     int set = 0;
     // a block's rows go round together (the barriers)
     for (uint64_t r0 = (uint64_t)blockIdx.x * kRows; r0 < a.rows;
@@ -166,16 +172,16 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kerne
         u32x4 h[V], w[V], b[V];
         const T *const x = static_cast<const T *>(a.x) + r * a.x_stride;
 #pragma unroll
-        for (int k = 0; k < V; ++k) h[k] = load_vec<T, true, true>(x, a.cols, at(k));
+        for (int k = 0; k < V; ++k) h[k] = load_piece<T, true>(x, a.cols, piece(k));
         const auto fetch_affine = [&](int k) {
-            if (weight) w[k] = load_vec<T, false, true>(weight, a.cols, at(k));
-            if (bias) b[k] = load_vec<T, false, true>(bias, a.cols, at(k));
+            if (weight) w[k] = load_piece<T, false>(weight, a.cols, piece(k));
+            if (bias) b[k] = load_piece<T, false>(bias, a.cols, piece(k));
         };
         if (a.residual) {
             const T *const p = static_cast<const T *>(a.residual) + r * a.residual_stride;
             u32x4 res[V];
 #pragma unroll
-            for (int k = 0; k < V; ++k) res[k] = load_vec<T, true, true>(p, a.cols, at(k));
+            for (int k = 0; k < V; ++k) res[k] = load_piece<T, true>(p, a.cols, piece(k));
             if constexpr (kEarly)
 #pragma unroll
                 for (int k = 0; k < V; ++k) fetch_affine(k);
@@ -186,25 +192,35 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kerne
 #pragma unroll
             for (int k = 0; k < V; ++k) fetch_affine(k);
         }
-        double sum = 0.0;
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            h[k] = settle<T>(h[k], a.cols, at(k));
-            sum += sum64<T>(h[k]);
+        const uint32_t wave = Waves > 1 ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(i / 64)) : 0;
+        WaveSums own = wave_sums<T, V, Tiny>(h, a.cols, elements(wave), piece);
+        double mean;
+        float sq;
+        if constexpr (Waves == 1) {
+            mean = divide((double)own.near * (double)a.cols + (double)own.sum, a.cols, a.by_cols);
+            sq = squares_about(own, a.cols, mean);
+        } else {
+            // the outputs may be the inputs: nothing is stored before every
+            // wave of the row has loaded (a row of one wave loads before it
+            // stores)
+            WaveSums *const sums = shared[set] + group * Waves;
+            if (threadIdx.x % 64 == 0) sums[wave] = own;
+            __syncthreads();
+            const uint32_t at = threadIdx.x % lanes_of_waves(Waves);
+            const bool some = at < (uint32_t)Waves;
+            const WaveSums of = sums[some ? at : 0];
+            const uint32_t n = some ? elements(at) : 0;
+            const double sum = n ? (double)of.near * (double)n + (double)of.sum : 0.0;
+            mean = divide(sum_of_waves<Waves>(sum), a.cols, a.by_cols);
+            sq = sum_of_waves<Waves>(n ? squares_about(of, n, mean) : 0.0f);
         }
-        // the outputs may be the inputs: nothing is stored before every wave
-        // of the row has loaded (a row of one wave loads before it stores)
-        const double m64 = row_sum<Waves>(sum, sums[set] + group * Waves) / (double)a.cols;
-        const Mean m(m64);
+        sq = sq < 0.0f ? 0.0f : sq;        // (a rounding below 0)
+        const Mean m(mean);
         if (live && a.total) {
             T *const total = static_cast<T *>(a.total) + r * a.total_stride;
 #pragma unroll
-            for (int k = 0; k < V; ++k) store_vec<T, true>(total, a.cols, at(k), h[k]);
+            for (int k = 0; k < V; ++k) store_piece(total, a.cols, piece(k), h[k]);
         }
-        float sq = 0.0f;
-#pragma unroll
-        for (int k = 0; k < V; ++k) sq += squares<T>(h[k], m, a.cols, at(k));
-        sq = row_sum<Waves>(sq, sqs[set] + group * Waves);
         const float rstd = 1.0f / __builtin_sqrtf(sq / (float)a.cols + a.eps);
         if (live && i == 0) {
             if (a.mean) a.mean[r] = m.hi;
@@ -215,9 +231,9 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kerne
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             if constexpr (!kEarly) fetch_affine(k);
-            const auto wide = affine<T>(weight, settle<T>(w[k], a.cols, at(k)), 1.0f);
-            const auto shift = affine<T>(bias, settle<T>(b[k], a.cols, at(k)), 0.0f);
-            store_vec<T, true>(y, a.cols, at(k), normed<T>(h[k], m, rstd, wide, shift));
+            store_piece(y, a.cols, piece(k),
+                        normed<T>(h[k], m, rstd, affine<T>(weight, w[k], 1.0f),
+                                  affine<T>(bias, b[k], 0.0f)));
         }
     }
 }
@@ -229,10 +245,27 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kerne
 constexpr int kLongBlock = 1024;
 constexpr int kLongWaves = kLongBlock / 64;
 
+// Sum over a block of kLongWaves waves, in all of them.
+__device__ __forceinline__ double long_sum(double x, double *scratch)
+{
+    x = wave_sum64(x);
+    if (threadIdx.x % 64 == 0) scratch[threadIdx.x / 64] = x;
+    __syncthreads();
+    return sum_of_waves<kLongWaves>(scratch[threadIdx.x % kLongWaves]);
+}
+__device__ __forceinline__ float long_sum(float x, float *scratch)
+{
+    x = wave_reduce<Sum>(x);
+    if (threadIdx.x % 64 == 0) scratch[threadIdx.x / 64] = x;
+    __syncthreads();
+    return sum_of_waves<kLongWaves>(scratch[threadIdx.x % kLongWaves]);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kLongBlock) ew_layernorm_long_kernel(LayerNormArgs a)
 {
     constexpr uint32_t N = Vec<T>::N;
+    using Wide = typename Vec<T>::wide;
     __shared__ double sums[2][kLongWaves];
     __shared__ float sqs[2][kLongWaves];
     const T *const weight = static_cast<const T *>(a.weight), *const bias = static_cast<const T *>(a.bias);
@@ -242,30 +275,31 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_long_kernel(LayerNorm
         const T *const res =
             a.residual ? static_cast<const T *>(a.residual) + r * a.residual_stride : nullptr;
         T *const total = a.total ? static_cast<T *>(a.total) + r * a.total_stride : nullptr;
-        const auto value = [&](uint32_t at) {
-            u32x4 h = settle<T>(load_vec<T, false>(x, a.cols, at), a.cols, at);
-            if (res)
-                h = Vec<T>::narrow(Vec<T>::widen(h) + Vec<T>::widen(settle<T>(
-                                       load_vec<T, false>(res, a.cols, at), a.cols, at)));
-            return h;
+        const auto value = [&](const LongPiece<T> &p) {
+            const u32x4 h = p.template load<false>(x);
+            return res ? Vec<T>::narrow(Vec<T>::widen(h) + Vec<T>::widen(p.template load<false>(res))) : h;
         };
         // (the first pass stores total where its thread reads it back: total
         // may be x or residual)
-        const auto again = [&](uint32_t at) {
-            return total ? settle<T>(load_vec<T, false>(total, a.cols, at), a.cols, at) : value(at);
-        };
+        const auto again = [&](const LongPiece<T> &p) { return total ? p.template load<false>(total) : value(p); };
         double sum = 0.0;
         for (uint32_t at = threadIdx.x * N; at < a.cols; at += kLongBlock * N) {
-            const u32x4 h = value(at);
-            sum += sum64<T>(h);
-            if (total) store_vec(total, a.cols, at, h);
+            const LongPiece<T> p(at, a.cols);
+            const u32x4 h = value(p);
+            const Wide f = Vec<T>::widen(h);
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j) sum += j >= p.p.skip ? (double)f[j] : 0.0;
+            if (total) p.store(total, h);
         }
-        const double m64 = row_sum<kLongWaves>(sum, sums[set]) / (double)a.cols;
-        const Mean m(m64);
+        const Mean m(divide(long_sum(sum, sums[set]), a.cols, a.by_cols));
         float sq = 0.0f;
-        for (uint32_t at = threadIdx.x * N; at < a.cols; at += kLongBlock * N)
-            sq += squares<T>(again(at), m, a.cols, at);
-        sq = row_sum<kLongWaves>(sq, sqs[set]);
+        for (uint32_t at = threadIdx.x * N; at < a.cols; at += kLongBlock * N) {
+            const LongPiece<T> p(at, a.cols);
+            const Wide d = (Vec<T>::widen(again(p)) - m.hi) - m.lo;
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j) sq = j >= p.p.skip ? __builtin_fmaf(d[j], d[j], sq) : sq;
+        }
+        sq = long_sum(sq, sqs[set]);
         const float rstd = 1.0f / __builtin_sqrtf(sq / (float)a.cols + a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[r] = m.hi;
@@ -273,11 +307,11 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_long_kernel(LayerNorm
         }
         T *const y = static_cast<T *>(a.y) + r * a.y_stride;
         for (uint32_t at = threadIdx.x * N; at < a.cols; at += kLongBlock * N) {
+            const LongPiece<T> p(at, a.cols);
             u32x4 w{}, b{};
-            if (weight) w = settle<T>(load_vec<T, false>(weight, a.cols, at), a.cols, at);
-            if (bias) b = settle<T>(load_vec<T, false>(bias, a.cols, at), a.cols, at);
-            store_vec(y, a.cols, at, normed<T>(again(at), m, rstd, affine<T>(weight, w, 1.0f),
-                                               affine<T>(bias, b, 0.0f)));
+            if (weight) w = p.template load<false>(weight);
+            if (bias) b = p.template load<false>(bias);
+            p.store(y, normed<T>(again(p), m, rstd, affine<T>(weight, w, 1.0f), affine<T>(bias, b, 0.0f)));
         }
     }
 }
@@ -293,26 +327,26 @@ constexpr uint32_t kParts = 256;
 // Floats of one part's sums of dweight (those of dbias follow): whole vectors.
 __host__ __device__ constexpr uint64_t sums_pitch(uint64_t cols) { return (cols + 7) & ~(uint64_t)7; }
 
-// Two sums over a row's Waves waves with one barrier.
-template <int Waves>
-__device__ __forceinline__ void row_sum2(float &x, float &y, float *xs, float *ys)
+// A piece's sums over rows to a row of floats (elements that two pieces hold
+// have the same sums in both).
+template <typename T, bool Tiny>
+__device__ __forceinline__ void store_sums(float *row, uint32_t cols, const Piece<T, Tiny> &p,
+                                           typename Vec<T>::wide v)
 {
-    x = wave_reduce<Sum>(x);
-    y = wave_reduce<Sum>(y);
-    if constexpr (Waves > 1) {
-        if (threadIdx.x % 64 == 0) {
-            xs[threadIdx.x / 64 % Waves] = x;
-            ys[threadIdx.x / 64 % Waves] = y;
-        }
-        __syncthreads();
-        x = join_waves<Waves>(xs);
-        y = join_waves<Waves>(ys);
+    typedef float Sums __attribute__((ext_vector_type(Vec<T>::N), aligned(4)));
+    if (!p.live) return;
+    if constexpr (Tiny) {
+#pragma unroll
+        for (uint32_t j = 0; j < Vec<T>::N; ++j)
+            if (j < cols) row[j] = v[j];
+    } else {
+        *reinterpret_cast<Sums *>(row + p.first) = v;
     }
 }
 
 // Rows that fit in registers: Waves waves a row, V vectors a lane, Groups rows
 // at a time in a block, which adds up dweight and dbias over its rows.
-template <typename T, int Waves, int V, int Groups>
+template <typename T, int Waves, int V, int Groups, bool Tiny = false>
 __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(LayerNormGradArgs a)
 {
     constexpr uint32_t N = Vec<T>::N, kThreads = Waves * 64;
@@ -324,11 +358,10 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
     // stays, unless they would not fit in registers
     constexpr bool kAhead = V < 3;
     const T *const weight = static_cast<const T *>(a.weight);
-    const auto at = [&](int k) { return (i + k * kThreads) * N; };
+    const auto piece = [&](int k) { return Piece<T, Tiny>((i + k * kThreads) * N, a.cols); };
     u32x4 wv[kAhead ? V : 1];
     const auto fetch_weight = [&](int k) {
-        return weight ? settle<T>(load_vec<T, false, true>(weight, a.cols, at(k)), a.cols, at(k))
-                      : u32x4{};
+        return weight ? load_piece<T, false>(weight, a.cols, piece(k)) : u32x4{};
     };
     if constexpr (kAhead)
 #pragma unroll
@@ -339,7 +372,7 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
     const auto fetch = [&](u32x4 (&v)[V], const void *p, uint64_t first) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            v[k] = load_vec<T, true, true>(static_cast<const T *>(p) + first, a.cols, at(k));
+            v[k] = load_piece<T, true>(static_cast<const T *>(p) + first, a.cols, piece(k));
     };
     Wide dw[V], db[V];
 #pragma unroll
@@ -369,8 +402,8 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
         u32x4 dyv[V], xv[V], dtv[kAhead ? V : 1];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            dyv[k] = settle<T>(dy[k], a.cols, at(k));
-            xv[k] = settle<T>(x[k], a.cols, at(k));
+            dyv[k] = dy[k];
+            xv[k] = x[k];
             if constexpr (kAhead) dtv[k] = dt[k];
         }
         if constexpr (kAhead)
@@ -378,22 +411,37 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
         float first = 0.0f, second = 0.0f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            // (past the row dy is 0)
+            const Piece<T, Tiny> p = piece(k);
+            // (past a tiny row and in dead pieces dy is 0)
             const Wide d = Vec<T>::widen(dyv[k]), h = (Vec<T>::widen(xv[k]) - mu) * rs;
-            const Wide g = d * factor(k);
+            Wide g = d * factor(k);
+            if (live) {
+                dw[k] += d * h;
+                db[k] += d;
+            }
+            if (p.skip) {        // the elements that are another piece's too
+                g = Vec<T>::widen(dyv[k] & own_bits(a.cols, p)) * factor(k);
+            }
 #pragma unroll
             for (uint32_t j = 0; j < N; ++j) {
                 first += g[j];
                 second = __builtin_fmaf(g[j], h[j], second);
             }
-            if (live) {
-                dw[k] += d * h;
-                db[k] += d;
-            }
         }
         // dx may be an input: nothing is stored before every wave of the row
         // has loaded
-        row_sum2<Waves>(first, second, firsts[set] + group * Waves, seconds[set] + group * Waves);
+        first = wave_reduce<Sum>(first);
+        second = wave_reduce<Sum>(second);
+        if constexpr (Waves > 1) {
+            const uint32_t wave = group * Waves + i / 64, at = threadIdx.x % Waves;
+            if (threadIdx.x % 64 == 0) {
+                firsts[set][wave] = first;
+                seconds[set][wave] = second;
+            }
+            __syncthreads();
+            first = sum_of_waves<Waves>(firsts[set][group * Waves + at]);
+            second = sum_of_waves<Waves>(seconds[set][group * Waves + at]);
+        }
         first /= (float)a.cols;
         second /= (float)a.cols;
         if (!live) continue;
@@ -403,13 +451,12 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
             const Wide h = (Vec<T>::widen(xv[k]) - mu) * rs;
             Wide g = rs * ((Vec<T>::widen(dyv[k]) * factor(k) - first) - h * second);
             if (a.dtotal) {
-                const u32x4 v = kAhead ? dtv[kAhead ? k : 0]
-                                       : load_vec<T, true, true>(static_cast<const T *>(a.dtotal) +
-                                                                    r * a.dtotal_stride,
-                                                                a.cols, at(k));
-                g += Vec<T>::widen(settle<T>(v, a.cols, at(k)));
+                if constexpr (kAhead) g += Vec<T>::widen(dtv[k]);
+                else
+                    g += Vec<T>::widen(load_piece<T, true>(
+                        static_cast<const T *>(a.dtotal) + r * a.dtotal_stride, a.cols, piece(k)));
             }
-            store_vec<T, true>(dx, a.cols, at(k), Vec<T>::narrow(g));
+            store_piece(dx, a.cols, piece(k), Vec<T>::narrow(g));
         }
     }
     if (!a.dweight && !a.dbias) return;
@@ -434,24 +481,14 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
         join(db);
     }
     if (group != 0) return;
-    const bool only = gridDim.x == 1;      // the one part is the sum
-    // the workspace is 16-byte aligned, a vector of sums of 16-bit data is 32 bytes
-    typedef float Sums __attribute__((ext_vector_type(N), aligned(16)));
+    // the one part of a small call is the sum
     float *const part = static_cast<float *>(a.workspace) + blockIdx.x * (2 * sums_pitch(a.cols));
+    float *const to_w = gridDim.x == 1 ? a.dweight : part;
+    float *const to_b = gridDim.x == 1 ? a.dbias : part + sums_pitch(a.cols);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        const uint32_t c = at(k);
-        if (only) {
-#pragma unroll
-            for (uint32_t j = 0; j < N; ++j)
-                if (c + j < a.cols) {
-                    if (a.dweight) a.dweight[c + j] = dw[k][j];
-                    if (a.dbias) a.dbias[c + j] = db[k][j];
-                }
-        } else if (c < a.cols) {
-            *reinterpret_cast<Sums *>(part + c) = dw[k];
-            *reinterpret_cast<Sums *>(part + sums_pitch(a.cols) + c) = db[k];
-        }
+        if (to_w) store_sums<T, Tiny>(to_w, a.cols, piece(k), dw[k]);
+        if (to_b) store_sums<T, Tiny>(to_b, a.cols, piece(k), db[k]);
     }
 }
 
@@ -496,22 +533,20 @@ template <typename T>
 __global__ void __launch_bounds__(kColsBlock) ew_layernorm_cols_kernel(LayerNormGradArgs a,
                                                                       uint32_t parts)
 {
-    constexpr uint32_t N = Vec<T>::N;
     using Wide = typename Vec<T>::wide;
-    const uint32_t at = (blockIdx.x * kColsBlock + threadIdx.x) * N;
+    const uint32_t at = (blockIdx.x * kColsBlock + threadIdx.x) * Vec<T>::N;
     if (at >= a.cols) return;
+    const LongPiece<T> p(at, a.cols);
     Wide dw(0.0f), db(0.0f);
     for (uint64_t r = blockIdx.y; r < a.rows; r += parts) {
-        const u32x4 dy = load_vec<T, true>(static_cast<const T *>(a.dy) + r * a.dy_stride, a.cols, at);
-        const u32x4 x = load_vec<T, true>(static_cast<const T *>(a.x) + r * a.x_stride, a.cols, at);
-        const Wide d = Vec<T>::widen(settle<T>(dy, a.cols, at));
-        dw += d * ((Vec<T>::widen(settle<T>(x, a.cols, at)) - a.mean[r]) * a.rstd[r]);
+        const Wide d = Vec<T>::widen(p.template load<true>(static_cast<const T *>(a.dy) + r * a.dy_stride));
+        const Wide x = Vec<T>::widen(p.template load<true>(static_cast<const T *>(a.x) + r * a.x_stride));
+        dw += d * ((x - a.mean[r]) * a.rstd[r]);
         db += d;
     }
-    typedef float Sums __attribute__((ext_vector_type(N), aligned(16)));
     float *const part = static_cast<float *>(a.workspace) + blockIdx.y * (2 * sums_pitch(a.cols));
-    *reinterpret_cast<Sums *>(part + at) = dw;
-    *reinterpret_cast<Sums *>(part + sums_pitch(a.cols) + at) = db;
+    store_sums<T, false>(part + p.first, a.cols, p.p, dw);
+    store_sums<T, false>(part + sums_pitch(a.cols) + p.first, a.cols, p.p, db);
 }
 
 template <typename T>
@@ -529,30 +564,36 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_dx_kernel(LayerNormGr
             a.dtotal ? static_cast<const T *>(a.dtotal) + r * a.dtotal_stride : nullptr;
         T *const dx = static_cast<T *>(a.dx) + r * a.dx_stride;
         const float mu = a.mean[r], rs = a.rstd[r];
-        const auto wide = [&](const T *p, uint32_t at) {
-            return Vec<T>::widen(settle<T>(load_vec<T, false>(p, a.cols, at), a.cols, at));
+        const auto slope = [&](const LongPiece<T> &p) {
+            const Wide d = Vec<T>::widen(p.template load<false>(dy));
+            return weight ? d * Vec<T>::widen(p.template load<false>(weight)) : d;
         };
-        const auto slope = [&](uint32_t at) {
-            const Wide d = wide(dy, at);
-            return weight ? d * wide(weight, at) : d;
-        };
+        const auto place = [&](const LongPiece<T> &p) { return (Vec<T>::widen(p.template load<false>(x)) - mu) * rs; };
         float first = 0.0f, second = 0.0f;
         for (uint32_t at = threadIdx.x * N; at < a.cols; at += kLongBlock * N) {
-            const Wide g = slope(at), h = (wide(x, at) - mu) * rs;
+            const LongPiece<T> p(at, a.cols);
+            const Wide g = slope(p), h = place(p);
 #pragma unroll
             for (uint32_t j = 0; j < N; ++j) {
-                first += g[j];
-                second = __builtin_fmaf(g[j], h[j], second);
+                const bool own = j >= p.p.skip;
+                first += own ? g[j] : 0.0f;
+                second = own ? __builtin_fmaf(g[j], h[j], second) : second;
             }
         }
-        row_sum2<kLongWaves>(first, second, firsts[set], seconds[set]);
-        first /= (float)a.cols;
-        second /= (float)a.cols;
+        first = wave_reduce<Sum>(first);
+        second = wave_reduce<Sum>(second);
+        if (threadIdx.x % 64 == 0) {
+            firsts[set][threadIdx.x / 64] = first;
+            seconds[set][threadIdx.x / 64] = second;
+        }
+        __syncthreads();
+        first = sum_of_waves<kLongWaves>(firsts[set][threadIdx.x % kLongWaves]) / (float)a.cols;
+        second = sum_of_waves<kLongWaves>(seconds[set][threadIdx.x % kLongWaves]) / (float)a.cols;
         for (uint32_t at = threadIdx.x * N; at < a.cols; at += kLongBlock * N) {
-            const Wide h = (wide(x, at) - mu) * rs;
-            Wide g = rs * ((slope(at) - first) - h * second);
-            if (dt) g += wide(dt, at);
-            store_vec(dx, a.cols, at, Vec<T>::narrow(g));
+            const LongPiece<T> p(at, a.cols);
+            Wide g = rs * ((slope(p) - first) - place(p) * second);
+            if (dt) g += Vec<T>::widen(p.template load<false>(dt));
+            p.store(dx, Vec<T>::narrow(g));
         }
     }
 }
@@ -565,11 +606,13 @@ template <typename T>
 static hipError_t layernorm_rows(const LayerNormArgs &a, uint32_t vectors, hipStream_t s)
 {
 #define EW_LAYERNORM_ROWS(W, V)                                                                  \
-    if (vectors <= W * 64 * V)                                                                   \
-        return start(reinterpret_cast<const void *>(&ew_layernorm_row_kernel<T, W, V>),          \
-                     dim3(row_blocks(((uint64_t)a.rows * W * 64 + layernorm_block(W) - 1) /      \
-                                     layernorm_block(W))),                                       \
-                     layernorm_block(W), 0, s, a);
+    if (vectors <= W * 64 * V) EW_LAYERNORM_LAUNCH(W, V, false)
+#define EW_LAYERNORM_LAUNCH(W, V, TINY)                                                          \
+    return start(reinterpret_cast<const void *>(&ew_layernorm_row_kernel<T, W, V, TINY>),        \
+                 dim3(row_blocks(((uint64_t)a.rows * W * 64 + layernorm_block(W) - 1) /          \
+                                 layernorm_block(W))),                                           \
+                 layernorm_block(W), 0, s, a);
+    if (a.cols < (uint32_t)Vec<T>::N) EW_LAYERNORM_LAUNCH(1, 1, true)
     EW_LAYERNORM_ROWS(1, 1)
     EW_LAYERNORM_ROWS(2, 1)
     EW_LAYERNORM_ROWS(3, 1)
@@ -585,6 +628,7 @@ static hipError_t layernorm_rows(const LayerNormArgs &a, uint32_t vectors, hipSt
         EW_LAYERNORM_ROWS(12, 4)
     }
 #undef EW_LAYERNORM_ROWS
+#undef EW_LAYERNORM_LAUNCH
     return hipErrorInvalidValue;
 }
 static uint32_t register_vectors(RowType t) { return (t == kRowF32 ? 16 : 12) * 64 * 4; }
@@ -615,14 +659,17 @@ template <typename T>
 static hipError_t layernorm_grad_rows(const LayerNormGradArgs &a, uint32_t vectors, hipStream_t s,
                                       uint32_t *parts)
 {
-#define EW_LAYERNORM_GRAD_ROWS(W, V)                                                              \
-    if (vectors <= W * 64 * V) {                                                                  \
-        constexpr int kGroups = W < 8 ? 8 / W : 1;                                                \
-        const uint64_t blocks = ((uint64_t)a.rows + kGroups - 1) / kGroups;                       \
-        *parts = blocks <= kOnePart ? 1 : (uint32_t)(blocks < kParts ? blocks : kParts);          \
-        return start(reinterpret_cast<const void *>(&ew_layernorm_grad_kernel<T, W, V, kGroups>), \
-                     dim3(*parts), W * 64 * kGroups, 0, s, a);                                    \
+#define EW_LAYERNORM_GRAD_LAUNCH(W, V, TINY)                                                         \
+    {                                                                                                \
+        constexpr int kGroups = W < 8 ? 8 / W : 1;                                                   \
+        const uint64_t blocks = ((uint64_t)a.rows + kGroups - 1) / kGroups;                          \
+        *parts = blocks <= kOnePart ? 1 : (uint32_t)(blocks < kParts ? blocks : kParts);             \
+        return start(reinterpret_cast<const void *>(&ew_layernorm_grad_kernel<T, W, V, kGroups, TINY>), \
+                     dim3(*parts), W * 64 * kGroups, 0, s, a);                                       \
     }
+#define EW_LAYERNORM_GRAD_ROWS(W, V) \
+    if (vectors <= W * 64 * V) EW_LAYERNORM_GRAD_LAUNCH(W, V, false)
+    if (a.cols < (uint32_t)Vec<T>::N) EW_LAYERNORM_GRAD_LAUNCH(1, 1, true)
     EW_LAYERNORM_GRAD_ROWS(1, 1)
     EW_LAYERNORM_GRAD_ROWS(2, 1)
     EW_LAYERNORM_GRAD_ROWS(4, 1)
@@ -630,12 +677,13 @@ static hipError_t layernorm_grad_rows(const LayerNormGradArgs &a, uint32_t vecto
     EW_LAYERNORM_GRAD_ROWS(8, 2)
     EW_LAYERNORM_GRAD_ROWS(8, 4)
     if constexpr (sizeof(T) == 4) {
-        EW_LAYERNORM_GRAD_ROWS(12, 4)
+        EW_LAYERNORM_GRAD_ROWS(16, 4)
     }
 #undef EW_LAYERNORM_GRAD_ROWS
+#undef EW_LAYERNORM_GRAD_LAUNCH
     return hipErrorInvalidValue;
 }
-static uint32_t grad_vectors(RowType t) { return t == kRowF32 ? 12 * 64 * 4 : 8 * 64 * 4; }
+static uint32_t grad_vectors(RowType t) { return t == kRowF32 ? 16 * 64 * 4 : 8 * 64 * 4; }
 
 hipError_t launch_layernorm_grad(RowType t, const LayerNormGradArgs &a, hipStream_t s, const char **path)
 {

@@ -57,12 +57,6 @@ __device__ __forceinline__ Token token(const PolicyTokens &in, float logp, float
     return t;
 }
 
-// Four neighbouring tokens of a row, and which of them count.
-struct Four {
-    f32x4 logp, old, ref, a;
-    uint32_t counted;          // bits
-};
-
 // A row's pointers.
 struct PolicyRow {
     const float *logp, *old, *ref, *advantage;
@@ -77,54 +71,42 @@ struct PolicyRow {
     }
 };
 
-__device__ __forceinline__ f32x4 load4(const float *row, uint32_t cols, uint32_t at)
-{
-    return __builtin_bit_cast(f32x4, load_vec<float, true>(row, cols, at));
-}
+// Four neighbouring tokens of a row: the piece at token `at` (below cols).
+// Few: rows of less than four.
+template <bool Few>
+struct Four {
+    LongPiece<float, Few> piece;
+    f32x4 logp, old, ref, a;
+    uint32_t counted;          // bytes that are not 0: tokens of the piece's own that count
 
-// Four tokens from `at` on (at < cols).
-template <bool Ref>
-__device__ __forceinline__ Four load_four(const PolicyTokens &in, const PolicyRow &row, uint32_t cols,
-                                          uint32_t at)
-{
-    typedef uint32_t word __attribute__((aligned(1)));
-    Four f;
-    f.logp = load4(row.logp, cols, at);
-    f.old = load4(row.old, cols, at);
-    f.ref = Ref ? load4(row.ref, cols, at) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    f.a = in.advantage_stride ? load4(row.advantage, cols, at)
-                              : f32x4{row.each, row.each, row.each, row.each};
-    f.counted = 0;
-    uint32_t bytes = 0x01010101u;
-    if (in.mask) {
-        if (cols >= 4) {
-            bytes = __builtin_nontemporal_load(
-                reinterpret_cast<const word *>(row.mask + (at + 4 <= cols ? at : cols - 4)));
-        } else {
-            bytes = 0;
-            for (uint32_t j = 0; j < cols; ++j) bytes |= (uint32_t)row.mask[j] << 8 * j;
+    template <bool Ref>
+    __device__ static Four load(const PolicyTokens &in, const PolicyRow &row, uint32_t cols, uint32_t at)
+    {
+        typedef uint32_t word __attribute__((aligned(1)));
+        Four f{LongPiece<float, Few>(at, cols), {}, {}, {}, {}, 0};
+        const auto take = [&](const float *p) {
+            return __builtin_bit_cast(f32x4, f.piece.template load<true>(p));
+        };
+        f.logp = take(row.logp);
+        f.old = take(row.old);
+        f.ref = Ref ? take(row.ref) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        f.a = in.advantage_stride ? take(row.advantage) : f32x4{row.each, row.each, row.each, row.each};
+        f.counted = 0x01010101u;
+        if (in.mask) {
+            if constexpr (Few) {
+                f.counted = 0;
+                for (uint32_t j = 0; j < cols; ++j) f.counted |= (uint32_t)row.mask[j] << 8 * j;
+            } else {
+                f.counted =
+                    __builtin_nontemporal_load(reinterpret_cast<const word *>(row.mask + f.piece.first));
+            }
         }
+        if (Few) f.counted &= (1u << 8 * cols) - 1;
+        else f.counted = f.counted >> 8 * f.piece.p.skip << 8 * f.piece.p.skip;
+        return f;
     }
-    if (at + 4 > cols) {
-        const uint32_t past = at + 4 - cols;
-        if (cols >= 4) {
-            const auto shift = [&](f32x4 v) {
-                return __builtin_bit_cast(f32x4, drop_first<float>(__builtin_bit_cast(u32x4, v), past));
-            };
-            f.logp = shift(f.logp);
-            f.old = shift(f.old);
-            if constexpr (Ref) f.ref = shift(f.ref);
-            if (in.advantage_stride) f.a = shift(f.a);
-            bytes >>= 8 * past;
-        } else {
-            bytes &= (1u << 8 * cols) - 1;
-        }
-        if (!in.mask) bytes = (1u << 8 * (4 - past)) - 1;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f.counted |= (bytes >> 8 * j & 0xffu ? 1u : 0u) << j;
-    return f;
-}
+    __device__ bool counts(int j) const { return (counted >> 8 * j & 0xffu) != 0; }
+};
 
 // ---------------------------------------------------------------------------
 // Forward: sums over parts of the batch, then their join.  Both in one block
@@ -175,30 +157,30 @@ __device__ __forceinline__ PolicySums block_sums(PolicySums s, PolicySums *scrat
 }
 
 // What a thread sums of a row's tokens [from, to): steps of `step` tokens.
-template <bool Ref>
+template <bool Ref, bool Few>
 __device__ __forceinline__ void sum_tokens(const PolicyTokens &in, uint64_t r, uint32_t cols,
                                            uint64_t from, uint64_t to, uint32_t step, PolicySums &s)
 {
     if (from >= to) return;        // (the advantage of no tokens may be absent)
     const PolicyRow row(in, r);
     for (uint64_t at = from; at < to; at += step) {
-        const Four f = load_four<Ref>(in, row, cols, (uint32_t)at);
+        const auto f = Four<Few>::template load<Ref>(in, row, cols, (uint32_t)at);
         float policy = 0.0f, kl = 0.0f, fall = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const Token t = token<Ref>(in, f.logp[j], f.old[j], f.ref[j], f.a[j]);
-            const bool counted = f.counted >> j & 1u;
+            const bool counted = f.counts(j);
             const float bound = f.a[j] > 0.0f ? in.most : in.least;
             const float loss = -f.a[j] * (t.clipped ? bound : t.ratio);
             policy += counted ? loss : 0.0f;
             kl += counted ? t.line : 0.0f;
             fall -= counted ? t.x : 0.0f;
             s.clipped += counted && t.clipped;
+            s.tokens += counted;
         }
         s.policy += (double)policy;
         s.kl += (double)kl;
         s.fall += (double)fall;
-        s.tokens += (uint64_t)__builtin_popcount(f.counted);
     }
 }
 
@@ -250,7 +232,7 @@ __device__ __forceinline__ void add_sequence(PolicySums &all, const PolicySums &
 }
 
 // Few tokens: one block, `lanes` lanes a sequence at a time.
-template <bool Ref>
+template <bool Ref, bool Few>
 __global__ void __launch_bounds__(kSmallBlock) ew_policy_small_kernel(PolicyLossArgs a, uint32_t lanes)
 {
     __shared__ PolicySums scratch[kSmallBlock / 64];
@@ -262,7 +244,7 @@ __global__ void __launch_bounds__(kSmallBlock) ew_policy_small_kernel(PolicyLoss
         const uint32_t r = r0 + threadIdx.x / lanes;
         PolicySums s{};
         if (r < a.rows)
-            sum_tokens<Ref>(a.in, r, a.cols, (uint64_t)lane * 4, a.cols, lanes * 4, s);
+            sum_tokens<Ref, Few>(a.in, r, a.cols, (uint64_t)lane * 4, a.cols, lanes * 4, s);
         const uint32_t tokens = lanes_sum((uint32_t)s.tokens, lanes);
         add_sequence(all, s, a.mean == EW_MEAN_SEQUENCES, tokens, lane == 0);
         if (r < a.rows && lane == 0) counts[r] = tokens;
@@ -281,7 +263,7 @@ __global__ void __launch_bounds__(kSmallBlock) ew_policy_small_kernel(PolicyLoss
 
 // Whole sequences: `lanes` lanes each; a record of sums a block, a count of
 // tokens a sequence.
-template <bool Ref>
+template <bool Ref, bool Few>
 __global__ void __launch_bounds__(kPolicyBlock) ew_policy_rows_kernel(PolicyLossArgs a, uint32_t lanes,
                                                                      PolicySums *records,
                                                                      uint32_t *counts)
@@ -293,7 +275,7 @@ __global__ void __launch_bounds__(kPolicyBlock) ew_policy_rows_kernel(PolicyLoss
         const uint64_t r = r0 + threadIdx.x / lanes;
         PolicySums s{};
         if (r < a.rows)
-            sum_tokens<Ref>(a.in, r, a.cols, (uint64_t)lane * 4, a.cols, lanes * 4, s);
+            sum_tokens<Ref, Few>(a.in, r, a.cols, (uint64_t)lane * 4, a.cols, lanes * 4, s);
         const uint32_t tokens = lanes_sum((uint32_t)s.tokens, lanes);
         add_sequence(all, s, a.mean == EW_MEAN_SEQUENCES, tokens, lane == 0);
         if (r < a.rows && lane == 0) counts[r] = tokens;
@@ -311,7 +293,7 @@ __global__ void __launch_bounds__(kPolicyBlock) ew_policy_parts_kernel(PolicyLos
     __shared__ PolicySums scratch[kPolicyBlock / 64];
     PolicySums s{};
     const uint64_t from = blockIdx.x * part_tokens, to = from + part_tokens;
-    sum_tokens<Ref>(a.in, blockIdx.y, a.cols, from + threadIdx.x * 4, to < a.cols ? to : a.cols,
+    sum_tokens<Ref, false>(a.in, blockIdx.y, a.cols, from + threadIdx.x * 4, to < a.cols ? to : a.cols,
                     kPolicyBlock * 4, s);
     s = block_sums<kPolicyBlock / 64>(s, scratch);
     if (threadIdx.x == 0) records[(uint64_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
@@ -371,7 +353,7 @@ __global__ void __launch_bounds__(kSmallBlock) ew_policy_join_kernel(PolicyLossA
 // Gradient: `lanes` lanes a sequence (or a part of one)
 // ---------------------------------------------------------------------------
 
-template <bool Ref>
+template <bool Ref, bool Few>
 __global__ void __launch_bounds__(kPolicyBlock) ew_policy_grad_kernel(PolicyGradArgs a, uint32_t lanes,
                                                                      uint64_t part_tokens)
 {
@@ -386,16 +368,16 @@ __global__ void __launch_bounds__(kPolicyBlock) ew_policy_grad_kernel(PolicyGrad
         float *const out = a.dlogp + r * a.dlogp_stride;
         const float w = a.weights[r] * dloss;
         for (uint64_t at = from + (uint64_t)lane * 4; at < to; at += (uint64_t)lanes * 4) {
-            const Four f = load_four<Ref>(a.in, row, a.cols, (uint32_t)at);
+            const auto f = Four<Few>::template load<Ref>(a.in, row, a.cols, (uint32_t)at);
             f32x4 g;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const Token t = token<Ref>(a.in, f.logp[j], f.old[j], f.ref[j], f.a[j]);
                 float slope = t.clipped ? 0.0f : -f.a[j] * t.ratio;
                 if constexpr (Ref) slope -= a.in.kl * t.one;
-                g[j] = f.counted >> j & 1u ? w * slope : 0.0f;
+                g[j] = f.counts(j) ? w * slope : 0.0f;
             }
-            store_vec(out, a.cols, (uint32_t)at, __builtin_bit_cast(u32x4, g));
+            f.piece.store(out, __builtin_bit_cast(u32x4, g));
         }
     }
 }
@@ -431,15 +413,20 @@ size_t policy_loss_workspace(uint64_t rows, uint64_t cols)
     return kRecords * sizeof(PolicySums) + (rows * sizeof(uint32_t) + 15) / 16 * 16;
 }
 
+// A kernel with or without the reference, of short rows or others.
+#define EW_POLICY_KERNEL(K, ref, cols)                                                     \
+    ((ref) ? ((cols) < 4 ? reinterpret_cast<const void *>(&K<true, true>)                  \
+                         : reinterpret_cast<const void *>(&K<true, false>))                \
+           : ((cols) < 4 ? reinterpret_cast<const void *>(&K<false, true>)                 \
+                         : reinterpret_cast<const void *>(&K<false, false>)))
+
 hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, const char **path)
 {
     const bool ref = a.in.ref;
     if ((uint64_t)a.rows * (a.cols ? a.cols : 1) <= kSmallTokens) {
         *path = "one block";
         const uint32_t lanes = lanes_for(a.cols, 64);
-        return start(ref ? reinterpret_cast<const void *>(&ew_policy_small_kernel<true>)
-                         : reinterpret_cast<const void *>(&ew_policy_small_kernel<false>),
-                     dim3(1), kSmallBlock, 0, s, a, lanes);
+        return start(EW_POLICY_KERNEL(ew_policy_small_kernel, ref, a.cols), dim3(1), kSmallBlock, 0, s, a, lanes);
     }
     PolicySums *const records = static_cast<PolicySums *>(a.workspace);
     uint32_t *const counts = reinterpret_cast<uint32_t *>(records + kRecords);
@@ -463,9 +450,7 @@ hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, c
     const uint32_t lanes = lanes_for(a.cols, 64);
     const uint64_t blocks = ((uint64_t)a.rows * lanes + kPolicyBlock - 1) / kPolicyBlock;
     n = (uint32_t)(blocks < kRecords ? blocks : kRecords);
-    e = start(ref ? reinterpret_cast<const void *>(&ew_policy_rows_kernel<true>)
-                  : reinterpret_cast<const void *>(&ew_policy_rows_kernel<false>),
-              dim3(n), kPolicyBlock, 0, s, a, lanes, records, counts);
+    e = start(EW_POLICY_KERNEL(ew_policy_rows_kernel, ref, a.cols), dim3(n), kPolicyBlock, 0, s, a, lanes, records, counts);
     if (e != hipSuccess) return e;
     const uint64_t joins = a.weights ? ((uint64_t)a.rows + kSmallBlock - 1) / kSmallBlock : 1;
     return start(reinterpret_cast<const void *>(&ew_policy_join_kernel),
@@ -484,9 +469,7 @@ hipError_t launch_policy_grad(RowType, const PolicyGradArgs &a, hipStream_t s, c
     const uint32_t used = (uint32_t)((a.cols + tokens - 1) / tokens);
     *path = used > 1 ? "parts of sequences" : "whole sequences";
     // a KL term that does not count is not read
-    return start(a.in.ref && a.in.kl != 0.0f
-                     ? reinterpret_cast<const void *>(&ew_policy_grad_kernel<true>)
-                     : reinterpret_cast<const void *>(&ew_policy_grad_kernel<false>),
+    return start(EW_POLICY_KERNEL(ew_policy_grad_kernel, a.in.ref && a.in.kl != 0.0f, a.cols),
                  dim3(row_blocks(blocks), used), kPolicyBlock, 0, s, a, lanes, tokens);
 }
 

@@ -98,6 +98,7 @@ struct LayerNormArgs {
     void *y, *total;
     float *mean, *rstd;
     uint64_t x_stride, residual_stride, y_stride, total_stride;
+    double by_cols;             // 1 / cols
     uint32_t rows, cols;
     float eps;
 };

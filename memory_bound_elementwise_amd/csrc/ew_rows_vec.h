@@ -1,86 +1,116 @@
-// ew_rows_vec.h -- rows as 16-byte vectors from the row's start, whatever its
-// alignment and length: loads and stores whose last vector may be a part, and
-// launches (ew_layernorm.hip, ew_policy.hip, ew_experts.hip).  Not installed;
-// not part of the C ABI.
+// ew_rows_vec.h -- rows as 16-byte vectors whatever their alignment and length,
+// sums in binary64 and launches, for ew_layernorm.hip, ew_policy.hip and
+// ew_experts.hip.  Not installed; not part of the C ABI.
 #pragma once
 
 #include "ew_rows_device.h"
 
 namespace ew {
 
-template <bool C, class A, class B>
-struct Conditional {
-    using type = A;
-};
-template <class A, class B>
-struct Conditional<false, A, B> {
-    using type = B;
-};
-
-// A vector's elements without the first n (0 < n < its number), 0 behind them.
-template <typename T>
-__device__ __forceinline__ u32x4 drop_first(u32x4 v, uint32_t n)
-{
-    const uint32_t bits = n * 8 * (uint32_t)sizeof(T);
-    uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
-    if (bits >= 64) {
-        lo = hi >> (bits - 64);
-        hi = 0;
-    } else {
-        lo = lo >> bits | hi << (64 - bits);
-        hi >>= bits;
+// Where a vector of a row of cols elements lies: element `first` of the row on,
+// N of them.  A row's vectors start at its start, one behind another; its last,
+// partial one is taken as the last N elements of the row instead, of which the
+// first `skip` are the vector's before it.  Loads and stores are so of 16 bytes
+// everywhere (elements one by one, each waited for, cost 0.5-2 us a row); both
+// vectors hold, compute and store the same there, and only sums and stores of
+// what depends on an output's old value leave out what is not their own.
+// Tiny: a row shorter than a vector, one piece with zeros behind the row.
+template <typename T, bool Tiny = false>
+struct Piece {
+    static constexpr uint32_t N = Vec<T>::N;
+    uint32_t first, skip;
+    bool live;
+    // back: elements of the row before element 0 of the stretch
+    __device__ Piece(uint32_t at, uint32_t cols, uint32_t back = 0)
+        : first(back + (Tiny || at + N <= cols ? at : cols - N)), skip(back + at - first),
+          live(at < cols)
+    {
     }
-    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-}
+    // whether element j of a live piece is its own
+    __device__ bool own(uint32_t j, uint32_t cols) const { return Tiny ? j < cols : j >= skip; }
+};
 
-// The vector of a row of cols elements from element `at` on, 0 past the row.
-// Its last, partial one is read as the last whole 16 bytes of the row and
-// shifted (`settle`, apart so that loads can be on their way together): the
-// elements one by one, each waited for, cost 0.5-2 us a row.  Nt: a stream
-// read once, else data that other rows read too.  Short: a row below 2^32 bytes.
-template <typename T, bool Nt, bool Short = false>
-__device__ __forceinline__ u32x4 load_vec(const T *row, uint32_t cols, uint32_t at)
+// Loads and stores of a piece; `row` is best the same in all lanes, whose
+// offsets are of 32 bits then.  A stretch of a row far below 2^32 bytes.
+// Nt: a stream read once, else data that others read too.
+template <typename T, bool Nt, bool Tiny>
+__device__ __forceinline__ u32x4 load_piece(const T *row, uint32_t cols, const Piece<T, Tiny> &p)
 {
-    constexpr uint32_t N = Vec<T>::N;
-    if (at >= cols) return u32x4{0, 0, 0, 0};
-    if (cols < N) {
+    if (!p.live) return u32x4{0, 0, 0, 0};
+    if constexpr (Tiny) {
         typename Vec<T>::type t{};
 #pragma unroll
-        for (uint32_t j = 0; j < N; ++j)
+        for (uint32_t j = 0; j < Vec<T>::N; ++j)
             if (j < cols) t[j] = row[j];
         return __builtin_bit_cast(u32x4, t);
     }
-    // (Short: one register of offset to a row that is the same in all lanes)
-    using Offset = typename Conditional<Short, uint32_t, uint64_t>::type;
-    const char *const p = reinterpret_cast<const char *>(row) +
-                          (Offset)(at + N <= cols ? at : cols - N) * (Offset)sizeof(T);
-    if constexpr (Nt) return load16<false, sizeof(T)>(p);
-    else if constexpr (sizeof(T) == 4) return *reinterpret_cast<const u32x4_a4 *>(p);
-    else return *reinterpret_cast<const u32x4_a2 *>(p);
+    const char *const at = reinterpret_cast<const char *>(row) + p.first * (uint32_t)sizeof(T);
+    if constexpr (Nt) return load16<false, sizeof(T)>(at);
+    else if constexpr (sizeof(T) == 4) return *reinterpret_cast<const u32x4_a4 *>(at);
+    else return *reinterpret_cast<const u32x4_a2 *>(at);
 }
 
-template <typename T>
-__device__ __forceinline__ u32x4 settle(u32x4 v, uint32_t cols, uint32_t at)
+template <typename T, bool Tiny>
+__device__ __forceinline__ void store_piece(T *row, uint32_t cols, const Piece<T, Tiny> &p, u32x4 v)
 {
-    constexpr uint32_t N = Vec<T>::N;
-    if (at < cols && at + N > cols && cols >= N) return drop_first<T>(v, at + N - cols);
-    return v;
-}
-
-template <typename T, bool Short = false>
-__device__ __forceinline__ void store_vec(T *row, uint32_t cols, uint32_t at, u32x4 v)
-{
-    constexpr uint32_t N = Vec<T>::N;
-    using Offset = typename Conditional<Short, uint32_t, uint64_t>::type;
-    if (at + N <= cols) {
-        store16_row<T>(reinterpret_cast<char *>(row) + (Offset)at * (Offset)sizeof(T), v);
-    } else if (at < cols) {
+    if (!p.live) return;
+    if constexpr (Tiny) {
         const typename Vec<T>::type t = __builtin_bit_cast(typename Vec<T>::type, v);
 #pragma unroll
-        for (uint32_t j = 0; j < N; ++j)
-            if (at + j < cols) row[at + j] = t[j];
+        for (uint32_t j = 0; j < Vec<T>::N; ++j)
+            if (j < cols) row[j] = t[j];
+    } else {
+        store16_row<T>(reinterpret_cast<char *>(row) + p.first * (uint32_t)sizeof(T), v);
     }
 }
+
+// The elements of a piece that are its own, one by one where those are not all.
+template <typename T, bool Tiny>
+__device__ __forceinline__ void store_own(T *row, uint32_t cols, const Piece<T, Tiny> &p, u32x4 v)
+{
+    if (Tiny || p.skip == 0) return store_piece(row, cols, p, v);
+    const typename Vec<T>::type t = __builtin_bit_cast(typename Vec<T>::type, v);
+#pragma unroll
+    for (uint32_t j = 0; j < Vec<T>::N; ++j)
+        if (p.live && j >= p.skip) row[p.first + j] = t[j];
+}
+
+// Bits of the elements that are a piece's own (0 of a piece past the row).
+template <typename T, bool Tiny>
+__device__ __forceinline__ u32x4 own_bits(uint32_t cols, const Piece<T, Tiny> &p)
+{
+    constexpr uint32_t kPerWord = 4 / (uint32_t)sizeof(T);
+    u32x4 m;
+#pragma unroll
+    for (uint32_t w = 0; w < 4; ++w) {
+        uint32_t bits = 0;
+#pragma unroll
+        for (uint32_t h = 0; h < kPerWord; ++h)
+            if (p.live && p.own(w * kPerWord + h, cols))
+                bits |= (kPerWord == 1 ? 0xffffffffu : 0xffffu) << (16 * h);
+        m[w] = bits;
+    }
+    return m;
+}
+
+// The piece at element `at` of a row of any length: element `first` of the row
+// on, with offsets of 64 bits.
+template <typename T, bool Tiny = false>
+struct LongPiece {
+    uint64_t first;
+    uint32_t cols;
+    Piece<T, Tiny> p;          // of the vector at `first`, a row of its own
+    __device__ LongPiece(uint32_t at, uint32_t cols_)
+        : first(Tiny || at + Vec<T>::N <= cols_ ? at : cols_ - Vec<T>::N), cols(cols_),
+          p(0, Tiny ? cols_ : Vec<T>::N)
+    {
+        p.skip = at - (uint32_t)first;
+    }
+    template <bool Nt>
+    __device__ u32x4 load(const T *row) const { return load_piece<T, Nt>(row + first, cols, p); }
+    // (an output may be an input, whose other elements are another thread's)
+    __device__ void store(T *row, u32x4 v) const { store_own(row + first, cols, p, v); }
+};
 
 // The value of another lane of the same 16 (binary64).
 template <int Ctrl>

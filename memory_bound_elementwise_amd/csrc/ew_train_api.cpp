@@ -42,6 +42,7 @@ ew_status_t layernorm(RowType t, const void *x, size_t x_stride, const void *wei
     a.residual_stride = residual_stride;
     a.y_stride = y_stride;
     a.total_stride = total_stride;
+    a.by_cols = 1.0 / (double)cols;
     a.rows = (uint32_t)rows;
     a.cols = (uint32_t)cols;
     a.eps = eps;

@@ -153,7 +153,7 @@ def test_layernorm_of_nan_and_infinities(t, cols):
     y, mean, rstd = torch.empty_like(x), f32(4), f32(4)
     getattr(ew, "ew_layernorm_" + t)(x, None, None, y, mean=mean, rstd=rstd)
     assert bool(torch.isnan(y[2:]).all()) and bool(torch.isnan(rstd[2:]).all())
-    assert math.isnan(float(mean[2])) and float(mean[3]) == math.inf
+    assert bool(torch.isnan(mean[2:]).all())
     check_norm(t, x[:2], None, None, None, y[:2], None, mean[:2], rstd[:2])
 
 
@@ -495,7 +495,7 @@ def sort(ids, experts, align):
 
 
 @pytest.mark.parametrize("entries", (0, 1, 2, 63, 64, 65, 100, 1000, 1025, 8191, 8192, 8193, 30001,
-                                     200000))
+                                     200000, 600001))
 @pytest.mark.parametrize("experts", (1, 2, 3, 8, 100, 256, 512, 513, 1000, 1024))
 def test_sort(entries, experts):
     g = gen(entries + experts)

@@ -22,13 +22,21 @@ def rounded(want, tol, dt):
 # Layer norm
 # ---------------------------------------------------------------------------
 
+def norm_adds(cols):
+    """The longest chain of additions of a row's sums: 32 elements a lane and
+    the joins, or a long row's 1024th part of it."""
+    return 48 + cols / 1024
+
+
 def layernorm(total, weight, bias, eps):
     """(y, mean, rstd, tolerances of y before its rounding, of mean, of rstd).
 
-    d = (h - hi) - lo is off by two roundings, and by that of lo, U^2 of the
-    mean; the sum of squares by four roundings a term and its additions; rstd
-    by half of that, the mean's division, eps's addition, the root and the
-    division."""
+    The mean is that of numbers near the row's parts (exact) and of the
+    differences from them: their sum is off by its additions, at most twice
+    the mean difference in size.  d = (h - hi) - lo is off by two roundings, by
+    that of lo (U^2 of the mean), and with the mean; the sum of squares by
+    four roundings a term, its additions and four of the join; rstd by half of
+    that, the mean's division, eps's addition, the root and the division."""
     h = total.double()
     n = h.shape[1]
     one = torch.ones(n, dtype=torch.float64, device=h.device)
@@ -39,9 +47,10 @@ def layernorm(total, weight, bias, eps):
     var = d.square().sum(1) / n
     rstd = (var + eps).rsqrt()
     y = d * rstd[:, None] * w + b
-    lost = U * U * mean.abs()
-    rel = ((adds(n) + 8) / 2 + 3) * U + (lost * var.sqrt() / (var + eps)).nan_to_num()
-    tol_mean = mean.abs() * U + h.abs().mean(1) * n * 2.0 ** -52 + 2.0 ** -149
+    off = 2 * (norm_adds(n) + 3) * d.abs().mean(1) * U
+    lost = U * U * mean.abs() + off
+    rel = ((norm_adds(n) + 12) / 2 + 3) * U + (lost * var.sqrt() / (var + eps)).nan_to_num()
+    tol_mean = mean.abs() * U + off + h.abs().mean(1) * n * 2.0 ** -52 + 2.0 ** -149
     tol = (d * rstd[:, None] * w).abs() * (rel[:, None] + 4 * U) + y.abs() * U
     tol = tol + (w.abs() * (lost * rstd)[:, None])
     return y, mean, rstd, tol, tol_mean, rstd * rel
