@@ -158,17 +158,22 @@ __global__ void __launch_bounds__(1024) ew_experts_sort_kernel(ExpertsSortArgs a
         }
         const uint32_t e = e0 + threadIdx.x;
         const bool live = threadIdx.x < tile && e < experts;
-        if (One && live)
-            for (uint32_t w = 0; w < split.waves; ++w) all += counters[w * experts + e];
+        uint32_t counted[16];            // by the block's waves, read together
+#pragma unroll
+        for (uint32_t w = 0; w < 16; ++w)
+            counted[w] = live && w < split.waves ? counters[w * experts + e] : 0;
+        if constexpr (One)
+#pragma unroll
+            for (uint32_t w = 0; w < 16; ++w) all += counted[w];
         const uint32_t room = live ? (all + a.align - 1) / a.align * a.align : 0;
         const uint32_t after = start + block_scan(room, scratch);
         if (live) {
             const uint32_t first = after - room;
             uint32_t next = first + before;
-            for (uint32_t w = 0; w < split.waves; ++w) {
-                const uint32_t n = counters[w * experts + e];
-                counters[w * experts + e] = next;
-                next += n;
+#pragma unroll
+            for (uint32_t w = 0; w < 16; ++w) {
+                if (w < split.waves) counters[w * experts + e] = next;
+                next += counted[w];
             }
             if (blockIdx.x == 0) {
                 a.offsets[e] = (int32_t)first;
@@ -267,7 +272,7 @@ struct Weights {
 // A lane's vectors of a stretch of columns, from column `from` on: pieces of
 // the stretch, whose row starts `back` elements before it (the last piece of a
 // stretch shorter than a vector does).
-template <typename T, uint32_t Lanes, uint32_t U, bool Tiny>
+template <typename T, uint32_t Lanes, uint32_t U, RowFit Fit>
 struct Stretch {
     static constexpr uint32_t N = Vec<T>::N, kCols = Lanes * U * N;
     uint64_t from;
@@ -277,9 +282,9 @@ struct Stretch {
           back(from_ ? N : 0)
     {
     }
-    __device__ Piece<T, Tiny> piece(uint32_t u) const
+    __device__ Piece<T, Fit> piece(uint32_t u) const
     {
-        return Piece<T, Tiny>((place + u * Lanes) * N, cols, back);
+        return Piece<T, Fit>((place + u * Lanes) * N, cols, back);
     }
     __device__ const T *row(const void *base, uint64_t r, uint64_t stride) const
     {
@@ -297,10 +302,10 @@ struct Stretch {
 };
 
 // Zeros in the padding rows of expert e, by a block.
-template <typename T, bool Tiny>
+template <typename T, RowFit Fit>
 __device__ __forceinline__ void clear_padding(const ExpertsMoveArgs &a, uint32_t e)
 {
-    using Cols = Stretch<T, kMoveBlock, 1, Tiny>;
+    using Cols = Stretch<T, kMoveBlock, 1, Fit>;
     const int64_t first = (int64_t)a.offsets[e] + a.counts[e], after = a.offsets[e + 1];
     const int64_t from = first < 0 ? 0 : first, to = after < a.places ? after : a.places;
     for (int64_t r = from; r < to; ++r) {
@@ -312,13 +317,13 @@ __device__ __forceinline__ void clear_padding(const ExpertsMoveArgs &a, uint32_t
     }
 }
 
-template <typename T, uint32_t Waves, bool Tiny>
+template <typename T, uint32_t Waves, RowFit Fit>
 __global__ void __launch_bounds__(kMoveBlock) ew_experts_gather_kernel(ExpertsMoveArgs a, uint32_t blocks)
 {
-    constexpr uint32_t U = 4;
-    using Cols = Stretch<T, Waves * 64, U, Tiny>;
+    constexpr uint32_t U = 1;
+    using Cols = Stretch<T, Waves * 64, U, Fit>;
     if (blockIdx.x >= blocks) {
-        clear_padding<T, Tiny>(a, blockIdx.x - blocks);
+        clear_padding<T, Fit>(a, blockIdx.x - blocks);
         return;
     }
     const Worker<Waves> worker;
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_gather_kernel(ExpertsMo
             const Cols part(first, a.cols, worker.place);
             u32x4 v[U];
 #pragma unroll
-            for (uint32_t u = 0; u < U; ++u) v[u] = part.template load<true>(a.in, t, a.in_stride, u);
+            for (uint32_t u = 0; u < U; ++u) v[u] = part.template load<false>(a.in, t, a.in_stride, u);
             for (uint32_t j = 0; j < a.top; ++j) {
                 const int32_t s = slots.of(j);
                 if (s < 0) continue;
@@ -344,10 +349,10 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_gather_kernel(ExpertsMo
 }
 
 // C choices of U vectors are on their way together.
-template <typename T, uint32_t Waves, uint32_t C, uint32_t U, bool Tiny>
+template <typename T, uint32_t Waves, uint32_t C, uint32_t U, RowFit Fit>
 __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_kernel(ExpertsMoveArgs a, uint32_t blocks)
 {
-    using Cols = Stretch<T, Waves * 64, U, Tiny>;
+    using Cols = Stretch<T, Waves * 64, U, Fit>;
     using Wide = typename Vec<T>::wide;
     const Worker<Waves> worker;
     for (uint64_t t0 = (uint64_t)blockIdx.x * worker.kTokens; t0 < a.rows;
@@ -402,16 +407,16 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_kernel(ExpertsM
 
 // dz and the weights' gradients, C choices of U vectors at a time; dy is read
 // again for each C choices.
-template <typename T, uint32_t Waves, uint32_t C, uint32_t U, bool Tiny>
+template <typename T, uint32_t Waves, uint32_t C, uint32_t U, RowFit Fit>
 __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_grad_kernel(ExpertsMoveArgs a,
                                                                             uint32_t blocks)
 {
-    using Cols = Stretch<T, Waves * 64, U, Tiny>;
+    using Cols = Stretch<T, Waves * 64, U, Fit>;
     using Wide = typename Vec<T>::wide;
     // two sets, used in turn: a wave is at most one barrier ahead of another
     __shared__ float scratch[2][kMoveWaves][C];
     if (blockIdx.x >= blocks) {
-        clear_padding<T, Tiny>(a, blockIdx.x - blocks);
+        clear_padding<T, Fit>(a, blockIdx.x - blocks);
         return;
     }
     const Worker<Waves> worker;
@@ -442,12 +447,8 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_grad_kernel(Exp
                             v[c][u] = part.template load<true>(a.z, (uint32_t)s, a.z_stride, u);
                 }
                 Wide g[U];
-                u32x4 own[U];
 #pragma unroll
-                for (uint32_t u = 0; u < U; ++u) {
-                    g[u] = Vec<T>::widen(d[u]);
-                    own[u] = own_bits(part.cols, part.piece(u));
-                }
+                for (uint32_t u = 0; u < U; ++u) g[u] = Vec<T>::widen(d[u]);
 #pragma unroll
                 for (uint32_t c = 0; c < C; ++c) {
                     const int32_t s = slots.of(j0 + c);
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_grad_kernel(Exp
                     T *const dz = part.row(a.out, (uint32_t)s, a.out_stride);
 #pragma unroll
                     for (uint32_t u = 0; u < U; ++u) {
-                        const Wide z = Vec<T>::widen(v[c][u] & own[u]);
+                        const Wide z = Vec<T>::widen(own_bits(v[c][u], part.cols, part.piece(u)));
 #pragma unroll
                         for (uint32_t k = 0; k < Cols::N; ++k) dots[c] = __builtin_fmaf(g[u][k], z[k], dots[c]);
                         store_piece(dz, part.cols, part.piece(u), Vec<T>::narrow(w * g[u]));
@@ -544,15 +545,15 @@ hipError_t launch_experts_sort(RowType, const ExpertsSortArgs &a, hipStream_t s,
 
 // The kernel of a type for rows that a block shares (each), those that a wave
 // takes, and those shorter than a vector.
-#define EW_MOVE_OF(T, K, W, TINY, ...) K<T, W, ##__VA_ARGS__, TINY>
-#define EW_MOVE_BY_TYPE(t, K, W, TINY, ...)                                                            \
-    ((t) == kRowF32   ? reinterpret_cast<const void *>(&EW_MOVE_OF(float, K, W, TINY, ##__VA_ARGS__))    \
-     : (t) == kRowF16 ? reinterpret_cast<const void *>(&EW_MOVE_OF(_Float16, K, W, TINY, ##__VA_ARGS__)) \
-                      : reinterpret_cast<const void *>(&EW_MOVE_OF(__bf16, K, W, TINY, ##__VA_ARGS__)))
-#define EW_MOVE_KERNEL(t, split, K, ...)                                      \
-    ((split).each   ? EW_MOVE_BY_TYPE(t, K, kMoveWaves, false, ##__VA_ARGS__) \
-     : (split).tiny ? EW_MOVE_BY_TYPE(t, K, 1, true, ##__VA_ARGS__)           \
-                    : EW_MOVE_BY_TYPE(t, K, 1, false, ##__VA_ARGS__))
+#define EW_MOVE_OF(T, K, W, FIT, ...) K<T, W, ##__VA_ARGS__, FIT>
+#define EW_MOVE_BY_TYPE(t, K, W, FIT, ...)                                                              \
+    ((t) == kRowF32   ? reinterpret_cast<const void *>(&EW_MOVE_OF(float, K, W, FIT, ##__VA_ARGS__))    \
+     : (t) == kRowF16 ? reinterpret_cast<const void *>(&EW_MOVE_OF(_Float16, K, W, FIT, ##__VA_ARGS__)) \
+                      : reinterpret_cast<const void *>(&EW_MOVE_OF(__bf16, K, W, FIT, ##__VA_ARGS__)))
+#define EW_MOVE_KERNEL(t, split, K, ...)                                       \
+    ((split).tiny   ? EW_MOVE_BY_TYPE(t, K, 1, kTiny, ##__VA_ARGS__)           \
+     : (split).each ? EW_MOVE_BY_TYPE(t, K, kMoveWaves, kPart, ##__VA_ARGS__)  \
+                    : EW_MOVE_BY_TYPE(t, K, 1, kPart, ##__VA_ARGS__))
 
 struct MoveSplit {
     bool each, tiny;      // a block a token; rows shorter than a vector
@@ -583,7 +584,7 @@ hipError_t launch_experts_combine(RowType t, const ExpertsMoveArgs &a, hipStream
 {
     const MoveSplit m = move_split(t, a, path);
     return start(a.top <= 2 ? EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 2, 4)
-                            : EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 8, 1),
+                            : EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 4, 2),
                  dim3(m.blocks), kMoveBlock, 0, s, a, m.blocks);
 }
 
@@ -592,7 +593,7 @@ hipError_t launch_experts_combine_grad(RowType t, const ExpertsMoveArgs &a, hipS
 {
     const MoveSplit m = move_split(t, a, path);
     return start(a.top <= 2 ? EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 2, 4)
-                            : EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 8, 1),
+                            : EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 4, 2),
                  dim3(m.blocks + a.experts), kMoveBlock, 0, s, a, m.blocks);
 }
 

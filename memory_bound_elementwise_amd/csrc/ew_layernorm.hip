@@ -62,53 +62,49 @@ __device__ __forceinline__ float sum_of_waves(float x)
 constexpr uint32_t lanes_of_waves(int waves) { return waves > 8 ? 16 : waves > 4 ? 8 : waves > 2 ? 4 : waves; }
 
 // What a wave knows of its elements of a row: a number near them, and the sums
-// of the differences from it and of their squares.  The number is the wave's
-// own mean, taken from its first element, so that neither rows far from 0 nor
-// an outlier cost bits, and a row of equal values gives differences of 0.
+// of the differences from it and of their squares.
 struct WaveSums {
     float near, sum, squares;
 };
 
-template <typename T, int V, bool Tiny, class At>
+// The number is the mean of the wave's first vector (of equal values: exactly
+// theirs, so that their differences are 0).  Where it lies so far from the
+// wave's mean that the squares about it are more than four times those about
+// the mean, two bits, the wave sums again from its mean: neither an outlier nor
+// the distance of the row from 0 costs more.
+template <typename T, int V, RowFit Fit, class At>
 __device__ __forceinline__ WaveSums wave_sums(const u32x4 (&h)[V], uint32_t cols, uint32_t n, At piece)
 {
     constexpr uint32_t N = Vec<T>::N;
     using Wide = typename Vec<T>::wide;
-    const float start = lane_value(Vec<T>::widen(h[0])[0], 0);
-    const float by = n ? 1.0f / (float)n : 0.0f;
-    // differences from x of a lane's own elements, 0 for others
-    const auto own = [&](int k, float x) {
-        Wide d = Vec<T>::widen(h[k]) - x;
-        const Piece<T, Tiny> p = piece(k);
-        if (Tiny || !p.live || p.skip) {
+    const auto about = [&](float x) {
+        WaveSums w{x, 0.0f, 0.0f};
 #pragma unroll
-            for (uint32_t j = 0; j < N; ++j)
-                if (!p.live || !p.own(j, cols)) d[j] = 0.0f;
+        for (int k = 0; k < V; ++k) {
+            Wide d = Vec<T>::widen(h[k]) - x;
+            if (Fit == kTiny || (Fit == kPart && n < V * 64 * N)) {     // the same in all lanes
+                const Piece<T, Fit> p = piece(k);
+#pragma unroll
+                for (uint32_t j = 0; j < N; ++j)
+                    if (!p.live || !p.own(j, cols)) d[j] = 0.0f;
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j) {
+                w.sum += d[j];
+                w.squares = __builtin_fmaf(d[j], d[j], w.squares);
+            }
         }
-        return d;
+        w.sum = wave_reduce<Sum>(w.sum);
+        w.squares = wave_reduce<Sum>(w.squares);
+        return w;
     };
-    float sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const Wide d = own(k, start);
-#pragma unroll
-        for (uint32_t j = 0; j < N; ++j) sum += d[j];
-    }
-    WaveSums w;
-    w.near = __builtin_fmaf(wave_reduce<Sum>(sum), by, start);
-    w.sum = 0.0f;
-    w.squares = 0.0f;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const Wide d = own(k, w.near);
-#pragma unroll
-        for (uint32_t j = 0; j < N; ++j) {
-            w.sum += d[j];
-            w.squares = __builtin_fmaf(d[j], d[j], w.squares);
-        }
-    }
-    w.sum = wave_reduce<Sum>(w.sum);
-    w.squares = wave_reduce<Sum>(w.squares);
+    const Wide f = Vec<T>::widen(h[0]) * (1.0f / N);
+    float first = (f[0] + f[1]) + (f[2] + f[3]);
+    if constexpr (N == 8) first += (f[4] + f[5]) + (f[6] + f[7]);
+    if constexpr (Fit == kTiny) first = Vec<T>::widen(h[0])[0];
+    WaveSums w = about(lane_value(first, 0));
+    // (the values are the same in all lanes)
+    if (w.sum * w.sum > 0.75f * (float)n * w.squares) w = about(w.near + w.sum / (float)n);
     return w;
 }
 
@@ -117,6 +113,17 @@ __device__ __forceinline__ float squares_about(const WaveSums &w, uint32_t n, do
 {
     const float off = (float)((double)w.near - mean);
     return __builtin_fmaf(off, __builtin_fmaf(off, (float)n, 2.0f * w.sum), w.squares);
+}
+
+// 1 / sqrt(squares / n + eps), by = 1 / n, through the hardware's reciprocal
+// root (off by a last place), which wants no subnormal.
+__device__ __forceinline__ float reciprocal_root(float squares, float by, float eps)
+{
+    squares = squares < 0.0f ? 0.0f : squares;       // (a rounding below 0)
+    const float v = __builtin_fmaf(squares, by, eps);
+    const bool small = v < 0x1p-100f;
+    const float root = __builtin_amdgcn_rsqf(small ? v * 0x1p100f : v);
+    return small ? root * 0x1p50f : root;
 }
 
 template <typename T>
@@ -140,26 +147,27 @@ __device__ __forceinline__ typename Vec<T>::wide affine(const void *p, u32x4 v, 
 // Forward, rows that fit in registers: Waves waves a row, V vectors a lane
 // ---------------------------------------------------------------------------
 
-template <typename T, int Waves, int V, bool Tiny = false>
-__global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kernel(LayerNormArgs a)
+template <typename T, int Waves, int V, RowFit Fit>
+__device__ __forceinline__ void layernorm_row(const LayerNormArgs &a, WaveSums (*shared)[layernorm_block(Waves) / 64])
 {
     constexpr uint32_t N = Vec<T>::N, kThreads = Waves * 64;
     constexpr uint32_t kRows = layernorm_block(Waves) / kThreads;
     // weight and bias are on their way with the row, unless they would not fit
     // in registers
     constexpr bool kEarly = V < 3;
-    // two sets, used in turn: a wave is at most one barrier ahead of another
-    __shared__ WaveSums shared[2][layernorm_block(Waves) / 64];
     const uint32_t group = row_of_thread<kThreads, kRows>(), i = place_in_row<kThreads, kRows>();
+    const uint32_t wave = Waves > 1 ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(i / 64)) : 0;
     const T *const weight = static_cast<const T *>(a.weight), *const bias = static_cast<const T *>(a.bias);
-    const auto piece = [&](int k) { return Piece<T, Tiny>((i + k * kThreads) * N, a.cols); };
+    const uint32_t cols = Fit == kWhole ? kThreads * V * N : a.cols;
+    const auto piece = [&](int k) { return Piece<T, Fit>((i + k * kThreads) * N, cols); };
     // elements of wave w of a row
     const auto elements = [&](uint32_t w) {
+        if constexpr (Fit == kWhole) return 64 * V * N;
         uint32_t n = 0;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const uint32_t from = (w * 64 + k * kThreads) * N;
-            n += from >= a.cols ? 0 : a.cols - from < 64 * N ? a.cols - from : 64 * N;
+            n += from >= cols ? 0 : cols - from < 64 * N ? cols - from : 64 * N;
         }
         return n;
     };
@@ -172,16 +180,16 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kerne
         u32x4 h[V], w[V], b[V];
         const T *const x = static_cast<const T *>(a.x) + r * a.x_stride;
 #pragma unroll
-        for (int k = 0; k < V; ++k) h[k] = load_piece<T, true>(x, a.cols, piece(k));
+        for (int k = 0; k < V; ++k) h[k] = load_piece<T, true>(x, cols, piece(k));
         const auto fetch_affine = [&](int k) {
-            if (weight) w[k] = load_piece<T, false>(weight, a.cols, piece(k));
-            if (bias) b[k] = load_piece<T, false>(bias, a.cols, piece(k));
+            if (weight) w[k] = load_piece<T, false>(weight, cols, piece(k));
+            if (bias) b[k] = load_piece<T, false>(bias, cols, piece(k));
         };
         if (a.residual) {
             const T *const p = static_cast<const T *>(a.residual) + r * a.residual_stride;
             u32x4 res[V];
 #pragma unroll
-            for (int k = 0; k < V; ++k) res[k] = load_piece<T, true>(p, a.cols, piece(k));
+            for (int k = 0; k < V; ++k) res[k] = load_piece<T, true>(p, cols, piece(k));
             if constexpr (kEarly)
 #pragma unroll
                 for (int k = 0; k < V; ++k) fetch_affine(k);
@@ -192,13 +200,12 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kerne
 #pragma unroll
             for (int k = 0; k < V; ++k) fetch_affine(k);
         }
-        const uint32_t wave = Waves > 1 ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(i / 64)) : 0;
-        WaveSums own = wave_sums<T, V, Tiny>(h, a.cols, elements(wave), piece);
+        const WaveSums own = wave_sums<T, V, Fit>(h, cols, elements(wave), piece);
         double mean;
         float sq;
         if constexpr (Waves == 1) {
-            mean = divide((double)own.near * (double)a.cols + (double)own.sum, a.cols, a.by_cols);
-            sq = squares_about(own, a.cols, mean);
+            mean = divide((double)own.near * (double)cols + (double)own.sum, cols, a.by_cols);
+            sq = squares_about(own, cols, mean);
         } else {
             // the outputs may be the inputs: nothing is stored before every
             // wave of the row has loaded (a row of one wave loads before it
@@ -211,17 +218,16 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kerne
             const WaveSums of = sums[some ? at : 0];
             const uint32_t n = some ? elements(at) : 0;
             const double sum = n ? (double)of.near * (double)n + (double)of.sum : 0.0;
-            mean = divide(sum_of_waves<Waves>(sum), a.cols, a.by_cols);
+            mean = divide(sum_of_waves<Waves>(sum), cols, a.by_cols);
             sq = sum_of_waves<Waves>(n ? squares_about(of, n, mean) : 0.0f);
         }
-        sq = sq < 0.0f ? 0.0f : sq;        // (a rounding below 0)
         const Mean m(mean);
         if (live && a.total) {
             T *const total = static_cast<T *>(a.total) + r * a.total_stride;
 #pragma unroll
-            for (int k = 0; k < V; ++k) store_piece(total, a.cols, piece(k), h[k]);
+            for (int k = 0; k < V; ++k) store_piece(total, cols, piece(k), h[k]);
         }
-        const float rstd = 1.0f / __builtin_sqrtf(sq / (float)a.cols + a.eps);
+        const float rstd = reciprocal_root(sq, (float)a.by_cols, a.eps);
         if (live && i == 0) {
             if (a.mean) a.mean[r] = m.hi;
             if (a.rstd) a.rstd[r] = rstd;
@@ -231,11 +237,21 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kerne
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             if constexpr (!kEarly) fetch_affine(k);
-            store_piece(y, a.cols, piece(k),
+            store_piece(y, cols, piece(k),
                         normed<T>(h[k], m, rstd, affine<T>(weight, w[k], 1.0f),
                                   affine<T>(bias, b[k], 0.0f)));
         }
     }
+}
+
+template <typename T, int Waves, int V, bool Tiny = false>
+__global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kernel(LayerNormArgs a)
+{
+    // two sets, used in turn: a wave is at most one barrier ahead of another
+    __shared__ WaveSums shared[2][layernorm_block(Waves) / 64];
+    if constexpr (Tiny) layernorm_row<T, Waves, V, kTiny>(a, shared);
+    else if (a.cols == Waves * 64 * V * Vec<T>::N) layernorm_row<T, Waves, V, kWhole>(a, shared);
+    else layernorm_row<T, Waves, V, kPart>(a, shared);
 }
 
 // ---------------------------------------------------------------------------
@@ -300,7 +316,7 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_long_kernel(LayerNorm
             for (uint32_t j = 0; j < N; ++j) sq = j >= p.p.skip ? __builtin_fmaf(d[j], d[j], sq) : sq;
         }
         sq = long_sum(sq, sqs[set]);
-        const float rstd = 1.0f / __builtin_sqrtf(sq / (float)a.cols + a.eps);
+        const float rstd = reciprocal_root(sq, (float)a.by_cols, a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[r] = m.hi;
             if (a.rstd) a.rstd[r] = rstd;
@@ -329,13 +345,13 @@ __host__ __device__ constexpr uint64_t sums_pitch(uint64_t cols) { return (cols 
 
 // A piece's sums over rows to a row of floats (elements that two pieces hold
 // have the same sums in both).
-template <typename T, bool Tiny>
-__device__ __forceinline__ void store_sums(float *row, uint32_t cols, const Piece<T, Tiny> &p,
+template <typename T, RowFit Fit>
+__device__ __forceinline__ void store_sums(float *row, uint32_t cols, const Piece<T, Fit> &p,
                                            typename Vec<T>::wide v)
 {
     typedef float Sums __attribute__((ext_vector_type(Vec<T>::N), aligned(4)));
     if (!p.live) return;
-    if constexpr (Tiny) {
+    if constexpr (Fit == kTiny) {
 #pragma unroll
         for (uint32_t j = 0; j < Vec<T>::N; ++j)
             if (j < cols) row[j] = v[j];
@@ -346,22 +362,29 @@ __device__ __forceinline__ void store_sums(float *row, uint32_t cols, const Piec
 
 // Rows that fit in registers: Waves waves a row, V vectors a lane, Groups rows
 // at a time in a block, which adds up dweight and dbias over its rows.
-template <typename T, int Waves, int V, int Groups, bool Tiny = false>
-__global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(LayerNormGradArgs a)
+template <typename T, int Waves, int V, int Groups>
+struct GradShared {
+    // two sets, used in turn: a wave is at most one barrier ahead of another
+    float firsts[2][Waves * Groups], seconds[2][Waves * Groups];
+    float joined[Groups > 1 ? Waves * 64 * V * Vec<T>::N : 1];
+};
+
+template <typename T, int Waves, int V, int Groups, RowFit Fit>
+__device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
+                                                    GradShared<T, Waves, V, Groups> &shared)
 {
     constexpr uint32_t N = Vec<T>::N, kThreads = Waves * 64;
     using Wide = typename Vec<T>::wide;
-    __shared__ float firsts[2][Waves * Groups], seconds[2][Waves * Groups];
-    __shared__ float joined[Groups > 1 ? kThreads * V * N : 1];
     const uint32_t group = row_of_thread<kThreads, Groups>(), i = place_in_row<kThreads, Groups>();
     // the next row is on its way while this one is worked on, and the weight
     // stays, unless they would not fit in registers
     constexpr bool kAhead = V < 3;
     const T *const weight = static_cast<const T *>(a.weight);
-    const auto piece = [&](int k) { return Piece<T, Tiny>((i + k * kThreads) * N, a.cols); };
+    const uint32_t cols = a.cols;
+    const auto piece = [&](int k) { return Piece<T, Fit>((i + k * kThreads) * N, cols); };
     u32x4 wv[kAhead ? V : 1];
     const auto fetch_weight = [&](int k) {
-        return weight ? load_piece<T, false>(weight, a.cols, piece(k)) : u32x4{};
+        return weight ? load_piece<T, false>(weight, cols, piece(k)) : u32x4{};
     };
     if constexpr (kAhead)
 #pragma unroll
@@ -372,7 +395,7 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
     const auto fetch = [&](u32x4 (&v)[V], const void *p, uint64_t first) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            v[k] = load_piece<T, true>(static_cast<const T *>(p) + first, a.cols, piece(k));
+            v[k] = load_piece<T, true>(static_cast<const T *>(p) + first, cols, piece(k));
     };
     Wide dw[V], db[V];
 #pragma unroll
@@ -391,6 +414,7 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
         mean = a.mean[r];
         rstd = a.rstd[r];
     };
+    const float by = (float)(1.0 / (double)cols);
     uint64_t r0 = (uint64_t)blockIdx.x * Groups;
     const uint64_t step = (uint64_t)gridDim.x * Groups;
     if (kAhead && r0 < a.rows) fetch_row(r0);
@@ -406,26 +430,27 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
             xv[k] = x[k];
             if constexpr (kAhead) dtv[k] = dt[k];
         }
-        if constexpr (kAhead)
+        if constexpr (kAhead) {
             if (r0 + step < a.rows) fetch_row(r0 + step);
+            __builtin_amdgcn_sched_barrier(0);       // the loads stay ahead of the sums
+        }
+        // with h = (x - mean) * rstd: rstd comes in once a row
         float first = 0.0f, second = 0.0f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const Piece<T, Tiny> p = piece(k);
             // (past a tiny row and in dead pieces dy is 0)
-            const Wide d = Vec<T>::widen(dyv[k]), h = (Vec<T>::widen(xv[k]) - mu) * rs;
+            const Wide d = Vec<T>::widen(dyv[k]), off = Vec<T>::widen(xv[k]) - mu;
             Wide g = d * factor(k);
             if (live) {
-                dw[k] += d * h;
+                dw[k] += (d * rs) * off;
                 db[k] += d;
             }
-            if (p.skip) {        // the elements that are another piece's too
-                g = Vec<T>::widen(dyv[k] & own_bits(a.cols, p)) * factor(k);
-            }
+            if constexpr (Fit == kPart)        // without what is another piece's too
+                g = Vec<T>::widen(own_bits(dyv[k], cols, piece(k))) * factor(k);
 #pragma unroll
             for (uint32_t j = 0; j < N; ++j) {
                 first += g[j];
-                second = __builtin_fmaf(g[j], h[j], second);
+                second = __builtin_fmaf(g[j], off[j], second);
             }
         }
         // dx may be an input: nothing is stored before every wave of the row
@@ -433,30 +458,34 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
         first = wave_reduce<Sum>(first);
         second = wave_reduce<Sum>(second);
         if constexpr (Waves > 1) {
-            const uint32_t wave = group * Waves + i / 64, at = threadIdx.x % Waves;
+            const uint32_t wave = group * Waves + i / 64, at = threadIdx.x % lanes_of_waves(Waves);
             if (threadIdx.x % 64 == 0) {
-                firsts[set][wave] = first;
-                seconds[set][wave] = second;
+                shared.firsts[set][wave] = first;
+                shared.seconds[set][wave] = second;
             }
             __syncthreads();
-            first = sum_of_waves<Waves>(firsts[set][group * Waves + at]);
-            second = sum_of_waves<Waves>(seconds[set][group * Waves + at]);
+            const uint32_t of = group * Waves + (at < Waves ? at : 0);
+            first = sum_of_waves<Waves>(at < Waves ? shared.firsts[set][of] : 0.0f);
+            second = sum_of_waves<Waves>(at < Waves ? shared.seconds[set][of] : 0.0f);
         }
-        first /= (float)a.cols;
-        second /= (float)a.cols;
+        first *= by;
+        second = second * rs * (rs * by);
         if (!live) continue;
         T *const dx = static_cast<T *>(a.dx) + r * a.dx_stride;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const Wide h = (Vec<T>::widen(xv[k]) - mu) * rs;
-            Wide g = rs * ((Vec<T>::widen(dyv[k]) * factor(k) - first) - h * second);
+            const Wide off = Vec<T>::widen(xv[k]) - mu;
+            Wide g = Vec<T>::widen(dyv[k]) * factor(k) - first, dt(0.0f);
             if (a.dtotal) {
-                if constexpr (kAhead) g += Vec<T>::widen(dtv[k]);
+                if constexpr (kAhead) dt = Vec<T>::widen(dtv[k]);
                 else
-                    g += Vec<T>::widen(load_piece<T, true>(
-                        static_cast<const T *>(a.dtotal) + r * a.dtotal_stride, a.cols, piece(k)));
+                    dt = Vec<T>::widen(load_piece<T, true>(
+                        static_cast<const T *>(a.dtotal) + r * a.dtotal_stride, cols, piece(k)));
             }
-            store_piece(dx, a.cols, piece(k), Vec<T>::narrow(g));
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j)
+                g[j] = __builtin_fmaf(rs, __builtin_fmaf(-off[j], second, g[j]), dt[j]);
+            store_piece(dx, cols, piece(k), Vec<T>::narrow(g));
         }
     }
     if (!a.dweight && !a.dbias) return;
@@ -467,13 +496,15 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
 #pragma unroll
                     for (int k = 0; k < V; ++k)
 #pragma unroll
-                        for (uint32_t j = 0; j < N; ++j) joined[(k * N + j) * kThreads + i] = v[k][j];
+                        for (uint32_t j = 0; j < N; ++j)
+                            shared.joined[(k * N + j) * kThreads + i] = v[k][j];
                 __syncthreads();
                 if (group == 0)
 #pragma unroll
                     for (int k = 0; k < V; ++k)
 #pragma unroll
-                        for (uint32_t j = 0; j < N; ++j) v[k][j] += joined[(k * N + j) * kThreads + i];
+                        for (uint32_t j = 0; j < N; ++j)
+                            v[k][j] += shared.joined[(k * N + j) * kThreads + i];
                 __syncthreads();
             }
         };
@@ -482,14 +513,22 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(
     }
     if (group != 0) return;
     // the one part of a small call is the sum
-    float *const part = static_cast<float *>(a.workspace) + blockIdx.x * (2 * sums_pitch(a.cols));
+    float *const part = static_cast<float *>(a.workspace) + blockIdx.x * (2 * sums_pitch(cols));
     float *const to_w = gridDim.x == 1 ? a.dweight : part;
-    float *const to_b = gridDim.x == 1 ? a.dbias : part + sums_pitch(a.cols);
+    float *const to_b = gridDim.x == 1 ? a.dbias : part + sums_pitch(cols);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        if (to_w) store_sums<T, Tiny>(to_w, a.cols, piece(k), dw[k]);
-        if (to_b) store_sums<T, Tiny>(to_b, a.cols, piece(k), db[k]);
+        if (to_w) store_sums(to_w, cols, piece(k), dw[k]);
+        if (to_b) store_sums(to_b, cols, piece(k), db[k]);
     }
+}
+
+template <typename T, int Waves, int V, int Groups, bool Tiny = false>
+__global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(LayerNormGradArgs a)
+{
+    __shared__ GradShared<T, Waves, V, Groups> shared;
+    if constexpr (Tiny) layernorm_grad_rows<T, Waves, V, Groups, kTiny>(a, shared);
+    else layernorm_grad_rows<T, Waves, V, Groups, kPart>(a, shared);
 }
 
 // dweight (blockIdx.y 0) and dbias (1) from the parts' sums: 32 columns a
@@ -509,6 +548,7 @@ __global__ void __launch_bounds__(kSumCols * kSumParts) ew_layernorm_sums_kernel
         const uint64_t c = c0 + col;
         float sum = 0.0f;
         if (c < a.cols)
+#pragma unroll 8
             for (uint32_t p = p0; p < parts; p += kSumParts) sum += in[p * 2 * pitch + c];
         sums[p0][col] = sum;
         __syncthreads();
@@ -545,8 +585,8 @@ __global__ void __launch_bounds__(kColsBlock) ew_layernorm_cols_kernel(LayerNorm
         db += d;
     }
     float *const part = static_cast<float *>(a.workspace) + blockIdx.y * (2 * sums_pitch(a.cols));
-    store_sums<T, false>(part + p.first, a.cols, p.p, dw);
-    store_sums<T, false>(part + sums_pitch(a.cols) + p.first, a.cols, p.p, db);
+    store_sums(part + p.first, a.cols, p.p, dw);
+    store_sums(part + sums_pitch(a.cols) + p.first, a.cols, p.p, db);
 }
 
 template <typename T>
@@ -602,6 +642,10 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_dx_kernel(LayerNormGr
 // Dispatch
 // ---------------------------------------------------------------------------
 
+// Rows for which a block each is at most one a CU, and at most what the CUs hold
+// at once.
+constexpr uint32_t kRowACu = 256, kOneRound = 1280;
+
 template <typename T>
 static hipError_t layernorm_rows(const LayerNormArgs &a, uint32_t vectors, hipStream_t s)
 {
@@ -617,14 +661,26 @@ static hipError_t layernorm_rows(const LayerNormArgs &a, uint32_t vectors, hipSt
     EW_LAYERNORM_ROWS(2, 1)
     EW_LAYERNORM_ROWS(3, 1)
     EW_LAYERNORM_ROWS(4, 1)
-    EW_LAYERNORM_ROWS(5, 1)
-    EW_LAYERNORM_ROWS(8, 1)
-    EW_LAYERNORM_ROWS(8, 2)
-    EW_LAYERNORM_ROWS(12, 2)
-    EW_LAYERNORM_ROWS(16, 2)
+    if (a.rows <= kRowACu) {
+        EW_LAYERNORM_ROWS(5, 1)
+        EW_LAYERNORM_ROWS(8, 1)
+        EW_LAYERNORM_ROWS(16, 1)
+    }
+    if (a.rows <= kOneRound) {
+        EW_LAYERNORM_ROWS(2, 4)
+    }
+    EW_LAYERNORM_ROWS(3, 2)
+    EW_LAYERNORM_ROWS(4, 2)
+    EW_LAYERNORM_ROWS(3, 4)
+    EW_LAYERNORM_ROWS(4, 4)
     if constexpr (sizeof(T) == 4) {
+        EW_LAYERNORM_ROWS(5, 4)
+        EW_LAYERNORM_ROWS(6, 4)
+        EW_LAYERNORM_ROWS(8, 4)
         EW_LAYERNORM_ROWS(16, 4)
     } else {
+        EW_LAYERNORM_ROWS(12, 2)
+        EW_LAYERNORM_ROWS(16, 2)
         EW_LAYERNORM_ROWS(12, 4)
     }
 #undef EW_LAYERNORM_ROWS
@@ -656,28 +712,32 @@ size_t layernorm_grad_workspace(uint64_t rows, uint64_t cols)
 constexpr uint64_t kOnePart = 2;
 
 template <typename T>
-static hipError_t layernorm_grad_rows(const LayerNormGradArgs &a, uint32_t vectors, hipStream_t s,
+static hipError_t layernorm_grad_by(const LayerNormGradArgs &a, uint32_t vectors, hipStream_t s,
                                       uint32_t *parts)
 {
-#define EW_LAYERNORM_GRAD_LAUNCH(W, V, TINY)                                                         \
-    {                                                                                                \
-        constexpr int kGroups = W < 8 ? 8 / W : 1;                                                   \
-        const uint64_t blocks = ((uint64_t)a.rows + kGroups - 1) / kGroups;                          \
-        *parts = blocks <= kOnePart ? 1 : (uint32_t)(blocks < kParts ? blocks : kParts);             \
-        return start(reinterpret_cast<const void *>(&ew_layernorm_grad_kernel<T, W, V, kGroups, TINY>), \
-                     dim3(*parts), W * 64 * kGroups, 0, s, a);                                       \
+#define EW_LAYERNORM_GRAD_LAUNCH(W, V, G, TINY)                                                   \
+    {                                                                                             \
+        const uint64_t blocks = ((uint64_t)a.rows + G - 1) / G;                                   \
+        *parts = blocks <= kOnePart ? 1 : (uint32_t)(blocks < kParts ? blocks : kParts);          \
+        return start(reinterpret_cast<const void *>(&ew_layernorm_grad_kernel<T, W, V, G, TINY>), \
+                     dim3(*parts), W * 64 * G, 0, s, a);                                          \
     }
-#define EW_LAYERNORM_GRAD_ROWS(W, V) \
-    if (vectors <= W * 64 * V) EW_LAYERNORM_GRAD_LAUNCH(W, V, false)
-    if (a.cols < (uint32_t)Vec<T>::N) EW_LAYERNORM_GRAD_LAUNCH(1, 1, true)
-    EW_LAYERNORM_GRAD_ROWS(1, 1)
-    EW_LAYERNORM_GRAD_ROWS(2, 1)
-    EW_LAYERNORM_GRAD_ROWS(4, 1)
-    EW_LAYERNORM_GRAD_ROWS(8, 1)
-    EW_LAYERNORM_GRAD_ROWS(8, 2)
-    EW_LAYERNORM_GRAD_ROWS(8, 4)
+#define EW_LAYERNORM_GRAD_ROWS(W, V, G) \
+    if (vectors <= W * 64 * V) EW_LAYERNORM_GRAD_LAUNCH(W, V, G, false)
+    if (a.cols < (uint32_t)Vec<T>::N) EW_LAYERNORM_GRAD_LAUNCH(1, 1, 8, true)
+    EW_LAYERNORM_GRAD_ROWS(1, 1, 8)
+    EW_LAYERNORM_GRAD_ROWS(2, 1, 4)
+    EW_LAYERNORM_GRAD_ROWS(4, 1, 4)
     if constexpr (sizeof(T) == 4) {
-        EW_LAYERNORM_GRAD_ROWS(16, 4)
+        EW_LAYERNORM_GRAD_ROWS(8, 1, 2)
+        EW_LAYERNORM_GRAD_ROWS(16, 1, 1)
+        EW_LAYERNORM_GRAD_ROWS(16, 2, 1)
+        EW_LAYERNORM_GRAD_ROWS(16, 4, 1)
+    } else {
+        EW_LAYERNORM_GRAD_ROWS(6, 1, 2)
+        EW_LAYERNORM_GRAD_ROWS(16, 1, 1)
+        EW_LAYERNORM_GRAD_ROWS(12, 2, 1)
+        EW_LAYERNORM_GRAD_ROWS(8, 4, 1)
     }
 #undef EW_LAYERNORM_GRAD_ROWS
 #undef EW_LAYERNORM_GRAD_LAUNCH
@@ -698,9 +758,9 @@ hipError_t launch_layernorm_grad(RowType t, const LayerNormGradArgs &a, hipStrea
     uint32_t parts = 0;
     if (vectors <= grad_vectors(t)) {
         *path = "rows in registers";
-        const hipError_t e = t == kRowF32   ? layernorm_grad_rows<float>(a, vectors, s, &parts)
-                             : t == kRowF16 ? layernorm_grad_rows<_Float16>(a, vectors, s, &parts)
-                                            : layernorm_grad_rows<__bf16>(a, vectors, s, &parts);
+        const hipError_t e = t == kRowF32   ? layernorm_grad_by<float>(a, vectors, s, &parts)
+                             : t == kRowF16 ? layernorm_grad_by<_Float16>(a, vectors, s, &parts)
+                                            : layernorm_grad_by<__bf16>(a, vectors, s, &parts);
         return e != hipSuccess || !sums || parts == 1 ? e : sum(parts);
     }
     *path = "two passes, dweight and dbias by columns";

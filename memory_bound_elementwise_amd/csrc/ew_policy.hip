@@ -75,7 +75,7 @@ struct PolicyRow {
 // Few: rows of less than four.
 template <bool Few>
 struct Four {
-    LongPiece<float, Few> piece;
+    LongPiece<float, Few ? kTiny : kPart> piece;
     f32x4 logp, old, ref, a;
     uint32_t counted;          // bytes that are not 0: tokens of the piece's own that count
 
@@ -83,7 +83,7 @@ struct Four {
     __device__ static Four load(const PolicyTokens &in, const PolicyRow &row, uint32_t cols, uint32_t at)
     {
         typedef uint32_t word __attribute__((aligned(1)));
-        Four f{LongPiece<float, Few>(at, cols), {}, {}, {}, {}, 0};
+        Four f{LongPiece<float, Few ? kTiny : kPart>(at, cols), {}, {}, {}, {}, 0};
         const auto take = [&](const float *p) {
             return __builtin_bit_cast(f32x4, f.piece.template load<true>(p));
         };
@@ -105,6 +105,10 @@ struct Four {
         else f.counted = f.counted >> 8 * f.piece.p.skip << 8 * f.piece.p.skip;
         return f;
     }
+    __device__ uint32_t number() const
+    {
+        return (uint32_t)counts(0) + counts(1) + counts(2) + counts(3);
+    }
     __device__ bool counts(int j) const { return (counted >> 8 * j & 0xffu) != 0; }
 };
 
@@ -114,90 +118,115 @@ struct Four {
 // ---------------------------------------------------------------------------
 
 // Sums over tokens: of -gain, of exp(d) - 1 - d (both weighed within their
-// sequence where the mean is over sequences), of old_logp - logp, and counts.
+// sequence where the mean is over sequences), of old_logp - logp, and counts
+// (exact below 2^53).
 struct PolicySums {
     double policy, kl, fall;
-    uint64_t clipped, tokens, rows;     // rows: sequences with counted tokens
+    double clipped, tokens, rows;       // rows: sequences with counted tokens
+    __device__ void add(const PolicySums &o)
+    {
+        policy += o.policy;
+        kl += o.kl;
+        fall += o.fall;
+        clipped += o.clipped;
+        tokens += o.tokens;
+        rows += o.rows;
+    }
 };
 
 constexpr int kPolicyBlock = 256;
 constexpr int kSmallBlock = 1024;
 
-// Lanes join: sums in a fixed order.
-__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t x)
+__device__ __forceinline__ double sixteen_sum(double x)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) x += (uint64_t)__shfl_xor((unsigned long long)x, d);
-    return x;
+    x += dpp64<0xB1>(x);
+    x += dpp64<0x4E>(x);
+    x += dpp64<0x141>(x);
+    return x + dpp64<0x140>(x);
 }
 
-// The sums of a block in its thread 0.
+// F of each of the sums.
+template <class F>
+__device__ __forceinline__ PolicySums each_sum(const PolicySums &s, F f)
+{
+    return PolicySums{f(s.policy), f(s.kl), f(s.fall), f(s.clipped), f(s.tokens), f(s.rows)};
+}
+
+// The sums of a block of Waves waves (at most 16) in all its threads, in a
+// fixed order.
 template <int Waves>
-__device__ __forceinline__ PolicySums block_sums(PolicySums s, PolicySums *scratch)
+__device__ __forceinline__ PolicySums block_sums(const PolicySums &mine, PolicySums *scratch)
 {
-    s.policy = wave_sum64(s.policy);
-    s.kl = wave_sum64(s.kl);
-    s.fall = wave_sum64(s.fall);
-    s.clipped = wave_sum_u64(s.clipped);
-    s.tokens = wave_sum_u64(s.tokens);
-    s.rows = wave_sum_u64(s.rows);
+    const PolicySums wave = each_sum(mine, [](double x) { return wave_sum64(x); });
+    if (threadIdx.x % 64 == 0) scratch[threadIdx.x / 64] = wave;
     __syncthreads();
-    if (threadIdx.x % 64 == 0) scratch[threadIdx.x / 64] = s;
-    __syncthreads();
-    if (threadIdx.x == 0)
-        for (int w = 1; w < Waves; ++w) {
-            s.policy += scratch[w].policy;
-            s.kl += scratch[w].kl;
-            s.fall += scratch[w].fall;
-            s.clipped += scratch[w].clipped;
-            s.tokens += scratch[w].tokens;
-            s.rows += scratch[w].rows;
-        }
-    return s;
+    const uint32_t at = threadIdx.x % 16;
+    const PolicySums some = at < Waves ? scratch[at] : PolicySums{};
+    return each_sum(some, [](double x) { return sixteen_sum(x); });
 }
 
-// What a thread sums of a row's tokens [from, to): steps of `step` tokens.
+// What a thread sums of a row's tokens [from, to): steps of `step` tokens, two
+// of them on their way together.
+struct Counts {
+    uint64_t clipped, tokens;
+};
+
 template <bool Ref, bool Few>
-__device__ __forceinline__ void sum_tokens(const PolicyTokens &in, uint64_t r, uint32_t cols,
-                                           uint64_t from, uint64_t to, uint32_t step, PolicySums &s)
+__device__ __forceinline__ void add_four(const PolicyTokens &in, const Four<Few> &f, PolicySums &s, Counts &n)
 {
-    if (from >= to) return;        // (the advantage of no tokens may be absent)
-    const PolicyRow row(in, r);
-    for (uint64_t at = from; at < to; at += step) {
-        const auto f = Four<Few>::template load<Ref>(in, row, cols, (uint32_t)at);
-        float policy = 0.0f, kl = 0.0f, fall = 0.0f;
+    float policy = 0.0f, kl = 0.0f, fall = 0.0f;
+    uint32_t clipped = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const Token t = token<Ref>(in, f.logp[j], f.old[j], f.ref[j], f.a[j]);
-            const bool counted = f.counts(j);
-            const float bound = f.a[j] > 0.0f ? in.most : in.least;
-            const float loss = -f.a[j] * (t.clipped ? bound : t.ratio);
-            policy += counted ? loss : 0.0f;
-            kl += counted ? t.line : 0.0f;
-            fall -= counted ? t.x : 0.0f;
-            s.clipped += counted && t.clipped;
-            s.tokens += counted;
-        }
-        s.policy += (double)policy;
-        s.kl += (double)kl;
-        s.fall += (double)fall;
+    for (int j = 0; j < 4; ++j) {
+        const Token t = token<Ref>(in, f.logp[j], f.old[j], f.ref[j], f.a[j]);
+        const bool counted = f.counts(j);
+        const float bound = f.a[j] > 0.0f ? in.most : in.least;
+        const float loss = -f.a[j] * (t.clipped ? bound : t.ratio);
+        policy += counted ? loss : 0.0f;
+        if constexpr (Ref) kl += counted ? t.line : 0.0f;
+        fall -= counted ? t.x : 0.0f;
+        clipped += counted && t.clipped;
     }
+    s.policy += (double)policy;
+    if constexpr (Ref) s.kl += (double)kl;
+    s.fall += (double)fall;
+    n.clipped += clipped;
+    n.tokens += f.number();
 }
 
-// Loss, stats and the weights of rows [first, last) from the batch's sums.
+template <bool Ref, bool Few>
+__device__ __forceinline__ Counts sum_tokens(const PolicyTokens &in, uint64_t r, uint32_t cols,
+                                             uint64_t from, uint64_t to, uint32_t step, PolicySums &s)
+{
+    Counts n{0, 0};
+    if (from >= to) return n;      // (the advantage of no tokens may be absent)
+    const PolicyRow row(in, r);
+    uint64_t at = from;
+    if constexpr (!Few)
+        for (; at + step < to; at += 2 * (uint64_t)step) {
+            const auto f = Four<Few>::template load<Ref>(in, row, cols, (uint32_t)at);
+            const auto g = Four<Few>::template load<Ref>(in, row, cols, (uint32_t)(at + step));
+            add_four<Ref, Few>(in, f, s, n);
+            add_four<Ref, Few>(in, g, s, n);
+        }
+    if (at < to) add_four<Ref, Few>(in, Four<Few>::template load<Ref>(in, row, cols, (uint32_t)at), s, n);
+    return n;
+}
+
+// Loss and stats from the batch's sums.
 __device__ __forceinline__ void write_loss(const PolicyLossArgs &a, const PolicySums &s)
 {
-    const double n = a.mean == EW_MEAN_TOKENS ? (double)s.tokens
-                     : a.mean == EW_MEAN_SEQUENCES ? (double)s.rows : 1.0;
-    const double w = s.tokens ? (double)a.scale / n : 0.0;
-    const double policy = s.tokens ? s.policy * w : 0.0, kl = s.tokens ? s.kl * w : 0.0;
+    const bool some = s.tokens > 0.0;
+    const double n = a.mean == EW_MEAN_TOKENS ? s.tokens : a.mean == EW_MEAN_SEQUENCES ? s.rows : 1.0;
+    const double w = some ? (double)a.scale / n : 0.0;
+    const double policy = some ? s.policy * w : 0.0, kl = some ? s.kl * w : 0.0;
     // (a KL term that does not count may be infinite)
     a.loss[0] = (float)(a.in.kl != 0.0f ? policy + (double)a.in.kl * kl : policy);
     if (a.stats) {
         a.stats[0] = (float)policy;
         a.stats[1] = (float)kl;
-        a.stats[2] = s.tokens ? (float)((double)s.clipped / (double)s.tokens) : 0.0f;
-        a.stats[3] = s.tokens ? (float)(s.fall / (double)s.tokens) : 0.0f;
+        a.stats[2] = some ? (float)(s.clipped / s.tokens) : 0.0f;
+        a.stats[3] = some ? (float)(s.fall / s.tokens) : 0.0f;
     }
 }
 
@@ -205,9 +234,9 @@ __device__ __forceinline__ void write_loss(const PolicyLossArgs &a, const Policy
 __device__ __forceinline__ float token_weight(const PolicyLossArgs &a, const PolicySums &s, uint32_t n)
 {
     if (n == 0) return 0.0f;
-    if (a.mean == EW_MEAN_TOKENS) return (float)((double)a.scale / (double)s.tokens);
+    if (a.mean == EW_MEAN_TOKENS) return (float)((double)a.scale / s.tokens);
     if (a.mean == EW_MEAN_NONE) return a.scale;
-    return (float)((double)a.scale / ((double)n * (double)s.rows));
+    return (float)((double)a.scale / ((double)n * s.rows));
 }
 
 // Sum over `lanes` neighbouring lanes (a power of two), in each of them.
@@ -217,8 +246,8 @@ __device__ __forceinline__ uint32_t lanes_sum(uint32_t x, uint32_t lanes)
     return x;
 }
 
-// A sequence's sums as the batch counts them: divided by its tokens where the
-// mean is over sequences.  Lane 0 of its lanes counts the sequence.
+// A sequence's sums (or a part's, or a lane's of them) as the batch counts
+// them: divided by the sequence's tokens where the mean is over sequences.
 __device__ __forceinline__ void add_sequence(PolicySums &all, const PolicySums &s, bool by_sequence,
                                              uint32_t tokens, bool first)
 {
@@ -228,41 +257,46 @@ __device__ __forceinline__ void add_sequence(PolicySums &all, const PolicySums &
     all.fall += s.fall;
     all.clipped += s.clipped;
     all.tokens += s.tokens;
-    all.rows += first && tokens;
+    all.rows += first && tokens ? 1.0 : 0.0;
 }
 
-// Few tokens: one block, `lanes` lanes a sequence at a time.
+// Sequences from r0 on, `step` of them apart and `lanes` lanes each, added to
+// all; their tokens to counts.  Whole waves go round together (lanes_sum).
+template <bool Ref, bool Few>
+__device__ __forceinline__ void add_sequences(const PolicyLossArgs &a, uint64_t r0, uint64_t step,
+                                              uint32_t lanes, uint32_t *counts, PolicySums &all)
+{
+    const uint32_t lane = threadIdx.x % lanes;
+    for (; r0 < a.rows; r0 += step) {
+        const uint64_t r = r0 + threadIdx.x / lanes;
+        PolicySums s{};
+        Counts n{0, 0};
+        if (r < a.rows)
+            n = sum_tokens<Ref, Few>(a.in, r, a.cols, (uint64_t)lane * 4, a.cols, lanes * 4, s);
+        s.clipped = (double)n.clipped;
+        s.tokens = (double)n.tokens;
+        const uint32_t tokens = lanes_sum((uint32_t)n.tokens, lanes);
+        add_sequence(all, s, a.mean == EW_MEAN_SEQUENCES, tokens, lane == 0);
+        if (r < a.rows && lane == 0) counts[r] = tokens;
+    }
+}
+
+// Few tokens: one block.
 template <bool Ref, bool Few>
 __global__ void __launch_bounds__(kSmallBlock) ew_policy_small_kernel(PolicyLossArgs a, uint32_t lanes)
 {
     __shared__ PolicySums scratch[kSmallBlock / 64];
     uint32_t *const counts = static_cast<uint32_t *>(a.workspace);
     PolicySums all{};
-    const uint32_t lane = threadIdx.x % lanes;
-    // (whole waves go round together: lanes_sum)
-    for (uint32_t r0 = 0; r0 < a.rows; r0 += kSmallBlock / lanes) {
-        const uint32_t r = r0 + threadIdx.x / lanes;
-        PolicySums s{};
-        if (r < a.rows)
-            sum_tokens<Ref, Few>(a.in, r, a.cols, (uint64_t)lane * 4, a.cols, lanes * 4, s);
-        const uint32_t tokens = lanes_sum((uint32_t)s.tokens, lanes);
-        add_sequence(all, s, a.mean == EW_MEAN_SEQUENCES, tokens, lane == 0);
-        if (r < a.rows && lane == 0) counts[r] = tokens;
-    }
+    add_sequences<Ref, Few>(a, 0, kSmallBlock / lanes, lanes, counts, all);
     all = block_sums<kSmallBlock / 64>(all, scratch);
-    if (threadIdx.x == 0) {
-        scratch[0] = all;
-        write_loss(a, all);
-    }
-    __syncthreads();
-    all = scratch[0];
+    if (threadIdx.x == 0) write_loss(a, all);
     if (a.weights)
         for (uint32_t r = threadIdx.x; r < a.rows; r += kSmallBlock)
             a.weights[r] = token_weight(a, all, counts[r]);
 }
 
-// Whole sequences: `lanes` lanes each; a record of sums a block, a count of
-// tokens a sequence.
+// Whole sequences: a record of sums a block, a count of tokens a sequence.
 template <bool Ref, bool Few>
 __global__ void __launch_bounds__(kPolicyBlock) ew_policy_rows_kernel(PolicyLossArgs a, uint32_t lanes,
                                                                      PolicySums *records,
@@ -270,16 +304,8 @@ __global__ void __launch_bounds__(kPolicyBlock) ew_policy_rows_kernel(PolicyLoss
 {
     __shared__ PolicySums scratch[kPolicyBlock / 64];
     PolicySums all{};
-    const uint32_t lane = threadIdx.x % lanes, per = kPolicyBlock / lanes;
-    for (uint64_t r0 = (uint64_t)blockIdx.x * per; r0 < a.rows; r0 += (uint64_t)gridDim.x * per) {
-        const uint64_t r = r0 + threadIdx.x / lanes;
-        PolicySums s{};
-        if (r < a.rows)
-            sum_tokens<Ref, Few>(a.in, r, a.cols, (uint64_t)lane * 4, a.cols, lanes * 4, s);
-        const uint32_t tokens = lanes_sum((uint32_t)s.tokens, lanes);
-        add_sequence(all, s, a.mean == EW_MEAN_SEQUENCES, tokens, lane == 0);
-        if (r < a.rows && lane == 0) counts[r] = tokens;
-    }
+    const uint64_t per = kPolicyBlock / lanes;
+    add_sequences<Ref, Few>(a, blockIdx.x * per, gridDim.x * per, lanes, counts, all);
     all = block_sums<kPolicyBlock / 64>(all, scratch);
     if (threadIdx.x == 0) records[blockIdx.x] = all;
 }
@@ -293,8 +319,10 @@ __global__ void __launch_bounds__(kPolicyBlock) ew_policy_parts_kernel(PolicyLos
     __shared__ PolicySums scratch[kPolicyBlock / 64];
     PolicySums s{};
     const uint64_t from = blockIdx.x * part_tokens, to = from + part_tokens;
-    sum_tokens<Ref, false>(a.in, blockIdx.y, a.cols, from + threadIdx.x * 4, to < a.cols ? to : a.cols,
-                    kPolicyBlock * 4, s);
+    const Counts n = sum_tokens<Ref, false>(a.in, blockIdx.y, a.cols, from + threadIdx.x * 4,
+                                            to < a.cols ? to : a.cols, kPolicyBlock * 4, s);
+    s.clipped = (double)n.clipped;
+    s.tokens = (double)n.tokens;
     s = block_sums<kPolicyBlock / 64>(s, scratch);
     if (threadIdx.x == 0) records[(uint64_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
@@ -311,8 +339,8 @@ __global__ void __launch_bounds__(kSmallBlock) ew_policy_join_kernel(PolicyLossA
                                                                     const uint32_t *counts)
 {
     __shared__ PolicySums scratch[kSmallBlock / 64];
-    PolicySums all{};
     __shared__ uint32_t tokens_of[kCutRows];
+    PolicySums all{};
     if (parts) {
         for (uint32_t r = threadIdx.x / 64; r < a.rows; r += kSmallBlock / 64) {
             uint32_t tokens = 0;
@@ -326,27 +354,16 @@ __global__ void __launch_bounds__(kSmallBlock) ew_policy_join_kernel(PolicyLossA
             add_sequence(all, records[i], a.mean == EW_MEAN_SEQUENCES, tokens_of[i / parts],
                          i % parts == 0);
     } else {
-        for (uint32_t i = threadIdx.x; i < n; i += kSmallBlock) {
-            const PolicySums &s = records[i];
-            all.policy += s.policy;
-            all.kl += s.kl;
-            all.fall += s.fall;
-            all.clipped += s.clipped;
-            all.tokens += s.tokens;
-            all.rows += s.rows;
-        }
+        for (uint32_t i = threadIdx.x; i < n; i += kSmallBlock) all.add(records[i]);
     }
+    // (on their way meanwhile)
+    const uint64_t first = (uint64_t)blockIdx.x * kSmallBlock + threadIdx.x;
+    const uint32_t mine = a.weights && !parts && first < a.rows ? counts[first] : 0;
     all = block_sums<kSmallBlock / 64>(all, scratch);
-    if (threadIdx.x == 0) {
-        scratch[0] = all;
-        if (blockIdx.x == 0) write_loss(a, all);
-    }
-    __syncthreads();
-    all = scratch[0];
+    if (blockIdx.x == 0 && threadIdx.x == 0) write_loss(a, all);
     if (!a.weights) return;
-    for (uint64_t r = (uint64_t)blockIdx.x * kSmallBlock + threadIdx.x; r < a.rows;
-         r += (uint64_t)gridDim.x * kSmallBlock)
-        a.weights[r] = token_weight(a, all, parts ? tokens_of[r] : counts[r]);
+    for (uint64_t r = first; r < a.rows; r += (uint64_t)gridDim.x * kSmallBlock)
+        a.weights[r] = token_weight(a, all, parts ? tokens_of[r] : r == first ? mine : counts[r]);
 }
 
 // ---------------------------------------------------------------------------

@@ -7,6 +7,10 @@
 
 namespace ew {
 
+// What is known of a row's vectors: all are whole; the last may be a part; the
+// row is shorter than one.
+enum RowFit : int { kWhole = 0, kPart, kTiny };
+
 // Where a vector of a row of cols elements lies: element `first` of the row on,
 // N of them.  A row's vectors start at its start, one behind another; its last,
 // partial one is taken as the last N elements of the row instead, of which the
@@ -14,30 +18,33 @@ namespace ew {
 // everywhere (elements one by one, each waited for, cost 0.5-2 us a row); both
 // vectors hold, compute and store the same there, and only sums and stores of
 // what depends on an output's old value leave out what is not their own.
-// Tiny: a row shorter than a vector, one piece with zeros behind the row.
-template <typename T, bool Tiny = false>
+// A tiny row is one piece with zeros behind the row.
+template <typename T, RowFit Fit>
 struct Piece {
     static constexpr uint32_t N = Vec<T>::N;
     uint32_t first, skip;
     bool live;
     // back: elements of the row before element 0 of the stretch
     __device__ Piece(uint32_t at, uint32_t cols, uint32_t back = 0)
-        : first(back + (Tiny || at + N <= cols ? at : cols - N)), skip(back + at - first),
-          live(at < cols)
+        : first(back + (Fit != kPart || at + N <= cols ? at : cols - N)), skip(back + at - first),
+          live(Fit == kWhole || at < cols)
     {
     }
     // whether element j of a live piece is its own
-    __device__ bool own(uint32_t j, uint32_t cols) const { return Tiny ? j < cols : j >= skip; }
+    __device__ bool own(uint32_t j, uint32_t cols) const
+    {
+        return Fit == kWhole || (Fit == kTiny ? j < cols : j >= skip);
+    }
 };
 
 // Loads and stores of a piece; `row` is best the same in all lanes, whose
 // offsets are of 32 bits then.  A stretch of a row far below 2^32 bytes.
 // Nt: a stream read once, else data that others read too.
-template <typename T, bool Nt, bool Tiny>
-__device__ __forceinline__ u32x4 load_piece(const T *row, uint32_t cols, const Piece<T, Tiny> &p)
+template <typename T, bool Nt, RowFit Fit>
+__device__ __forceinline__ u32x4 load_piece(const T *row, uint32_t cols, const Piece<T, Fit> &p)
 {
     if (!p.live) return u32x4{0, 0, 0, 0};
-    if constexpr (Tiny) {
+    if constexpr (Fit == kTiny) {
         typename Vec<T>::type t{};
 #pragma unroll
         for (uint32_t j = 0; j < Vec<T>::N; ++j)
@@ -50,11 +57,11 @@ __device__ __forceinline__ u32x4 load_piece(const T *row, uint32_t cols, const P
     else return *reinterpret_cast<const u32x4_a2 *>(at);
 }
 
-template <typename T, bool Tiny>
-__device__ __forceinline__ void store_piece(T *row, uint32_t cols, const Piece<T, Tiny> &p, u32x4 v)
+template <typename T, RowFit Fit>
+__device__ __forceinline__ void store_piece(T *row, uint32_t cols, const Piece<T, Fit> &p, u32x4 v)
 {
     if (!p.live) return;
-    if constexpr (Tiny) {
+    if constexpr (Fit == kTiny) {
         const typename Vec<T>::type t = __builtin_bit_cast(typename Vec<T>::type, v);
 #pragma unroll
         for (uint32_t j = 0; j < Vec<T>::N; ++j)
@@ -65,44 +72,45 @@ __device__ __forceinline__ void store_piece(T *row, uint32_t cols, const Piece<T
 }
 
 // The elements of a piece that are its own, one by one where those are not all.
-template <typename T, bool Tiny>
-__device__ __forceinline__ void store_own(T *row, uint32_t cols, const Piece<T, Tiny> &p, u32x4 v)
+template <typename T, RowFit Fit>
+__device__ __forceinline__ void store_own(T *row, uint32_t cols, const Piece<T, Fit> &p, u32x4 v)
 {
-    if (Tiny || p.skip == 0) return store_piece(row, cols, p, v);
+    if (Fit != kPart || p.skip == 0) return store_piece(row, cols, p, v);
     const typename Vec<T>::type t = __builtin_bit_cast(typename Vec<T>::type, v);
 #pragma unroll
     for (uint32_t j = 0; j < Vec<T>::N; ++j)
         if (p.live && j >= p.skip) row[p.first + j] = t[j];
 }
 
-// Bits of the elements that are a piece's own (0 of a piece past the row).
-template <typename T, bool Tiny>
-__device__ __forceinline__ u32x4 own_bits(uint32_t cols, const Piece<T, Tiny> &p)
+// The bits of v that are a piece's own, 0 elsewhere.
+template <typename T, RowFit Fit>
+__device__ __forceinline__ u32x4 own_bits(u32x4 v, uint32_t cols, const Piece<T, Fit> &p)
 {
-    constexpr uint32_t kPerWord = 4 / (uint32_t)sizeof(T);
-    u32x4 m;
+    if constexpr (Fit == kPart) {
+        constexpr uint32_t kPerWord = 4 / (uint32_t)sizeof(T);
 #pragma unroll
-    for (uint32_t w = 0; w < 4; ++w) {
-        uint32_t bits = 0;
+        for (uint32_t w = 0; w < 4; ++w) {
+            uint32_t bits = 0;
 #pragma unroll
-        for (uint32_t h = 0; h < kPerWord; ++h)
-            if (p.live && p.own(w * kPerWord + h, cols))
-                bits |= (kPerWord == 1 ? 0xffffffffu : 0xffffu) << (16 * h);
-        m[w] = bits;
+            for (uint32_t h = 0; h < kPerWord; ++h)
+                if (p.own(w * kPerWord + h, cols))
+                    bits |= (kPerWord == 1 ? 0xffffffffu : 0xffffu) << (16 * h);
+            v[w] &= bits;
+        }
     }
-    return m;
+    return v;             // (a tiny row's and dead pieces' others are 0)
 }
 
 // The piece at element `at` of a row of any length: element `first` of the row
 // on, with offsets of 64 bits.
-template <typename T, bool Tiny = false>
+template <typename T, RowFit Fit = kPart>
 struct LongPiece {
     uint64_t first;
     uint32_t cols;
-    Piece<T, Tiny> p;          // of the vector at `first`, a row of its own
+    Piece<T, Fit> p;           // of the vector at `first`, a row of its own
     __device__ LongPiece(uint32_t at, uint32_t cols_)
-        : first(Tiny || at + Vec<T>::N <= cols_ ? at : cols_ - Vec<T>::N), cols(cols_),
-          p(0, Tiny ? cols_ : Vec<T>::N)
+        : first(Fit == kTiny || at + Vec<T>::N <= cols_ ? at : cols_ - Vec<T>::N), cols(cols_),
+          p(0, Fit == kTiny ? cols_ : Vec<T>::N)
     {
         p.skip = at - (uint32_t)first;
     }
