@@ -729,12 +729,14 @@ static hipError_t layernorm_grad_by(const LayerNormGradArgs &a, uint32_t vectors
     EW_LAYERNORM_GRAD_ROWS(2, 1, 4)
     EW_LAYERNORM_GRAD_ROWS(4, 1, 4)
     if constexpr (sizeof(T) == 4) {
-        EW_LAYERNORM_GRAD_ROWS(8, 1, 2)
+        if (vectors <= 384) EW_LAYERNORM_GRAD_LAUNCH(8, 1, 2, false)
+        EW_LAYERNORM_GRAD_ROWS(8, 1, 1)
         EW_LAYERNORM_GRAD_ROWS(16, 1, 1)
         EW_LAYERNORM_GRAD_ROWS(16, 2, 1)
         EW_LAYERNORM_GRAD_ROWS(16, 4, 1)
     } else {
         EW_LAYERNORM_GRAD_ROWS(6, 1, 2)
+        EW_LAYERNORM_GRAD_ROWS(8, 1, 1)
         EW_LAYERNORM_GRAD_ROWS(16, 1, 1)
         EW_LAYERNORM_GRAD_ROWS(12, 2, 1)
         EW_LAYERNORM_GRAD_ROWS(8, 4, 1)

@@ -24,10 +24,13 @@ struct Growth {
         p = __builtin_fmaf(p, d, 1.0f / 24.0f);
         p = __builtin_fmaf(p, d, 1.0f / 6.0f);
         p = __builtin_fmaf(p, d, 0.5f);
-        const bool near = __builtin_fabsf(d) < 1.0f;
-        const float bend = p * d * d, e = exp_nat(d) - 1.0f;
-        one = near ? d + bend : e;
-        line = near ? bend : e == kInf ? e : e - d;          // (not inf - inf)
+        const float bend = p * d * d;
+        one = d + bend;
+        line = bend;
+        if (!(__builtin_fabsf(d) < 1.0f)) {                  // (few lanes, if any)
+            one = exp_nat(d) - 1.0f;
+            line = one == kInf ? one : one - d;              // (not inf - inf)
+        }
     }
 };
 
@@ -71,46 +74,114 @@ struct PolicyRow {
     }
 };
 
-// Four neighbouring tokens of a row: the piece at token `at` (below cols).
-// Few: rows of less than four.
-template <bool Few>
-struct Four {
-    LongPiece<float, Few ? kTiny : kPart> piece;
-    f32x4 logp, old, ref, a;
-    uint32_t counted;          // bytes that are not 0: tokens of the piece's own that count
+// A stretch of a row: `lanes` lanes take four neighbouring tokens of it each,
+// from token `from` on.
+template <RowFit Fit>
+struct Tokens {
+    using Place = Piece<float, Fit>;
+    uint64_t from;
+    uint32_t cols, back;       // its tokens; tokens before it that a piece may reach
+    __device__ Tokens(uint64_t from_, uint32_t all, uint32_t lanes)
+        : from(from_), cols(all - from_ < lanes * 4 ? (uint32_t)(all - from_) : lanes * 4),
+          back(from_ ? 4 : 0)
+    {
+    }
+    __device__ Place place(uint32_t lane) const { return Place(lane * 4, cols, back); }
+    template <class E>
+    __device__ E *row(E *p) const { return p + (from - back); }
+};
 
-    template <bool Ref>
-    __device__ static Four load(const PolicyTokens &in, const PolicyRow &row, uint32_t cols, uint32_t at)
+// Four tokens of a lane.  Which of them count comes first: of tokens that do
+// not, nothing else is read.
+struct Four {
+    uint32_t counted;          // bit 8 j + 7: token j is the piece's own and counts
+    f32x4 logp, old, ref, a;
+
+    // The mask's bytes of the lane's piece.
+    template <RowFit Fit>
+    __device__ static uint32_t mark(const PolicyTokens &in, const PolicyRow &row, const Tokens<Fit> &t,
+                                    uint32_t lane)
     {
         typedef uint32_t word __attribute__((aligned(1)));
-        Four f{LongPiece<float, Few ? kTiny : kPart>(at, cols), {}, {}, {}, {}, 0};
-        const auto take = [&](const float *p) {
-            return __builtin_bit_cast(f32x4, f.piece.template load<true>(p));
-        };
-        f.logp = take(row.logp);
-        f.old = take(row.old);
-        f.ref = Ref ? take(row.ref) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        f.a = in.advantage_stride ? take(row.advantage) : f32x4{row.each, row.each, row.each, row.each};
-        f.counted = 0x01010101u;
-        if (in.mask) {
-            if constexpr (Few) {
-                f.counted = 0;
-                for (uint32_t j = 0; j < cols; ++j) f.counted |= (uint32_t)row.mask[j] << 8 * j;
-            } else {
-                f.counted =
-                    __builtin_nontemporal_load(reinterpret_cast<const word *>(row.mask + f.piece.first));
-            }
+        const auto p = t.place(lane);
+        if (!p.live) return 0;
+        if (!in.mask) return 0x01010101u;
+        if constexpr (Fit == kTiny) {
+            uint32_t bytes = 0;
+            for (uint32_t j = 0; j < t.cols; ++j) bytes |= (uint32_t)row.mask[j] << 8 * j;
+            return bytes;
         }
-        if (Few) f.counted &= (1u << 8 * cols) - 1;
-        else f.counted = f.counted >> 8 * f.piece.p.skip << 8 * f.piece.p.skip;
-        return f;
+        return __builtin_nontemporal_load(reinterpret_cast<const word *>(t.row(row.mask) + p.first));
     }
-    __device__ uint32_t number() const
+    template <bool Ref, RowFit Fit>
+    __device__ void load(const PolicyTokens &in, const PolicyRow &row, const Tokens<Fit> &t,
+                         uint32_t lane, uint32_t mark)
     {
-        return (uint32_t)counts(0) + counts(1) + counts(2) + counts(3);
+        const auto p = t.place(lane);
+        counted = (((mark & 0x7f7f7f7fu) + 0x7f7f7f7fu) | mark) & 0x80808080u;   // bytes not 0
+        if constexpr (Fit == kTiny) counted &= (1u << 8 * t.cols) - 1;
+        if constexpr (Fit == kPart) counted = counted >> 8 * p.skip << 8 * p.skip;
+        if (!counted) return;
+        const auto take = [&](const float *v) {
+            return __builtin_bit_cast(f32x4, load_piece<float, true>(t.row(v), t.cols, p));
+        };
+        logp = take(row.logp);
+        old = take(row.old);
+        if constexpr (Ref) ref = take(row.ref);
+        a = in.advantage_stride ? take(row.advantage) : f32x4{row.each, row.each, row.each, row.each};
     }
-    __device__ bool counts(int j) const { return (counted >> 8 * j & 0xffu) != 0; }
+    template <bool Ref>
+    __device__ Token token(const PolicyTokens &in, int j) const
+    {
+        return ew::token<Ref>(in, logp[j], old[j], Ref ? ref[j] : 0.0f, a[j]);
+    }
+    __device__ uint32_t number() const { return (uint32_t)__builtin_popcount(counted); }
+    __device__ bool counts(int j) const { return (counted >> (8 * j + 7) & 1u) != 0; }
 };
+
+// Calls f for a lane's pieces of a row's tokens [from, to), stretch by stretch
+// of `lanes` lanes.  Two whole stretches' pieces are on their way together, and
+// the marks of the next two.  One: the row is one stretch.
+template <bool Ref, bool Few, bool One, class F>
+__device__ __forceinline__ void each_four(const PolicyTokens &in, const PolicyRow &row, uint64_t from,
+                                          uint32_t to, uint32_t lanes, uint32_t lane, F f)
+{
+    const auto last = [&](uint64_t at) {
+        const Tokens<Few ? kTiny : kPart> t(at, to, lanes);
+        Four four;
+        four.load<Ref>(in, row, t, lane, Four::mark(in, row, t, lane));
+        f(four, t);
+    };
+    if constexpr (One) {
+        last(0);
+        return;
+    }
+    const auto step = (uint64_t)lanes * 4;
+    using Whole = Tokens<kWhole>;
+    const auto mark = [&](uint64_t at) {
+        return at + step <= to ? Four::mark(in, row, Whole(at, to, lanes), lane) : 0;
+    };
+    uint32_t next1 = mark(from), next2 = mark(from + step);
+    uint64_t at = from;
+    for (; at + step <= to; at += 2 * step) {
+        const uint32_t mark1 = next1, mark2 = next2;
+        next1 = mark(at + 2 * step);
+        next2 = mark(at + 3 * step);
+        const bool more = at + 2 * step <= to;
+        const Whole t1(at, to, lanes), t2(more ? at + step : at, to, lanes);
+        Four f1, f2;
+        f1.load<Ref>(in, row, t1, lane, mark1);
+        f2.load<Ref>(in, row, t2, lane, mark2);
+        f(f1, t1);
+        __builtin_amdgcn_sched_barrier(0);      // one piece's numbers in registers at a time
+        if (!more) {
+            at += step;
+            break;
+        }
+        f(f2, t2);
+    }
+    if (at < to) last(at);
+}
 
 // ---------------------------------------------------------------------------
 // Forward: sums over parts of the batch, then their join.  Both in one block
@@ -165,20 +236,19 @@ __device__ __forceinline__ PolicySums block_sums(const PolicySums &mine, PolicyS
     return each_sum(some, [](double x) { return sixteen_sum(x); });
 }
 
-// What a thread sums of a row's tokens [from, to): steps of `step` tokens, two
-// of them on their way together.
+// What a lane sums of a row's tokens [from, to).
 struct Counts {
     uint64_t clipped, tokens;
 };
 
-template <bool Ref, bool Few>
-__device__ __forceinline__ void add_four(const PolicyTokens &in, const Four<Few> &f, PolicySums &s, Counts &n)
+template <bool Ref>
+__device__ __forceinline__ void add_four(const PolicyTokens &in, const Four &f, PolicySums &s, Counts &n)
 {
     float policy = 0.0f, kl = 0.0f, fall = 0.0f;
     uint32_t clipped = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const Token t = token<Ref>(in, f.logp[j], f.old[j], f.ref[j], f.a[j]);
+        const Token t = f.token<Ref>(in, j);
         const bool counted = f.counts(j);
         const float bound = f.a[j] > 0.0f ? in.most : in.least;
         const float loss = -f.a[j] * (t.clipped ? bound : t.ratio);
@@ -194,22 +264,16 @@ __device__ __forceinline__ void add_four(const PolicyTokens &in, const Four<Few>
     n.tokens += f.number();
 }
 
-template <bool Ref, bool Few>
-__device__ __forceinline__ Counts sum_tokens(const PolicyTokens &in, uint64_t r, uint32_t cols,
-                                             uint64_t from, uint64_t to, uint32_t step, PolicySums &s)
+template <bool Ref, bool Few, bool One>
+__device__ __forceinline__ Counts sum_tokens(const PolicyTokens &in, uint64_t r, uint64_t from,
+                                             uint32_t to, uint32_t lanes, uint32_t lane, PolicySums &s)
 {
     Counts n{0, 0};
     if (from >= to) return n;      // (the advantage of no tokens may be absent)
     const PolicyRow row(in, r);
-    uint64_t at = from;
-    if constexpr (!Few)
-        for (; at + step < to; at += 2 * (uint64_t)step) {
-            const auto f = Four<Few>::template load<Ref>(in, row, cols, (uint32_t)at);
-            const auto g = Four<Few>::template load<Ref>(in, row, cols, (uint32_t)(at + step));
-            add_four<Ref, Few>(in, f, s, n);
-            add_four<Ref, Few>(in, g, s, n);
-        }
-    if (at < to) add_four<Ref, Few>(in, Four<Few>::template load<Ref>(in, row, cols, (uint32_t)at), s, n);
+    each_four<Ref, Few, One>(in, row, from, to, lanes, lane, [&](const Four &f, const auto &) {
+        if (f.counted) add_four<Ref>(in, f, s, n);
+    });
     return n;
 }
 
@@ -260,35 +324,52 @@ __device__ __forceinline__ void add_sequence(PolicySums &all, const PolicySums &
     all.rows += first && tokens ? 1.0 : 0.0;
 }
 
-// Sequences from r0 on, `step` of them apart and `lanes` lanes each, added to
-// all; their tokens to counts.  Whole waves go round together (lanes_sum).
-template <bool Ref, bool Few>
+// Which sequence of a round a thread works on; Wave: the same for a wave.
+template <bool Wave>
+__device__ __forceinline__ uint32_t row_in_round(uint32_t lanes)
+{
+    const uint32_t row = threadIdx.x / lanes;
+    return Wave ? (uint32_t)__builtin_amdgcn_readfirstlane((int)row) : row;
+}
+
+// Sequences from r0 on, `step` of them apart and `lanes` lanes each (up to a
+// wave, or Block: the block's), added to all; their tokens to counts.  Whole
+// waves and blocks go round together.
+template <bool Ref, bool Few, bool Wave, uint32_t Block>
 __device__ __forceinline__ void add_sequences(const PolicyLossArgs &a, uint64_t r0, uint64_t step,
                                               uint32_t lanes, uint32_t *counts, PolicySums &all)
 {
+    // two sets, used in turn: a wave is at most one barrier ahead of another
+    __shared__ uint32_t tokens_of[2][Block / 64];
     const uint32_t lane = threadIdx.x % lanes;
-    for (; r0 < a.rows; r0 += step) {
-        const uint64_t r = r0 + threadIdx.x / lanes;
+    for (int set = 0; r0 < a.rows; r0 += step, set ^= 1) {
+        const uint64_t r = r0 + row_in_round<Wave>(lanes);
         PolicySums s{};
         Counts n{0, 0};
-        if (r < a.rows)
-            n = sum_tokens<Ref, Few>(a.in, r, a.cols, (uint64_t)lane * 4, a.cols, lanes * 4, s);
+        if (r < a.rows) n = sum_tokens<Ref, Few, !Wave>(a.in, r, 0, a.cols, lanes, lane, s);
         s.clipped = (double)n.clipped;
         s.tokens = (double)n.tokens;
-        const uint32_t tokens = lanes_sum((uint32_t)n.tokens, lanes);
+        uint32_t tokens = lanes_sum((uint32_t)n.tokens, lanes < 64 ? lanes : 64);
+        if (lanes > 64) {
+            if (threadIdx.x % 64 == 0) tokens_of[set][threadIdx.x / 64] = tokens;
+            __syncthreads();
+            tokens = 0;
+#pragma unroll
+            for (uint32_t w = 0; w < Block / 64; ++w) tokens += tokens_of[set][w];
+        }
         add_sequence(all, s, a.mean == EW_MEAN_SEQUENCES, tokens, lane == 0);
         if (r < a.rows && lane == 0) counts[r] = tokens;
     }
 }
 
 // Few tokens: one block.
-template <bool Ref, bool Few>
+template <bool Ref, bool Few, bool Wave>
 __global__ void __launch_bounds__(kSmallBlock) ew_policy_small_kernel(PolicyLossArgs a, uint32_t lanes)
 {
     __shared__ PolicySums scratch[kSmallBlock / 64];
     uint32_t *const counts = static_cast<uint32_t *>(a.workspace);
     PolicySums all{};
-    add_sequences<Ref, Few>(a, 0, kSmallBlock / lanes, lanes, counts, all);
+    add_sequences<Ref, Few, Wave, kSmallBlock>(a, 0, kSmallBlock / lanes, lanes, counts, all);
     all = block_sums<kSmallBlock / 64>(all, scratch);
     if (threadIdx.x == 0) write_loss(a, all);
     if (a.weights)
@@ -297,7 +378,7 @@ __global__ void __launch_bounds__(kSmallBlock) ew_policy_small_kernel(PolicyLoss
 }
 
 // Whole sequences: a record of sums a block, a count of tokens a sequence.
-template <bool Ref, bool Few>
+template <bool Ref, bool Few, bool Wave>
 __global__ void __launch_bounds__(kPolicyBlock) ew_policy_rows_kernel(PolicyLossArgs a, uint32_t lanes,
                                                                      PolicySums *records,
                                                                      uint32_t *counts)
@@ -305,7 +386,7 @@ __global__ void __launch_bounds__(kPolicyBlock) ew_policy_rows_kernel(PolicyLoss
     __shared__ PolicySums scratch[kPolicyBlock / 64];
     PolicySums all{};
     const uint64_t per = kPolicyBlock / lanes;
-    add_sequences<Ref, Few>(a, blockIdx.x * per, gridDim.x * per, lanes, counts, all);
+    add_sequences<Ref, Few, Wave, kPolicyBlock>(a, blockIdx.x * per, gridDim.x * per, lanes, counts, all);
     all = block_sums<kPolicyBlock / 64>(all, scratch);
     if (threadIdx.x == 0) records[blockIdx.x] = all;
 }
@@ -319,8 +400,8 @@ __global__ void __launch_bounds__(kPolicyBlock) ew_policy_parts_kernel(PolicyLos
     __shared__ PolicySums scratch[kPolicyBlock / 64];
     PolicySums s{};
     const uint64_t from = blockIdx.x * part_tokens, to = from + part_tokens;
-    const Counts n = sum_tokens<Ref, false>(a.in, blockIdx.y, a.cols, from + threadIdx.x * 4,
-                                            to < a.cols ? to : a.cols, kPolicyBlock * 4, s);
+    const Counts n = sum_tokens<Ref, false, false>(a.in, blockIdx.y, from, to < a.cols ? (uint32_t)to : a.cols,
+                                            kPolicyBlock, threadIdx.x, s);
     s.clipped = (double)n.clipped;
     s.tokens = (double)n.tokens;
     s = block_sums<kPolicyBlock / 64>(s, scratch);
@@ -370,32 +451,35 @@ __global__ void __launch_bounds__(kSmallBlock) ew_policy_join_kernel(PolicyLossA
 // Gradient: `lanes` lanes a sequence (or a part of one)
 // ---------------------------------------------------------------------------
 
-template <bool Ref, bool Few>
+template <bool Ref, bool Few, bool Wave>
 __global__ void __launch_bounds__(kPolicyBlock) ew_policy_grad_kernel(PolicyGradArgs a, uint32_t lanes,
                                                                      uint64_t part_tokens)
 {
     const uint32_t lane = threadIdx.x % lanes, per = kPolicyBlock / lanes;
     const float dloss = a.dloss ? a.dloss[0] : 1.0f;
     const uint64_t from = blockIdx.y * part_tokens, end = from + part_tokens;
-    const uint64_t to = end < a.cols ? end : a.cols;
+    const uint32_t to = end < a.cols ? (uint32_t)end : a.cols;
     for (uint64_t r0 = (uint64_t)blockIdx.x * per; r0 < a.rows; r0 += (uint64_t)gridDim.x * per) {
-        const uint64_t r = r0 + threadIdx.x / lanes;
+        const uint64_t r = r0 + row_in_round<Wave>(lanes);
         if (r >= a.rows) break;
         const PolicyRow row(a.in, r);
         float *const out = a.dlogp + r * a.dlogp_stride;
         const float w = a.weights[r] * dloss;
-        for (uint64_t at = from + (uint64_t)lane * 4; at < to; at += (uint64_t)lanes * 4) {
-            const auto f = Four<Few>::template load<Ref>(a.in, row, a.cols, (uint32_t)at);
-            f32x4 g;
+        each_four<Ref, Few, !Wave>(
+            a.in, row, from, to, lanes, lane, [&](const Four &f, const auto &t) {
+                f32x4 g{0.0f, 0.0f, 0.0f, 0.0f};
+                if (f.counted) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const Token t = token<Ref>(a.in, f.logp[j], f.old[j], f.ref[j], f.a[j]);
-                float slope = t.clipped ? 0.0f : -f.a[j] * t.ratio;
-                if constexpr (Ref) slope -= a.in.kl * t.one;
-                g[j] = f.counts(j) ? w * slope : 0.0f;
-            }
-            f.piece.store(out, __builtin_bit_cast(u32x4, g));
-        }
+                    for (int j = 0; j < 4; ++j) {
+                        const Token k = f.token<Ref>(a.in, j);
+                        float slope = k.clipped ? 0.0f : -f.a[j] * k.ratio;
+                        if constexpr (Ref) slope -= a.in.kl * k.one;
+                        g[j] = f.counts(j) ? w * slope : 0.0f;
+                    }
+                }
+                // (dlogp may be an input, whose other elements another lane takes)
+                store_own(t.row(out), t.cols, t.place(lane), __builtin_bit_cast(u32x4, g));
+            });
     }
 }
 
@@ -405,10 +489,13 @@ __global__ void __launch_bounds__(kPolicyBlock) ew_policy_grad_kernel(PolicyGrad
 
 // One block sums up to this many tokens.
 constexpr uint64_t kSmallTokens = 16384;
+// A sequence of more than this many tokens is a block's, else a wave's or less.
+constexpr uint32_t kBlockTokens = 1024;
 // Records of sums: at most this many blocks.
 constexpr uint64_t kRecords = 1024;
 
-// Lanes that share a sequence: each takes four tokens at a time.
+// Lanes that share a sequence: each takes four tokens at a time.  (Fewer than
+// a wave hold all of it.)
 static uint32_t lanes_for(uint64_t cols, uint32_t most)
 {
     uint32_t lanes = 1;
@@ -430,12 +517,14 @@ size_t policy_loss_workspace(uint64_t rows, uint64_t cols)
     return kRecords * sizeof(PolicySums) + (rows * sizeof(uint32_t) + 15) / 16 * 16;
 }
 
-// A kernel with or without the reference, of short rows or others.
-#define EW_POLICY_KERNEL(K, ref, cols)                                                     \
-    ((ref) ? ((cols) < 4 ? reinterpret_cast<const void *>(&K<true, true>)                  \
-                         : reinterpret_cast<const void *>(&K<true, false>))                \
-           : ((cols) < 4 ? reinterpret_cast<const void *>(&K<false, true>)                 \
-                         : reinterpret_cast<const void *>(&K<false, false>)))
+// A kernel with or without the reference, of sequences below four tokens, below
+// a wave's or others.
+#define EW_POLICY_OF(K, REF, cols, lanes)                                            \
+    ((cols) < 4     ? reinterpret_cast<const void *>(&K<REF, true, false>)           \
+     : (lanes) < 64 ? reinterpret_cast<const void *>(&K<REF, false, false>)          \
+                    : reinterpret_cast<const void *>(&K<REF, false, true>))
+#define EW_POLICY_KERNEL(K, ref, cols, lanes) \
+    ((ref) ? EW_POLICY_OF(K, true, cols, lanes) : EW_POLICY_OF(K, false, cols, lanes))
 
 hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, const char **path)
 {
@@ -443,7 +532,7 @@ hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, c
     if ((uint64_t)a.rows * (a.cols ? a.cols : 1) <= kSmallTokens) {
         *path = "one block";
         const uint32_t lanes = lanes_for(a.cols, 64);
-        return start(EW_POLICY_KERNEL(ew_policy_small_kernel, ref, a.cols), dim3(1), kSmallBlock, 0, s, a, lanes);
+        return start(EW_POLICY_KERNEL(ew_policy_small_kernel, ref, a.cols, lanes), dim3(1), kSmallBlock, 0, s, a, lanes);
     }
     PolicySums *const records = static_cast<PolicySums *>(a.workspace);
     uint32_t *const counts = reinterpret_cast<uint32_t *>(records + kRecords);
@@ -464,10 +553,10 @@ hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, c
                      a, (const PolicySums *)records, n, used, (const uint32_t *)counts);
     }
     *path = "whole sequences";
-    const uint32_t lanes = lanes_for(a.cols, 64);
+    const uint32_t lanes = a.cols > kBlockTokens ? kPolicyBlock : lanes_for(a.cols, 64);
     const uint64_t blocks = ((uint64_t)a.rows * lanes + kPolicyBlock - 1) / kPolicyBlock;
     n = (uint32_t)(blocks < kRecords ? blocks : kRecords);
-    e = start(EW_POLICY_KERNEL(ew_policy_rows_kernel, ref, a.cols), dim3(n), kPolicyBlock, 0, s, a, lanes, records, counts);
+    e = start(EW_POLICY_KERNEL(ew_policy_rows_kernel, ref, a.cols, lanes), dim3(n), kPolicyBlock, 0, s, a, lanes, records, counts);
     if (e != hipSuccess) return e;
     const uint64_t joins = a.weights ? ((uint64_t)a.rows + kSmallBlock - 1) / kSmallBlock : 1;
     return start(reinterpret_cast<const void *>(&ew_policy_join_kernel),
@@ -486,7 +575,7 @@ hipError_t launch_policy_grad(RowType, const PolicyGradArgs &a, hipStream_t s, c
     const uint32_t used = (uint32_t)((a.cols + tokens - 1) / tokens);
     *path = used > 1 ? "parts of sequences" : "whole sequences";
     // a KL term that does not count is not read
-    return start(EW_POLICY_KERNEL(ew_policy_grad_kernel, a.in.ref && a.in.kl != 0.0f, a.cols),
+    return start(EW_POLICY_KERNEL(ew_policy_grad_kernel, a.in.ref && a.in.kl != 0.0f, a.cols, lanes),
                  dim3(row_blocks(blocks), used), kPolicyBlock, 0, s, a, lanes, tokens);
 }
 
