@@ -18,9 +18,8 @@ __device__ __forceinline__ uint64_t lanes_of(uint32_t key, bool live, uint32_t b
 {
     uint64_t same = __ballot(live);
     for (uint32_t b = 0; b < bits; ++b) {
-        const bool one = key >> b & 1u;
-        const uint64_t ones = __ballot(one);
-        same &= one ? ones : ~ones;
+        const uint64_t ones = __ballot((key & 1u << b) != 0);
+        same &= key & 1u << b ? ones : ~ones;
     }
     return same;
 }
@@ -33,9 +32,9 @@ __device__ __forceinline__ uint32_t expert_of(const ExpertsSortArgs &a, uint64_t
     return id >= 0 && id < (int64_t)a.cols ? (uint32_t)id : a.cols;
 }
 
-// A wave's entries, 64 at a time: it holds this many rounds of them in
-// registers from the counting to the placing (their loads are on their way
-// together), and reads longer ones twice.
+// A wave holds this many rounds of 64 entries in registers from the counting
+// to the placing (their loads are on their way together), and reads longer
+// ones twice.
 constexpr uint32_t kHeld = 8;
 
 // How a sorting is split: `chunk` entries a block, `per` (a multiple of 64) a
@@ -59,57 +58,87 @@ struct WaveEntries {
     }
 };
 
-// Calls f(expert, entry) for a wave's entries, round by round.
-template <bool Held, class F>
-__device__ __forceinline__ void each_entry(const ExpertsSortArgs &a, const WaveEntries &own,
-                                           const uint32_t (&held)[kHeld], F f)
+// A lane's entry: its expert, and its place among the wave's entries of that
+// expert.
+struct Entry {
+    uint32_t expert, place;
+};
+
+// Counts a round's entries, one a lane, in the wave's counters.
+__device__ __forceinline__ Entry count_entry(uint32_t expert, uint32_t experts, uint32_t bits,
+                                             uint32_t *counter)
 {
-    const uint32_t lane = threadIdx.x % 64;
-    if constexpr (Held) {
-#pragma unroll
-        for (uint32_t k = 0; k < kHeld; ++k)
-            if (own.from + 64 * k < own.end) f(held[k], own.from + 64 * k + lane);
-    } else {
-        for (uint64_t i = own.from; i < own.end; i += 64) f(expert_of(a, i + lane, own.end), i + lane);
-    }
+    const bool live = expert < experts;
+    const uint64_t same = lanes_of(expert, live, bits);
+    const uint32_t lane = threadIdx.x % 64, first = live ? counter[expert] : 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (live && (uint32_t)__builtin_ctzll(same) == lane)
+        counter[expert] = first + (uint32_t)__builtin_popcountll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    return Entry{expert, first + (uint32_t)__builtin_popcountll(same & (((uint64_t)1 << lane) - 1))};
 }
 
-// The waves' counters of a block's entries by expert (and `held`).
+// The waves' counters of a block's entries by expert, and the entries (Held).
 template <bool Held>
 __device__ __forceinline__ void count_entries(const ExpertsSortArgs &a, const SortSplit &split,
-                                              const WaveEntries &own, uint32_t (&held)[kHeld],
+                                              const WaveEntries &own, Entry (&held)[kHeld],
                                               uint32_t *counters)
 {
     const uint32_t experts = a.cols, lane = threadIdx.x % 64;
     uint32_t *const mine = counters + threadIdx.x / 64 * experts;
     if constexpr (Held)
 #pragma unroll
-        for (uint32_t k = 0; k < kHeld; ++k) held[k] = expert_of(a, own.from + 64 * k + lane, own.end);
+        for (uint32_t k = 0; k < kHeld; ++k)
+            held[k].expert = expert_of(a, own.from + 64 * k + lane, own.end);
     for (uint32_t i = threadIdx.x; i < split.waves * experts; i += blockDim.x) counters[i] = 0;
     __syncthreads();
-    each_entry<Held>(a, own, held, [&](uint32_t e, uint64_t) {
-        const uint64_t same = lanes_of(e, e < experts, split.bits);
-        if (e < experts && (uint32_t)__builtin_ctzll(same) == lane)
-            mine[e] += (uint32_t)__builtin_popcountll(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    });
+    if constexpr (Held) {
+#pragma unroll
+        for (uint32_t k = 0; k < kHeld; ++k)
+            if (own.from + 64 * k < own.end) held[k] = count_entry(held[k].expert, experts, split.bits, mine);
+    } else {
+        for (uint64_t i = own.from; i < own.end; i += 64)
+            count_entry(expert_of(a, i + lane, own.end), experts, split.bits, mine);
+    }
     __syncthreads();
 }
 
-// Inclusive sum over a block's threads; scratch: a value a wave.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *scratch)
+// The value n lanes before this one in its 16, 0 before the first.
+template <int N>
+__device__ __forceinline__ uint32_t lanes_before(uint32_t x)
 {
-    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-#pragma unroll
-    for (uint32_t d = 1; d < 64; d *= 2) {
-        const uint32_t up = (uint32_t)__shfl_up((int)x, d);
-        if (lane >= d) x += up;
-    }
-    __syncthreads();
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x110 + N, 0xf, 0xf, true);
+}
+
+__device__ __forceinline__ uint32_t lane_value_u32(uint32_t x, int lane)
+{
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
+}
+
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x)
+{
+    x += lanes_before<1>(x);
+    x += lanes_before<2>(x);
+    x += lanes_before<4>(x);
+    x += lanes_before<8>(x);
+    const uint32_t a = lane_value_u32(x, 15), b = a + lane_value_u32(x, 31), c = b + lane_value_u32(x, 47);
+    const uint32_t row = threadIdx.x % 64 / 16;
+    return x + (row == 0 ? 0 : row == 1 ? a : row == 2 ? b : c);
+}
+
+// Inclusive sum over a block's threads (at most 16 waves), and the block's sum;
+// scratch: a value a wave.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *scratch, uint32_t &all)
+{
+    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, waves = blockDim.x / 64;
+    x = wave_scan(x);
     if (lane == 63) scratch[wave] = x;
     __syncthreads();
-    for (uint32_t w = 0; w < wave; ++w) x += scratch[w];
-    return x;
+    const uint32_t before = wave_scan(lane < waves ? scratch[lane] : 0);
+    all = lane_value_u32(before, 63);
+    const uint32_t mine = (uint32_t)__builtin_amdgcn_readfirstlane((int)wave);
+    return x + (mine ? lane_value_u32(before, (int)mine - 1) : 0);
 }
 
 // The first row of each expert and the places of a block's entries.  One: all
@@ -125,35 +154,41 @@ __global__ void __launch_bounds__(1024) ew_experts_sort_kernel(ExpertsSortArgs a
     const uint32_t experts = a.cols, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     const WaveEntries own(a, split);
     uint32_t *const mine = counters + wave * experts;
-    uint32_t held[kHeld];
+    // (a tile of the blocks' counts is on its way while the entries are counted)
+    const uint32_t tile = experts < blockDim.x ? 1u << split.bits : blockDim.x;
+    const auto add_totals = [&](uint32_t e0, uint32_t &before, uint32_t &all) {
+        // threads of the same expert share the blocks
+        const uint32_t e = e0 + threadIdx.x % tile, part = threadIdx.x / tile;
+        const uint32_t parts = blockDim.x / tile;
+        before = all = 0;
+        if (e < experts) {
+#pragma unroll 8
+            for (uint32_t b = part; b < gridDim.x; b += parts) {
+                const uint32_t n = totals[b * experts + e];
+                all += n;
+                before += b < blockIdx.x ? n : 0;
+            }
+        }
+    };
+    uint32_t mine_before = 0, mine_all = 0;
+    if constexpr (!One) add_totals(0, mine_before, mine_all);
+    Entry held[kHeld];
     count_entries<Held>(a, split, own, held, counters);
     // the experts' rows, a tile of them at a time
-    const uint32_t tile = experts < blockDim.x ? 1u << split.bits : blockDim.x;
     uint32_t start = 0;
     for (uint32_t e0 = 0; e0 < experts; e0 += tile) {
         uint32_t before = 0, all = 0;
         if constexpr (!One) {
-            // threads of the same expert share the blocks
             uint32_t *const sums = counters + split.waves * experts;
-            const uint32_t e = e0 + threadIdx.x % tile, part = threadIdx.x / tile;
-            const uint32_t parts = blockDim.x / tile;
-            if (e < experts) {
-#pragma unroll 8
-                for (uint32_t b = part; b < gridDim.x; b += parts) {
-                    const uint32_t n = totals[b * experts + e];
-                    all += n;
-                    before += b < blockIdx.x ? n : 0;
-                }
-            }
+            if (e0) add_totals(e0, mine_before, mine_all);
+            sums[threadIdx.x] = mine_before;
+            sums[blockDim.x + threadIdx.x] = mine_all;
             __syncthreads();
-            sums[threadIdx.x] = before;
-            sums[blockDim.x + threadIdx.x] = all;
-            __syncthreads();
-            before = all = 0;
             if (threadIdx.x < tile)
-                for (uint32_t q = 0; q < parts; ++q) {
-                    before += sums[q * tile + threadIdx.x];
-                    all += sums[blockDim.x + q * tile + threadIdx.x];
+#pragma unroll 8
+                for (uint32_t q = threadIdx.x; q < blockDim.x; q += tile) {
+                    before += sums[q];
+                    all += sums[blockDim.x + q];
                 }
         }
         const uint32_t e = e0 + threadIdx.x;
@@ -166,7 +201,9 @@ __global__ void __launch_bounds__(1024) ew_experts_sort_kernel(ExpertsSortArgs a
 #pragma unroll
             for (uint32_t w = 0; w < 16; ++w) all += counted[w];
         const uint32_t room = live ? (all + a.align - 1) / a.align * a.align : 0;
-        const uint32_t after = start + block_scan(room, scratch);
+        uint32_t tile_room;
+        const uint32_t after = start + block_scan(room, scratch, tile_room);
+        start += tile_room;
         if (live) {
             const uint32_t first = after - room;
             uint32_t next = first + before;
@@ -184,27 +221,31 @@ __global__ void __launch_bounds__(1024) ew_experts_sort_kernel(ExpertsSortArgs a
             if (a.source && e % gridDim.x == blockIdx.x)
                 for (uint32_t r = first + all; r < after; ++r) a.source[r] = -1;
         }
-        for (uint32_t w = 0; w < blockDim.x / 64; ++w) start += scratch[w];
         __syncthreads();
+    }
+    const auto put = [&](uint64_t i, const Entry &entry, uint32_t row) {
+        if (i >= own.end) return;
+        const bool live = entry.expert < experts;
+        a.slot[i] = live ? (int32_t)row : -1;
+        if (live && a.source) a.source[row] = (int32_t)i;
+    };
+    if constexpr (Held) {
+#pragma unroll
+        for (uint32_t k = 0; k < kHeld; ++k)
+            if (own.from + 64 * k < own.end)
+                put(own.from + 64 * k + lane, held[k],
+                    held[k].place + (held[k].expert < experts ? mine[held[k].expert] : 0));
+    } else {
+        // (the counters start at the experts' rows now)
+        for (uint64_t i = own.from; i < own.end; i += 64) {
+            const Entry entry = count_entry(expert_of(a, i + lane, own.end), experts, split.bits, mine);
+            put(i + lane, entry, entry.place);
+        }
     }
     if (a.source)
         for (uint64_t r = start + (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.source_rows;
              r += (uint64_t)gridDim.x * blockDim.x)
             a.source[r] = -1;
-    each_entry<Held>(a, own, held, [&](uint32_t e, uint64_t i) {
-        const bool live = e < experts;
-        const uint64_t same = lanes_of(e, live, split.bits);
-        const uint32_t first = live ? mine[e] : 0;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (live && (uint32_t)__builtin_ctzll(same) == lane)
-            mine[e] = first + (uint32_t)__builtin_popcountll(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const uint32_t row = first + (uint32_t)__builtin_popcountll(same & (((uint64_t)1 << lane) - 1));
-        if (i < own.end) {
-            a.slot[i] = live ? (int32_t)row : -1;
-            if (live && a.source) a.source[row] = (int32_t)i;
-        }
-    });
 }
 
 // Counts of each block's entries by expert.
@@ -214,10 +255,11 @@ __global__ void __launch_bounds__(1024) ew_experts_count_kernel(ExpertsSortArgs 
 {
     extern __shared__ uint32_t counters[];
     const uint32_t experts = a.cols;
-    uint32_t held[kHeld];
+    Entry held[kHeld];
     count_entries<Held>(a, split, WaveEntries(a, split), held, counters);
     for (uint32_t e = threadIdx.x; e < experts; e += blockDim.x) {
         uint32_t n = 0;
+#pragma unroll 16
         for (uint32_t w = 0; w < split.waves; ++w) n += counters[w * experts + e];
         totals[blockIdx.x * experts + e] = n;
     }
@@ -301,14 +343,17 @@ struct Stretch {
     }
 };
 
-// Zeros in the padding rows of expert e, by a block.
+// Zeros in the padding rows of an expert, by one of kPadBlocks blocks of it.
+constexpr uint32_t kPadBlocks = 8;
+
 template <typename T, RowFit Fit>
-__device__ __forceinline__ void clear_padding(const ExpertsMoveArgs &a, uint32_t e)
+__device__ __forceinline__ void clear_padding(const ExpertsMoveArgs &a, uint32_t block)
 {
+    const uint32_t e = block / kPadBlocks;
     using Cols = Stretch<T, kMoveBlock, 1, Fit>;
     const int64_t first = (int64_t)a.offsets[e] + a.counts[e], after = a.offsets[e + 1];
     const int64_t from = first < 0 ? 0 : first, to = after < a.places ? after : a.places;
-    for (int64_t r = from; r < to; ++r) {
+    for (int64_t r = from + block % kPadBlocks; r < to; r += kPadBlocks) {
         for (uint64_t first = 0; first < a.cols; first += Cols::kCols) {
             const Cols part(first, a.cols, threadIdx.x);
             store_piece(part.row(a.out, (uint64_t)r, a.out_stride), part.cols, part.piece(0),
@@ -557,6 +602,7 @@ hipError_t launch_experts_sort(RowType, const ExpertsSortArgs &a, hipStream_t s,
 
 struct MoveSplit {
     bool each, tiny;      // a block a token; rows shorter than a vector
+    bool narrow;          // a vector a lane at most
     uint32_t blocks;      // of tokens
 };
 
@@ -567,6 +613,7 @@ static MoveSplit move_split(RowType t, const ExpertsMoveArgs &a, const char **pa
     const uint32_t vectors = vectors_of(t, a.cols);
     MoveSplit m;
     m.each = vectors > (a.rows < 1024 ? 64u : 256u);
+    m.narrow = !m.each && vectors <= 64;
     m.tiny = a.cols < 16 / (uint32_t)row_elem_size(t);
     m.blocks = row_blocks(m.each ? a.rows : ((uint64_t)a.rows + kMoveWaves - 1) / kMoveWaves);
     *path = m.each ? "a block a token" : m.tiny ? "short rows" : "a wave a token";
@@ -576,14 +623,15 @@ static MoveSplit move_split(RowType t, const ExpertsMoveArgs &a, const char **pa
 hipError_t launch_experts_gather(RowType t, const ExpertsMoveArgs &a, hipStream_t s, const char **path)
 {
     const MoveSplit m = move_split(t, a, path);
-    return start(EW_MOVE_KERNEL(t, m, ew_experts_gather_kernel), dim3(m.blocks + a.experts), kMoveBlock,
+    return start(EW_MOVE_KERNEL(t, m, ew_experts_gather_kernel), dim3(m.blocks + a.experts * kPadBlocks), kMoveBlock,
                  0, s, a, m.blocks);
 }
 
 hipError_t launch_experts_combine(RowType t, const ExpertsMoveArgs &a, hipStream_t s, const char **path)
 {
     const MoveSplit m = move_split(t, a, path);
-    return start(a.top <= 2 ? EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 2, 4)
+    return start(a.top <= 2  ? EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 2, 4)
+                 : m.narrow ? EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 8, 1)
                             : EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 4, 2),
                  dim3(m.blocks), kMoveBlock, 0, s, a, m.blocks);
 }
@@ -592,9 +640,10 @@ hipError_t launch_experts_combine_grad(RowType t, const ExpertsMoveArgs &a, hipS
                                        const char **path)
 {
     const MoveSplit m = move_split(t, a, path);
-    return start(a.top <= 2 ? EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 2, 4)
+    return start(a.top <= 2  ? EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 2, 4)
+                 : m.narrow ? EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 8, 1)
                             : EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 4, 2),
-                 dim3(m.blocks + a.experts), kMoveBlock, 0, s, a, m.blocks);
+                 dim3(m.blocks + a.experts * kPadBlocks), kMoveBlock, 0, s, a, m.blocks);
 }
 
 }  // namespace ew

@@ -661,15 +661,17 @@ static hipError_t layernorm_rows(const LayerNormArgs &a, uint32_t vectors, hipSt
     EW_LAYERNORM_ROWS(2, 1)
     EW_LAYERNORM_ROWS(3, 1)
     EW_LAYERNORM_ROWS(4, 1)
-    if (a.rows <= kRowACu) {
+    if (a.rows <= kOneRound) {
         EW_LAYERNORM_ROWS(5, 1)
+    }
+    if (a.rows <= kRowACu) {
         EW_LAYERNORM_ROWS(8, 1)
         EW_LAYERNORM_ROWS(16, 1)
     }
+    EW_LAYERNORM_ROWS(3, 2)
     if (a.rows <= kOneRound) {
         EW_LAYERNORM_ROWS(2, 4)
     }
-    EW_LAYERNORM_ROWS(3, 2)
     EW_LAYERNORM_ROWS(4, 2)
     EW_LAYERNORM_ROWS(3, 4)
     EW_LAYERNORM_ROWS(4, 4)

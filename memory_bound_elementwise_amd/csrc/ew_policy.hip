@@ -332,9 +332,9 @@ __device__ __forceinline__ uint32_t row_in_round(uint32_t lanes)
     return Wave ? (uint32_t)__builtin_amdgcn_readfirstlane((int)row) : row;
 }
 
-// Sequences from r0 on, `step` of them apart and `lanes` lanes each (up to a
-// wave, or Block: the block's), added to all; their tokens to counts.  Whole
-// waves and blocks go round together.
+// Sequences from r0 on, `step` of them apart and `lanes` lanes each (a power of
+// two up to Block), added to all; their tokens to counts.  Whole waves and
+// blocks go round together.
 template <bool Ref, bool Few, bool Wave, uint32_t Block>
 __device__ __forceinline__ void add_sequences(const PolicyLossArgs &a, uint64_t r0, uint64_t step,
                                               uint32_t lanes, uint32_t *counts, PolicySums &all)
@@ -354,8 +354,8 @@ __device__ __forceinline__ void add_sequences(const PolicyLossArgs &a, uint64_t 
             if (threadIdx.x % 64 == 0) tokens_of[set][threadIdx.x / 64] = tokens;
             __syncthreads();
             tokens = 0;
-#pragma unroll
-            for (uint32_t w = 0; w < Block / 64; ++w) tokens += tokens_of[set][w];
+            const uint32_t waves = lanes / 64, mine = threadIdx.x / lanes * waves;
+            for (uint32_t w = 0; w < waves; ++w) tokens += tokens_of[set][mine + w];
         }
         add_sequence(all, s, a.mean == EW_MEAN_SEQUENCES, tokens, lane == 0);
         if (r < a.rows && lane == 0) counts[r] = tokens;
@@ -531,8 +531,17 @@ hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, c
     const bool ref = a.in.ref;
     if ((uint64_t)a.rows * (a.cols ? a.cols : 1) <= kSmallTokens) {
         *path = "one block";
-        const uint32_t lanes = lanes_for(a.cols, 64);
-        return start(EW_POLICY_KERNEL(ew_policy_small_kernel, ref, a.cols, lanes), dim3(1), kSmallBlock, 0, s, a, lanes);
+        // more than a wave a sequence where that takes fewer rounds
+        uint32_t lanes = lanes_for(a.cols, 64);
+        const auto rounds = [&](uint64_t l) {
+            const uint64_t at_once = kSmallBlock / l;
+            return (a.rows + at_once - 1) / at_once * ((a.cols + 8 * l - 1) / (8 * l));
+        };
+        if (lanes == 64)
+            for (uint32_t more = 128; more <= kSmallBlock; more *= 2)
+                if (rounds(more) < rounds(lanes)) lanes = more;
+        return start(EW_POLICY_KERNEL(ew_policy_small_kernel, ref, a.cols, lanes), dim3(1), kSmallBlock, 0,
+                     s, a, lanes);
     }
     PolicySums *const records = static_cast<PolicySums *>(a.workspace);
     uint32_t *const counts = reinterpret_cast<uint32_t *>(records + kRecords);
@@ -556,7 +565,8 @@ hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, c
     const uint32_t lanes = a.cols > kBlockTokens ? kPolicyBlock : lanes_for(a.cols, 64);
     const uint64_t blocks = ((uint64_t)a.rows * lanes + kPolicyBlock - 1) / kPolicyBlock;
     n = (uint32_t)(blocks < kRecords ? blocks : kRecords);
-    e = start(EW_POLICY_KERNEL(ew_policy_rows_kernel, ref, a.cols, lanes), dim3(n), kPolicyBlock, 0, s, a, lanes, records, counts);
+    e = start(EW_POLICY_KERNEL(ew_policy_rows_kernel, ref, a.cols, lanes), dim3(n), kPolicyBlock, 0, s, a,
+              lanes, records, counts);
     if (e != hipSuccess) return e;
     const uint64_t joins = a.weights ? ((uint64_t)a.rows + kSmallBlock - 1) / kSmallBlock : 1;
     return start(reinterpret_cast<const void *>(&ew_policy_join_kernel),
