@@ -505,7 +505,8 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_grad_kernel(Exp
                         const Wide z = Vec<T>::widen(own_bits(v[c][u], part.cols, part.piece(u)));
 #pragma unroll
                         for (uint32_t k = 0; k < Cols::N; ++k) dots[c] = __builtin_fmaf(g[u][k], z[k], dots[c]);
-                        store_piece(dz, part.cols, part.piece(u), Vec<T>::narrow(w * g[u]));
+                        // (dz may be z, whose other elements another wave may yet read)
+                        store_own(dz, part.cols, part.piece(u), Vec<T>::narrow(w * g[u]));
                     }
                 }
             }

@@ -472,6 +472,8 @@ __device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
         second = second * rs * (rs * by);
         if (!live) continue;
         T *const dx = static_cast<T *>(a.dx) + r * a.dx_stride;
+        u32x4 part{};              // what is the partial vector's own, stored last
+        uint32_t part_skip = 0;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const Wide off = Vec<T>::widen(xv[k]) - mu;
@@ -485,7 +487,20 @@ __device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
 #pragma unroll
             for (uint32_t j = 0; j < N; ++j)
                 g[j] = __builtin_fmaf(rs, __builtin_fmaf(-off[j], second, g[j]), dt[j]);
-            store_piece(dx, cols, piece(k), Vec<T>::narrow(g));
+            // (dx may be dtotal, whose other elements another wave may yet read)
+            const Piece<T, Fit> p = piece(k);
+            if (kAhead || Fit != kPart || p.skip == 0) {
+                store_piece(dx, cols, p, Vec<T>::narrow(g));
+            } else if (p.live) {
+                part = Vec<T>::narrow(g);
+                part_skip = p.skip;
+            }
+        }
+        if (part_skip) {
+            const typename Vec<T>::type v = __builtin_bit_cast(typename Vec<T>::type, part);
+#pragma unroll
+            for (uint32_t j = 1; j < N; ++j)
+                if (j >= part_skip) dx[cols - N + j] = v[j];
         }
     }
     if (!a.dweight && !a.dbias) return;
