@@ -505,10 +505,25 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_grad_kernel(Exp
                         const Wide z = Vec<T>::widen(own_bits(v[c][u], part.cols, part.piece(u)));
 #pragma unroll
                         for (uint32_t k = 0; k < Cols::N; ++k) dots[c] = __builtin_fmaf(g[u][k], z[k], dots[c]);
-                        // (dz may be z, whose other elements another wave may yet read)
-                        store_own(dz, part.cols, part.piece(u), Vec<T>::narrow(w * g[u]));
+                        // (a partial vector: below)
+                        if (Fit != kPart || part.piece(u).skip == 0)
+                            store_piece(dz, part.cols, part.piece(u), Vec<T>::narrow(w * g[u]));
                     }
                 }
+                // what is a partial vector's own, one by one: dz may be z, whose
+                // other elements another wave may yet read
+                if (Fit == kPart && part.cols % Cols::N != 0)
+#pragma unroll 1
+                    for (uint32_t c = 0; c < C; ++c) {
+                        const int32_t s = slots.of(j0 + c);
+                        if (s < 0) continue;
+                        const float w = weights.of(j0 + c);
+                        T *const dz = part.row(a.out, (uint32_t)s, a.out_stride);
+#pragma unroll
+                        for (uint32_t u = 0; u < U; ++u)
+                            if (part.piece(u).skip != 0)
+                                store_own(dz, part.cols, part.piece(u), Vec<T>::narrow(w * g[u]));
+                    }
             }
             float mine = 0.0f;             // choice j0 + c in lane c
 #pragma unroll
