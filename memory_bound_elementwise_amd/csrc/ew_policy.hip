@@ -451,11 +451,14 @@ __global__ void __launch_bounds__(kSmallBlock) ew_policy_join_kernel(PolicyLossA
 // Gradient: `lanes` lanes a sequence (or a part of one)
 // ---------------------------------------------------------------------------
 
+// Threads of a block: of sequences of more tokens than kWideTokens, of others.
+constexpr uint32_t kWideBlock = 512, kWideTokens = 2560;
+
 template <bool Ref, bool Few, bool Wave>
-__global__ void __launch_bounds__(kPolicyBlock) ew_policy_grad_kernel(PolicyGradArgs a, uint32_t lanes,
+__global__ void __launch_bounds__(kWideBlock) ew_policy_grad_kernel(PolicyGradArgs a, uint32_t lanes,
                                                                      uint64_t part_tokens)
 {
-    const uint32_t lane = threadIdx.x % lanes, per = kPolicyBlock / lanes;
+    const uint32_t lane = threadIdx.x % lanes, per = blockDim.x / lanes;
     const float dloss = a.dloss ? a.dloss[0] : 1.0f;
     const uint64_t from = blockIdx.y * part_tokens, end = from + part_tokens;
     const uint32_t to = end < a.cols ? (uint32_t)end : a.cols;
@@ -576,17 +579,18 @@ hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, c
 
 hipError_t launch_policy_grad(RowType, const PolicyGradArgs &a, hipStream_t s, const char **path)
 {
-    const uint32_t lanes = lanes_for(a.cols, kPolicyBlock);
-    const uint64_t blocks = ((uint64_t)a.rows * lanes + kPolicyBlock - 1) / kPolicyBlock;
+    const uint64_t cut = a.cols > kPolicyBlock * 2 ? parts_of(a.rows, a.cols) : 1;
+    const uint32_t block = cut == 1 && a.cols > kWideTokens ? kWideBlock : kPolicyBlock;
+    const uint32_t lanes = lanes_for(a.cols, block);
+    const uint64_t blocks = ((uint64_t)a.rows * lanes + block - 1) / block;
     constexpr uint64_t kStep = kPolicyBlock * 4;
-    const uint64_t parts = lanes == kPolicyBlock ? parts_of(a.rows, a.cols) : 1;
-    const uint64_t tokens = parts > 1 ? ((a.cols + parts - 1) / parts + kStep - 1) / kStep * kStep
-                                      : (uint64_t)a.cols;
+    const uint64_t tokens = cut > 1 ? ((a.cols + cut - 1) / cut + kStep - 1) / kStep * kStep
+                                    : (uint64_t)a.cols;
     const uint32_t used = (uint32_t)((a.cols + tokens - 1) / tokens);
     *path = used > 1 ? "parts of sequences" : "whole sequences";
     // a KL term that does not count is not read
     return start(EW_POLICY_KERNEL(ew_policy_grad_kernel, a.in.ref && a.in.kl != 0.0f, a.cols, lanes),
-                 dim3(row_blocks(blocks), used), kPolicyBlock, 0, s, a, lanes, tokens);
+                 dim3(row_blocks(blocks), used), block, 0, s, a, lanes, tokens);
 }
 
 }  // namespace ew
