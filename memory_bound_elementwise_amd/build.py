@@ -15,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -31,6 +32,8 @@ ROW_KERNEL_SOURCES = [os.path.join(CSRC, f) for f in
                        "ew_experts.hip")]
 SOURCES = [os.path.join(CSRC, "ew_api.cpp"), os.path.join(CSRC, "ew_rows_api.cpp"),
            os.path.join(CSRC, "ew_train_api.cpp"), *KERNEL_SOURCES, *ROW_KERNEL_SOURCES]
+
+JOBS = 8         # sources compiled at once: 22 s on 8 CPUs, 105 s one by one
 
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 COMMON_FLAGS = [
@@ -62,7 +65,8 @@ def _run(cmd, verbose):
 def build(verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
     """Compile every HIP source of the library for gfx950; returns the .so path."""
     tmp = out + ".tmp"
-    cmd = [hipcc(), *COMMON_FLAGS, *extra_flags, "-shared", "-o", tmp, *SOURCES]
+    cmd = [hipcc(), *COMMON_FLAGS, *extra_flags, f"-parallel-jobs={JOBS}", "-shared", "-o", tmp,
+           *SOURCES]
     _run(cmd, verbose)
     os.replace(tmp, out)
     return out
@@ -74,14 +78,17 @@ def device_asm(dest_dir: str, verbose: bool = False, extra_flags=(),
     unless others are given) to ``dest_dir``, one file per source plus their
     concatenation; returns the concatenation's path."""
     os.makedirs(dest_dir, exist_ok=True)
-    parts = []
-    for src in sources:
+
+    def compile_one(src):
         stem = os.path.splitext(os.path.basename(src))[0]
         path = os.path.join(dest_dir, f"{stem}-{ARCH}.s")
-        cmd = [hipcc(), *COMMON_FLAGS, *extra_flags, "--cuda-device-only", "-S", "-o", path, src]
-        _run(cmd, verbose)
+        _run([hipcc(), *COMMON_FLAGS, *extra_flags, "--cuda-device-only", "-S", "-o", path, src],
+             verbose)
         with open(path) as f:
-            parts.append(f.read())
+            return f.read()
+
+    with ThreadPoolExecutor(JOBS) as pool:
+        parts = list(pool.map(compile_one, sources))
     path = os.path.join(dest_dir, f"ew_kernels-{ARCH}.s")
     with open(path, "w") as f:
         f.write("\n".join(parts))

@@ -245,7 +245,7 @@ __device__ __forceinline__ void layernorm_row(const LayerNormArgs &a, WaveSums (
 }
 
 template <typename T, int Waves, int V, bool Tiny = false>
-__global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_row_kernel(LayerNormArgs a)
+__global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_kernel(LayerNormArgs a)
 {
     // two sets, used in turn: a wave is at most one barrier ahead of another
     __shared__ WaveSums shared[2][layernorm_block(Waves) / 64];
@@ -539,7 +539,7 @@ __device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
 }
 
 template <typename T, int Waves, int V, int Groups, bool Tiny = false>
-__global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_grad_kernel(LayerNormGradArgs a)
+__global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_back_kernel(LayerNormGradArgs a)
 {
     __shared__ GradShared<T, Waves, V, Groups> shared;
     if constexpr (Tiny) layernorm_grad_rows<T, Waves, V, Groups, kTiny>(a, shared);
@@ -667,7 +667,7 @@ static hipError_t layernorm_rows(const LayerNormArgs &a, uint32_t vectors, hipSt
 #define EW_LAYERNORM_ROWS(W, V)                                                                  \
     if (vectors <= W * 64 * V) EW_LAYERNORM_LAUNCH(W, V, false)
 #define EW_LAYERNORM_LAUNCH(W, V, TINY)                                                          \
-    return start(reinterpret_cast<const void *>(&ew_layernorm_row_kernel<T, W, V, TINY>),        \
+    return start(reinterpret_cast<const void *>(&ew_layernorm_kernel<T, W, V, TINY>),        \
                  dim3(row_blocks(((uint64_t)a.rows * W * 64 + layernorm_block(W) - 1) /          \
                                  layernorm_block(W))),                                           \
                  layernorm_block(W), 0, s, a);
@@ -736,7 +736,7 @@ static hipError_t layernorm_grad_by(const LayerNormGradArgs &a, uint32_t vectors
     {                                                                                             \
         const uint64_t blocks = ((uint64_t)a.rows + G - 1) / G;                                   \
         *parts = blocks <= kOnePart ? 1 : (uint32_t)(blocks < kParts ? blocks : kParts);          \
-        return start(reinterpret_cast<const void *>(&ew_layernorm_grad_kernel<T, W, V, G, TINY>), \
+        return start(reinterpret_cast<const void *>(&ew_layernorm_back_kernel<T, W, V, G, TINY>), \
                      dim3(*parts), W * 64 * G, 0, s, a);                                          \
     }
 #define EW_LAYERNORM_GRAD_ROWS(W, V, G) \
