@@ -181,12 +181,17 @@ __global__ void __launch_bounds__(1024) ew_experts_sort_kernel(ExpertsSortArgs a
         if constexpr (!One) {
             uint32_t *const sums = counters + split.waves * experts;
             if (e0) add_totals(e0, mine_before, mine_all);
+            // within a wave by lane exchanges, then the waves
+            for (uint32_t d = tile; d < 64; d *= 2) {
+                mine_before += (uint32_t)__shfl_xor((int)mine_before, (int)d);
+                mine_all += (uint32_t)__shfl_xor((int)mine_all, (int)d);
+            }
             sums[threadIdx.x] = mine_before;
             sums[blockDim.x + threadIdx.x] = mine_all;
             __syncthreads();
             if (threadIdx.x < tile)
 #pragma unroll 8
-                for (uint32_t q = threadIdx.x; q < blockDim.x; q += tile) {
+                for (uint32_t q = threadIdx.x; q < blockDim.x; q += tile < 64 ? 64 : tile) {
                     before += sums[q];
                     all += sums[blockDim.x + q];
                 }
@@ -588,7 +593,8 @@ hipError_t launch_experts_sort(RowType, const ExpertsSortArgs &a, hipStream_t s,
                      (const uint32_t *)nullptr);
     }
     *path = "counts, then places";
-    const uint32_t chunk = ((a.rows + kSortBlocks - 1) / kSortBlocks + 1023) / 1024 * 1024;
+    const uint32_t least = (a.rows + kSortBlocks - 1) / kSortBlocks;
+    const uint32_t chunk = ((least > 2 * experts ? least : 2 * experts) + 1023) / 1024 * 1024;
     const uint32_t blocks = (a.rows + chunk - 1) / chunk, threads = waves_for(chunk);
     const bool held = split.per <= kHeld * 64;
     const size_t lds = split.waves * experts * sizeof(uint32_t);
