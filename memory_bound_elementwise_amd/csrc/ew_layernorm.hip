@@ -147,12 +147,14 @@ __device__ __forceinline__ typename Vec<T>::wide affine(const void *p, u32x4 v, 
 // Forward, rows that fit in registers: Waves waves a row, V vectors a lane
 // ---------------------------------------------------------------------------
 
-template <typename T, int Waves, int V, RowFit Fit>
-__device__ __forceinline__ void layernorm_row(const LayerNormArgs &a, WaveSums (*shared)[layernorm_block(Waves) / 64])
+// Of R rows at a time, whose loads are on their way together.
+template <typename T, int Waves, int V, int R, RowFit Fit>
+__device__ __forceinline__ void layernorm_rows_of(const LayerNormArgs &a,
+                                                  WaveSums (*shared)[R][layernorm_block(Waves) / 64])
 {
     constexpr uint32_t N = Vec<T>::N, kThreads = Waves * 64;
     constexpr uint32_t kRows = layernorm_block(Waves) / kThreads;
-    // weight and bias are on their way with the row, unless they would not fit
+    // weight and bias are on their way with the rows, unless they would not fit
     // in registers
     constexpr bool kEarly = V < 3;
     const uint32_t group = row_of_thread<kThreads, kRows>(), i = place_in_row<kThreads, kRows>();
@@ -173,85 +175,105 @@ __device__ __forceinline__ void layernorm_row(const LayerNormArgs &a, WaveSums (
     };
     int set = 0;
     // a block's rows go round together (the barriers)
-    for (uint64_t r0 = (uint64_t)blockIdx.x * kRows; r0 < a.rows;
-         r0 += (uint64_t)gridDim.x * kRows, set ^= 1) {
-        const bool live = r0 + group < a.rows;
-        const uint64_t r = live ? r0 + group : r0;
-        u32x4 h[V], w[V], b[V];
-        const T *const x = static_cast<const T *>(a.x) + r * a.x_stride;
+    for (uint64_t r0 = (uint64_t)blockIdx.x * (kRows * R); r0 < a.rows;
+         r0 += (uint64_t)gridDim.x * (kRows * R), set ^= 1) {
+        const auto live = [&](int q) { return r0 + q * kRows + group < a.rows; };
+        const auto row = [&](int q) { return live(q) ? r0 + q * kRows + group : r0; };
+        u32x4 h[R][V], w[V], b[V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) h[k] = load_piece<T, true>(x, cols, piece(k));
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                h[q][k] = load_piece<T, true>(static_cast<const T *>(a.x) + row(q) * a.x_stride, cols, piece(k));
         const auto fetch_affine = [&](int k) {
             if (weight) w[k] = load_piece<T, false>(weight, cols, piece(k));
             if (bias) b[k] = load_piece<T, false>(bias, cols, piece(k));
         };
         if (a.residual) {
-            const T *const p = static_cast<const T *>(a.residual) + r * a.residual_stride;
-            u32x4 res[V];
+            u32x4 res[R][V];
 #pragma unroll
-            for (int k = 0; k < V; ++k) res[k] = load_piece<T, true>(p, cols, piece(k));
+            for (int q = 0; q < R; ++q)
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    res[q][k] = load_piece<T, true>(
+                        static_cast<const T *>(a.residual) + row(q) * a.residual_stride, cols, piece(k));
             if constexpr (kEarly)
 #pragma unroll
                 for (int k = 0; k < V; ++k) fetch_affine(k);
 #pragma unroll
-            for (int k = 0; k < V; ++k)
-                h[k] = Vec<T>::narrow(Vec<T>::widen(h[k]) + Vec<T>::widen(res[k]));
+            for (int q = 0; q < R; ++q)
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    h[q][k] = Vec<T>::narrow(Vec<T>::widen(h[q][k]) + Vec<T>::widen(res[q][k]));
         } else if constexpr (kEarly) {
 #pragma unroll
             for (int k = 0; k < V; ++k) fetch_affine(k);
         }
-        const WaveSums own = wave_sums<T, V, Fit>(h, cols, elements(wave), piece);
-        double mean;
-        float sq;
+        double mean[R];
+        float sq[R];
+        WaveSums own[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) own[q] = wave_sums<T, V, Fit>(h[q], cols, elements(wave), piece);
         if constexpr (Waves == 1) {
-            mean = divide((double)own.near * (double)cols + (double)own.sum, cols, a.by_cols);
-            sq = squares_about(own, cols, mean);
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                mean[q] = divide((double)own[q].near * (double)cols + (double)own[q].sum, cols, a.by_cols);
+                sq[q] = squares_about(own[q], cols, mean[q]);
+            }
         } else {
             // the outputs may be the inputs: nothing is stored before every
-            // wave of the row has loaded (a row of one wave loads before it
+            // wave of the rows has loaded (a row of one wave loads before it
             // stores)
-            WaveSums *const sums = shared[set] + group * Waves;
-            if (threadIdx.x % 64 == 0) sums[wave] = own;
+            if (threadIdx.x % 64 == 0)
+#pragma unroll
+                for (int q = 0; q < R; ++q) shared[set][q][group * Waves + wave] = own[q];
             __syncthreads();
             const uint32_t at = threadIdx.x % lanes_of_waves(Waves);
             const bool some = at < (uint32_t)Waves;
-            const WaveSums of = sums[some ? at : 0];
             const uint32_t n = some ? elements(at) : 0;
-            const double sum = n ? (double)of.near * (double)n + (double)of.sum : 0.0;
-            mean = divide(sum_of_waves<Waves>(sum), cols, a.by_cols);
-            sq = sum_of_waves<Waves>(n ? squares_about(of, n, mean) : 0.0f);
-        }
-        const Mean m(mean);
-        if (live && a.total) {
-            T *const total = static_cast<T *>(a.total) + r * a.total_stride;
 #pragma unroll
-            for (int k = 0; k < V; ++k) store_piece(total, cols, piece(k), h[k]);
+            for (int q = 0; q < R; ++q) {
+                const WaveSums of = shared[set][q][group * Waves + (some ? at : 0)];
+                const double sum = n ? (double)of.near * (double)n + (double)of.sum : 0.0;
+                mean[q] = divide(sum_of_waves<Waves>(sum), cols, a.by_cols);
+                sq[q] = sum_of_waves<Waves>(n ? squares_about(of, n, mean[q]) : 0.0f);
+            }
         }
-        const float rstd = reciprocal_root(sq, (float)a.by_cols, a.eps);
-        if (live && i == 0) {
-            if (a.mean) a.mean[r] = m.hi;
-            if (a.rstd) a.rstd[r] = rstd;
-        }
-        if (!live) continue;
-        T *const y = static_cast<T *>(a.y) + r * a.y_stride;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            if constexpr (!kEarly) fetch_affine(k);
-            store_piece(y, cols, piece(k),
-                        normed<T>(h[k], m, rstd, affine<T>(weight, w[k], 1.0f),
-                                  affine<T>(bias, b[k], 0.0f)));
+        for (int q = 0; q < R; ++q) {
+            const Mean m(mean[q]);
+            const uint64_t r = row(q);
+            if (live(q) && a.total) {
+                T *const total = static_cast<T *>(a.total) + r * a.total_stride;
+#pragma unroll
+                for (int k = 0; k < V; ++k) store_piece(total, cols, piece(k), h[q][k]);
+            }
+            const float rstd = reciprocal_root(sq[q], (float)a.by_cols, a.eps);
+            if (live(q) && i == 0) {
+                if (a.mean) a.mean[r] = m.hi;
+                if (a.rstd) a.rstd[r] = rstd;
+            }
+            if (!live(q)) continue;
+            T *const y = static_cast<T *>(a.y) + r * a.y_stride;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                if (!kEarly && q == 0) fetch_affine(k);
+                store_piece(y, cols, piece(k),
+                            normed<T>(h[q][k], m, rstd, affine<T>(weight, w[k], 1.0f),
+                                      affine<T>(bias, b[k], 0.0f)));
+            }
         }
     }
 }
 
-template <typename T, int Waves, int V, bool Tiny = false>
+template <typename T, int Waves, int V, int R = 1, bool Tiny = false>
 __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_kernel(LayerNormArgs a)
 {
     // two sets, used in turn: a wave is at most one barrier ahead of another
-    __shared__ WaveSums shared[2][layernorm_block(Waves) / 64];
-    if constexpr (Tiny) layernorm_row<T, Waves, V, kTiny>(a, shared);
-    else if (a.cols == Waves * 64 * V * Vec<T>::N) layernorm_row<T, Waves, V, kWhole>(a, shared);
-    else layernorm_row<T, Waves, V, kPart>(a, shared);
+    __shared__ WaveSums shared[2][R][layernorm_block(Waves) / 64];
+    if constexpr (Tiny) layernorm_rows_of<T, Waves, V, R, kTiny>(a, shared);
+    else if (a.cols == Waves * 64 * V * Vec<T>::N) layernorm_rows_of<T, Waves, V, R, kWhole>(a, shared);
+    else layernorm_rows_of<T, Waves, V, R, kPart>(a, shared);
 }
 
 // ---------------------------------------------------------------------------
@@ -664,30 +686,40 @@ constexpr uint32_t kRowACu = 256, kOneRound = 1280;
 template <typename T>
 static hipError_t layernorm_rows(const LayerNormArgs &a, uint32_t vectors, hipStream_t s)
 {
-#define EW_LAYERNORM_ROWS(W, V)                                                                  \
-    if (vectors <= W * 64 * V) EW_LAYERNORM_LAUNCH(W, V, false)
-#define EW_LAYERNORM_LAUNCH(W, V, TINY)                                                          \
-    return start(reinterpret_cast<const void *>(&ew_layernorm_kernel<T, W, V, TINY>),        \
-                 dim3(row_blocks(((uint64_t)a.rows * W * 64 + layernorm_block(W) - 1) /          \
-                                 layernorm_block(W))),                                           \
-                 layernorm_block(W), 0, s, a);
-    if (a.cols < (uint32_t)Vec<T>::N) EW_LAYERNORM_LAUNCH(1, 1, true)
+#define EW_LAYERNORM_LAUNCH(W, V, R, TINY)                                               \
+    return start(reinterpret_cast<const void *>(&ew_layernorm_kernel<T, W, V, R, TINY>), \
+                 dim3(row_blocks((blocks_of(W) + R - 1) / R)), layernorm_block(W), 0, s, a);
+#define EW_LAYERNORM_ROWS(W, V) \
+    if (vectors <= W * 64 * V) EW_LAYERNORM_LAUNCH(W, V, 1, false)
+#define EW_LAYERNORM_PAIRS(W, V) \
+    if (vectors <= W * 64 * V && blocks_of(W) > kOneRound) EW_LAYERNORM_LAUNCH(W, V, 2, false)
+    const auto blocks_of = [&](uint32_t waves) {
+        const uint64_t rows = (uint64_t)layernorm_block((int)waves) / (waves * 64);
+        return (a.rows + rows - 1) / rows;
+    };
+    if (a.cols < (uint32_t)Vec<T>::N) EW_LAYERNORM_LAUNCH(1, 1, 1, true)
+    EW_LAYERNORM_PAIRS(1, 1)
     EW_LAYERNORM_ROWS(1, 1)
+    EW_LAYERNORM_PAIRS(2, 1)
     EW_LAYERNORM_ROWS(2, 1)
+    EW_LAYERNORM_PAIRS(3, 1)
     EW_LAYERNORM_ROWS(3, 1)
+    EW_LAYERNORM_PAIRS(4, 1)
     EW_LAYERNORM_ROWS(4, 1)
+    EW_LAYERNORM_PAIRS(3, 2)
+    if (a.residual && a.rows > 2 * kOneRound) {
+        EW_LAYERNORM_ROWS(4, 2)
+    }
+    EW_LAYERNORM_PAIRS(4, 2)
     if (a.rows <= kOneRound) {
         EW_LAYERNORM_ROWS(5, 1)
-    }
-    if (a.rows <= kRowACu) {
-        EW_LAYERNORM_ROWS(8, 1)
-        EW_LAYERNORM_ROWS(16, 1)
-    }
-    EW_LAYERNORM_ROWS(3, 2)
-    if (a.rows <= kOneRound) {
+        if (a.rows <= kRowACu) {
+            EW_LAYERNORM_ROWS(8, 1)
+            EW_LAYERNORM_ROWS(16, 1)
+        }
+        EW_LAYERNORM_ROWS(3, 2)
         EW_LAYERNORM_ROWS(2, 4)
     }
-    EW_LAYERNORM_ROWS(4, 2)
     EW_LAYERNORM_ROWS(3, 4)
     EW_LAYERNORM_ROWS(4, 4)
     if constexpr (sizeof(T) == 4) {
@@ -696,10 +728,13 @@ static hipError_t layernorm_rows(const LayerNormArgs &a, uint32_t vectors, hipSt
         EW_LAYERNORM_ROWS(8, 4)
         EW_LAYERNORM_ROWS(16, 4)
     } else {
+        EW_LAYERNORM_PAIRS(12, 2)
         EW_LAYERNORM_ROWS(12, 2)
+        EW_LAYERNORM_PAIRS(16, 2)
         EW_LAYERNORM_ROWS(16, 2)
         EW_LAYERNORM_ROWS(12, 4)
     }
+#undef EW_LAYERNORM_PAIRS
 #undef EW_LAYERNORM_ROWS
 #undef EW_LAYERNORM_LAUNCH
     return hipErrorInvalidValue;

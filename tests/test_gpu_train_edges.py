@@ -9,7 +9,7 @@ import torch
 import memory_bound_elementwise_amd as ew
 from tests import train_ref as ref
 from tests.rows_ref import TYPES, U, close
-from tests.test_gpu_rows import DEV, gen, randn
+from tests.test_gpu_rows import DEV, GUARD, gen, randn
 from tests.test_gpu_train import (Batch, Routed, check_grad, check_norm, f32, grad_inputs, i32,
                                   norm_inputs, space)
 
@@ -340,6 +340,24 @@ def test_experts_offsets_past_32_bits():
     assert torch.equal(out[slot[-4:, 0].long()], 2 * tail)
     dots = tail.double().square().sum(1)
     close(dw[-4:, 0], dots, dots * (cols / 64 + 40) * U, "dweights")
+
+
+@every_type
+@pytest.mark.parametrize("rows,cols", ((5203, 3), (5201, 4), (5203, 250), (5131, 512), (2565, 513),
+                                       (2567, 1000), (1283, 1540), (1281, 2049), (1285, 2600),
+                                       (1283, 4096), (2561, 4096), (2563, 3900), (1281, 8191),
+                                       (1281, 12289), (1283, 16001)))
+def test_norm_of_odd_numbers_of_rows(t, rows, cols):
+    """More blocks than the chip holds at once, which then take rows in pairs
+    or several a block: the last one is not full."""
+    x, res, w, b = norm_inputs(t, rows, cols, 3, 1, 17)
+    for residual in (res, None):
+        y, mean, rstd = torch.empty(rows, cols, dtype=TYPES[t], device=DEV), f32(rows + 1), f32(rows + 1)
+        total = torch.empty_like(y) if residual is not None else None
+        getattr(ew, "ew_layernorm_" + t)(x, w, b, y, residual=residual, total=total,
+                                         mean=mean[:rows], rstd=rstd[:rows])
+        check_norm(t, x, residual, w, b, y, total, mean[:rows], rstd[:rows])
+        assert float(mean[rows]) == GUARD and float(rstd[rows]) == GUARD
 
 
 def test_more_rows_than_a_grid_holds():

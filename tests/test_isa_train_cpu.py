@@ -16,7 +16,7 @@ def of(kernels, pattern):  # noqa: F811
 
 
 def test_every_operator_has_its_kernels(kernels):  # noqa: F811
-    for pattern, least in (("ew_layernorm_kernel", 3 * 14), ("ew_layernorm_back_kernel", 3 * 9),
+    for pattern, least in (("ew_layernorm_kernel", 3 * 20), ("ew_layernorm_back_kernel", 3 * 9),
                            ("ew_layernorm_long", 3), ("ew_layernorm_dx", 3), ("ew_policy_small", 6),
                            ("ew_policy_rows", 6), ("ew_policy_grad", 6), ("ew_experts_sort", 4),
                            ("ew_experts_gather", 9), ("ew_experts_combine_kernel", 27),
@@ -42,7 +42,7 @@ def test_streams_use_16_byte_accesses(kernels):  # noqa: F811
 
 def test_rows_in_registers_fit_a_cu(kernels):  # noqa: F811
     """512 registers a lane and SIMD, shared by a block's waves on it."""
-    for name, (_, d, m) in of(kernels, r"layernorm_kernelI\w*?Li(\d+)ELi\d+ELb").items():
+    for name, (_, d, m) in of(kernels, r"layernorm_kernelI\w*?Li(\d+)ELi\d+ELi\d+ELb").items():
         waves = max(int(m.group(1)), 4)
         assert int(d["next_free_vgpr"]) <= 512 // (-(-waves // 4)), name
     for name, (_, d, m) in of(kernels, r"layernorm_back_kernelI\w*?Li(\d+)ELi\d+ELi(\d+)E").items():
@@ -52,7 +52,7 @@ def test_rows_in_registers_fit_a_cu(kernels):  # noqa: F811
 
 def test_one_row_a_wave_leaves_room_for_eight(kernels):  # noqa: F811
     """Short rows' loads are hidden by other waves: eight a SIMD, 64 registers each."""
-    for name, (_, d, _) in of(kernels, r"layernorm_kernelI\w+Li1ELi1ELb0E").items():
+    for name, (_, d, _) in of(kernels, r"layernorm_kernelI\w+Li1ELi1ELi1ELb0E").items():
         assert int(d["next_free_vgpr"]) <= 64, name
 
 
