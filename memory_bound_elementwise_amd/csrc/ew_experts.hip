@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_gather_kernel(ExpertsMo
     constexpr uint32_t U = 1;
     using Cols = Stretch<T, Waves * 64, U, Fit>;
     if (blockIdx.x >= blocks) {
-        clear_padding<T, Fit>(a, blockIdx.x - blocks);
+        if (blockIdx.y == 0) clear_padding<T, Fit>(a, blockIdx.x - blocks);
         return;
     }
     const Worker<Waves> worker;
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_gather_kernel(ExpertsMo
         const uint64_t t = t0 + worker.token;
         if (t >= a.rows) break;
         const Slots slots(a, t);
-        for (uint64_t first = 0; first < a.cols; first += Cols::kCols) {
+        for (uint64_t first = blockIdx.y * Cols::kCols; first < a.cols; first += gridDim.y * Cols::kCols) {
             const Cols part(first, a.cols, worker.place);
             u32x4 v[U];
 #pragma unroll
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_kernel(ExpertsM
         if (t >= a.rows) break;
         const Slots slots(a, t);
         const Weights weights(a, t);
-        for (uint64_t first = 0; first < a.cols; first += Cols::kCols) {
+        for (uint64_t first = blockIdx.y * Cols::kCols; first < a.cols; first += gridDim.y * Cols::kCols) {
             const Cols part(first, a.cols, worker.place);
             u32x4 r[U];
             if (a.residual)
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_grad_kernel(Exp
     // two sets, used in turn: a wave is at most one barrier ahead of another
     __shared__ float scratch[2][kMoveWaves][C];
     if (blockIdx.x >= blocks) {
-        clear_padding<T, Fit>(a, blockIdx.x - blocks);
+        if (blockIdx.y == 0) clear_padding<T, Fit>(a, blockIdx.x - blocks);
         return;
     }
     const Worker<Waves> worker;
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_grad_kernel(Exp
         if (t >= a.rows) break;
         const Slots slots(a, t);
         const Weights weights(a, t);
-        for (uint32_t j0 = 0; j0 < a.top; j0 += C, set ^= 1) {
+        for (uint32_t j0 = blockIdx.y * C; j0 < a.top; j0 += gridDim.y * C, set ^= 1) {
             float dots[C];
 #pragma unroll
             for (uint32_t c = 0; c < C; ++c) dots[c] = 0.0f;
@@ -610,62 +610,75 @@ hipError_t launch_experts_sort(RowType, const ExpertsSortArgs &a, hipStream_t s,
                  (const uint32_t *)totals);
 }
 
-// The kernel of a type for rows that a block shares (each), those that a wave
-// takes, and those shorter than a vector.
-#define EW_MOVE_OF(T, K, W, FIT, ...) K<T, W, ##__VA_ARGS__, FIT>
-#define EW_MOVE_BY_TYPE(t, K, W, FIT, ...)                                                              \
-    ((t) == kRowF32   ? reinterpret_cast<const void *>(&EW_MOVE_OF(float, K, W, FIT, ##__VA_ARGS__))    \
-     : (t) == kRowF16 ? reinterpret_cast<const void *>(&EW_MOVE_OF(_Float16, K, W, FIT, ##__VA_ARGS__)) \
-                      : reinterpret_cast<const void *>(&EW_MOVE_OF(__bf16, K, W, FIT, ##__VA_ARGS__)))
-#define EW_MOVE_KERNEL(t, split, K, ...)                                       \
-    ((split).tiny   ? EW_MOVE_BY_TYPE(t, K, 1, kTiny, ##__VA_ARGS__)           \
-     : (split).each ? EW_MOVE_BY_TYPE(t, K, kMoveWaves, kPart, ##__VA_ARGS__)  \
-                    : EW_MOVE_BY_TYPE(t, K, 1, kPart, ##__VA_ARGS__))
+// Of fewer tokens than kFewTokens several blocks share each, of fewer than
+// kSomeTokens one, where their rows are longer than a vector a lane of a wave.
+constexpr uint32_t kFewTokens = 512, kSomeTokens = 1024;
+
+// The kernel of a type and the row's fit.
+#define EW_MOVE_OF(t, K, W, ...)                                             \
+    ((t) == kRowF32   ? reinterpret_cast<const void *>(&K<float, W, ##__VA_ARGS__>)    \
+     : (t) == kRowF16 ? reinterpret_cast<const void *>(&K<_Float16, W, ##__VA_ARGS__>) \
+                      : reinterpret_cast<const void *>(&K<__bf16, W, ##__VA_ARGS__>))
 
 struct MoveSplit {
     bool each, tiny;      // a block a token; rows shorter than a vector
+    bool few;             // a block a token, and blocks a token are more than one
     bool narrow;          // a vector a lane at most
+    uint32_t vectors;     // of a row
     uint32_t blocks;      // of tokens
 };
 
-// A block shares a token where its row has more than four vectors a lane of a
-// wave; of few tokens, more than one.
 static MoveSplit move_split(RowType t, const ExpertsMoveArgs &a, const char **path)
 {
-    const uint32_t vectors = vectors_of(t, a.cols);
     MoveSplit m;
-    m.each = vectors > (a.rows < 1024 ? 64u : 256u);
-    m.narrow = !m.each && vectors <= 64;
+    m.vectors = vectors_of(t, a.cols);
+    m.few = a.rows < kFewTokens && m.vectors > 64;
+    m.each = m.vectors > (a.rows < kSomeTokens ? 64u : 256u);
+    m.narrow = m.vectors <= 64;
     m.tiny = a.cols < 16 / (uint32_t)row_elem_size(t);
     m.blocks = row_blocks(m.each ? a.rows : ((uint64_t)a.rows + kMoveWaves - 1) / kMoveWaves);
-    *path = m.each ? "a block a token" : m.tiny ? "short rows" : "a wave a token";
+    *path = m.few ? "blocks a token" : m.each ? "a block a token" : m.tiny ? "short rows" : "a wave a token";
     return m;
 }
 
 hipError_t launch_experts_gather(RowType t, const ExpertsMoveArgs &a, hipStream_t s, const char **path)
 {
     const MoveSplit m = move_split(t, a, path);
-    return start(EW_MOVE_KERNEL(t, m, ew_experts_gather_kernel), dim3(m.blocks + a.experts * kPadBlocks), kMoveBlock,
-                 0, s, a, m.blocks);
+    return start(m.tiny   ? EW_MOVE_OF(t, ew_experts_gather_kernel, 1, kTiny)
+                 : m.each ? EW_MOVE_OF(t, ew_experts_gather_kernel, kMoveWaves, kPart)
+                          : EW_MOVE_OF(t, ew_experts_gather_kernel, 1, kPart),
+                 dim3(m.blocks + a.experts * kPadBlocks, m.few ? (m.vectors + kMoveBlock - 1) / kMoveBlock : 1),
+                 kMoveBlock, 0, s, a, m.blocks);
 }
 
 hipError_t launch_experts_combine(RowType t, const ExpertsMoveArgs &a, hipStream_t s, const char **path)
 {
     const MoveSplit m = move_split(t, a, path);
-    return start(a.top <= 2  ? EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 2, 4)
-                 : m.narrow ? EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 8, 1)
-                            : EW_MOVE_KERNEL(t, m, ew_experts_combine_kernel, 4, 2),
-                 dim3(m.blocks), kMoveBlock, 0, s, a, m.blocks);
+#define EW_COMBINE(W, C, U, FIT) EW_MOVE_OF(t, ew_experts_combine_kernel, W, C, U, FIT)
+    return start(m.tiny         ? EW_COMBINE(1, 8, 1, kTiny)
+                 : m.few        ? EW_COMBINE(kMoveWaves, 8, 1, kPart)
+                 : m.narrow     ? EW_COMBINE(1, 8, 1, kPart)
+                 : a.top <= 2   ? m.each ? EW_COMBINE(kMoveWaves, 2, 4, kPart) : EW_COMBINE(1, 2, 4, kPart)
+                 : m.each       ? EW_COMBINE(kMoveWaves, 4, 2, kPart)
+                                : EW_COMBINE(1, 4, 2, kPart),
+                 dim3(m.blocks, m.few ? (m.vectors + kMoveBlock - 1) / kMoveBlock : 1), kMoveBlock, 0, s, a,
+                 m.blocks);
+#undef EW_COMBINE
 }
 
 hipError_t launch_experts_combine_grad(RowType t, const ExpertsMoveArgs &a, hipStream_t s,
                                        const char **path)
 {
     const MoveSplit m = move_split(t, a, path);
-    return start(a.top <= 2  ? EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 2, 4)
-                 : m.narrow ? EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 8, 1)
-                            : EW_MOVE_KERNEL(t, m, ew_experts_combine_grad_kernel, 4, 2),
-                 dim3(m.blocks + a.experts * kPadBlocks), kMoveBlock, 0, s, a, m.blocks);
+#define EW_GRAD(W, C, U, FIT) EW_MOVE_OF(t, ew_experts_combine_grad_kernel, W, C, U, FIT)
+    return start(m.tiny                 ? EW_GRAD(1, 8, 1, kTiny)
+                 : m.narrow             ? EW_GRAD(1, 8, 1, kPart)
+                 : m.few || a.top <= 2  ? m.each ? EW_GRAD(kMoveWaves, 2, 4, kPart) : EW_GRAD(1, 2, 4, kPart)
+                 : m.each               ? EW_GRAD(kMoveWaves, 4, 2, kPart)
+                                        : EW_GRAD(1, 4, 2, kPart),
+                 dim3(m.blocks + a.experts * kPadBlocks, m.few ? (a.top + 1) / 2 : 1), kMoveBlock, 0, s, a,
+                 m.blocks);
+#undef EW_GRAD
 }
 
 }  // namespace ew
