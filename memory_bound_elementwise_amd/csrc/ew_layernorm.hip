@@ -400,7 +400,7 @@ __device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
     const uint32_t group = row_of_thread<kThreads, Groups>(), i = place_in_row<kThreads, Groups>();
     // the next row is on its way while this one is worked on, and the weight
     // stays, unless they would not fit in registers
-    constexpr bool kAhead = V < 3;
+    constexpr bool kAhead = V * N <= 8 || (V * N <= 16 && Waves <= 12);
     const T *const weight = static_cast<const T *>(a.weight);
     const uint32_t cols = a.cols;
     const auto piece = [&](int k) { return Piece<T, Fit>((i + k * kThreads) * N, cols); };
@@ -759,9 +759,18 @@ size_t layernorm_grad_workspace(uint64_t rows, uint64_t cols)
     return (rows < kParts ? rows : kParts) * 2 * sums_pitch(cols) * sizeof(float);
 }
 
-// Up to this many rounds of rows are one block's, which writes dweight and
-// dbias itself and saves the second launch.
-constexpr uint64_t kOnePart = 2;
+// Up to kOnePart rounds of rows are one block's, which writes dweight and dbias
+// itself and saves the second launch (of more, the rounds would cost more).
+// Long rows, a block each, go two to a part where that still fills half of the
+// chip: each part's sums are as many bytes as a row and its gradient.
+constexpr uint64_t kOnePart = 2, kTwoRowsFrom = 160, kTwoRowsTo = 384;
+
+static uint32_t parts_for(uint64_t blocks, int groups)
+{
+    if (blocks <= kOnePart) return 1;
+    if (groups == 1 && blocks > kTwoRowsFrom && blocks <= kTwoRowsTo) return (uint32_t)((blocks + 1) / 2);
+    return (uint32_t)(blocks < kParts ? blocks : kParts);
+}
 
 template <typename T>
 static hipError_t layernorm_grad_by(const LayerNormGradArgs &a, uint32_t vectors, hipStream_t s,
@@ -770,7 +779,7 @@ static hipError_t layernorm_grad_by(const LayerNormGradArgs &a, uint32_t vectors
 #define EW_LAYERNORM_GRAD_LAUNCH(W, V, G, TINY)                                                   \
     {                                                                                             \
         const uint64_t blocks = ((uint64_t)a.rows + G - 1) / G;                                   \
-        *parts = blocks <= kOnePart ? 1 : (uint32_t)(blocks < kParts ? blocks : kParts);          \
+        *parts = parts_for(blocks, G);                                                            \
         return start(reinterpret_cast<const void *>(&ew_layernorm_back_kernel<T, W, V, G, TINY>), \
                      dim3(*parts), W * 64 * G, 0, s, a);                                          \
     }
@@ -791,13 +800,13 @@ static hipError_t layernorm_grad_by(const LayerNormGradArgs &a, uint32_t vectors
         EW_LAYERNORM_GRAD_ROWS(8, 1, 1)
         EW_LAYERNORM_GRAD_ROWS(16, 1, 1)
         EW_LAYERNORM_GRAD_ROWS(12, 2, 1)
-        EW_LAYERNORM_GRAD_ROWS(8, 4, 1)
+        EW_LAYERNORM_GRAD_ROWS(16, 2, 1)
     }
 #undef EW_LAYERNORM_GRAD_ROWS
 #undef EW_LAYERNORM_GRAD_LAUNCH
     return hipErrorInvalidValue;
 }
-static uint32_t grad_vectors(RowType t) { return t == kRowF32 ? 16 * 64 * 4 : 8 * 64 * 4; }
+static uint32_t grad_vectors(RowType t) { return 16 * 64 * (t == kRowF32 ? 4 : 2); }
 
 hipError_t launch_layernorm_grad(RowType t, const LayerNormGradArgs &a, hipStream_t s, const char **path)
 {

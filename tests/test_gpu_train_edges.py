@@ -360,6 +360,19 @@ def test_norm_of_odd_numbers_of_rows(t, rows, cols):
         assert float(mean[rows]) == GUARD and float(rstd[rows]) == GUARD
 
 
+@every_type
+@pytest.mark.parametrize("rows,cols", ((161, 12801), (200, 4100), (383, 8200), (384, 2500),
+                                       (385, 6000), (511, 9000), (300, 16384)))
+def test_norm_grad_of_some_long_rows(t, rows, cols):
+    """Numbers of rows around those whose sums are of one or two rows a part."""
+    dy, x, w, mean, rstd, dto = grad_inputs(t, rows, cols, 0, 0, 33)
+    dx, dw, db = torch.empty_like(x), f32(cols), f32(cols)
+    getattr(ew, "ew_layernorm_grad_" + t)(dy, x, w, mean, rstd, dx, dw, db,
+                                          space(ew.ew_layernorm_grad_workspace(rows, cols)),
+                                          dtotal=dto)
+    check_grad(t, dy, x, w, mean, rstd, dto, dx, dw, db)
+
+
 def test_more_rows_than_a_grid_holds():
     """Norms, losses and movements of more than 2^20 blocks' rows."""
     rows = (1 << 22) + 5                           # four rows a block
