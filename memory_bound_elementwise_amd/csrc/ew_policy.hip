@@ -490,10 +490,10 @@ __global__ void __launch_bounds__(kWideBlock) ew_policy_grad_kernel(PolicyGradAr
 // Dispatch
 // ---------------------------------------------------------------------------
 
-// One block sums up to this many tokens.
-constexpr uint64_t kSmallTokens = 16384;
+// One block sums up to so many tokens, if it takes no more than so many rounds.
+constexpr uint64_t kSmallTokens = 16384, kSmallRounds = 4;
 // A sequence of more than this many tokens is a block's, else a wave's or less.
-constexpr uint32_t kBlockTokens = 1024;
+constexpr uint32_t kBlockTokens = 1024, kSomeTokens = 512, kSomeRows = 1024;
 // Records of sums: at most this many blocks.
 constexpr uint64_t kRecords = 1024;
 
@@ -533,7 +533,6 @@ hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, c
 {
     const bool ref = a.in.ref;
     if ((uint64_t)a.rows * (a.cols ? a.cols : 1) <= kSmallTokens) {
-        *path = "one block";
         // more than a wave a sequence where that takes fewer rounds
         uint32_t lanes = lanes_for(a.cols, 64);
         const auto rounds = [&](uint64_t l) {
@@ -543,8 +542,11 @@ hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, c
         if (lanes == 64)
             for (uint32_t more = 128; more <= kSmallBlock; more *= 2)
                 if (rounds(more) < rounds(lanes)) lanes = more;
-        return start(EW_POLICY_KERNEL(ew_policy_small_kernel, ref, a.cols, lanes), dim3(1), kSmallBlock, 0,
-                     s, a, lanes);
+        if (rounds(lanes) <= kSmallRounds) {
+            *path = "one block";
+            return start(EW_POLICY_KERNEL(ew_policy_small_kernel, ref, a.cols, lanes), dim3(1), kSmallBlock,
+                         0, s, a, lanes);
+        }
     }
     PolicySums *const records = static_cast<PolicySums *>(a.workspace);
     uint32_t *const counts = reinterpret_cast<uint32_t *>(records + kRecords);
@@ -565,7 +567,9 @@ hipError_t launch_policy_loss(RowType, const PolicyLossArgs &a, hipStream_t s, c
                      a, (const PolicySums *)records, n, used, (const uint32_t *)counts);
     }
     *path = "whole sequences";
-    const uint32_t lanes = a.cols > kBlockTokens ? kPolicyBlock : lanes_for(a.cols, 64);
+    const uint32_t lanes = a.cols > (a.rows < kSomeRows ? kSomeTokens : kBlockTokens)
+                               ? kPolicyBlock
+                               : lanes_for(a.cols, 64);
     const uint64_t blocks = ((uint64_t)a.rows * lanes + kPolicyBlock - 1) / kPolicyBlock;
     n = (uint32_t)(blocks < kRecords ? blocks : kRecords);
     e = start(EW_POLICY_KERNEL(ew_policy_rows_kernel, ref, a.cols, lanes), dim3(n), kPolicyBlock, 0, s, a,
