@@ -144,10 +144,21 @@ __device__ __forceinline__ typename Vec<T>::wide affine(const void *p, u32x4 v, 
 }
 
 // ---------------------------------------------------------------------------
-// Forward, rows that fit in registers: Waves waves a row, V vectors a lane
+// Forward, rows that fit in registers: Waves waves a row, V vectors a lane.
+//
+// The mean comes before the squares about it, so the row stays in registers:
+// it is read once and written once, and its waves meet at one barrier.  Each
+// has summed differences from a number of its own (WaveSums) by then, which
+// every wave brings to the common mean in binary64 by itself.
+// Bound by memory: 8192 x 4096 bf16 with residual, total and statistics take
+// 46.0 us, 5.8 TB/s (the vector unit is busy 41 % of the cycles), 1 x 4096 2.5
+// us, the latency of one load and the join.  A block that stays and has its
+// next row's loads on their way took 51-58 us: new blocks overlap as well, and
+// their registers are free earlier.
 // ---------------------------------------------------------------------------
 
-// Of R rows at a time, whose loads are on their way together.
+// R rows at a time, whose loads are on their way together and whose sums hide
+// each other's latency; weight and bias are read once for both.
 template <typename T, int Waves, int V, int R, RowFit Fit>
 __device__ __forceinline__ void layernorm_rows_of(const LayerNormArgs &a,
                                                   WaveSums (*shared)[R][layernorm_block(Waves) / 64])
@@ -277,7 +288,10 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_kernel(La
 }
 
 // ---------------------------------------------------------------------------
-// Forward, longer rows: a block a row, three passes over it
+// Forward, longer rows: a block a row, three passes over it (sum, squares,
+// output), of which the caches serve the later ones in part: 1820 x 18432 f32
+// with a residual 142 us, 1000 x 40000 bf16 95 us (3.8 and 3.4 TB/s of what it
+// cannot do without).
 // ---------------------------------------------------------------------------
 
 constexpr int kLongBlock = 1024;
@@ -359,7 +373,9 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_long_kernel(LayerNorm
 // ---------------------------------------------------------------------------
 
 // dweight and dbias are added up in two steps: at most this many blocks sum a
-// part of the rows each, then the parts are summed.
+// part of the rows each, then the parts are summed.  One block a CU (512: 5-10
+// us slower at 8192 x 4096, a row's bytes of sums more a part; 128: 66.0 us
+// against 48.0 at 3000 x 8960 bf16).
 constexpr uint32_t kParts = 256;
 
 // Floats of one part's sums of dweight (those of dbias follow): whole vectors.
@@ -383,7 +399,9 @@ __device__ __forceinline__ void store_sums(float *row, uint32_t cols, const Piec
 }
 
 // Rows that fit in registers: Waves waves a row, V vectors a lane, Groups rows
-// at a time in a block, which adds up dweight and dbias over its rows.
+// at a time in a block, which adds up dweight and dbias over its rows in
+// registers.  Bound by memory: 8192 x 4096 bf16 with dtotal 45 us, 6.0 TB/s,
+// then 4.0-4.7 us for the sum of the parts.
 template <typename T, int Waves, int V, int Groups>
 struct GradShared {
     // two sets, used in turn: a wave is at most one barrier ahead of another
@@ -399,7 +417,8 @@ __device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
     using Wide = typename Vec<T>::wide;
     const uint32_t group = row_of_thread<kThreads, Groups>(), i = place_in_row<kThreads, Groups>();
     // the next row is on its way while this one is worked on, and the weight
-    // stays, unless they would not fit in registers
+    // stays, unless they would not fit in registers (bf16 rows of 12288: 64.4 us
+    // for 3000, 80.0 without)
     constexpr bool kAhead = V * N <= 8 || (V * N <= 16 && Waves <= 12);
     const T *const weight = static_cast<const T *>(a.weight);
     const uint32_t cols = a.cols;
@@ -569,7 +588,8 @@ __global__ void __launch_bounds__(Waves * 64 * Groups) ew_layernorm_back_kernel(
 }
 
 // dweight (blockIdx.y 0) and dbias (1) from the parts' sums: 32 columns a
-// block, 32 threads a column.
+// block, 32 threads a column, eight parts a thread on their way together.
+// Latency: 4.0-4.7 us for 256 parts of 4096 columns (8 MB).
 constexpr uint32_t kSumCols = 32, kSumParts = 32;
 
 __global__ void __launch_bounds__(kSumCols * kSumParts) ew_layernorm_sums_kernel(LayerNormGradArgs a,
@@ -679,8 +699,25 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_dx_kernel(LayerNormGr
 // Dispatch
 // ---------------------------------------------------------------------------
 
-// Rows for which a block each is at most one a CU, and at most what the CUs hold
-// at once.
+// Waves and vectors a lane by the row's length, so that few lanes are idle, and
+// by the number of rows: more waves where a block a row is at most one a CU
+// (kRowACu), few where the blocks are all there at once (kOneRound), two rows
+// at a time where they are more.  us, in a graph, waves x vectors of bf16 with a
+// residual, 2^25 elements where no rows are given:
+//   512 columns   1x1 45.9, 1x2 56.5         5120    3x4 50.9, 5x2 52.2
+//   1024          2x1 44.6, 1x2 47.0         6144    3x4 48.9, 4x4 52.7
+//   2048          4x1 45.3, 2x2 46.3         8192    4x4 50.1, 8x2 50.6, 16x1 59.1
+//   2560          3x2 48.6, 5x1 52.1         12288   12x2 53.0, 6x4 61.9
+//   4096          4x2 47.3, 2x4 48.7, 8x1 49.1   16384   16x2 52.7, 8x4 54.1
+//   1024 rows: of 2560 5x1 5.8, 3x2 6.1, 2x4 7.1; of 4096 2x4 7.1, 4x2 8.2, 8x1 8.8
+//   one row of 4096: 8x1 2.45, 4x2 2.62, 2x4 3.39
+//   f32: 1021 x 5003 without a residual 5x4 9.9, 7x3 10.4, 12x2 11.8
+// Two rows at a time against one, without and with a residual: 10000 x 4096
+// 27.1, 34.3 and (8192) 48.9, 48.1; 20000 x 1000 18.3, 21.0 and 30.8, 30.6;
+// 3000 x 12288 34.3, 42.5 and 58.3, 58.9; of fewer blocks 2600 x 256 3.7, 3.1.
+// With a residual a lane of 4x2 has four vectors on their way already: from two
+// rounds of blocks on it stays with one row (3000 x 4096 20.2, 20.9; 1300 10.8,
+// 10.0).
 constexpr uint32_t kRowACu = 256, kOneRound = 1280;
 
 template <typename T>
@@ -760,9 +797,12 @@ size_t layernorm_grad_workspace(uint64_t rows, uint64_t cols)
 }
 
 // Up to kOnePart rounds of rows are one block's, which writes dweight and dbias
-// itself and saves the second launch (of more, the rounds would cost more).
+// itself and saves the second launch (2 x 4096 bf16 3.8 us; 4 rows in one
+// block 5.2, in four 5.5, but of 16384 columns 16.0 and 9.9).
 // Long rows, a block each, go two to a part where that still fills half of the
-// chip: each part's sums are as many bytes as a row and its gradient.
+// chip: each part's sums are as many bytes as a row and its gradient (250 x
+// 4096 bf16 9.1 us, 10.9 with a row a part; 300 x 8192 f32 15.2, 17.6; but 130 x
+// 16384 bf16 20.7, 18.8).
 constexpr uint64_t kOnePart = 2, kTwoRowsFrom = 160, kTwoRowsTo = 384;
 
 static uint32_t parts_for(uint64_t blocks, int groups)
@@ -783,11 +823,18 @@ static hipError_t layernorm_grad_by(const LayerNormGradArgs &a, uint32_t vectors
         return start(reinterpret_cast<const void *>(&ew_layernorm_back_kernel<T, W, V, G, TINY>), \
                      dim3(*parts), W * 64 * G, 0, s, a);                                          \
     }
+    // us, in a graph, 2^25 elements with dtotal, waves x vectors x rows at a time:
+    //   bf16  2560 6x1x2 52.7, 8x1x1 56.9; 4096 8x1x1 51.3, 16x1x1 57-60; 5120
+    //         16x1x1 54.7, 8x2x1 56.0; 3000 x 16384 16x2x1 96.5, 8x4x1 128.9
+    //   f32   1280 8x1x2 52.1, 8x1x1 56.7; 6144 16x2x1 53.8; 8192 56.0
+    //   short rows: 2000 x 1000 bf16 2x1x4 9.7, 2x1x8 12.3; 250 x 100 1x1x8 6.7,
+    //   1x1x16 8.7; 1000 x 1281 3x1x4 11.3, 4x1x4 11.6
 #define EW_LAYERNORM_GRAD_ROWS(W, V, G) \
     if (vectors <= W * 64 * V) EW_LAYERNORM_GRAD_LAUNCH(W, V, G, false)
     if (a.cols < (uint32_t)Vec<T>::N) EW_LAYERNORM_GRAD_LAUNCH(1, 1, 8, true)
     EW_LAYERNORM_GRAD_ROWS(1, 1, 8)
     EW_LAYERNORM_GRAD_ROWS(2, 1, 4)
+    EW_LAYERNORM_GRAD_ROWS(3, 1, 4)
     EW_LAYERNORM_GRAD_ROWS(4, 1, 4)
     if constexpr (sizeof(T) == 4) {
         if (vectors <= 384) EW_LAYERNORM_GRAD_LAUNCH(8, 1, 2, false)
