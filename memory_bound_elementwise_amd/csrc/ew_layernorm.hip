@@ -796,18 +796,21 @@ size_t layernorm_grad_workspace(uint64_t rows, uint64_t cols)
     return (rows < kParts ? rows : kParts) * 2 * sums_pitch(cols) * sizeof(float);
 }
 
-// Up to kOnePart rounds of rows are one block's, which writes dweight and dbias
-// itself and saves the second launch (2 x 4096 bf16 3.8 us; 4 rows in one
-// block 5.2, in four 5.5, but of 16384 columns 16.0 and 9.9).
+// Up to kOneShort rounds of short rows (of kShort vectors), kOneLong of others,
+// are one block's, which writes dweight and dbias itself and saves the second
+// launch, 3 us of the host's.  us, in a graph, one block and a block a round:
+// bf16 3 x 4096 4.6, 5.6; 32 x 512 6.4, 6.5; 16 x 2048 8.9, 7.1; f32 16 x 1000
+// 6.9, 6.0; of longer rows 4 x 12288 bf16 10.1, 8.6; 4 x 16384 16.0, 9.9.
 // Long rows, a block each, go two to a part where that still fills half of the
 // chip: each part's sums are as many bytes as a row and its gradient (250 x
 // 4096 bf16 9.1 us, 10.9 with a row a part; 300 x 8192 f32 15.2, 17.6; but 130 x
 // 16384 bf16 20.7, 18.8).
-constexpr uint64_t kOnePart = 2, kTwoRowsFrom = 160, kTwoRowsTo = 384;
+constexpr uint64_t kOneShort = 4, kOneLong = 2, kTwoRowsFrom = 160, kTwoRowsTo = 384;
+constexpr uint32_t kShort = 512;
 
-static uint32_t parts_for(uint64_t blocks, int groups)
+static uint32_t parts_for(uint64_t blocks, int groups, uint32_t vectors)
 {
-    if (blocks <= kOnePart) return 1;
+    if (blocks <= (vectors <= kShort ? kOneShort : kOneLong)) return 1;
     if (groups == 1 && blocks > kTwoRowsFrom && blocks <= kTwoRowsTo) return (uint32_t)((blocks + 1) / 2);
     return (uint32_t)(blocks < kParts ? blocks : kParts);
 }
@@ -819,7 +822,7 @@ static hipError_t layernorm_grad_by(const LayerNormGradArgs &a, uint32_t vectors
 #define EW_LAYERNORM_GRAD_LAUNCH(W, V, G, TINY)                                                   \
     {                                                                                             \
         const uint64_t blocks = ((uint64_t)a.rows + G - 1) / G;                                   \
-        *parts = parts_for(blocks, G);                                                            \
+        *parts = parts_for(blocks, G, vectors);                                                   \
         return start(reinterpret_cast<const void *>(&ew_layernorm_back_kernel<T, W, V, G, TINY>), \
                      dim3(*parts), W * 64 * G, 0, s, a);                                          \
     }
