@@ -635,6 +635,8 @@ hipError_t launch_experts_sort(RowType, const ExpertsSortArgs &a, hipStream_t s,
 // 300 x 4096 14.6, 16.5; 600 x 4096 24.3, 21.6.  A block and a wave a token, 600
 // x 1024: combine 7.3, 7.6; 8192 x 4096: combine 115, 144, gradient 108, 152.
 constexpr uint32_t kFewTokens = 512, kSomeTokens = 1024;
+// (more stretches of columns than this go round)
+constexpr uint32_t kMaxShares = 256;
 
 // The kernel of a type and the row's fit.
 #define EW_MOVE_OF(t, K, W, ...)                                             \
@@ -646,17 +648,18 @@ struct MoveSplit {
     bool each, tiny;      // a block a token; rows shorter than a vector
     bool few;             // a block a token, and blocks a token are more than one
     bool narrow;          // a vector a lane at most
-    uint32_t vectors;     // of a row
+    uint32_t shares;      // blocks that share a token's columns
     uint32_t blocks;      // of tokens
 };
 
 static MoveSplit move_split(RowType t, const ExpertsMoveArgs &a, const char **path)
 {
     MoveSplit m;
-    m.vectors = vectors_of(t, a.cols);
-    m.few = a.rows < kFewTokens && m.vectors > 64;
-    m.each = m.vectors > (a.rows < kSomeTokens ? 64u : 256u);
-    m.narrow = m.vectors <= 64;
+    const uint32_t vectors = vectors_of(t, a.cols), stretches = (vectors + kMoveBlock - 1) / kMoveBlock;
+    m.few = a.rows < kFewTokens && vectors > 64;
+    m.each = vectors > (a.rows < kSomeTokens ? 64u : 256u);
+    m.narrow = vectors <= 64;
+    m.shares = !m.few ? 1 : stretches < kMaxShares ? stretches : kMaxShares;
     m.tiny = a.cols < 16 / (uint32_t)row_elem_size(t);
     m.blocks = row_blocks(m.each ? a.rows : ((uint64_t)a.rows + kMoveWaves - 1) / kMoveWaves);
     *path = m.few ? "blocks a token" : m.each ? "a block a token" : m.tiny ? "short rows" : "a wave a token";
@@ -669,8 +672,7 @@ hipError_t launch_experts_gather(RowType t, const ExpertsMoveArgs &a, hipStream_
     return start(m.tiny   ? EW_MOVE_OF(t, ew_experts_gather_kernel, 1, kTiny)
                  : m.each ? EW_MOVE_OF(t, ew_experts_gather_kernel, kMoveWaves, kPart)
                           : EW_MOVE_OF(t, ew_experts_gather_kernel, 1, kPart),
-                 dim3(m.blocks + a.experts * kPadBlocks, m.few ? (m.vectors + kMoveBlock - 1) / kMoveBlock : 1),
-                 kMoveBlock, 0, s, a, m.blocks);
+                 dim3(m.blocks + a.experts * kPadBlocks, m.shares), kMoveBlock, 0, s, a, m.blocks);
 }
 
 hipError_t launch_experts_combine(RowType t, const ExpertsMoveArgs &a, hipStream_t s, const char **path)
@@ -683,8 +685,7 @@ hipError_t launch_experts_combine(RowType t, const ExpertsMoveArgs &a, hipStream
                  : a.top <= 2   ? m.each ? EW_COMBINE(kMoveWaves, 2, 4, kPart) : EW_COMBINE(1, 2, 4, kPart)
                  : m.each       ? EW_COMBINE(kMoveWaves, 4, 2, kPart)
                                 : EW_COMBINE(1, 4, 2, kPart),
-                 dim3(m.blocks, m.few ? (m.vectors + kMoveBlock - 1) / kMoveBlock : 1), kMoveBlock, 0, s, a,
-                 m.blocks);
+                 dim3(m.blocks, m.shares), kMoveBlock, 0, s, a, m.blocks);
 #undef EW_COMBINE
 }
 

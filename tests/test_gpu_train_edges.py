@@ -373,6 +373,27 @@ def test_norm_grad_of_some_long_rows(t, rows, cols):
     check_grad(t, dy, x, w, mean, rstd, dto, dx, dw, db)
 
 
+@every_type
+def test_experts_of_the_longest_rows(t):
+    """One token whose columns are more than the blocks that share them."""
+    cols, dt = 140_000_003, TYPES[t]
+    x = torch.arange(cols, device=DEV).remainder_(251).to(dt)[None]
+    slot = torch.tensor([[1, -1]], dtype=torch.int32, device=DEV)
+    out = torch.full((2, cols), 7.0, dtype=dt, device=DEV)
+    getattr(ew, "ew_experts_gather_" + t)(x, slot, out)
+    assert torch.equal(out[1:], x) and bool((out[0] == 7).all())
+    y = torch.empty_like(x)
+    w = torch.tensor([[0.5, 3.0]], device=DEV)
+    getattr(ew, "ew_experts_combine_" + t)(out, slot, y, weights=w, residual=x)
+    assert torch.equal(y, (1.5 * x.float()).to(dt))
+    dw = f32(1, 2)
+    getattr(ew, "ew_experts_combine_grad_" + t)(x, out, slot, w, out, dw)
+    assert torch.equal(out[1:], (0.5 * x.float()).to(dt)) and float(dw[0, 1]) == 0
+    dot = sum(float(p.double().square().sum()) for p in x[0].split(1 << 26))
+    # a lane adds up cols / 256 terms one after another
+    assert abs(float(dw[0, 0]) - dot) <= dot * (cols / 256 + 40) * U
+
+
 def test_more_rows_than_a_grid_holds():
     """Norms, losses and movements of more than 2^20 blocks' rows."""
     rows = (1 << 22) + 5                           # four rows a block
