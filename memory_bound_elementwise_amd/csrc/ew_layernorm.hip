@@ -621,7 +621,9 @@ __global__ void __launch_bounds__(kSumCols * kSumParts) ew_layernorm_sums_kernel
 // ---------------------------------------------------------------------------
 // Gradient, longer rows: the parts' sums of dweight and dbias (a thread a
 // vector of columns over a part of the rows), their sum, then dx (a block a
-// row, two passes over it).  dx comes last: it may be dy or x.
+// row, two passes over it).  dx comes last: it may be dy or x.  1820 x 18432 with
+// dtotal 191 us of f32 and 112 of bf16, 1000 x 40000 bf16 141: dy and x are read
+// three times, the second pass over a row from the caches.
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kColsBlock = 256;
