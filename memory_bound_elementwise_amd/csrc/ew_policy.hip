@@ -189,10 +189,10 @@ __device__ __forceinline__ void each_four(const PolicyTokens &in, const PolicyRo
 // ---------------------------------------------------------------------------
 // Forward: sums over parts of the batch, then their join (a second launch: a
 // last block that joins would need a counter that is 0 before the call).  Both
-// in one block for few tokens.  4096 x 4096 tokens, half of them counted: 38.0
+// in one block for few tokens.  4096 x 4096 tokens, half of them counted: 37
 // us, of which 5 are the join's.  140 MB are read, 21 us; the rest is that
-// sequences end at different times, and a block's four sequences after another
-// on the way (every block is on the chip at once).  8 x 512 tokens: 5.5 us,
+// sequences end at different times, and a block's sequences after another on
+// the way (every block is on the chip at once).  8 x 512 tokens: 5.5 us,
 // latency.
 // ---------------------------------------------------------------------------
 
@@ -244,13 +244,22 @@ __device__ __forceinline__ PolicySums block_sums(const PolicySums &mine, PolicyS
     return each_sum(some, [](double x) { return sixteen_sum(x); });
 }
 
-// What a lane sums of a row's tokens [from, to).
-struct Counts {
-    uint64_t clipped, tokens;
+// What a lane sums.  Its counts fit in 32 bits: a launch has a thousand blocks or
+// a lane's tokens are of one sequence.
+struct LaneSums {
+    double policy, kl, fall;
+    uint32_t clipped, tokens, rows;
+    __device__ LaneSums() : policy(0.0), kl(0.0), fall(0.0), clipped(0), tokens(0), rows(0) {}
+    __device__ PolicySums all() const
+    {
+        return PolicySums{policy, kl, fall, (double)clipped, (double)tokens, (double)rows};
+    }
 };
 
+// Four tokens: policy and kl of their sequence's sums, the rest of all.
 template <bool Ref>
-__device__ __forceinline__ void add_four(const PolicyTokens &in, const Four &f, PolicySums &s, Counts &n)
+__device__ __forceinline__ void add_four(const PolicyTokens &in, const Four &f, double &row_policy,
+                                         double &row_kl, LaneSums &s)
 {
     float policy = 0.0f, kl = 0.0f, fall = 0.0f;
     uint32_t clipped = 0;
@@ -265,24 +274,25 @@ __device__ __forceinline__ void add_four(const PolicyTokens &in, const Four &f, 
         fall -= counted ? t.x : 0.0f;
         clipped += counted && t.clipped;
     }
-    s.policy += (double)policy;
-    if constexpr (Ref) s.kl += (double)kl;
+    row_policy += (double)policy;
+    if constexpr (Ref) row_kl += (double)kl;
     s.fall += (double)fall;
-    n.clipped += clipped;
-    n.tokens += f.number();
+    s.clipped += clipped;
+    s.tokens += f.number();
 }
 
+// A lane's share of a sequence's tokens [from, to): its sums of them, and of the
+// rest in s.
 template <bool Ref, bool Few, bool One>
-__device__ __forceinline__ Counts sum_tokens(const PolicyTokens &in, uint64_t r, uint64_t from,
-                                             uint32_t to, uint32_t lanes, uint32_t lane, PolicySums &s)
+__device__ __forceinline__ void sum_tokens(const PolicyTokens &in, uint64_t r, uint64_t from, uint32_t to,
+                                           uint32_t lanes, uint32_t lane, double &row_policy,
+                                           double &row_kl, LaneSums &s)
 {
-    Counts n{0, 0};
-    if (from >= to) return n;      // (the advantage of no tokens may be absent)
+    if (from >= to) return;        // (the advantage of no tokens may be absent)
     const PolicyRow row(in, r);
     each_four<Ref, Few, One>(in, row, from, to, lanes, lane, [&](const Four &f, const auto &) {
-        if (f.counted) add_four<Ref>(in, f, s, n);
+        if (f.counted) add_four<Ref>(in, f, row_policy, row_kl, s);
     });
-    return n;
 }
 
 // Loss and stats from the batch's sums.
@@ -345,19 +355,17 @@ __device__ __forceinline__ uint32_t row_in_round(uint32_t lanes)
 // blocks go round together.
 template <bool Ref, bool Few, bool Wave, uint32_t Block>
 __device__ __forceinline__ void add_sequences(const PolicyLossArgs &a, uint64_t r0, uint64_t step,
-                                              uint32_t lanes, uint32_t *counts, PolicySums &all)
+                                              uint32_t lanes, uint32_t *counts, LaneSums &all)
 {
     // two sets, used in turn: a wave is at most one barrier ahead of another
     __shared__ uint32_t tokens_of[2][Block / 64];
     const uint32_t lane = threadIdx.x % lanes;
     for (int set = 0; r0 < a.rows; r0 += step, set ^= 1) {
         const uint64_t r = r0 + row_in_round<Wave>(lanes);
-        PolicySums s{};
-        Counts n{0, 0};
-        if (r < a.rows) n = sum_tokens<Ref, Few, !Wave>(a.in, r, 0, a.cols, lanes, lane, s);
-        s.clipped = (double)n.clipped;
-        s.tokens = (double)n.tokens;
-        uint32_t tokens = lanes_sum((uint32_t)n.tokens, lanes < 64 ? lanes : 64);
+        double policy = 0.0, kl = 0.0;
+        const uint32_t before = all.tokens;
+        if (r < a.rows) sum_tokens<Ref, Few, !Wave>(a.in, r, 0, a.cols, lanes, lane, policy, kl, all);
+        uint32_t tokens = lanes_sum(all.tokens - before, lanes < 64 ? lanes : 64);
         if (lanes > 64) {
             if (threadIdx.x % 64 == 0) tokens_of[set][threadIdx.x / 64] = tokens;
             __syncthreads();
@@ -365,7 +373,10 @@ __device__ __forceinline__ void add_sequences(const PolicyLossArgs &a, uint64_t 
             const uint32_t waves = lanes / 64, mine = threadIdx.x / lanes * waves;
             for (uint32_t w = 0; w < waves; ++w) tokens += tokens_of[set][mine + w];
         }
-        add_sequence(all, s, a.mean == EW_MEAN_SEQUENCES, tokens, lane == 0);
+        const double w = a.mean == EW_MEAN_SEQUENCES && tokens ? 1.0 / (double)tokens : 1.0;
+        all.policy += policy * w;
+        all.kl += kl * w;
+        all.rows += lane == 0 && tokens ? 1 : 0;
         if (r < a.rows && lane == 0) counts[r] = tokens;
     }
 }
@@ -376,9 +387,9 @@ __global__ void __launch_bounds__(kSmallBlock) ew_policy_small_kernel(PolicyLoss
 {
     __shared__ PolicySums scratch[kSmallBlock / 64];
     uint32_t *const counts = static_cast<uint32_t *>(a.workspace);
-    PolicySums all{};
-    add_sequences<Ref, Few, Wave, kSmallBlock>(a, 0, kSmallBlock / lanes, lanes, counts, all);
-    all = block_sums<kSmallBlock / 64>(all, scratch);
+    LaneSums mine;
+    add_sequences<Ref, Few, Wave, kSmallBlock>(a, 0, kSmallBlock / lanes, lanes, counts, mine);
+    const PolicySums all = block_sums<kSmallBlock / 64>(mine.all(), scratch);
     if (threadIdx.x == 0) write_loss(a, all);
     if (a.weights)
         for (uint32_t r = threadIdx.x; r < a.rows; r += kSmallBlock)
@@ -392,10 +403,10 @@ __global__ void __launch_bounds__(kPolicyBlock) ew_policy_rows_kernel(PolicyLoss
                                                                      uint32_t *counts)
 {
     __shared__ PolicySums scratch[kPolicyBlock / 64];
-    PolicySums all{};
+    LaneSums mine;
     const uint64_t per = kPolicyBlock / lanes;
-    add_sequences<Ref, Few, Wave, kPolicyBlock>(a, blockIdx.x * per, gridDim.x * per, lanes, counts, all);
-    all = block_sums<kPolicyBlock / 64>(all, scratch);
+    add_sequences<Ref, Few, Wave, kPolicyBlock>(a, blockIdx.x * per, gridDim.x * per, lanes, counts, mine);
+    const PolicySums all = block_sums<kPolicyBlock / 64>(mine.all(), scratch);
     if (threadIdx.x == 0) records[blockIdx.x] = all;
 }
 
@@ -406,13 +417,11 @@ __global__ void __launch_bounds__(kPolicyBlock) ew_policy_parts_kernel(PolicyLos
                                                                       PolicySums *records)
 {
     __shared__ PolicySums scratch[kPolicyBlock / 64];
-    PolicySums s{};
+    LaneSums mine;
     const uint64_t from = blockIdx.x * part_tokens, to = from + part_tokens;
-    const Counts n = sum_tokens<Ref, false, false>(a.in, blockIdx.y, from, to < a.cols ? (uint32_t)to : a.cols,
-                                            kPolicyBlock, threadIdx.x, s);
-    s.clipped = (double)n.clipped;
-    s.tokens = (double)n.tokens;
-    s = block_sums<kPolicyBlock / 64>(s, scratch);
+    sum_tokens<Ref, false, false>(a.in, blockIdx.y, from, to < a.cols ? (uint32_t)to : a.cols, kPolicyBlock,
+                                  threadIdx.x, mine.policy, mine.kl, mine);
+    const PolicySums s = block_sums<kPolicyBlock / 64>(mine.all(), scratch);
     if (threadIdx.x == 0) records[(uint64_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
@@ -513,9 +522,11 @@ constexpr uint64_t kSmallTokens = 16384, kSmallRounds = 4;
 // wave: 30 x 1000 7.6, 9.6; 1000 x 1000 11.3, 12.5; 1000 x 512 10.8, 9.1; 2000 x
 // 1000 15.0, 14.3; 1500 x 4001 22.9, 29.8; 4096 x 4096 40.4, 42.4.
 constexpr uint32_t kBlockTokens = 1024, kSomeTokens = 512, kSomeRows = 1024;
-// Records of sums: at most this many blocks (4096 x 4096: 39.4 us, with 2048
-// 40.7, with 512 and blocks twice as large 45.7).
-constexpr uint64_t kRecords = 1024;
+// Records of sums: at most this many blocks, five a CU, which the kernel's
+// registers (96 a lane) leave room for.  4096 x 4096 and 1115 x 13042 37.3 and
+// 38.0 us; with 1024 39.4, 44.3; 1536 40.0, 37.8; 2048 39.5, 39.1; 4096 39.8,
+// 38.1 (with 106 registers, four blocks a CU, 40.0 and 44.3).
+constexpr uint64_t kRecords = 1280;
 
 // Lanes that share a sequence: each takes four tokens at a time.  (Fewer than
 // a wave hold all of it.)

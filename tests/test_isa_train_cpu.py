@@ -56,6 +56,12 @@ def test_one_row_a_wave_leaves_room_for_eight(kernels):  # noqa: F811
         assert int(d["next_free_vgpr"]) <= 64, name
 
 
+def test_five_blocks_of_sequences_a_cu(kernels):  # noqa: F811
+    """Their number is what the chip holds at once: five waves a SIMD."""
+    for name, (_, d, _) in of(kernels, r"policy_(rows|parts)_kernel").items():
+        assert int(d["next_free_vgpr"]) <= 96, name
+
+
 def test_sums_of_a_batch_are_binary64(kernels):  # noqa: F811
     for name, (body, _, _) in of(kernels, r"policy_(small|rows|parts|join)_kernel").items():
         assert "v_add_f64" in body, name
