@@ -244,8 +244,9 @@ __device__ __forceinline__ PolicySums block_sums(const PolicySums &mine, PolicyS
     return each_sum(some, [](double x) { return sixteen_sum(x); });
 }
 
-// What a lane sums.  Its counts fit in 32 bits: a launch has a thousand blocks or
-// a lane's tokens are of one sequence.
+// What a lane sums.  Its counts fit in 32 bits: its tokens are of one sequence
+// (below 2^31), or there are kRecords blocks, whose lanes share what the memory
+// holds (below 2^37 tokens) in equal numbers of sequences.
 struct LaneSums {
     double policy, kl, fall;
     uint32_t clipped, tokens, rows;
