@@ -606,8 +606,10 @@ ew_status_t ew_distill_grad_bf16(const uint16_t *logits, size_t stride, const fl
  *   y = round((total - mean) * rstd * weight + bias).
  * Differences are taken from the row's mean to 24 bits of the difference,
  * however far the row lies from 0: a row of equal values has y = bias exactly
- * (for eps > 0).  A row that holds a NaN or an infinity has NaN in mean, rstd
- * and y.
+ * (for eps > 0).  The numbers of total may be of any size, also where their
+ * differences or the squares of these leave binary32 (rstd does for eps = 0 and
+ * a standard deviation below 2^-128).  A row that holds a NaN or an infinity has
+ * NaN in mean, rstd and y.
  * weight, bias  each optional: 1 and 0 where absent
  * residual      optional: without it total is x itself
  * total         optional, requires residual: the rounded sum

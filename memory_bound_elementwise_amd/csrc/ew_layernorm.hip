@@ -27,6 +27,7 @@ __device__ __forceinline__ uint32_t place_in_row()
 // the mean's rounding in it (a row of equal values would not give 0).
 struct Mean {
     float hi, lo;
+    __device__ Mean() {}
     __device__ explicit Mean(double m) : hi((float)m), lo((float)(m - (double)(float)m)) {}
 };
 
@@ -62,26 +63,45 @@ __device__ __forceinline__ float sum_of_waves(float x)
 constexpr uint32_t lanes_of_waves(int waves) { return waves > 8 ? 16 : waves > 4 ? 8 : waves > 2 ? 4 : waves; }
 
 // What a wave knows of its elements of a row: a number near them, and the sums
-// of the differences from it and of their squares.
+// of the differences from it and of their squares.  Where binary32 does not hold
+// these, the sums are of differences times 2^-up.
 struct WaveSums {
     float near, sum, squares;
+    int up;
 };
+
+// The power of two by which differences are multiplied so that binary32 holds
+// the sum of their squares: 0, or another where that is past its range, as that
+// of numbers above 2^50 may be, or below it and eps does not cover it.  (Numbers
+// within 2^-30 of one above 1 are equal to it.)
+constexpr int kShift = 80;
+__device__ __forceinline__ int shift_for(float squares, float eps, float near)
+{
+    const float least = eps < 0x1p-60f ? 0x1p-60f : -1.0f;
+    if (squares < 0x1p100f && squares >= least) return 0;
+    return !(squares < 1.0f) ? -kShift : __builtin_fabsf(near) <= 1.0f ? kShift : 0;
+}
 
 // The number is the mean of the wave's first vector (of equal values: exactly
 // theirs, so that their differences are 0).  Where it lies so far from the
 // wave's mean that the squares about it are more than four times those about
 // the mean, two bits, the wave sums again from its mean: neither an outlier nor
-// the distance of the row from 0 costs more.
+// the distance of the row from 0 costs more.  Where binary32 loses the squares,
+// it sums again with differences times a power of two.
 template <typename T, int V, RowFit Fit, class At>
-__device__ __forceinline__ WaveSums wave_sums(const u32x4 (&h)[V], uint32_t cols, uint32_t n, At piece)
+__device__ __forceinline__ WaveSums wave_sums(const u32x4 (&h)[V], uint32_t cols, uint32_t n, float eps,
+                                              At piece)
 {
     constexpr uint32_t N = Vec<T>::N;
     using Wide = typename Vec<T>::wide;
-    const auto about = [&](float x) {
-        WaveSums w{x, 0.0f, 0.0f};
+    const auto about = [&](float near, float scale, int up) {
+        WaveSums w{near, 0.0f, 0.0f, up};
+        const float at = near * scale;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            Wide d = Vec<T>::widen(h[k]) - x;
+            Wide d = Vec<T>::widen(h[k]);
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j) d[j] = __builtin_fmaf(d[j], scale, -at);
             if (Fit == kTiny || (Fit == kPart && n < V * 64 * N)) {     // the same in all lanes
                 const Piece<T, Fit> p = piece(k);
 #pragma unroll
@@ -98,21 +118,36 @@ __device__ __forceinline__ WaveSums wave_sums(const u32x4 (&h)[V], uint32_t cols
         w.squares = wave_reduce<Sum>(w.squares);
         return w;
     };
+    const auto off_centre = [&](const WaveSums &w) { return w.sum * w.sum > 0.75f * (float)n * w.squares; };
     const Wide f = Vec<T>::widen(h[0]) * (1.0f / N);
     float first = (f[0] + f[1]) + (f[2] + f[3]);
     if constexpr (N == 8) first += (f[4] + f[5]) + (f[6] + f[7]);
     if constexpr (Fit == kTiny) first = Vec<T>::widen(h[0])[0];
-    WaveSums w = about(lane_value(first, 0));
-    // (the values are the same in all lanes)
-    if (w.sum * w.sum > 0.75f * (float)n * w.squares) w = about(w.near + w.sum / (float)n);
+    WaveSums w = about(lane_value(first, 0), 1.0f, 0);
+    const int shift = shift_for(w.squares, eps, w.near);
+    // (what decides on other turns is the same in all lanes)
+    if (shift != 0 || off_centre(w)) {
+        for (bool more = true; more;) {
+            more = w.up != -shift;
+            if (!more) w.near += __builtin_ldexpf(w.sum / (float)n, w.up);
+            w = about(w.near, __builtin_ldexpf(1.0f, shift), -shift);
+            more = more && off_centre(w);
+        }
+    }
     return w;
 }
 
-// The squares about the row's mean of a wave of n elements.
-__device__ __forceinline__ float squares_about(const WaveSums &w, uint32_t n, double mean)
+// The sum of a wave's n elements, and the squares about the row's mean times
+// 2^(2 shift).
+__device__ __forceinline__ double sum_of(const WaveSums &w, uint32_t n)
 {
-    const float off = (float)((double)w.near - mean);
-    return __builtin_fmaf(off, __builtin_fmaf(off, (float)n, 2.0f * w.sum), w.squares);
+    return __builtin_fma((double)w.near, (double)n, __builtin_ldexp((double)w.sum, w.up));
+}
+__device__ __forceinline__ float squares_about(const WaveSums &w, uint32_t n, double mean, int shift)
+{
+    const float off = (float)__builtin_ldexp((double)w.near - mean, shift);
+    return __builtin_fmaf(off, __builtin_fmaf(off, (float)n, __builtin_ldexpf(w.sum, w.up + shift + 1)),
+                          __builtin_ldexpf(w.squares, 2 * (w.up + shift)));
 }
 
 // 1 / sqrt(squares / n + eps), by = 1 / n, through the hardware's reciprocal
@@ -126,13 +161,46 @@ __device__ __forceinline__ float reciprocal_root(float squares, float by, float 
     return small ? root * 0x1p50f : root;
 }
 
+// How a row is normed: differences from the mean times scale, a power of two
+// that keeps them inside binary32 and is 1 for all but rows that shift_for()
+// names, times root.
+struct Place {
+    Mean mean;          // times scale
+    float root, scale;
+    __device__ Place() {}
+    // squares: of differences times 2^shift
+    __device__ Place(double mean_, float squares, float by, float eps, int shift)
+    {
+        const float s = __builtin_ldexpf(1.0f, shift);
+        root = reciprocal_root(squares, by, eps * s * s);
+        // equal numbers, whose mean may be any, are not shifted up; others that
+        // close are close to 0
+        const bool equal = shift > 0 && !(squares > 0.0f);
+        if (equal) root *= s;
+        scale = equal ? 1.0f : s;
+        mean = Mean(mean_ * (double)scale);
+    }
+    __device__ float rstd() const { return root * scale; }
+    // The same in all of a wave: in scalar registers, which leave room for a
+    // wave more a SIMD.  (A vector instruction takes one.)
+    __device__ void to_scalars()
+    {
+        mean.lo = lane_value(mean.lo, 0);
+        root = lane_value(root, 0);
+        scale = lane_value(scale, 0);
+    }
+};
+
 template <typename T>
-__device__ __forceinline__ u32x4 normed(u32x4 v, const Mean &m, float rstd,
-                                        typename Vec<T>::wide w, typename Vec<T>::wide b)
+__device__ __forceinline__ u32x4 normed(u32x4 v, const Place &p, typename Vec<T>::wide w,
+                                        typename Vec<T>::wide b)
 {
-    typename Vec<T>::wide y = (Vec<T>::widen(v) - m.hi) - m.lo;
+    typename Vec<T>::wide y = Vec<T>::widen(v);
 #pragma unroll
-    for (int j = 0; j < Vec<T>::N; ++j) y[j] = __builtin_fmaf(y[j] * rstd, w[j], b[j]);
+    for (int j = 0; j < Vec<T>::N; ++j) {
+        const float off = __builtin_fmaf(y[j], p.scale, -p.mean.hi) - p.mean.lo;
+        y[j] = __builtin_fmaf(off * p.root, w[j], b[j]);
+    }
     return Vec<T>::narrow(y);
 }
 
@@ -220,18 +288,10 @@ __device__ __forceinline__ void layernorm_rows_of(const LayerNormArgs &a,
 #pragma unroll
             for (int k = 0; k < V; ++k) fetch_affine(k);
         }
-        double mean[R];
-        float sq[R];
         WaveSums own[R];
 #pragma unroll
-        for (int q = 0; q < R; ++q) own[q] = wave_sums<T, V, Fit>(h[q], cols, elements(wave), piece);
-        if constexpr (Waves == 1) {
-#pragma unroll
-            for (int q = 0; q < R; ++q) {
-                mean[q] = divide((double)own[q].near * (double)cols + (double)own[q].sum, cols, a.by_cols);
-                sq[q] = squares_about(own[q], cols, mean[q]);
-            }
-        } else {
+        for (int q = 0; q < R; ++q) own[q] = wave_sums<T, V, Fit>(h[q], cols, elements(wave), a.eps, piece);
+        if constexpr (Waves > 1) {
             // the outputs may be the inputs: nothing is stored before every
             // wave of the rows has loaded (a row of one wave loads before it
             // stores)
@@ -239,30 +299,36 @@ __device__ __forceinline__ void layernorm_rows_of(const LayerNormArgs &a,
 #pragma unroll
                 for (int q = 0; q < R; ++q) shared[set][q][group * Waves + wave] = own[q];
             __syncthreads();
-            const uint32_t at = threadIdx.x % lanes_of_waves(Waves);
-            const bool some = at < (uint32_t)Waves;
-            const uint32_t n = some ? elements(at) : 0;
+        }
+        const uint32_t at = threadIdx.x % lanes_of_waves(Waves);
+        const bool some = at < (uint32_t)Waves;
+        const uint32_t n = Waves == 1 ? cols : some ? elements(at) : 0;
+        Place place[R];
 #pragma unroll
-            for (int q = 0; q < R; ++q) {
-                const WaveSums of = shared[set][q][group * Waves + (some ? at : 0)];
-                const double sum = n ? (double)of.near * (double)n + (double)of.sum : 0.0;
-                mean[q] = divide(sum_of_waves<Waves>(sum), cols, a.by_cols);
-                sq[q] = sum_of_waves<Waves>(n ? squares_about(of, n, mean[q]) : 0.0f);
+        for (int q = 0; q < R; ++q) {
+            const WaveSums of = Waves == 1 ? own[q] : shared[set][q][group * Waves + (some ? at : 0)];
+            const double mean = divide(sum_of_waves<Waves>(n ? sum_of(of, n) : 0.0), cols, a.by_cols);
+            const auto squares = [&](int shift) {
+                return sum_of_waves<Waves>(n ? squares_about(of, n, mean, shift) : 0.0f);
+            };
+            const float sq = squares(0);
+            place[q] = Place(mean, sq, (float)a.by_cols, a.eps, 0);
+            const int shift = shift_for(sq, a.eps, (float)mean);
+            if (shift != 0)                  // (the same in all of the wave)
+                place[q] = Place(mean, squares(shift), (float)a.by_cols, a.eps, shift);
+            if (live(q) && i == 0) {
+                if (a.mean) a.mean[row(q)] = (float)mean;
+                if (a.rstd) a.rstd[row(q)] = place[q].rstd();
             }
+            place[q].to_scalars();
         }
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            const Mean m(mean[q]);
             const uint64_t r = row(q);
             if (live(q) && a.total) {
                 T *const total = static_cast<T *>(a.total) + r * a.total_stride;
 #pragma unroll
                 for (int k = 0; k < V; ++k) store_piece(total, cols, piece(k), h[q][k]);
-            }
-            const float rstd = reciprocal_root(sq[q], (float)a.by_cols, a.eps);
-            if (live(q) && i == 0) {
-                if (a.mean) a.mean[r] = m.hi;
-                if (a.rstd) a.rstd[r] = rstd;
             }
             if (!live(q)) continue;
             T *const y = static_cast<T *>(a.y) + r * a.y_stride;
@@ -270,7 +336,7 @@ __device__ __forceinline__ void layernorm_rows_of(const LayerNormArgs &a,
             for (int k = 0; k < V; ++k) {
                 if (!kEarly && q == 0) fetch_affine(k);
                 store_piece(y, cols, piece(k),
-                            normed<T>(h[q][k], m, rstd, affine<T>(weight, w[k], 1.0f),
+                            normed<T>(h[q][k], place[q], affine<T>(weight, w[k], 1.0f),
                                       affine<T>(bias, b[k], 0.0f)));
             }
         }
@@ -289,7 +355,8 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_kernel(La
 
 // ---------------------------------------------------------------------------
 // Forward, longer rows: a block a row, three passes over it (sum, squares,
-// output), of which the caches serve the later ones in part: 1820 x 18432 f32
+// output; a second one of squares that leave binary32), of which
+// the caches serve the later ones in part: 1820 x 18432 f32
 // with a residual 142 us, 1000 x 40000 bf16 95 us (3.8 and 3.4 TB/s of what it
 // cannot do without).
 // ---------------------------------------------------------------------------
@@ -343,19 +410,32 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_long_kernel(LayerNorm
             for (uint32_t j = 0; j < N; ++j) sum += j >= p.p.skip ? (double)f[j] : 0.0;
             if (total) p.store(total, h);
         }
-        const Mean m(divide(long_sum(sum, sums[set]), a.cols, a.by_cols));
-        float sq = 0.0f;
-        for (uint32_t at = threadIdx.x * N; at < a.cols; at += kLongBlock * N) {
-            const LongPiece<T> p(at, a.cols);
-            const Wide d = (Vec<T>::widen(again(p)) - m.hi) - m.lo;
+        const double mean = divide(long_sum(sum, sums[set]), a.cols, a.by_cols);
+        const auto squares = [&](int shift) {
+            const float scale = __builtin_ldexpf(1.0f, shift);
+            const Mean m(mean * (double)scale);
+            float sq = 0.0f;
+            for (uint32_t at = threadIdx.x * N; at < a.cols; at += kLongBlock * N) {
+                const LongPiece<T> p(at, a.cols);
+                const Wide f = Vec<T>::widen(again(p));
 #pragma unroll
-            for (uint32_t j = 0; j < N; ++j) sq = j >= p.p.skip ? __builtin_fmaf(d[j], d[j], sq) : sq;
+                for (uint32_t j = 0; j < N; ++j) {
+                    const float d = __builtin_fmaf(f[j], scale, -m.hi) - m.lo;
+                    sq = j >= p.p.skip ? __builtin_fmaf(d, d, sq) : sq;
+                }
+            }
+            return long_sum(sq, sqs[set]);
+        };
+        const float sq = squares(0);
+        Place place(mean, sq, (float)a.by_cols, a.eps, 0);
+        const int shift = shift_for(sq, a.eps, (float)mean);
+        if (shift != 0) {                    // (the same in all of the block)
+            __syncthreads();                 // every thread has read the first sum
+            place = Place(mean, squares(shift), (float)a.by_cols, a.eps, shift);
         }
-        sq = long_sum(sq, sqs[set]);
-        const float rstd = reciprocal_root(sq, (float)a.by_cols, a.eps);
         if (threadIdx.x == 0) {
-            if (a.mean) a.mean[r] = m.hi;
-            if (a.rstd) a.rstd[r] = rstd;
+            if (a.mean) a.mean[r] = (float)mean;
+            if (a.rstd) a.rstd[r] = place.rstd();
         }
         T *const y = static_cast<T *>(a.y) + r * a.y_stride;
         for (uint32_t at = threadIdx.x * N; at < a.cols; at += kLongBlock * N) {
@@ -363,7 +443,7 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_long_kernel(LayerNorm
             u32x4 w{}, b{};
             if (weight) w = p.template load<false>(weight);
             if (bias) b = p.template load<false>(bias);
-            p.store(y, normed<T>(again(p), m, rstd, affine<T>(weight, w, 1.0f), affine<T>(bias, b, 0.0f)));
+            p.store(y, normed<T>(again(p), place, affine<T>(weight, w, 1.0f), affine<T>(bias, b, 0.0f)));
         }
     }
 }
