@@ -461,6 +461,28 @@ constexpr uint32_t kParts = 256;
 // Floats of one part's sums of dweight (those of dbias follow): whole vectors.
 __host__ __device__ constexpr uint64_t sums_pitch(uint64_t cols) { return (cols + 7) & ~(uint64_t)7; }
 
+// A row's differences from its mean in the gradient: times a power of two that
+// keeps them, and their products with a gradient, inside binary32, and is 1 for
+// standard deviations between 2^-50 and 2^50.  (Numbers that close to one above
+// 1 are equal to it.)
+struct Differences {
+    float scale, at, rstd;      // at: the mean times scale; rstd by scale
+    __device__ Differences(float mean, float root)
+        : scale(root < 0x1p-50f                                    ? 0x1p-80f
+                : root > 0x1p50f && __builtin_fabsf(mean) <= 1.0f ? 0x1p80f
+                                                                   : 1.0f),
+          at(mean * scale), rstd(root * (scale < 1.0f ? 0x1p80f : scale > 1.0f ? 0x1p-80f : 1.0f))
+    {
+    }
+    template <class Wide>
+    __device__ Wide of(Wide x) const
+    {
+#pragma unroll
+        for (uint32_t j = 0; j < sizeof(x) / sizeof(float); ++j) x[j] = __builtin_fmaf(x[j], scale, -at);
+        return x;
+    }
+};
+
 // A piece's sums over rows to a row of floats (elements that two pieces hold
 // have the same sums in both).
 template <typename T, RowFit Fit>
@@ -543,7 +565,8 @@ __device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
         const bool live = r0 + group < a.rows;
         const uint64_t r = live ? r0 + group : r0;
         if constexpr (!kAhead) fetch_row(r0);
-        const float rs = rstd, mu = mean;
+        const float rs = rstd;
+        const Differences diff(mean, rstd);
         u32x4 dyv[V], xv[V], dtv[kAhead ? V : 1];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -555,15 +578,15 @@ __device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
             if (r0 + step < a.rows) fetch_row(r0 + step);
             __builtin_amdgcn_sched_barrier(0);       // the loads stay ahead of the sums
         }
-        // with h = (x - mean) * rstd: rstd comes in once a row
+        // with h = off * diff.rstd: that comes in once a row
         float first = 0.0f, second = 0.0f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             // (past a tiny row and in dead pieces dy is 0)
-            const Wide d = Vec<T>::widen(dyv[k]), off = Vec<T>::widen(xv[k]) - mu;
+            const Wide d = Vec<T>::widen(dyv[k]), off = diff.of(Vec<T>::widen(xv[k]));
             Wide g = d * factor(k);
             if (live) {
-                dw[k] += (d * rs) * off;
+                dw[k] += (d * diff.rstd) * off;
                 db[k] += d;
             }
             if constexpr (Fit == kPart)        // without what is another piece's too
@@ -590,14 +613,14 @@ __device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
             second = sum_of_waves<Waves>(at < Waves ? shared.seconds[set][of] : 0.0f);
         }
         first *= by;
-        second = second * rs * (rs * by);
+        second = second * diff.rstd * (diff.rstd * by);
         if (!live) continue;
         T *const dx = static_cast<T *>(a.dx) + r * a.dx_stride;
         u32x4 part{};              // what is the partial vector's own, stored last
         uint32_t part_skip = 0;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const Wide off = Vec<T>::widen(xv[k]) - mu;
+            const Wide off = diff.of(Vec<T>::widen(xv[k]));
             Wide g = Vec<T>::widen(dyv[k]) * factor(k) - first, dt(0.0f);
             if (a.dtotal) {
                 if constexpr (kAhead) dt = Vec<T>::widen(dtv[k]);
@@ -720,7 +743,8 @@ __global__ void __launch_bounds__(kColsBlock) ew_layernorm_cols_kernel(LayerNorm
     for (uint64_t r = blockIdx.y; r < a.rows; r += parts) {
         const Wide d = Vec<T>::widen(p.template load<true>(static_cast<const T *>(a.dy) + r * a.dy_stride));
         const Wide x = Vec<T>::widen(p.template load<true>(static_cast<const T *>(a.x) + r * a.x_stride));
-        dw += d * ((x - a.mean[r]) * a.rstd[r]);
+        const Differences diff(a.mean[r], a.rstd[r]);
+        dw += d * (diff.of(x) * diff.rstd);
         db += d;
     }
     float *const part = static_cast<float *>(a.workspace) + blockIdx.y * (2 * sums_pitch(a.cols));
@@ -742,12 +766,15 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_dx_kernel(LayerNormGr
         const T *const dt =
             a.dtotal ? static_cast<const T *>(a.dtotal) + r * a.dtotal_stride : nullptr;
         T *const dx = static_cast<T *>(a.dx) + r * a.dx_stride;
-        const float mu = a.mean[r], rs = a.rstd[r];
+        const float rs = a.rstd[r];
+        const Differences diff(a.mean[r], rs);
         const auto slope = [&](const LongPiece<T> &p) {
             const Wide d = Vec<T>::widen(p.template load<false>(dy));
             return weight ? d * Vec<T>::widen(p.template load<false>(weight)) : d;
         };
-        const auto place = [&](const LongPiece<T> &p) { return (Vec<T>::widen(p.template load<false>(x)) - mu) * rs; };
+        const auto place = [&](const LongPiece<T> &p) {
+            return diff.of(Vec<T>::widen(p.template load<false>(x))) * diff.rstd;
+        };
         float first = 0.0f, second = 0.0f;
         for (uint32_t at = threadIdx.x * N; at < a.cols; at += kLongBlock * N) {
             const LongPiece<T> p(at, a.cols);
