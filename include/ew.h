@@ -640,9 +640,11 @@ ew_status_t ew_layernorm_bf16(const uint16_t *x, size_t x_stride, const uint16_t
  *   dx = round(rstd * (g - sum(g) / n - h * sum(g * h) / n) + dtotal)
  * (the gradient of the forward call's x and of its residual alike), and
  *   dweight[c] = sum over rows of dy * h, dbias[c] = sum over rows of dy,
- * in binary32, each optional.  dx may be exactly dy, x or dtotal.  The
- * workspace is needed for dweight and dbias only (without both it may be
- * NULL). */
+ * in binary32, each optional.  mean is taken as given, rounded to binary32; of
+ * rows whose mean is more than 2^12 standard deviations (1 / rstd) from 0, where
+ * that rounding is up to 2^-12 of one and more, h is about the row's own mean,
+ * sum(x) / n.  dx may be exactly dy, x or dtotal.  The workspace is needed for
+ * dweight and dbias only (without both it may be NULL). */
 size_t ew_layernorm_grad_workspace(size_t rows, size_t cols);
 ew_status_t ew_layernorm_grad_f32(const float *dy, size_t dy_stride, const float *x,
                                   size_t x_stride, const float *weight, const float *mean,

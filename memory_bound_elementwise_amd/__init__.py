@@ -1068,8 +1068,9 @@ def ew_layernorm_grad_f32(dy, x, weight, mean, rstd, dx, dweight=None, dbias=Non
     """Gradient of the layer norm: x is the normed matrix (the forward call's
     total); with h = (x - mean) * rstd and g = dy * weight,
     dx = rstd * (g - mean(g) - h * mean(g * h)) + dtotal, dweight and dbias
-    are the sums over rows of dy * h and of dy (binary32).  weight may be None
-    (1); dx may be dy, x or dtotal."""
+    are the sums over rows of dy * h and of dy (binary32).  Of a row more than
+    2^12 standard deviations from 0, h is about the mean of x, not the rounded
+    one.  weight may be None (1); dx may be dy, x or dtotal."""
     _layernorm_grad("ew_layernorm_grad_f32", 4, dy, x, weight, mean, rstd, dx, dweight, dbias,
                     workspace, dtotal, rows, cols, stream)
 

@@ -483,6 +483,14 @@ struct Differences {
     }
 };
 
+// Whether what the given mean's rounding lost (half of a last place, 2^-24 of it)
+// is more than 2^-12 of a deviation: such rows' mean difference, 0 but for that,
+// is found from the row again.
+__device__ __forceinline__ bool far_from_zero(float mean, float rstd)
+{
+    return __builtin_fabsf(mean) * rstd > 0x1p12f;
+}
+
 // A piece's sums over rows to a row of floats (elements that two pieces hold
 // have the same sums in both).
 template <typename T, RowFit Fit>
@@ -507,7 +515,7 @@ __device__ __forceinline__ void store_sums(float *row, uint32_t cols, const Piec
 template <typename T, int Waves, int V, int Groups>
 struct GradShared {
     // two sets, used in turn: a wave is at most one barrier ahead of another
-    float firsts[2][Waves * Groups], seconds[2][Waves * Groups];
+    float firsts[2][Waves * Groups], seconds[2][Waves * Groups], thirds[2][Waves * Groups];
     float joined[Groups > 1 ? Waves * 64 * V * Vec<T>::N : 1];
 };
 
@@ -565,8 +573,7 @@ __device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
         const bool live = r0 + group < a.rows;
         const uint64_t r = live ? r0 + group : r0;
         if constexpr (!kAhead) fetch_row(r0);
-        const float rs = rstd;
-        const Differences diff(mean, rstd);
+        const float rs = rstd, mu = mean;
         u32x4 dyv[V], xv[V], dtv[kAhead ? V : 1];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -578,8 +585,10 @@ __device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
             if (r0 + step < a.rows) fetch_row(r0 + step);
             __builtin_amdgcn_sched_barrier(0);       // the loads stay ahead of the sums
         }
-        // with h = off * diff.rstd: that comes in once a row
-        float first = 0.0f, second = 0.0f;
+        // with h = (off - low) * diff.rstd: low and that come in once a row
+        const Differences diff(mu, rs);
+        float first = 0.0f, second = 0.0f, third = 0.0f;
+        const bool far = far_from_zero(mu, rs);          // the same in all of the row
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             // (past a tiny row and in dead pieces dy is 0)
@@ -597,20 +606,43 @@ __device__ __forceinline__ void layernorm_grad_rows(const LayerNormGradArgs &a,
                 second = __builtin_fmaf(g[j], off[j], second);
             }
         }
+        const uint32_t wave = group * Waves + i / 64;
+        if (far) {
+            uint32_t n = cols;
+            asm("" : "+s"(n));             // (nothing is kept from above for this rare path)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const Wide off = diff.of(Vec<T>::widen(xv[k]));
+                const Piece<T, Fit> p((i + k * kThreads) * N, n);
+#pragma unroll
+                for (uint32_t j = 0; j < N; ++j) third += p.live && p.own(j, n) ? off[j] : 0.0f;
+            }
+            third = wave_reduce<Sum>(third);
+            if (Waves > 1 && threadIdx.x % 64 == 0) shared.thirds[set][wave] = third;
+        }
         // dx may be an input: nothing is stored before every wave of the row
         // has loaded
         first = wave_reduce<Sum>(first);
         second = wave_reduce<Sum>(second);
+        const uint32_t at = threadIdx.x % lanes_of_waves(Waves), of = group * Waves + (at < Waves ? at : 0);
         if constexpr (Waves > 1) {
-            const uint32_t wave = group * Waves + i / 64, at = threadIdx.x % lanes_of_waves(Waves);
             if (threadIdx.x % 64 == 0) {
                 shared.firsts[set][wave] = first;
                 shared.seconds[set][wave] = second;
             }
             __syncthreads();
-            const uint32_t of = group * Waves + (at < Waves ? at : 0);
             first = sum_of_waves<Waves>(at < Waves ? shared.firsts[set][of] : 0.0f);
             second = sum_of_waves<Waves>(at < Waves ? shared.seconds[set][of] : 0.0f);
+        }
+        if (far) {
+            if constexpr (Waves > 1) third = sum_of_waves<Waves>(at < Waves ? shared.thirds[set][of] : 0.0f);
+            const float low = third * by;
+            second -= low * first;
+            // (so that dx takes off as it is)
+            first -= low * (second * diff.rstd) * diff.rstd;
+            if (live)
+#pragma unroll
+                for (int k = 0; k < V; ++k) dw[k] -= (Vec<T>::widen(dyv[k]) * diff.rstd) * low;
         }
         first *= by;
         second = second * diff.rstd * (diff.rstd * by);
@@ -722,18 +754,53 @@ __global__ void __launch_bounds__(kSumCols * kSumParts) ew_layernorm_sums_kernel
 }
 
 // ---------------------------------------------------------------------------
-// Gradient, longer rows: the parts' sums of dweight and dbias (a thread a
-// vector of columns over a part of the rows), their sum, then dx (a block a
-// row, two passes over it).  dx comes last: it may be dy or x.  1820 x 18432 with
+// Gradient, longer rows: what the rounded means lost, the parts' sums of dweight
+// and dbias (a thread a vector of columns over a part of the rows), their sum,
+// then dx (a block a row, two passes over it).  dx comes last: it may be dy or x.  1820 x 18432 with
 // dtotal 191 us of f32 and 112 of bf16, 1000 x 40000 bf16 141: dy and x are read
 // three times, the second pass over a row from the caches.
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kColsBlock = 256;
 
+// The mean difference of row r of a block of Waves waves, where the row is far
+// from 0, else 0.
+template <typename T, int Waves>
+__device__ __forceinline__ float lost_mean(const LayerNormGradArgs &a, uint64_t r, const Differences &diff,
+                                           float *scratch)
+{
+    if (!far_from_zero(a.mean[r], a.rstd[r])) return 0.0f;
+    __syncthreads();               // scratch may be read for another row yet
+    const T *const x = static_cast<const T *>(a.x) + r * a.x_stride;
+    float sum = 0.0f;
+    for (uint64_t at = threadIdx.x * Vec<T>::N; at < a.cols; at += Waves * 64 * Vec<T>::N) {
+        const LongPiece<T> p((uint32_t)at, a.cols);
+        const typename Vec<T>::wide off = diff.of(Vec<T>::widen(p.template load<false>(x)));
+#pragma unroll
+        for (uint32_t j = 0; j < Vec<T>::N; ++j) sum += j >= p.p.skip ? off[j] : 0.0f;
+    }
+    if constexpr (Waves == kLongWaves) return long_sum(sum, scratch) / (float)a.cols;
+    else return block_reduce<Sum, Waves>(sum, scratch) / (float)a.cols;
+}
+
+// Rows of cols > kLongCols, in every type, take these kernels; lost: a value a
+// row behind the parts' sums.
+constexpr uint32_t kLongCols = 16384;
+constexpr int kLostWaves = 4;      // few: most rows are not far from 0
+
+template <typename T>
+__global__ void __launch_bounds__(kLostWaves * 64) ew_layernorm_lost_kernel(LayerNormGradArgs a, float *lost)
+{
+    __shared__ float scratch[kLostWaves];
+    for (uint64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const float low = lost_mean<T, kLostWaves>(a, r, Differences(a.mean[r], a.rstd[r]), scratch);
+        if (threadIdx.x == 0) lost[r] = low;
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kColsBlock) ew_layernorm_cols_kernel(LayerNormGradArgs a,
-                                                                      uint32_t parts)
+                                                                      uint32_t parts, const float *lost)
 {
     using Wide = typename Vec<T>::wide;
     const uint32_t at = (blockIdx.x * kColsBlock + threadIdx.x) * Vec<T>::N;
@@ -744,7 +811,7 @@ __global__ void __launch_bounds__(kColsBlock) ew_layernorm_cols_kernel(LayerNorm
         const Wide d = Vec<T>::widen(p.template load<true>(static_cast<const T *>(a.dy) + r * a.dy_stride));
         const Wide x = Vec<T>::widen(p.template load<true>(static_cast<const T *>(a.x) + r * a.x_stride));
         const Differences diff(a.mean[r], a.rstd[r]);
-        dw += d * (diff.of(x) * diff.rstd);
+        dw += d * ((diff.of(x) - lost[r]) * diff.rstd);
         db += d;
     }
     float *const part = static_cast<float *>(a.workspace) + blockIdx.y * (2 * sums_pitch(a.cols));
@@ -757,7 +824,7 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_dx_kernel(LayerNormGr
 {
     constexpr uint32_t N = Vec<T>::N;
     using Wide = typename Vec<T>::wide;
-    __shared__ float firsts[2][kLongWaves], seconds[2][kLongWaves];
+    __shared__ float firsts[2][kLongWaves], seconds[2][kLongWaves], thirds[kLongWaves];
     const T *const weight = static_cast<const T *>(a.weight);
     int set = 0;
     for (uint64_t r = blockIdx.x; r < a.rows; r += gridDim.x, set ^= 1) {
@@ -772,8 +839,9 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_dx_kernel(LayerNormGr
             const Wide d = Vec<T>::widen(p.template load<false>(dy));
             return weight ? d * Vec<T>::widen(p.template load<false>(weight)) : d;
         };
+        const float low = lost_mean<T, kLongWaves>(a, r, diff, thirds);
         const auto place = [&](const LongPiece<T> &p) {
-            return diff.of(Vec<T>::widen(p.template load<false>(x))) * diff.rstd;
+            return (diff.of(Vec<T>::widen(p.template load<false>(x))) - low) * diff.rstd;
         };
         float first = 0.0f, second = 0.0f;
         for (uint32_t at = threadIdx.x * N; at < a.cols; at += kLongBlock * N) {
@@ -902,7 +970,8 @@ hipError_t launch_layernorm(RowType t, const LayerNormArgs &a, hipStream_t s, co
 
 size_t layernorm_grad_workspace(uint64_t rows, uint64_t cols)
 {
-    return (rows < kParts ? rows : kParts) * 2 * sums_pitch(cols) * sizeof(float);
+    const uint64_t sums = (rows < kParts ? rows : kParts) * 2 * sums_pitch(cols);
+    return (sums + (cols > kLongCols ? sums_pitch(rows) : 0)) * sizeof(float);
 }
 
 // Up to kOneShort rounds of short rows (of kShort vectors), kOneLong of others,
@@ -965,7 +1034,7 @@ static hipError_t layernorm_grad_by(const LayerNormGradArgs &a, uint32_t vectors
 #undef EW_LAYERNORM_GRAD_LAUNCH
     return hipErrorInvalidValue;
 }
-static uint32_t grad_vectors(RowType t) { return 16 * 64 * (t == kRowF32 ? 4 : 2); }
+static_assert(16 * 64 * 4 * 4 == kLongCols && 16 * 64 * 2 * 8 == kLongCols);
 
 hipError_t launch_layernorm_grad(RowType t, const LayerNormGradArgs &a, hipStream_t s, const char **path)
 {
@@ -978,7 +1047,7 @@ hipError_t launch_layernorm_grad(RowType t, const LayerNormGradArgs &a, hipStrea
     if (a.rows == 0) return sum(0);
     const uint32_t vectors = vectors_of(t, a.cols);
     uint32_t parts = 0;
-    if (vectors <= grad_vectors(t)) {
+    if (a.cols <= kLongCols) {
         *path = "rows in registers";
         const hipError_t e = t == kRowF32   ? layernorm_grad_by<float>(a, vectors, s, &parts)
                              : t == kRowF16 ? layernorm_grad_by<_Float16>(a, vectors, s, &parts)
@@ -988,8 +1057,13 @@ hipError_t launch_layernorm_grad(RowType t, const LayerNormGradArgs &a, hipStrea
     *path = "two passes, dweight and dbias by columns";
     if (sums) {
         parts = a.rows < kParts ? a.rows : kParts;
-        hipError_t e = start(EW_KERNEL_OF(t, ew_layernorm_cols_kernel),
-                             dim3((vectors + kColsBlock - 1) / kColsBlock, parts), kColsBlock, 0, s, a, parts);
+        float *const lost = static_cast<float *>(a.workspace) + parts * 2 * sums_pitch(a.cols);
+        hipError_t e = start(EW_KERNEL_OF(t, ew_layernorm_lost_kernel), dim3(row_blocks(a.rows)),
+                             kLostWaves * 64, 0, s, a, lost);
+        if (e == hipSuccess)
+            e = start(EW_KERNEL_OF(t, ew_layernorm_cols_kernel),
+                      dim3((vectors + kColsBlock - 1) / kColsBlock, parts), kColsBlock, 0, s, a, parts,
+                      (const float *)lost);
         if (e == hipSuccess) e = sum(parts);
         if (e != hipSuccess) return e;
     }
