@@ -36,7 +36,7 @@ struct Growth {
 
 // What a token adds.
 struct Token {
-    float x;           // logp - old_logp
+    double x;          // logp - old_logp, exact
     float ratio;       // exp(x)
     bool clipped;      // the gain is that of the border
     float one, line;   // of d = ref_logp - logp: exp(d) - 1, exp(d) - 1 - d
@@ -46,10 +46,9 @@ template <bool Ref>
 __device__ __forceinline__ Token token(const PolicyTokens &in, float logp, float old, float ref, float a)
 {
     Token t;
-    const double x = (double)logp - (double)old;        // exact
-    t.clipped = (a > 0.0f && x > in.above) || (a < 0.0f && x < in.below);
-    t.x = (float)x;
-    t.ratio = exp_nat(t.x);
+    t.x = (double)logp - (double)old;
+    t.clipped = (a > 0.0f && t.x > in.above) || (a < 0.0f && t.x < in.below);
+    t.ratio = exp_nat((float)t.x);
     t.one = 0.0f;
     t.line = 0.0f;
     if constexpr (Ref) {
@@ -257,12 +256,12 @@ struct LaneSums {
     }
 };
 
-// Four tokens: policy and kl of their sequence's sums, the rest of all.
+// Four tokens: policy and kl of their sequence's sums, the rest of all.  Each
+// term is binary32, but the log ratio, which is exact, and every sum binary64.
 template <bool Ref>
 __device__ __forceinline__ void add_four(const PolicyTokens &in, const Four &f, double &row_policy,
                                          double &row_kl, LaneSums &s)
 {
-    float policy = 0.0f, kl = 0.0f, fall = 0.0f;
     uint32_t clipped = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -270,14 +269,11 @@ __device__ __forceinline__ void add_four(const PolicyTokens &in, const Four &f, 
         const bool counted = f.counts(j);
         const float bound = f.a[j] > 0.0f ? in.most : in.least;
         const float loss = -f.a[j] * (t.clipped ? bound : t.ratio);
-        policy += counted ? loss : 0.0f;
-        if constexpr (Ref) kl += counted ? t.line : 0.0f;
-        fall -= counted ? t.x : 0.0f;
+        row_policy += (double)(counted ? loss : 0.0f);
+        if constexpr (Ref) row_kl += (double)(counted ? t.line : 0.0f);
+        s.fall -= counted ? t.x : 0.0;
         clipped += counted && t.clipped;
     }
-    row_policy += (double)policy;
-    if constexpr (Ref) row_kl += (double)kl;
-    s.fall += (double)fall;
     s.clipped += clipped;
     s.tokens += f.number();
 }
