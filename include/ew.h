@@ -684,9 +684,11 @@ typedef enum ew_mean {
  * number of sequences that have any), or scale),
  *   loss = sum w * (kl * k - gain).
  * Which side of a border r lies on is decided exactly (x against the border's
- * logarithm, in binary64); sums are binary64.  A batch or sequence whose mask
- * leaves nothing adds nothing, whatever lies in its masked places: its weights
- * are 0, and a loss of no tokens is 0.
+ * logarithm, in binary64); r, k and each gain are binary32, r and exp(d) off by
+ * about |x| and |d| times 2^-24 of themselves; sums are binary64.  Where r is past
+ * binary32 (x above 88.7) it is infinite, but a token of advantage 0 adds 0.  A
+ * batch or sequence whose mask leaves nothing adds nothing, whatever lies in its
+ * masked places: its weights are 0, and a loss of no tokens is 0.
  * ref_logp    optional; kl weighs its term, which is left out where kl is 0
  * advantage   a matrix, or with advantage_stride 0 one value a sequence
  * mask        optional, rows x cols bytes with a stride of its own: tokens

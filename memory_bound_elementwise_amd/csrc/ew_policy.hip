@@ -37,7 +37,7 @@ struct Growth {
 // What a token adds.
 struct Token {
     double x;          // logp - old_logp, exact
-    float ratio;       // exp(x)
+    float ratio;       // exp(x), finite for an advantage of 0
     bool clipped;      // the gain is that of the border
     float one, line;   // of d = ref_logp - logp: exp(d) - 1, exp(d) - 1 - d
 };
@@ -49,6 +49,9 @@ __device__ __forceinline__ Token token(const PolicyTokens &in, float logp, float
     t.x = (double)logp - (double)old;
     t.clipped = (a > 0.0f && t.x > in.above) || (a < 0.0f && t.x < in.below);
     t.ratio = exp_nat((float)t.x);
+    // a token of no advantage gains nothing, also where binary32 does not hold the
+    // ratio (a NaN stays)
+    if (a == 0.0f && t.ratio == kInf) t.ratio = 1.0f;
     t.one = 0.0f;
     t.line = 0.0f;
     if constexpr (Ref) {
