@@ -2,6 +2,7 @@
 // for CDNA4 (gfx950).
 
 #include "ew.h"
+#include "ew_policy_marks.h"
 #include "ew_rows_vec.h"
 
 namespace ew {
@@ -120,9 +121,8 @@ struct Four {
                          uint32_t lane, uint32_t mark)
     {
         const auto p = t.place(lane);
-        counted = (((mark & 0x7f7f7f7fu) + 0x7f7f7f7fu) | mark) & 0x80808080u;   // bytes not 0
+        counted = counted_tokens(mark, Fit == kPart ? p.skip : 0);
         if constexpr (Fit == kTiny) counted &= (1u << 8 * t.cols) - 1;
-        if constexpr (Fit == kPart) counted = counted >> 8 * p.skip << 8 * p.skip;
         if (!counted) return;
         const auto take = [&](const float *v) {
             return __builtin_bit_cast(f32x4, load_piece<float, true>(t.row(v), t.cols, p));
