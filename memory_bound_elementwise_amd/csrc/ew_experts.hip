@@ -157,80 +157,71 @@ __global__ void __launch_bounds__(1024) ew_experts_sort_kernel(ExpertsSortArgs a
     const uint32_t experts = a.cols, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     const WaveEntries own(a, split);
     uint32_t *const mine = counters + wave * experts;
-    // (a tile of the blocks' counts is on its way while the entries are counted)
-    const uint32_t tile = experts < blockDim.x ? 1u << split.bits : blockDim.x;
-    const auto add_totals = [&](uint32_t e0, uint32_t &before, uint32_t &all) {
-        // threads of the same expert share the blocks
-        const uint32_t e = e0 + threadIdx.x % tile, part = threadIdx.x / tile;
-        const uint32_t parts = blockDim.x / tile;
-        before = all = 0;
-        if (e < experts) {
+    // a thread an expert (the host gives a block at least as many)
+    const uint32_t e = threadIdx.x, tile = 1u << split.bits;
+    // (the blocks' counts are on their way while the entries are counted; threads
+    // of the same expert share the blocks)
+    uint32_t before = 0, all = 0;
+    if constexpr (!One) {
+        const uint32_t of = threadIdx.x % tile, part = threadIdx.x / tile, parts = blockDim.x / tile;
+        if (of < experts) {
 #pragma unroll 8
             for (uint32_t b = part; b < gridDim.x; b += parts) {
-                const uint32_t n = totals[b * experts + e];
+                const uint32_t n = totals[b * experts + of];
                 all += n;
                 before += b < blockIdx.x ? n : 0;
             }
         }
-    };
-    uint32_t mine_before = 0, mine_all = 0;
-    if constexpr (!One) add_totals(0, mine_before, mine_all);
+    }
     Entry held[kHeld];
     count_entries<Held>(a, split, own, held, counters);
-    // the experts' rows, a tile of them at a time
-    uint32_t start = 0;
-    for (uint32_t e0 = 0; e0 < experts; e0 += tile) {
-        uint32_t before = 0, all = 0;
-        if constexpr (!One) {
-            uint32_t *const sums = counters + split.waves * experts;
-            if (e0) add_totals(e0, mine_before, mine_all);
-            // within a wave by lane exchanges, then the waves
-            for (uint32_t d = tile; d < 64; d *= 2) {
-                mine_before += (uint32_t)__shfl_xor((int)mine_before, (int)d);
-                mine_all += (uint32_t)__shfl_xor((int)mine_all, (int)d);
-            }
-            sums[threadIdx.x] = mine_before;
-            sums[blockDim.x + threadIdx.x] = mine_all;
-            __syncthreads();
-            if (threadIdx.x < tile)
-#pragma unroll 8
-                for (uint32_t q = threadIdx.x; q < blockDim.x; q += tile < 64 ? 64 : tile) {
-                    before += sums[q];
-                    all += sums[blockDim.x + q];
-                }
+    if constexpr (!One) {
+        uint32_t *const sums = counters + split.waves * experts;
+        // within a wave by lane exchanges, then the waves
+        for (uint32_t d = tile; d < 64; d *= 2) {
+            before += (uint32_t)__shfl_xor((int)before, (int)d);
+            all += (uint32_t)__shfl_xor((int)all, (int)d);
         }
-        const uint32_t e = e0 + threadIdx.x;
-        const bool live = threadIdx.x < tile && e < experts;
-        uint32_t counted[16];            // by the block's waves, read together
-#pragma unroll
-        for (uint32_t w = 0; w < 16; ++w)
-            counted[w] = live && w < split.waves ? counters[w * experts + e] : 0;
-        if constexpr (One)
-#pragma unroll
-            for (uint32_t w = 0; w < 16; ++w) all += counted[w];
-        const uint32_t room = live ? (all + a.align - 1) / a.align * a.align : 0;
-        uint32_t tile_room;
-        const uint32_t after = start + block_scan(room, scratch, tile_room);
-        start += tile_room;
-        if (live) {
-            const uint32_t first = after - room;
-            uint32_t next = first + before;
-#pragma unroll
-            for (uint32_t w = 0; w < 16; ++w) {
-                if (w < split.waves) counters[w * experts + e] = next;
-                next += counted[w];
-            }
-            if (blockIdx.x == 0) {
-                a.offsets[e] = (int32_t)first;
-                if (e + 1 == experts) a.offsets[experts] = (int32_t)after;
-                if (a.counts) a.counts[e] = (int32_t)all;
-            }
-            // rows without an entry; the blocks share the experts
-            if (a.source && e % gridDim.x == blockIdx.x)
-                for (uint32_t r = first + all; r < after; ++r) a.source[r] = -1;
-        }
+        sums[threadIdx.x] = before;
+        sums[blockDim.x + threadIdx.x] = all;
         __syncthreads();
+        before = all = 0;
+        if (threadIdx.x < tile)
+#pragma unroll 8
+            for (uint32_t q = threadIdx.x; q < blockDim.x; q += tile < 64 ? 64 : tile) {
+                before += sums[q];
+                all += sums[blockDim.x + q];
+            }
     }
+    const bool expert = e < experts;
+    uint32_t counted[16];                // by the block's waves, read together
+#pragma unroll
+    for (uint32_t w = 0; w < 16; ++w)
+        counted[w] = expert && w < split.waves ? counters[w * experts + e] : 0;
+    if constexpr (One)
+#pragma unroll
+        for (uint32_t w = 0; w < 16; ++w) all += counted[w];
+    const uint32_t room = expert ? (all + a.align - 1) / a.align * a.align : 0;
+    uint32_t rooms;                      // of all experts
+    const uint32_t after = block_scan(room, scratch, rooms);
+    if (expert) {
+        const uint32_t first = after - room;
+        uint32_t next = first + before;
+#pragma unroll
+        for (uint32_t w = 0; w < 16; ++w) {
+            if (w < split.waves) counters[w * experts + e] = next;
+            next += counted[w];
+        }
+        if (blockIdx.x == 0) {
+            a.offsets[e] = (int32_t)first;
+            if (e + 1 == experts) a.offsets[experts] = (int32_t)after;
+            if (a.counts) a.counts[e] = (int32_t)all;
+        }
+        // rows without an entry; the blocks share the experts
+        if (a.source && e % gridDim.x == blockIdx.x)
+            for (uint32_t r = first + all; r < after; ++r) a.source[r] = -1;
+    }
+    __syncthreads();
     const auto put = [&](uint64_t i, const Entry &entry, uint32_t row) {
         if (i >= own.end) return;
         const bool live = entry.expert < experts;
@@ -251,7 +242,7 @@ __global__ void __launch_bounds__(1024) ew_experts_sort_kernel(ExpertsSortArgs a
         }
     }
     if (a.source)
-        for (uint64_t r = start + (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.source_rows;
+        for (uint64_t r = rooms + (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.source_rows;
              r += (uint64_t)gridDim.x * blockDim.x)
             a.source[r] = -1;
 }
@@ -274,9 +265,9 @@ __global__ void __launch_bounds__(1024) ew_experts_count_kernel(ExpertsSortArgs 
 }
 
 // ---------------------------------------------------------------------------
-// Movement of rows, bound by memory.  8192 tokens of 4096 bf16 to 8 experts each:
-// gathered in 97 us, 6.2 TB/s, combined in 110 us, 6.1 TB/s; the gradient for
-// 4096 tokens 103.6 us, 5.5 TB/s.  A token at a time: its row is read once (an
+// Movement of rows, bound by memory.  8192 tokens of 4096 bf16 to 8 experts each,
+// one in sixteen dropped: gathered in 97 us, 6.0 TB/s of the rows moved, combined
+// in 110 us, 5.8 TB/s; the gradient for 4096 tokens 103.6 us, 5.3 TB/s.  A token at a time: its row is read once (an
 // expert's row at a time, which reads a token's row for each choice, took
 // 137-151 us, 98-101 this way).  Waves waves share a token (a wave each for short rows, the
 // block for long ones) and go along its columns a stretch at a time, 16 bytes a
