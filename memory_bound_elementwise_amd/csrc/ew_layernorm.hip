@@ -979,15 +979,20 @@ size_t layernorm_grad_workspace(uint64_t rows, uint64_t cols)
 // launch, 3 us of the host's.  us, in a graph, one block and a block a round:
 // bf16 3 x 4096 4.6, 5.6; 32 x 512 6.4, 6.5; 16 x 2048 8.9, 7.1; f32 16 x 1000
 // 6.9, 6.0; of longer rows 4 x 12288 bf16 10.1, 8.6; 4 x 16384 16.0, 9.9.
-// Long rows, a block each, go two to a part where that still fills half of the
-// chip: each part's sums are as many bytes as a row and its gradient (250 x
-// 4096 bf16 9.1 us, 10.9 with a row a part; 300 x 8192 f32 15.2, 17.6; but 130 x
-// 16384 bf16 20.7, 18.8).
+// Long rows, a block each, go two to a part where that still is 81 blocks or
+// more: each part's sums are as many bytes as a row and its gradient.  Two rows a
+// part and one: 200 and 250 x 4096 bf16 9.0, 10.0 and 9.2, 10.4; 250 x 8192 12.7,
+// 15.2; 250 x 16384 25.0, 27.6; 250 x 8192 f32 13.9, 15.6; but 161 x 16384 bf16
+// 22.3, 21.4 and f32 26.1, 23.3, where the blocks are few for so many bytes.
+// Without sums there is nothing of that to save: a block a round up to one a CU
+// (4 x 4096 bf16 2.9 us, 5.3 in one block; 32 x 512 2.7, 5.0; 170 x 16384 8.8,
+// 13.5 with two rows a block; 8192 x 4096 44.3, 47 with 512 blocks, 52 with all).
 constexpr uint64_t kOneShort = 4, kOneLong = 2, kTwoRowsFrom = 160, kTwoRowsTo = 384;
 constexpr uint32_t kShort = 512;
 
-static uint32_t parts_for(uint64_t blocks, int groups, uint32_t vectors)
+static uint32_t parts_for(uint64_t blocks, int groups, uint32_t vectors, bool sums)
 {
+    if (!sums) return (uint32_t)(blocks < kParts ? blocks : kParts);
     if (blocks <= (vectors <= kShort ? kOneShort : kOneLong)) return 1;
     if (groups == 1 && blocks > kTwoRowsFrom && blocks <= kTwoRowsTo) return (uint32_t)((blocks + 1) / 2);
     return (uint32_t)(blocks < kParts ? blocks : kParts);
@@ -1000,7 +1005,7 @@ static hipError_t layernorm_grad_by(const LayerNormGradArgs &a, uint32_t vectors
 #define EW_LAYERNORM_GRAD_LAUNCH(W, V, G, TINY)                                                   \
     {                                                                                             \
         const uint64_t blocks = ((uint64_t)a.rows + G - 1) / G;                                   \
-        *parts = parts_for(blocks, G, vectors);                                                   \
+        *parts = parts_for(blocks, G, vectors, a.dweight || a.dbias);                                                   \
         return start(reinterpret_cast<const void *>(&ew_layernorm_back_kernel<T, W, V, G, TINY>), \
                      dim3(*parts), W * 64 * G, 0, s, a);                                          \
     }
