@@ -129,7 +129,8 @@ __device__ __forceinline__ WaveSums wave_sums(const u32x4 (&h)[V], uint32_t cols
     if (shift != 0 || off_centre(w)) {
         for (bool more = true; more;) {
             more = w.up != -shift;
-            if (!more) w.near += __builtin_ldexpf(w.sum / (float)n, w.up);
+            // (without the difference by itself, which may be past binary32)
+            if (!more) w.near = __builtin_fmaf(w.sum / (float)n, __builtin_ldexpf(1.0f, w.up), w.near);
             w = about(w.near, __builtin_ldexpf(1.0f, shift), -shift);
             more = more && off_centre(w);
         }

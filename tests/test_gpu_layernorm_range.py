@@ -105,3 +105,19 @@ def test_rows_of_infinities_stay_nan(t, cols):
     for v in (y, mean, rstd):
         assert bool(torch.isnan(v[odd]).all())
     check_norm(t, x[fine], None, None, None, y[fine], None, mean[fine], rstd[fine])
+
+
+@pytest.mark.parametrize("t", ("f32", "bf16"))
+@pytest.mark.parametrize("cols", COLS[1:])
+def test_first_numbers_at_the_other_end(t, cols):
+    """A row, or a wave's part of it, whose first numbers are farther from its mean
+    than the largest binary32 number."""
+    at = torch.arange(cols, device=DEV)
+    x = torch.where(at < 8, -3e38, 3e38).expand(4, cols).clone()
+    x[1] = -x[1]
+    x[2] = torch.where(at % 512 < 8, -3.3e38, 3.3e38)
+    x[3, 8:] *= 1 - 2.0 ** -6 * (at[8:] % 5)
+    x = x.to(TYPES[t])
+    y, mean, rstd = torch.empty_like(x), f32(4), f32(4)
+    getattr(ew, "ew_layernorm_" + t)(x, None, None, y, mean=mean, rstd=rstd)
+    check_norm(t, x, None, None, None, y, None, mean, rstd)
