@@ -131,7 +131,8 @@ struct RowSplit {
 };
 
 // exp(x) through the hardware's power of two: relative error about
-// |x| * 2^-24 for the arguments of a softmax (x <= 0).
+// |x| * 2^-24, of either sign (the arguments of a softmax are x <= 0, log ratios
+// any).
 __device__ __forceinline__ float exp_nat(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 }  // namespace ew
