@@ -11,9 +11,9 @@ namespace ew {
 // expert find each other by ballots over the bits of its number, and the
 // lowest of them moves the counter on.  No atomics: an entry's place is a
 // function of the entries before it.
-// Latency: 64 entries 3.3 us, 8000 9.0 in one block; 65536 of 128 experts 11.6
+// Latency: 64 entries 3.0 us, 8000 8.6 in one block; 65536 of 128 experts 10.1
 // in two launches (blocks count; then each adds up all blocks' counts and
-// places its entries), 500000 of 256 experts 23.7.
+// places its entries), 500000 of 256 experts 22.2.
 // ---------------------------------------------------------------------------
 
 // Lanes whose key equals this lane's; keys below 2^bits, live lanes only.
@@ -562,8 +562,8 @@ __global__ void __launch_bounds__(kMoveBlock) ew_experts_combine_grad_kernel(Exp
 // One block sorts up to this many entries: what its 16 waves hold.
 constexpr uint32_t kOneSort = 16 * 64 * kHeld;
 // Blocks of a larger sorting: each adds up all the others' counts.  65536
-// entries of 128 experts take 14.0 us with 16, 11.9 with 32, 11.6 with 64 or 128;
-// 500000 of 256 experts 72.7, 42.5, 23.7, 21.9 (for twice the workspace).
+// entries of 128 experts take 12.2 us with 16, 10.3 with 32, 10.1 with 64 or 128;
+// 500000 of 256 experts 72.7, 42.2, 22.2, 20.5 (for twice the workspace).
 constexpr uint32_t kSortBlocks = 64;
 // Counters of a block's waves: 32 KB of LDS.
 constexpr uint32_t kCounters = 8192;
@@ -600,7 +600,7 @@ hipError_t launch_experts_sort(RowType, const ExpertsSortArgs &a, hipStream_t s,
     }
     *path = "counts, then places";
     // (fewer blocks where a block's entries are fewer than twice its counts:
-    // 65536 entries of 1024 experts 21.6 us with 32, 27.5 with 64)
+    // 65536 entries of 1024 experts 20.4 us with 32, 26.4 with 64)
     const uint32_t least = (a.rows + kSortBlocks - 1) / kSortBlocks;
     const uint32_t chunk = ((least > 2 * experts ? least : 2 * experts) + 1023) / 1024 * 1024;
     const uint32_t blocks = (a.rows + chunk - 1) / chunk, threads = waves_for(chunk);

@@ -220,8 +220,9 @@ __device__ __forceinline__ typename Vec<T>::wide affine(const void *p, u32x4 v, 
 // has summed differences from a number of its own (WaveSums) by then, which
 // every wave brings to the common mean in binary64 by itself.
 // Bound by memory: 8192 x 4096 bf16 with residual, total and statistics take
-// 46.0 us, 5.8 TB/s (the vector unit is busy 41 % of the cycles), 1 x 4096 2.5
-// us, the latency of one load and the join.  A block that stays and has its
+// 46.4 us, 5.8 TB/s (the vector unit is busy 44 % of the cycles), 1 x 4096 2.7
+// us, the latency of one load and the join (0.2 of it what keeps rows of any
+// numbers right: 2-8 % of short rows' time).  A block that stays and has its
 // next row's loads on their way took 51-58 us: new blocks overlap as well, and
 // their registers are free earlier.
 // ---------------------------------------------------------------------------
@@ -356,10 +357,9 @@ __global__ void __launch_bounds__(layernorm_block(Waves)) ew_layernorm_kernel(La
 
 // ---------------------------------------------------------------------------
 // Forward, longer rows: a block a row, three passes over it (sum, squares,
-// output; a second one of squares that leave binary32), of which
-// the caches serve the later ones in part: 1820 x 18432 f32
-// with a residual 142 us, 1000 x 40000 bf16 95 us (3.8 and 3.4 TB/s of what it
-// cannot do without).
+// output; squares that leave binary32 take one more), of which the caches serve
+// the later ones in part: 1820 x 18432 f32 with a residual 141 us, 1000 x 40000
+// bf16 94 us (3.8 and 3.4 TB/s of what it cannot do without).
 // ---------------------------------------------------------------------------
 
 constexpr int kLongBlock = 1024;
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(kSumCols * kSumParts) ew_layernorm_sums_kernel
 // Gradient, longer rows: what the rounded means lost, the parts' sums of dweight
 // and dbias (a thread a vector of columns over a part of the rows), their sum,
 // then dx (a block a row, two passes over it).  dx comes last: it may be dy or x.  1820 x 18432 with
-// dtotal 191 us of f32 and 112 of bf16, 1000 x 40000 bf16 141: dy and x are read
+// dtotal 196 us of f32 and 115 of bf16, 1000 x 40000 bf16 145: dy and x are read
 // three times, the second pass over a row from the caches.
 // ---------------------------------------------------------------------------
 
@@ -882,20 +882,20 @@ __global__ void __launch_bounds__(kLongBlock) ew_layernorm_dx_kernel(LayerNormGr
 // (kRowACu), few where the blocks are all there at once (kOneRound), two rows
 // at a time where they are more.  us, in a graph, waves x vectors of bf16 with a
 // residual, 2^25 elements where no rows are given:
-//   512 columns   1x1 45.9, 1x2 56.5         5120    3x4 50.9, 5x2 52.2
-//   1024          2x1 44.6, 1x2 47.0         6144    3x4 48.9, 4x4 52.7
-//   2048          4x1 45.3, 2x2 46.3         8192    4x4 50.1, 8x2 50.6, 16x1 59.1
-//   2560          3x2 48.6, 5x1 52.1         12288   12x2 53.0, 6x4 61.9
-//   4096          4x2 47.3, 2x4 48.7, 8x1 49.1   16384   16x2 52.7, 8x4 54.1
-//   1024 rows: of 2560 5x1 5.8, 3x2 6.1, 2x4 7.1; of 4096 2x4 7.1, 4x2 8.2, 8x1 8.8
-//   one row of 4096: 8x1 2.45, 4x2 2.62, 2x4 3.39
-//   f32: 1021 x 5003 without a residual 5x4 9.9, 7x3 10.4, 12x2 11.8
+//   512 columns   1x1 46.5, 1x2 60.1         5120    3x4 53.4, 5x2 53.0
+//   1024          2x1 46.7, 1x2 47.3         6144    3x4 49.4, 4x4 53.9
+//   2048          4x1 46.8, 2x2 47.1         8192    4x4 49.4, 8x2 51.1, 16x1 60.8
+//   2560          3x2 50.1, 5x1 54.4         12288   12x2 55.6, 6x4 61.1
+//   4096          4x2 48.4, 2x4 48.4, 8x1 49.3   16384   16x2 56.5, 8x4 54.9
+//   1024 rows: of 2560 5x1 5.7, 3x2 6.1, 2x4 7.7; of 4096 2x4 7.4, 4x2 7.8, 8x1 8.7
+//   one row of 4096: 8x1 2.7, 4x2 2.8, 2x4 3.8
+//   f32: 1021 x 5003 without a residual 5x4 9.5, 7x3 10.5, 12x2 12.3
 // Two rows at a time against one, without and with a residual: 10000 x 4096
-// 27.1, 34.3 and (8192) 48.9, 48.1; 20000 x 1000 18.3, 21.0 and 30.8, 30.6;
-// 3000 x 12288 34.3, 42.5 and 58.3, 58.9; of fewer blocks 2600 x 256 3.7, 3.1.
+// 32.4, 34.1 and (8192) 50.3, 47.9; 20000 x 1000 20.0, 22.9 and 31.7, 30.7;
+// 3000 x 12288 35.6, 44.0 and 58.6, 60.6; of fewer blocks 2600 x 256 4.0, 3.7.
 // With a residual a lane of 4x2 has four vectors on their way already: from two
-// rounds of blocks on it stays with one row (3000 x 4096 20.2, 20.9; 1300 10.8,
-// 10.0).
+// rounds of blocks on it stays with one row (one row, two: 3000 x 4096 20.4,
+// 21.1; 1300 10.6, 9.7).
 constexpr uint32_t kRowACu = 256, kOneRound = 1280;
 
 template <typename T>
@@ -978,8 +978,8 @@ size_t layernorm_grad_workspace(uint64_t rows, uint64_t cols)
 // Up to kOneShort rounds of short rows (of kShort vectors), kOneLong of others,
 // are one block's, which writes dweight and dbias itself and saves the second
 // launch, 3 us of the host's.  us, in a graph, one block and a block a round:
-// bf16 3 x 4096 4.6, 5.6; 32 x 512 6.4, 6.5; 16 x 2048 8.9, 7.1; f32 16 x 1000
-// 6.9, 6.0; of longer rows 4 x 12288 bf16 10.1, 8.6; 4 x 16384 16.0, 9.9.
+// bf16 3 x 4096 4.9, 5.7; 32 x 512 6.8, 6.6; 16 x 2048 8.9, 7.2; f32 16 x 1000
+// 7.7, 6.1; of longer rows 4 x 12288 bf16 10.7, 8.8; 4 x 16384 17.0, 10.7.
 // Long rows, a block each, go two to a part where that still is 81 blocks or
 // more: each part's sums are as many bytes as a row and its gradient.  Two rows a
 // part and one: 200 and 250 x 4096 bf16 9.0, 10.0 and 9.2, 10.4; 250 x 8192 12.7,

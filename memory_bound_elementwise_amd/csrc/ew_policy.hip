@@ -191,11 +191,11 @@ __device__ __forceinline__ void each_four(const PolicyTokens &in, const PolicyRo
 // ---------------------------------------------------------------------------
 // Forward: sums over parts of the batch, then their join (a second launch: a
 // last block that joins would need a counter that is 0 before the call).  Both
-// in one block for few tokens.  4096 x 4096 tokens, half of them counted: 37
-// us, of which 5 are the join's.  140 MB are read, 21 us; the rest is that
+// in one block for few tokens.  4096 x 4096 tokens, half of them counted: 37.5
+// us, of which 4.5 are the join's.  143 MB are read, 21 us; the rest is that
 // sequences end at different times, and a block's sequences after another on
-// the way (every block is on the chip at once).  8 x 512 tokens: 5.5 us,
-// latency.
+// the way (every block is on the chip at once; the vector unit is busy 49 % of
+// the cycles).  8 x 512 tokens: 5.6 us, latency.
 // ---------------------------------------------------------------------------
 
 // Sums over tokens: of -gain, of exp(d) - 1 - d (both weighed within their
@@ -466,14 +466,14 @@ __global__ void __launch_bounds__(kSmallBlock) ew_policy_join_kernel(PolicyLossA
 
 // ---------------------------------------------------------------------------
 // Gradient: `lanes` lanes a sequence (or a part of one).  Bound by memory: 4096
-// x 4096 tokens, half of them counted, 37.5-39.5 us for 207 MB read and
+// x 4096 tokens, half of them counted, 37.8-39.7 us for 210 MB read and
 // written, 5.4 TB/s.
 // ---------------------------------------------------------------------------
 
 // Threads of a block: kWideBlock for sequences of more than kWideTokens tokens
 // that are not cut into parts, else kPolicyBlock.  us, 512 and 256 threads: 4096
-// x 4096 39.5, 41.6; 1500 x 4001 18.6, 20.5; 2048 x 2500 17.5, 16.9; 2048 x 2048
-// 13.5, 12.8.
+// x 4096 39.7, 41.8; 1500 x 4001 19.0, 20.7; 2048 x 2500 17.8, 17.1; 2048 x 2048
+// 13.7, 12.9.
 constexpr uint32_t kWideBlock = 512, kWideTokens = 2560;
 
 template <bool Ref, bool Few, bool Wave>
@@ -513,19 +513,19 @@ __global__ void __launch_bounds__(kWideBlock) ew_policy_grad_kernel(PolicyGradAr
 // ---------------------------------------------------------------------------
 
 // One block sums up to so many tokens, if it takes no more than so many rounds:
-// 1 x 16000 tokens 8.1 us in two rounds, 7.1 in two launches, whose second
-// costs the host 3 us; 100 x 80 10.3 in four, 7.0; 160 x 100 13.8 in five, 6.9;
-// 1 x 32000 13.6, 7.2.
+// 1 x 16000 tokens 8.4 us in two rounds, 6.9 in two launches, whose second
+// costs the host 3 us; 100 x 80 10.8 in four, 6.9; 160 x 100 14.6 in five, 6.9;
+// 1 x 32000 14.4, 7.2.
 constexpr uint64_t kSmallTokens = 16384, kSmallRounds = 4;
 // A sequence of more than kBlockTokens tokens (of fewer than kSomeRows
 // sequences: kSomeTokens) is a block's, else a wave's or less.  us, a block, a
-// wave: 30 x 1000 7.6, 9.6; 1000 x 1000 11.3, 12.5; 1000 x 512 10.8, 9.1; 2000 x
-// 1000 15.0, 14.3; 1500 x 4001 22.9, 29.8; 4096 x 4096 40.4, 42.4.
+// wave: 30 x 1000 7.6, 9.9; 1000 x 1000 11.5, 12.8; 1000 x 512 10.9, 9.2; 2000 x
+// 1000 14.6, 14.6; 1500 x 4001 22.5, 31.3; 4096 x 4096 39.5, 43.5.
 constexpr uint32_t kBlockTokens = 1024, kSomeTokens = 512, kSomeRows = 1024;
 // Records of sums: at most this many blocks, five a CU, which the kernel's
-// registers (96 a lane) leave room for.  4096 x 4096 and 1115 x 13042 37.3 and
-// 38.0 us; with 1024 39.4, 44.3; 1536 40.0, 37.8; 2048 39.5, 39.1; 4096 39.8,
-// 38.1 (with 106 registers, four blocks a CU, 40.0 and 44.3).
+// registers (up to 96 a lane) leave room for.  4096 x 4096 and 1115 x 13042 39.8
+// and 39.0 us; with 1024 41.9, 45.7; 1536 41.6, 39.2; 2048 42.4, 39.0; 4096 42.5,
+// 39.3.
 constexpr uint64_t kRecords = 1280;
 
 // Lanes that share a sequence: each takes four tokens at a time.  (Fewer than
