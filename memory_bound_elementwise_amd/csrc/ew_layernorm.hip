@@ -757,9 +757,10 @@ __global__ void __launch_bounds__(kSumCols * kSumParts) ew_layernorm_sums_kernel
 // ---------------------------------------------------------------------------
 // Gradient, longer rows: what the rounded means lost, the parts' sums of dweight
 // and dbias (a thread a vector of columns over a part of the rows), their sum,
-// then dx (a block a row, two passes over it).  dx comes last: it may be dy or x.  1820 x 18432 with
-// dtotal 196 us of f32 and 115 of bf16, 1000 x 40000 bf16 145: dy and x are read
-// three times, the second pass over a row from the caches.
+// then dx (a block a row, two passes over it).  dx comes last: it may be dy or x.
+// 1820 x 18432 with dtotal 196 us of f32 and 115 of bf16, 1000 x 40000 bf16 145
+// (191, 111 and 142 without the first launch): dy and x are read three times, the
+// second pass over a row from the caches.
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kColsBlock = 256;
@@ -1006,7 +1007,7 @@ static hipError_t layernorm_grad_by(const LayerNormGradArgs &a, uint32_t vectors
 #define EW_LAYERNORM_GRAD_LAUNCH(W, V, G, TINY)                                                   \
     {                                                                                             \
         const uint64_t blocks = ((uint64_t)a.rows + G - 1) / G;                                   \
-        *parts = parts_for(blocks, G, vectors, a.dweight || a.dbias);                                                   \
+        *parts = parts_for(blocks, G, vectors, a.dweight || a.dbias);                             \
         return start(reinterpret_cast<const void *>(&ew_layernorm_back_kernel<T, W, V, G, TINY>), \
                      dim3(*parts), W * 64 * G, 0, s, a);                                          \
     }

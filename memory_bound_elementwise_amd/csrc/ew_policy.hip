@@ -48,11 +48,12 @@ __device__ __forceinline__ Token token(const PolicyTokens &in, float logp, float
 {
     Token t;
     t.x = (double)logp - (double)old;
-    t.clipped = (a > 0.0f && t.x > in.above) || (a < 0.0f && t.x < in.below);
+    const bool gains = a > 0.0f, pays = a < 0.0f;
+    t.clipped = (gains && t.x > in.above) || (pays && t.x < in.below);
     t.ratio = exp_nat((float)t.x);
     // a token of no advantage gains nothing, also where binary32 does not hold the
     // ratio (a NaN stays)
-    if (a == 0.0f && t.ratio == kInf) t.ratio = 1.0f;
+    if (t.ratio == kInf && !gains && !pays) t.ratio = 1.0f;
     t.one = 0.0f;
     t.line = 0.0f;
     if constexpr (Ref) {
