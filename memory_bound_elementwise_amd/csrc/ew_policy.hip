@@ -192,11 +192,11 @@ __device__ __forceinline__ void each_four(const PolicyTokens &in, const PolicyRo
 // ---------------------------------------------------------------------------
 // Forward: sums over parts of the batch, then their join (a second launch: a
 // last block that joins would need a counter that is 0 before the call).  Both
-// in one block for few tokens.  4096 x 4096 tokens, half of them counted: 37.5
+// in one block for few tokens.  4096 x 4096 tokens, half of them counted: 36.4
 // us, of which 4.5 are the join's.  143 MB are read, 21 us; the rest is that
 // sequences end at different times, and a block's sequences after another on
-// the way (every block is on the chip at once; the vector unit is busy 49 % of
-// the cycles).  8 x 512 tokens: 5.6 us, latency.
+// the way (every block is on the chip at once; the vector unit is busy 51 % of
+// the cycles).  8 x 512 tokens: 5.5 us, latency.
 // ---------------------------------------------------------------------------
 
 // Sums over tokens: of -gain, of exp(d) - 1 - d (both weighed within their
@@ -524,8 +524,8 @@ constexpr uint64_t kSmallTokens = 16384, kSmallRounds = 4;
 // 1000 14.6, 14.6; 1500 x 4001 22.5, 31.3; 4096 x 4096 39.5, 43.5.
 constexpr uint32_t kBlockTokens = 1024, kSomeTokens = 512, kSomeRows = 1024;
 // Records of sums: at most this many blocks, five a CU, which the kernel's
-// registers (up to 96 a lane) leave room for.  4096 x 4096 and 1115 x 13042 39.8
-// and 39.0 us; with 1024 41.9, 45.7; 1536 41.6, 39.2; 2048 42.4, 39.0; 4096 42.5,
+// registers (up to 96 a lane) leave room for.  4096 x 4096 and 1115 x 13042 38.7
+// and 38.8 us; with 1024 41.9, 45.7; 1536 41.6, 39.2; 2048 42.4, 39.0; 4096 42.5,
 // 39.3.
 constexpr uint64_t kRecords = 1280;
 
